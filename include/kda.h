@@ -45,11 +45,23 @@ extern "C" {
 
 /* Flags of kda_prefill_ex. */
 #define KDA_FLAG_BETA_LOGIT 1u /* beta holds logits; the operation uses sigmoid(beta) */
+/* Flags of the operators around the prefill (each lists the ones it takes). */
+#define KDA_FLAG_STATE_F32 2u     /* states are FP32 (BF16 without it) */
+#define KDA_FLAG_G_PER_HEAD 4u    /* g is [H], one constant decay for each head */
+#define KDA_FLAG_WEIGHT_F32 8u    /* norm weights (and a channel gate) are FP32 (BF16 without it) */
+#define KDA_FLAG_GATE_FIRST 16u   /* the gate multiplies before the norm */
+#define KDA_FLAG_RESIDUAL_F32 32u /* the residual stream is FP32 (BF16 without it) */
+
+/* Activations of kda_gated_norm. */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SIGMOID 1
+#define KDA_ACT_SILU 2
 
 /* Device-side status bits, reported by kda_device_status(). */
 #define KDA_DEV_BAD_SEQLENS 1  /* cu_seqlens broke its contract; out/final_state untouched */
 #define KDA_DEV_PIPE_TIMEOUT 2 /* an internal pipeline wait hit its bound; results incomplete */
 #define KDA_DEV_BAD_CHECKPOINTS 4 /* a checkpoint had no valid row in checkpoint_cu_starts; skipped */
+#define KDA_DEV_BAD_SLOTS 8    /* a state slot lay outside the pool; that row's state untouched, out zero */
 
 /*
  * KDA prefill, fixed or packed variable-length layout.
@@ -137,7 +149,8 @@ int kda_set_host_pieces(int n);
 
 /*
  * Number of kernels (HOST out) that the last kda_prefill, kda_prefill_checkpointed
- * or kda_prefill_host call made on this host thread enqueued (memsets and copies
+ * or kda_prefill_host call, or call of the operators at the end of this header, made on this host
+ * thread enqueued (memsets and copies
  * are not counted; after a call that returned an error the count may include
  * the launch that failed).
  */
@@ -398,6 +411,102 @@ int kda_prefill_noalloc(const void* q, const void* k, const void* v, const float
 
 /* Size in bytes of kda_prefill_noalloc's fixed scratch array. */
 int64_t kda_noalloc_scratch_bytes(void);
+
+/* ------------------------------------------------------------------------
+ * Operators around the prefill.  As above: DEVICE pointers, asynchronous on
+ * `stream`, no host synchronisation, CUDA-graph capturable, contiguous
+ * tensors, KDA_OK or a negative KDA_ERR_* code with nothing launched
+ * (KDA_ERR_ARG for a flag that the call does not take).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Linear attention with one decay per head and token, over whole prompts:
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ * with S a 128 x 128 matrix (value rows x key columns) per sequence and head.
+ * q and k are taken as they are (no normalisation).
+ *
+ *   q, k        : BF16 [B, T, Hk, 128]; head h uses key head h / (H / Hk), Hk divides H
+ *   v, out      : BF16 [B, T, H, 128]
+ *   g           : FP32 [B, T, H], natural-log decay, g <= 0 (-inf forgets the state);
+ *                 with KDA_FLAG_G_PER_HEAD FP32 [H], the same for every token
+ *   init_state  : [N, H, 128, 128] or NULL for zeros; BF16, or FP32 with KDA_FLAG_STATE_F32
+ *   final_state : the same type, or NULL (not written); may be init_state
+ * Fixed and packed layouts, cu_seqlens, empty sequences, alignment, overlap
+ * rules, limits and the T = 0 rule are those of kda_prefill (g: 4 bytes).
+ * The state is held in FP32 throughout; a NaN or an infinity in a token
+ * reaches no earlier token and no other sequence.
+ * When there are too few (sequence, head) chains to fill the GPU, each
+ * sequence is cut into segments of whole 128-token chunks: one launch forms
+ * the state each segment adds, one chains them, and one forms the outputs
+ * from the segments' incoming states.  kda_set_segments governs this too
+ * (off: never; a forced length is rounded up to whole 128-token chunks).
+ * Scratch comes from the library's stream-ordered pool.
+ */
+int kda_la_prefill(const void* q, const void* k, const void* v, const float* g,
+                   const void* init_state, void* out, void* final_state, int64_t B, int64_t T,
+                   int64_t H, int64_t Hk, const int64_t* cu_seqlens, float scale, uint32_t flags,
+                   void* stream);
+
+/*
+ * One token per sequence of the same operation, on a pool of states:
+ *   q, k [N, Hk, 128], v, out [N, H, 128] BF16; g FP32 [N, H] (or [H]);
+ *   state : [pool, H, 128, 128], BF16 or FP32 as above, updated in place
+ *   slots : int32 [N], the pool row of each sequence, no row twice; negative:
+ *           padding (out row zero, no state touched).  NULL: row n is slot n (N <= pool).
+ * A slot >= pool sets KDA_DEV_BAD_SLOTS and is treated as padding.  N = 0 does
+ * nothing.  Alignment: q, k, v, out, state 16 bytes, g and slots 4.
+ */
+int kda_la_decode(const void* q, const void* k, const void* v, const float* g, void* state,
+                  const int32_t* slots, void* out, int64_t N, int64_t H, int64_t Hk, int64_t pool,
+                  float scale, uint32_t flags, void* stream);
+
+/*
+ * One token per sequence of kda_prefill's operation (q and k L2-normalised
+ * inside, scale 1/sqrt(128)), on a pool of states: q, k, v, out BF16
+ * [N, H, 128], g FP32 [N, H, 128], beta BF16 [N, H] (logits with
+ * KDA_FLAG_BETA_LOGIT); state, slots and their errors as kda_la_decode
+ * (beta 2 bytes, g 16 bytes aligned).
+ */
+int kda_decode(const void* q, const void* k, const void* v, const float* g, const void* beta,
+               void* state, const int32_t* slots, void* out, int64_t N, int64_t H, int64_t pool,
+               uint32_t flags, void* stream);
+
+/*
+ * The norm after a mixer with its gate, for each row of 128 channels (a token's head):
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate),
+ * or, with KDA_FLAG_GATE_FIRST, the norm of x act(gate) times weight.
+ *   x, gate, out : BF16 [rows, 128]; weight: [128], BF16 or FP32 (KDA_FLAG_WEIGHT_F32)
+ *   activation   : KDA_ACT_NONE (gate is not read and may be NULL), KDA_ACT_SIGMOID
+ *                  or KDA_ACT_SILU.  out may be x or gate.  eps >= 0.
+ */
+int kda_gated_norm(const void* x, const void* weight, const void* gate, void* out, int64_t rows,
+                   int activation, float eps, uint32_t flags, void* stream);
+
+/*
+ * Between two blocks: the norm after a block, its gate and residual scale,
+ * the residual sum, and the norm before the next block, for each row:
+ *     u = x                                  (post_weight NULL), else
+ *     u = x / sqrt(mean(x^2) + eps) * post_weight
+ *     r' = residual + scale * gate * u       (gate NULL: 1)
+ *     out = r' / sqrt(mean(r'^2) + eps) * weight      (r' before its rounding)
+ *   x, out                 : BF16 [rows, dim], 1 <= dim <= 32768
+ *   residual, residual_out : [rows, dim], BF16 or FP32 (KDA_FLAG_RESIDUAL_F32)
+ *   weight, post_weight, gate : [dim], BF16 or FP32 (KDA_FLAG_WEIGHT_F32)
+ * residual_out may be residual, and out may be x; other overlaps are refused.
+ * Alignment: 16 bytes for every tensor.
+ */
+int kda_residual_norm(const void* x, const void* residual, const void* weight,
+                      const void* post_weight, const void* gate, void* out, void* residual_out,
+                      int64_t rows, int64_t dim, float scale, float eps, uint32_t flags,
+                      void* stream);
+
+/*
+ * Segments per sequence kda_la_prefill would use for a call of this shape
+ * (packed: a bound on all segments; 0: none), and the bytes of scratch it
+ * takes at most (HOST out).  As kda_plan_segments and kda_workspace_bytes.
+ */
+int kda_la_plan_segments(int64_t B, int64_t T, int64_t H, int packed, int64_t* segs);
+int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packed, int64_t* bytes);
 
 #ifdef __cplusplus
 }

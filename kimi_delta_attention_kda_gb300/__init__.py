@@ -9,7 +9,8 @@ streams.  There is no CPU path.
 from __future__ import annotations
 
 from . import _lib
-from ._lib import (KdaError, auto_split, device_status, packet_bytes, plan_fused,
+from ._lib import (KdaError, auto_split, device_status, la_plan_segments, la_workspace_bytes,
+                   packet_bytes, plan_fused,
                    plan_long_split, plan_segments, set_engine, set_fusion, set_segments,
                    set_split, workspace_bytes)
 
@@ -18,7 +19,20 @@ HEAD_DIM = 128
 __all__ = ["kda_prefill", "kda_prefill_host", "prep_only", "KdaError", "device_status", "set_split", "set_engine",
            "set_fusion", "plan_fused", "plan_long_split", "set_segments", "plan_segments",
            "auto_split",
-           "workspace_bytes", "packet_bytes", "HEAD_DIM"]
+           "workspace_bytes", "packet_bytes", "HEAD_DIM", "la_prefill", "la_decode", "kda_decode",
+           "gated_norm", "residual_norm", "la_plan_segments", "la_workspace_bytes"]
+
+_OPS = ("la_prefill", "la_decode", "kda_decode", "gated_norm", "residual_norm")
+
+
+def __getattr__(name):
+    # The operators around the prefill live in .ops, which needs torch at
+    # import time; this package itself imports without it.
+    if name in _OPS:
+        from . import ops
+        globals().update({op: getattr(ops, op) for op in _OPS})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def _require(cond, msg):

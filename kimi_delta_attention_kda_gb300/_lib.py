@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libkda.so")
 KDA_OK = 0
 KDA_DEV_BAD_SEQLENS = 1
 KDA_DEV_PIPE_TIMEOUT = 2
+KDA_DEV_BAD_SLOTS = 8
 
 _lock = threading.Lock()
 _lib = None
@@ -31,6 +32,8 @@ class KdaError(RuntimeError):
 def load():
     """Load ``libkda.so`` (built by ``kimi_delta_attention_kda_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -90,6 +93,17 @@ def load():
         lib.kda_prefill_noalloc.restype = I
         lib.kda_noalloc_scratch_bytes.argtypes = []
         lib.kda_noalloc_scratch_bytes.restype = I64
+        U32, F = ctypes.c_uint32, ctypes.c_float
+        lib.kda_la_prefill.argtypes = [P] * 7 + [I64] * 4 + [P, F, U32, P]
+        lib.kda_la_decode.argtypes = [P] * 7 + [I64] * 4 + [F, U32, P]
+        lib.kda_decode.argtypes = [P] * 8 + [I64] * 3 + [U32, P]
+        lib.kda_gated_norm.argtypes = [P] * 4 + [I64, I, F, U32, P]
+        lib.kda_residual_norm.argtypes = [P] * 7 + [I64, I64, F, F, U32, P]
+        lib.kda_la_plan_segments.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
+        lib.kda_la_workspace_bytes.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
+        for fn in (lib.kda_la_prefill, lib.kda_la_decode, lib.kda_decode, lib.kda_gated_norm,
+                   lib.kda_residual_norm, lib.kda_la_plan_segments, lib.kda_la_workspace_bytes):
+            fn.restype = I
         _lib = lib
         return lib
 
@@ -146,6 +160,11 @@ def prefill_checkpointed_raw(q, k, v, g, beta, init_state, out, final_state, B, 
 
 
 FLAG_BETA_LOGIT = 1
+FLAG_STATE_F32 = 2
+FLAG_G_PER_HEAD = 4
+FLAG_WEIGHT_F32 = 8
+FLAG_GATE_FIRST = 16
+FLAG_RESIDUAL_F32 = 32
 
 
 def prefill_ex_raw(q, k, v, g, beta, init_state, out, final_state, B, T, H, cu_seqlens, flags,
@@ -269,3 +288,18 @@ def prefill_noalloc_raw(q, k, v, g, beta, init_state, out, final_state, B, T, H,
 
 def noalloc_scratch_bytes() -> int:
     return int(load().kda_noalloc_scratch_bytes())
+
+
+def la_plan_segments(B: int, T: int, H: int, packed: bool) -> int:
+    """Segments per sequence la_prefill uses for this shape (0: one chain per sequence)."""
+    out = ctypes.c_int64(0)
+    _check(load().kda_la_plan_segments(int(B), int(T), int(H), 1 if packed else 0,
+                                       ctypes.byref(out)), "kda_la_plan_segments")
+    return int(out.value)
+
+
+def la_workspace_bytes(B: int, T: int, H: int, packed: bool) -> int:
+    out = ctypes.c_int64(0)
+    _check(load().kda_la_workspace_bytes(int(B), int(T), int(H), 1 if packed else 0,
+                                         ctypes.byref(out)), "kda_la_workspace_bytes")
+    return int(out.value)

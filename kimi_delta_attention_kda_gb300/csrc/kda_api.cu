@@ -446,6 +446,25 @@ int device_context(int** status, int64_t units, int* nsplit) {
     return KDA_OK;
 }
 
+int device_view(DeviceView* view) {
+    DeviceState* d = nullptr;
+    int rc = device_state(&d);
+    if (rc != KDA_OK) return rc;
+    view->status = d->status;
+    view->pool = d->pool;
+    view->sms = d->sms;
+    segment_settings(&view->segments, &view->seg_chunks);
+    return KDA_OK;
+}
+
+void segment_settings(int* segments, int64_t* seg_chunks) {
+    *segments = g_segments;
+    *seg_chunks = g_seg_chunks;
+}
+
+void reset_launches() { t_launches = 0; }
+void add_launches(int n) { t_launches += n; }
+
 }  // namespace kda
 
 using namespace kda;

@@ -176,6 +176,67 @@ cudaError_t encode_state_map(CUtensorMap* map, const void* base, int64_t rows, i
 // Recurrence engine: 0 automatic, 1 column-split warp MMA, 2 tcgen05.
 int recurrence_engine();
 
+// The per-device state that entry points outside kda_api.cu need.
+struct DeviceView {
+    int* status;          // device status word
+    cudaMemPool_t pool;   // the library's stream-ordered pool
+    int sms;
+    int segments;         // kda_set_segments: allowed, and the forced segment
+    int64_t seg_chunks;   // length in 16-token chunks (0: automatic)
+};
+int device_view(DeviceView* view);
+void segment_settings(int* segments, int64_t* seg_chunks);
+// kda_last_call_launches of this host thread: start at zero, and add.
+void reset_launches();
+void add_launches(int n);
+
+// --- Operators around the prefill ------------------------------------------
+
+struct LaArgs {
+    const void *q, *k, *v;
+    const float* g;
+    int64_t g_stride;          // H, or 0 for one decay per head
+    const void* init_state;
+    void *out, *final_state;
+    int64_t N, tokens, tokens_per_seq;   // tokens_per_seq: fixed layout only
+    int64_t H, Hk;
+    const int64_t* cu_seqlens;           // packed only
+    const int32_t* valid;                // packed only: the metadata's verdict
+    float scale;
+    bool state_f32;
+    int* status;
+};
+cudaError_t launch_la_prefill(const LaArgs& a, cudaStream_t stream);
+
+struct StepArgs {
+    const void *q, *k, *v;
+    const float* g;
+    int64_t g_stride;          // la: H, or 0
+    const void* beta;          // kda only
+    void* state;
+    const int32_t* slots;
+    void* out;
+    int64_t N, H, Hk, pool;
+    float scale;
+    bool state_f32, beta_logit;
+    int* status;
+};
+cudaError_t launch_step(const StepArgs& a, bool delta, int sms, cudaStream_t stream);
+
+cudaError_t launch_gated_norm(const void* x, const void* weight, const void* gate, void* out,
+                              int64_t rows, int activation, bool gate_first, bool weight_f32,
+                              float eps, cudaStream_t stream);
+
+struct ResidualNormArgs {
+    const void *x, *residual, *weight, *post_weight, *gate;
+    void *out, *residual_out;
+    int64_t rows, dim;
+    float scale, eps;
+    bool weight_f32, residual_f32;
+};
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, int sms, cudaStream_t stream);
+constexpr int64_t kMaxNormDim = 32768;
+
 // Per-device status word and the split kda_prefill picks for `units`
 // (sequence x head) recurrences, for entry points outside kda_api.cu.
 int device_context(int** status, int64_t units, int* nsplit);

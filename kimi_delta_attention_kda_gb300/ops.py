@@ -1,0 +1,272 @@
+"""The operators around the prefill: per-head-decay linear attention, the
+single-token steps, and the norms around a block.
+
+Argument checks and marshalling only: the work runs in ``libkda.so``
+(``include/kda.h``, "Operators around the prefill").  Every call is
+asynchronous on ``stream`` (default: the current PyTorch stream), takes
+contiguous CUDA tensors of the current device, and can be captured into a
+CUDA graph.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._lib import KdaError
+
+HEAD_DIM = 128
+_SCALE = HEAD_DIM ** -0.5
+_STATE_TYPES = (torch.float32, torch.bfloat16)
+_ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def _need(name, t, dtypes, shape):
+    """`t` is a contiguous CUDA tensor of one of `dtypes` with this shape."""
+    if not (t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s CUDA tensor"
+                         % (name, " or ".join(str(d) for d in dtypes)))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, list(shape), list(t.shape)))
+
+
+def _on_current_device(t):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+
+
+def _same_device(q, *others):
+    for t in others:
+        if t is not None and t.device != q.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_state=None,
+               output_final_state=True, state_dtype=torch.float32, scale=None, stream=None):
+    """Linear attention with one decay per head and token over whole prompts;
+    returns ``(out, final_state)``:
+
+        S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t
+
+    q, k: bf16 ``[B, T, Hk, 128]`` (Hk divides H; head h uses key head
+    ``h // (H // Hk)``); v: bf16 ``[B, T, H, 128]``; g: fp32 ``[B, T, H]``
+    log-decays <= 0, or ``[H]``, constant for each head; init_state:
+    ``[N, H, 128, 128]`` (value rows x key columns), fp32 or bf16, or None for
+    zeros; cu_seqlens: int64 ``[N + 1]`` on the device for the packed layout
+    (then ``B == 1``).  ``final_state`` may be ``init_state``; a new one takes
+    the type of ``init_state``, or ``state_dtype`` without one.  ``scale``
+    defaults to 1/sqrt(128).
+    """
+    if q.dim() != 4 or v.dim() != 4 or q.shape[3] != HEAD_DIM:
+        raise ValueError("q and v must be [B, T, heads, 128]")
+    B, T, Hk, _ = q.shape
+    H = v.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError("the heads of v must be a multiple of the heads of q")
+    _need("q", q, _BF16, q.shape)
+    _need("k", k, _BF16, q.shape)
+    _need("v", v, _BF16, (B, T, H, HEAD_DIM))
+    flags = 0
+    if g.dim() == 1:
+        _need("g", g, _F32, (H,))
+        flags = _lib.FLAG_G_PER_HEAD
+    else:
+        _need("g", g, _F32, (B, T, H))
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("packed input needs B == 1")
+        N = cu_seqlens.numel() - 1
+        _need("cu_seqlens", cu_seqlens, (torch.int64,), (N + 1,))
+    if init_state is not None:
+        _need("init_state", init_state, _STATE_TYPES, (N, H, HEAD_DIM, HEAD_DIM))
+        state_dtype = init_state.dtype
+    elif final_state is not None:
+        state_dtype = final_state.dtype
+    if state_dtype not in _STATE_TYPES:
+        raise ValueError("states are torch.float32 or torch.bfloat16")
+    if final_state is not None:
+        _need("final_state", final_state, (state_dtype,), (N, H, HEAD_DIM, HEAD_DIM))
+    elif output_final_state:
+        final_state = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=state_dtype, device=q.device)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, _BF16, v.shape)
+    _same_device(q, k, v, g, init_state, cu_seqlens, out, final_state)
+    _on_current_device(q)
+    if state_dtype is torch.float32:
+        flags |= _lib.FLAG_STATE_F32
+    rc = _lib.load().kda_la_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(init_state), _ptr(out),
+                                    _ptr(final_state), N, T, H, Hk, _ptr(cu_seqlens),
+                                    _SCALE if scale is None else scale, flags, _stream(stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_la_prefill")
+    return out, final_state
+
+
+def _step_args(q, k, v, state, slots, out):
+    """Checks of q, k, v, state and slots of a single-token step; (N, H, Hk, pool, out)."""
+    if q.dim() != 3 or v.dim() != 3 or q.shape[2] != HEAD_DIM or state.dim() != 4:
+        raise ValueError("q and v must be [N, heads, 128], and state [pool, H, 128, 128]")
+    N, Hk, _ = q.shape
+    H, pool = v.shape[1], state.shape[0]
+    _need("q", q, _BF16, (N, Hk, HEAD_DIM))
+    _need("k", k, _BF16, (N, Hk, HEAD_DIM))
+    _need("v", v, _BF16, (N, H, HEAD_DIM))
+    _need("state", state, _STATE_TYPES, (pool, H, HEAD_DIM, HEAD_DIM))
+    if slots is not None:
+        _need("slots", slots, (torch.int32,), (N,))
+    elif N > pool:
+        raise ValueError("state has fewer rows than there are sequences")
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, _BF16, (N, H, HEAD_DIM))
+    _same_device(q, k, v, state, slots, out)
+    _on_current_device(q)
+    return N, H, Hk, pool, out
+
+
+def la_decode(q, k, v, g, state, slots=None, out=None, scale=None, stream=None):
+    """One token per sequence of ``la_prefill``'s operation; returns ``out``
+    and updates ``state`` in place.
+
+    q, k: bf16 ``[N, Hk, 128]``; v: bf16 ``[N, H, 128]``; g: fp32 ``[N, H]`` or
+    ``[H]``; state: fp32 or bf16 ``[pool, H, 128, 128]``; slots: int32 ``[N]`` on
+    the device, the pool row of each sequence (no row twice; negative: a padding
+    row, whose output is zero), or None for rows 0 .. N - 1.  A slot beyond the
+    pool is treated as padding and sets ``KDA_DEV_BAD_SLOTS`` (``device_status``).
+    """
+    N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    if Hk < 1 or H % Hk:
+        raise ValueError("the heads of v must be a multiple of the heads of q")
+    flags = _lib.FLAG_STATE_F32 if state.dtype is torch.float32 else 0
+    if g.dim() == 1:
+        _need("g", g, _F32, (H,))
+        flags |= _lib.FLAG_G_PER_HEAD
+    else:
+        _need("g", g, _F32, (N, H))
+    _same_device(q, g)
+    rc = _lib.load().kda_la_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(slots),
+                                   _ptr(out), N, H, Hk, pool, _SCALE if scale is None else scale,
+                                   flags, _stream(stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_la_decode")
+    return out
+
+
+def kda_decode(q, k, v, g, beta, state, slots=None, out=None, beta_is_logit=False, stream=None):
+    """One token per sequence of ``kda_prefill``'s operation (q and k are
+    L2-normalised inside); returns ``out`` and updates ``state`` in place.
+
+    q, k, v: bf16 ``[N, H, 128]``; g: fp32 ``[N, H, 128]``; beta: bf16 ``[N, H]``;
+    state and slots as for ``la_decode``: ``kda_prefill``'s final state (bf16) is
+    such a state, and its fp32 copy keeps long generations from rounding it at
+    every token.
+    """
+    N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    if Hk != H:
+        raise ValueError("q must have the shape of v")
+    _need("g", g, _F32, (N, H, HEAD_DIM))
+    _need("beta", beta, _BF16, (N, H))
+    _same_device(q, g, beta)
+    flags = ((_lib.FLAG_STATE_F32 if state.dtype is torch.float32 else 0) |
+             (_lib.FLAG_BETA_LOGIT if beta_is_logit else 0))
+    rc = _lib.load().kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+                                _ptr(slots), _ptr(out), N, H, pool, flags, _stream(stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_decode")
+    return out
+
+
+def gated_norm(x, weight, gate=None, activation="sigmoid", gate_first=False, eps=1e-6, out=None,
+               stream=None):
+    """RMS norm over the last 128 channels with an output gate; returns ``out``:
+    ``x / rms(x) * weight * act(gate)``, or with ``gate_first`` the norm of
+    ``x * act(gate)`` times weight.
+
+    x, gate, out: bf16 ``[..., 128]``; weight: bf16 or fp32 ``[128]``;
+    activation: "sigmoid", "silu", or "none" (no gate).  Without a gate the
+    activation is "none".  ``out`` may be ``x`` or ``gate``.
+    """
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(sorted(_ACTIVATIONS)))
+    act = _ACTIVATIONS[activation] if gate is not None else 0
+    if x.dim() < 1 or x.shape[-1] != HEAD_DIM:
+        raise ValueError("x must be [..., 128]")
+    _need("x", x, _BF16, x.shape)
+    _need("weight", weight, _STATE_TYPES, (HEAD_DIM,))
+    if act:
+        _need("gate", gate, _BF16, x.shape)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need("out", out, _BF16, x.shape)
+    _same_device(x, weight, gate, out)
+    _on_current_device(x)
+    flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
+             (_lib.FLAG_GATE_FIRST if gate_first else 0))
+    rc = _lib.load().kda_gated_norm(_ptr(x), _ptr(weight), _ptr(gate) if act else None, _ptr(out),
+                                    x.numel() // HEAD_DIM, act, eps, flags, _stream(stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_gated_norm")
+    return out
+
+
+def residual_norm(x, residual, weight, post_weight=None, gate=None, scale=1.0, eps=1e-6, out=None,
+                  residual_out=None, stream=None):
+    """The residual sum between two blocks with the norms around it; returns
+    ``(out, residual_out)``:
+
+        u = x / rms(x) * post_weight          (x itself without post_weight)
+        residual_out = residual + scale * gate * u
+        out = residual_out / rms(residual_out) * weight
+
+    x, out: bf16 ``[..., D]``, D up to 32768; residual: bf16 or fp32 of that
+    shape; weight, post_weight, gate: bf16 or fp32 ``[D]``, all of one type.
+    ``residual_out`` may be ``residual`` and ``out`` may be ``x``.
+    """
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    _need("x", x, _BF16, x.shape)
+    _need("residual", residual, _STATE_TYPES, x.shape)
+    _need("weight", weight, _STATE_TYPES, (D,))
+    wt = (weight.dtype,)
+    if post_weight is not None:
+        _need("post_weight", post_weight, wt, (D,))
+    if gate is not None:
+        _need("gate", gate, wt, (D,))
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need("out", out, _BF16, x.shape)
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    else:
+        _need("residual_out", residual_out, (residual.dtype,), x.shape)
+    _same_device(x, residual, weight, post_weight, gate, out, residual_out)
+    _on_current_device(x)
+    flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
+             (_lib.FLAG_RESIDUAL_F32 if residual.dtype is torch.float32 else 0))
+    rc = _lib.load().kda_residual_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(post_weight),
+                                       _ptr(gate), _ptr(out), _ptr(residual_out), x.numel() // D, D,
+                                       scale, eps, flags, _stream(stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_residual_norm")
+    return out, residual_out
