@@ -78,7 +78,6 @@ enum DeviceStatus : int {
     kDevBadSeqlens = 1,     // cu_seqlens violated its contract; outputs untouched
     kDevPipeTimeout = 2,    // a pipeline wait ran past its bound; outputs incomplete
     kDevBadCheckpoints = 4, // a checkpoint had no valid row in the caller's offsets; not written
-    kDevBadSlots = 8,       // a state slot outside the pool; its row skipped
 };
 
 // Varlen metadata written by the metadata kernel at the start of the workspace.

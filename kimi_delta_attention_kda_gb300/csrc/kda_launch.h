@@ -192,6 +192,9 @@ void add_launches(int n);
 
 // --- Operators around the prefill ------------------------------------------
 
+// Device status bit beside those of kda_common.cuh: a state slot outside the pool.
+constexpr int kDevBadSlots = 8;
+
 struct LaArgs {
     const void *q, *k, *v;
     const float* g;
