@@ -209,7 +209,19 @@ struct LaArgs {
     bool state_f32;
     int* status;
 };
-cudaError_t launch_la_prefill(const LaArgs& a, cudaStream_t stream);
+constexpr int kLaChunk = 128;   // tokens of a chunk of kda_la_prefill
+// The cut of every sequence into segments of whole chunks (starts null: none).
+struct LaSegments {
+    float* starts;             // [total][H][128][128]: what a segment adds, then its incoming state
+    float* decay;              // [total][H]: its decay in base 2
+    int64_t total;             // segments (packed: a bound)
+    int64_t segs;              // fixed layout: segments of each sequence
+    int64_t seg_tokens_each;   // fixed layout: tokens of each but the last
+    const int64_t *seg_begin, *seg_tokens, *seg_seq;   // packed: launch_segment_meta's table
+};
+// Adds the kernels it launches to *launches.
+cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream,
+                              int* launches);
 
 struct StepArgs {
     const void *q, *k, *v;

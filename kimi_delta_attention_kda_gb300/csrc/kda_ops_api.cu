@@ -48,6 +48,52 @@ int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
     return KDA_OK;
 }
 
+// The cut of a call's sequences into segments (see kda_la_prefill).  Costs in
+// microseconds, measured on GB300: a chunk of a chain, of the pass that forms
+// what the segments add, and a step of the chain over the segments; the two
+// further launches.
+constexpr double kChunkUs = 1.8;
+constexpr double kAddChunkUs = 1.2;
+constexpr double kScanStepUs = 0.1;
+constexpr double kCutUs = 8.0;
+
+struct LaCut {
+    int64_t chunks = 0;        // chunks of a segment (0: no cut)
+    int64_t segs = 0;          // fixed: segments of each sequence; packed: a bound on all
+    int64_t total = 0;
+    int64_t bytes = 0;         // starts, decays and the packed segment table
+};
+
+LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64_t forced) {
+    LaCut c;
+    if (!allowed || pl.tokens <= 0) return c;
+    const int64_t units = pl.N * H;
+    // Packed lengths stay on the device: plan on their mean.
+    const double mean = static_cast<double>(pl.tokens) / static_cast<double>(pl.N) / kLaChunk;
+    const int64_t seq_chunks = pl.packed ? static_cast<int64_t>(mean) + 1 : (T + kLaChunk - 1) / kLaChunk;
+    if (forced > 0) {
+        c.chunks = (forced + kLaChunk / 16 - 1) / (kLaChunk / 16);
+    } else {
+        if (2 * units > sms) return c;
+        const int64_t want = sms / units;
+        c.chunks = (seq_chunks + want - 1) / want;
+        const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
+        const double cut = kCutUs + c.chunks * (kChunkUs + kAddChunkUs) + segs * kScanStepUs;
+        if (segs < 2 || cut >= seq_chunks * kChunkUs) return LaCut();
+    }
+    if (pl.packed) {
+        c.segs = pl.tokens / (c.chunks * kLaChunk) + pl.N;
+        c.total = c.segs;
+    } else {
+        c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
+        c.total = c.segs * pl.N;
+    }
+    if (c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return LaCut();
+    c.bytes = align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
+    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 3 * align256(8 * (c.segs + 1));
+    return c;
+}
+
 // q, k, v, out, state and slots of a single-token step.
 int check_step(const StepArgs& a, int64_t g_bytes, int64_t g_align) {
     if (a.N < 0 || a.H < 1 || a.Hk < 1 || a.H % a.Hk || a.pool < 0) return KDA_ERR_SHAPE;
@@ -133,28 +179,50 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
     a.Hk = Hk;
     a.scale = scale;
     a.status = d.status;
+    const LaCut cut = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks);
     uint8_t* ws = nullptr;
-    if (pl.meta_bytes > 0 &&
-        cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), static_cast<size_t>(pl.meta_bytes),
+    if (pl.meta_bytes + cut.bytes > 0 &&
+        cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), static_cast<size_t>(pl.meta_bytes + cut.bytes),
                                 d.pool, stream) != cudaSuccess) {
         cudaGetLastError();
         return KDA_ERR_CUDA;
     }
+    LaSegments sg = {};
+    if (cut.chunks > 0) {
+        sg.starts = reinterpret_cast<float*>(ws + pl.meta_bytes);
+        sg.decay = sg.starts + align256(cut.total * H * kStateElems * 4) / 4;
+        sg.total = cut.total;
+        sg.segs = cut.segs;
+        sg.seg_tokens_each = cut.chunks * kLaChunk;
+    }
     if (pl.packed) {
         int32_t* valid = reinterpret_cast<int32_t*>(ws);
-        if (launch_varlen_meta(cu_seqlens, B, T, valid, reinterpret_cast<int64_t*>(ws + 256), nullptr,
-                               d.status, stream) != cudaSuccess)
+        int64_t* cu_chunks = reinterpret_cast<int64_t*>(ws + 256);
+        if (launch_varlen_meta(cu_seqlens, B, T, valid, cu_chunks, nullptr, d.status, stream) != cudaSuccess)
             rc = KDA_ERR_CUDA;
         else
             add_launches(1);
+        if (rc == KDA_OK && cut.chunks > 0) {
+            int64_t* begin = reinterpret_cast<int64_t*>(sg.decay) + align256(cut.total * H * 4) / 8;
+            int64_t* chunk0 = begin + align256(8 * (B + 1)) / 8;
+            int64_t* tokens = chunk0 + align256(8 * (cut.segs + 1)) / 8;
+            int64_t* seq = tokens + align256(8 * (cut.segs + 1)) / 8;
+            if (launch_segment_meta(cu_seqlens, cu_chunks, valid, B, cut.chunks * (kLaChunk / kChunk), cut.segs,
+                                    begin, chunk0, tokens, seq, d.status, stream) != cudaSuccess)
+                rc = KDA_ERR_CUDA;
+            else
+                add_launches(1);
+            sg.seg_begin = begin;
+            sg.seg_tokens = tokens;
+            sg.seg_seq = seq;
+        }
         a.cu_seqlens = cu_seqlens;
         a.valid = valid;
     }
     if (rc == KDA_OK) {
-        if (launch_la_prefill(a, stream) != cudaSuccess)
-            rc = KDA_ERR_CUDA;
-        else
-            add_launches(1);
+        int launches = 0;
+        if (launch_la_prefill(a, sg, d.sms, stream, &launches) != cudaSuccess) rc = KDA_ERR_CUDA;
+        add_launches(launches);
     }
     if (ws) cudaFreeAsync(ws, stream);
     if (rc != KDA_OK) cudaGetLastError();
@@ -169,7 +237,7 @@ extern "C" int kda_la_plan_segments(int64_t B, int64_t T, int64_t H, int packed,
     DeviceView d;
     rc = device_view(&d);
     if (rc != KDA_OK) return rc;
-    *segs = 0;
+    *segs = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks).segs;
     return KDA_OK;
 }
 
@@ -178,7 +246,13 @@ extern "C" int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packe
     LaPlan pl;
     int rc = plan_la(B, T, H, packed != 0, &pl);
     if (rc != KDA_OK) return rc;
-    *bytes = pl.meta_bytes;
+    // As planned on the current device (on a 152-SM device when there is none).
+    DeviceView d;
+    if (device_view(&d) != KDA_OK) {
+        d.sms = 152;
+        segment_settings(&d.segments, &d.seg_chunks);
+    }
+    *bytes = pl.meta_bytes + cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks).bytes;
     return KDA_OK;
 }
 

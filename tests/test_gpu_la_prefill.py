@@ -107,6 +107,24 @@ def test_segments(kda, seg, packed, init):
         kda.set_segments(True, 0)
 
 
+def test_planned_segments(kda):
+    """A shape that the plan itself cuts agrees with the uncut chain."""
+    assert kda.la_plan_segments(1, 4100, 2, False) > 1
+    d, rnd = inputs(1, 4100, 2, seed=9, low=-0.02)
+    init = rnd(1, 2, D, D)
+    out, fin = run(kda, d, init)
+    kda.set_segments(False)
+    try:
+        assert kda.la_plan_segments(1, 4100, 2, False) == 0
+        out2, fin2 = run(kda, d, init)
+    finally:
+        kda.set_segments(True, 0)
+    o, f, oa, fa = ref.la_tokens(d["q"], d["k"], d["v"], d["g"], init)
+    for x, y in ((out, fin), (out2, fin2)):
+        ref.assert_close(x, o, ref.HALF_BF16 * o.abs() + 2.1 * ref.HALF_BF16 * oa, "out")
+        ref.assert_close(y, f, 2.0 ** -14 * fa, "final state")
+
+
 @pytest.mark.parametrize("seg", [0, 8])
 @pytest.mark.parametrize("value", [-5.0, -40.0, -200.0, -1e30, float("-inf"), 0.0, -0.0])
 def test_decay_extremes(kda, value, seg):
