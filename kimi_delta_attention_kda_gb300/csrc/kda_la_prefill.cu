@@ -15,8 +15,9 @@
 //     D1[i][j] = Q K^T              Q, K from shared memory
 //     P[i][j]  = scale exp(G_i - G_j) D1, causal, BF16, in tensor memory
 //     O[i][c]  = Q' S^T + P V       Q' = scale exp(G_i) Q (BF16), S^T BF16 in shared memory
-//     Z[d][c]  = K'^T V             K'^T[d][j] = exp(G - G_j) k_jd, in tensor memory
-//     S^T[d][c] <- exp(G) S^T + Z   FP32 registers of the state warps
+//     S^T[d][c] <- exp(G) S^T + K'^T V   K'^T[d][j] = exp(G - G_j) k_jd, in tensor memory
+// S^T is FP32 in tensor memory: the state warps read it, write its BF16 copy
+// to shared memory and exp(G) S^T back, and K'^T V accumulates on that.
 // K' is split by truncation into three BF16 parts whose sum is the FP32
 // value, so the state is accurate to FP32: with two parts (16 bits) the final
 // state was off by 2e-6 of its norm, against 1e-7 for FP32 arithmetic.
@@ -25,19 +26,19 @@
 //
 // One CTA per SM walks (sequence or segment, head) units.  Warps: 8 state
 // (K' parts, S), 4 score (P), 4 output (Q', O), one each for the loads, the
-// MMA issue and the decay sums.  Z does not depend on S, so the only chain
-// from chunk to chunk is one multiply-add per element of S.  Tensor memory
-// columns: D1 and P [0, 128), O [128, 256), Z [256, 384), K' [384, 480) (two
-// buffers of 32 tokens x 3 parts).
+// MMA issue and the decay sums.  Tensor memory columns: D1 and P [0, 128),
+// O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32 tokens x 3
+// parts).
 //
 // A value that is not finite must not reach earlier tokens of its chunk: a
-// zero of P times an infinite V is NaN.  Z shows it (its whole column is then
-// not finite).  The state warps clear such values in shared memory once Z has
-// them, and the output warps add their products for j <= i alone, with V from
-// global memory.
+// zero of P times an infinite V is NaN.  S^T shows it (its whole column is
+// then not finite).  The state warps clear such values in shared memory once
+// S^T has them, and the output warps add their products for j <= i alone,
+// with V from global memory.
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "kda_launch.h"
@@ -47,11 +48,12 @@ namespace kda {
 namespace {
 
 constexpr int kC = kLaChunk;
+constexpr uint32_t kSmemBase = 1024;
 constexpr uint32_t kSlab = 16384;   // 128 rows x 64 BF16, 128-byte swizzle
 constexpr uint32_t kTile = 2 * kSlab;
 constexpr int kStateWarps = 8, kScoreWarp = 8, kOutWarp = 12, kLoadWarp = 16, kMmaWarp = 17, kDecayWarp = 18;
 constexpr int kThreads = 19 * 32;
-constexpr uint32_t kColD1 = 0, kColO = 128, kColZ = 256, kColK = 384, kTmemCols = 512;
+constexpr uint32_t kColD1 = 0, kColO = 128, kColS = 256, kColK = 384, kTmemCols = 512;
 constexpr uint32_t kKBuf = 48, kKPart = 16;   // K' buffer and part, in columns
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinDecay = -150.f;           // in base 2: exp2 of it is 0 in FP32
@@ -73,7 +75,7 @@ struct Smem {
 
 struct Bars {
     uint64_t *full_k, *full_v, *full_q, *empty_k, *empty_v, *empty_q;   // [stages]
-    uint64_t *qk, *p, *kp_full, *kp_empty, *z_done, *z_free, *s_ready, *qs_done, *q_scaled, *o_done, *o_free;
+    uint64_t *qk, *p, *kp_full, *kp_empty, *z_done, *checked, *s_ready, *qs_done, *q_scaled, *o_done, *o_free;
     uint64_t *dec_full, *dec_empty, *done;
 };
 template <bool kStates>
@@ -92,7 +94,7 @@ __device__ __forceinline__ Bars make_bars(uint8_t* smem) {
     r.kp_full = b; b += 2;
     r.kp_empty = b; b += 2;
     r.z_done = b++;
-    r.z_free = b++;
+    r.checked = b++;
     r.s_ready = b++;
     r.qs_done = b++;
     r.q_scaled = b++;
@@ -167,13 +169,29 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t x, int32_
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(tmap), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
-// B operand whose N index is contiguous (MN-major, 128-byte swizzle): rows of
-// 64 N elements, 8-row groups of K 1024 B apart, the next 64 N elements one
-// slab further.
-__device__ __forceinline__ uint64_t desc_mn(const void* p) {
-    const uint64_t addr = smem_u32(p);
-    return ((addr >> 4) & 0x3FFFull) | (static_cast<uint64_t>(kSlab >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptors as (low word, constant high word): the low word
+// is the start address over 16 and the leading offset, so a step inside a
+// tile is an addition, and an MMA's operands cost the issuing warp one each.
+// K-major operands (128-byte swizzle): 8-row groups 1024 B apart.  Operands
+// whose M or N index is contiguous: rows of 64 elements of it, 8-row groups of
+// K 1024 B apart, the next 64 elements one slab (the leading offset) further.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (tc::kSwizzle128B << 29);
+constexpr uint32_t kLeadK = 1u << 16, kLeadMn = (kSlab >> 4) << 16;
+__host__ __device__ constexpr uint32_t k_step(int k) { return ((k >> 2) * kSlab + 32 * (k & 3)) >> 4; }   // K-major, 16 elements
+__host__ __device__ constexpr uint32_t mn_step(int k) { return (k * 2048) >> 4; }                        // 16 rows
+template <uint32_t kId>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %3, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(acc),
+        "n"(kDescHi), "n"(kId) : "memory");
+}
+template <uint32_t kId>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %3, 0;\n mov.b64 b, {%2, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %5, p;\n}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(acc),
+        "n"(kDescHi), "n"(kId) : "memory");
 }
 constexpr uint32_t kIdesc = tc::idesc_bf16(128, 128);
 constexpr uint32_t kIdescMn = kIdesc | (1u << 16);   // B is MN-major
@@ -189,6 +207,39 @@ __device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+// Wait, with the whole warp, for a phase of an mbarrier.  A wait that polls
+// takes issue slots from the other warps of its scheduler, so the loop is two
+// instructions a try, with a bound on tries in place of a clock (kTries x 8
+// tries of 20 cycles and more: over a second).
+constexpr uint32_t kTries = 1u << 24;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
+    uint32_t ok = 0;
+    const uint32_t at = smem_u32(bar);
+#pragma unroll 1
+    for (uint32_t n = 0; n < kTries; ++n) {
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "D%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(at), "r"(parity) : "memory");
+        if (ok) break;
+    }
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((threadIdx.x & 31) == 0) atomicOr(status, kDevPipeTimeout);
+    return false;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
@@ -215,7 +266,7 @@ __device__ __forceinline__ void load_role(const Kernel& p, const CUtensorMap* qm
             for (int t = 0; t < (kStates ? 2 : 3) && ok; ++t) {
                 uint64_t* empty = t == 0 ? b.empty_k : t == 1 ? b.empty_v : b.empty_q;
                 uint64_t* full = t == 0 ? b.full_k : t == 1 ? b.full_v : b.full_q;
-                if (it >= n) ok = mbar_wait_warp_sleep(&empty[s], ph, p.a.status);
+                if (it >= n) ok = wait_phase(&empty[s], ph, p.a.status);
                 if (!ok) break;
                 if (lane == 0) {
                     uint8_t* dst = smem + (t == 0 ? M::kK : t == 1 ? M::kV : M::kQ) + s * kTile;
@@ -286,7 +337,7 @@ __device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const
                 wt[r] = 4 * lane + r < valid ? exp2f(behind + suf[r]) : 0.f;
                 cf[r] = ex2(ref - g[r]);
             }
-            if (it >= 2 && !mbar_wait_warp_sleep(&b.dec_empty[buf], static_cast<uint32_t>((it >> 1) - 1) & 1u, p.a.status))
+            if (it >= 2 && !wait_phase(&b.dec_empty[buf], static_cast<uint32_t>((it >> 1) - 1) & 1u, p.a.status))
                 return;
             *reinterpret_cast<float4*>(smem + M::kG + buf * kC * 4 + 16 * lane) = make_float4(g[0], g[1], g[2], g[3]);
             *reinterpret_cast<float4*>(smem + M::kW + buf * kC * 4 + 16 * lane) = make_float4(wt[0], wt[1], wt[2], wt[3]);
@@ -298,94 +349,129 @@ __device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const
 }
 
 // ---------------------------------------------------------------- MMA warp
-// Per chunk: Z of the first 64 tokens, D1, Z of the other 64, Q' S^T, P V.
-// D1 overwrites the P of the chunk before, whose product is complete by then
-// (Z's first half runs meanwhile); the first chunk of the CTA starts with D1.
+// Per chunk: K'^T V of the first 64 tokens, D1, K'^T V of the other 64, Q' S^T,
+// P V.  D1 overwrites the P of the chunk before, whose product is complete by
+// then (the first half runs meanwhile); the CTA's first chunk starts with D1.
 template <bool kStates>
-__device__ __forceinline__ void mma_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
+struct Issue {
     using M = Smem<kStates>;
+    static constexpr uint32_t kBase = kSmemBase >> 4;
+    template <int s>
+    static __device__ __forceinline__ void scores() {
+        constexpr uint32_t dk = (kBase + ((M::kK + s * kTile) >> 4)) | kLeadK, dq = (kBase + ((M::kQ + s * kTile) >> 4)) | kLeadK;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ss<kIdesc>(kColD1, dq + k_step(k), dk + k_step(k), k > 0);
+    }
+    template <int s, int q>
+    static __device__ __forceinline__ void state(bool fresh) {
+        constexpr uint32_t dv = (kBase + ((M::kV + s * kTile) >> 4)) | kLeadMn;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                const uint32_t a = kColK + kKBuf * (q & 1) + kKPart * part + 8 * t;
+                if (q == 0 && t == 0 && part == 0)
+                    mma_ts<kIdescMn>(kColS, a, dv + mn_step(2 * q + t), fresh ? 0u : 1u);
+                else
+                    mma_ts<kIdescMn>(kColS, a, dv + mn_step(2 * q + t), 1u);
+            }
+    }
+    template <int s>
+    static __device__ __forceinline__ void incoming() {
+        constexpr uint32_t dq = (kBase + ((M::kQ + s * kTile) >> 4)) | kLeadK, ds = (kBase + (M::kS >> 4)) | kLeadMn;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ss<kIdescMn>(kColO, dq + k_step(k), ds + mn_step(k), k > 0);
+    }
+    template <int s>
+    static __device__ __forceinline__ void inside() {
+        constexpr uint32_t dv = (kBase + ((M::kV + s * kTile) >> 4)) | kLeadMn;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ts<kIdescMn>(kColO, kColD1 + 8 * k, dv + mn_step(k), 1u);
+    }
+};
+
+template <bool kStates, int s>
+__device__ __forceinline__ bool mma_chunk(const Kernel& p, uint8_t* smem, const Bars& b, bool leader, int64_t it, bool fresh) {
+    using M = Smem<kStates>;
+    using I = Issue<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
     const volatile int* flag = reinterpret_cast<const volatile int*>(smem + M::kFlag);
+    const uint32_t st = static_cast<uint32_t>(it / n) & 1u, ph = static_cast<uint32_t>(it & 1), pv = ph ^ 1u;
+    auto scores = [&]() {
+        if (!wait_phase(&b.full_k[s], st, status) || !wait_phase(&b.full_q[s], st, status)) return false;
+        if (it > 0) {
+            if (!wait_phase(b.o_done, pv, status)) return false;
+            if (flag[(it - 1) & 1] == static_cast<int>(it) && !wait_phase(b.o_free, pv, status)) return false;   // P still read
+        }
+        tc::fence_after_sync();
+        if (leader) {
+            I::template scores<s>();
+            tc::commit(b.qk);
+            tc::commit(&b.empty_k[s]);
+        }
+        __syncwarp();
+        return true;
+    };
+    auto state = [&](auto qc) {
+        constexpr int q = decltype(qc)::value;
+        if (!wait_phase(&b.kp_full[q & 1], q >> 1, status)) return false;   // two uses a chunk
+        tc::fence_after_sync();
+        if (leader) {
+            I::template state<s, q>(kStates && fresh);
+            tc::commit(&b.kp_empty[q & 1]);
+            if (q == 3) tc::commit(b.z_done);
+            if (kStates && q == 3) tc::commit(&b.empty_v[s]);
+        }
+        __syncwarp();
+        return true;
+    };
+    if (!kStates && it == 0 && !scores()) return false;
+    if (!wait_phase(&b.full_v[s], st, status) || !wait_phase(b.s_ready, ph, status)) return false;
+    if (!state(std::integral_constant<int, 0>()) || !state(std::integral_constant<int, 1>())) return false;
+    if (!kStates && it > 0 && !scores()) return false;
+    if (!state(std::integral_constant<int, 2>()) || !state(std::integral_constant<int, 3>())) return false;
+    if (kStates) return true;
+    if (!wait_phase(b.q_scaled, ph, status) || (it > 0 && !wait_phase(b.o_free, pv, status))) return false;
+    tc::fence_after_sync();
+    if (leader) {
+        I::template incoming<s>();
+        tc::commit(b.qs_done);
+    }
+    __syncwarp();
+    if (!wait_phase(b.checked, ph, status) || !wait_phase(b.p, ph, status)) return false;
+    tc::fence_after_sync();
+    if (leader) {
+        I::template inside<s>();
+        tc::commit(b.o_done);
+    }
+    __syncwarp();
+    return true;
+}
+
+template <bool kStates>
+__device__ __forceinline__ void mma_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
+    constexpr int n = Smem<kStates>::kStages;
+    const bool leader = elect_one();
     int64_t it = 0;
+    int s = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
         const Unit w = unit_at<kStates>(p, u);
         for (int c = 0; c < w.nch && ok; ++c, ++it) {
-            const int s = static_cast<int>(it % n);
-            const uint32_t st = static_cast<uint32_t>(it / n) & 1u, ph = static_cast<uint32_t>(it & 1), pv = ph ^ 1u;
-            const uint8_t* K = smem + M::kK + s * kTile;
-            const uint8_t* V = smem + M::kV + s * kTile;
-            const uint8_t* Q = smem + M::kQ + s * kTile;
-            auto scores = [&]() {
-                if (!mbar_wait_warp(&b.full_k[s], st, status) || !mbar_wait_warp(&b.full_q[s], st, status)) return false;
-                if (it > 0) {
-                    if (!mbar_wait_warp(b.o_done, pv, status)) return false;
-                    if (flag[(it - 1) & 1] == static_cast<int>(it) && !mbar_wait_warp(b.o_free, pv, status)) return false;   // P still read
-                }
-                tc::fence_after_sync();
-                if (lane == 0) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc::mma_bf16(tmem + kColD1, tc::smem_desc(Q + (k >> 2) * kSlab + 32 * (k & 3), 1024, tc::kSwizzle128B),
-                                     tc::smem_desc(K + (k >> 2) * kSlab + 32 * (k & 3), 1024, tc::kSwizzle128B), kIdesc,
-                                     k > 0);
-                    tc::commit(b.qk);
-                    tc::commit(&b.empty_k[s]);
-                }
-                __syncwarp();
-                return true;
-            };
-            if (!kStates && it == 0) ok = scores();
-            if (ok) ok = mbar_wait_warp(&b.full_v[s], st, status);
-            if (kStates && it > 0 && ok) ok = mbar_wait_warp(b.z_free, pv, status);
-            for (int q = 0; q < 4 && ok; ++q) {
-                if (!kStates && q == 2 && it > 0) ok = scores();
-                if (ok) ok = mbar_wait_warp(&b.kp_full[q & 1], static_cast<uint32_t>(q >> 1), status);   // 2 uses a chunk
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-                            tc::mma_ta(tmem + kColZ, tmem + kColK + kKBuf * (q & 1) + kKPart * part + 8 * t,
-                                       desc_mn(V + (2 * q + t) * 2048), kIdescMn, q > 0 || t > 0 || part > 0);
-                    tc::commit(&b.kp_empty[q & 1]);
-                    if (q == 3) tc::commit(b.z_done);
-                    if (kStates && q == 3) tc::commit(&b.empty_v[s]);
-                }
-                __syncwarp();
-            }
-            if (kStates || !ok) continue;
-            ok = mbar_wait_warp(b.s_ready, ph, status) && mbar_wait_warp(b.q_scaled, ph, status) &&
-                 (it == 0 || mbar_wait_warp(b.o_free, pv, status));
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc::mma_bf16(tmem + kColO, tc::smem_desc(Q + (k >> 2) * kSlab + 32 * (k & 3), 1024, tc::kSwizzle128B),
-                                 desc_mn(smem + M::kS + k * 2048), kIdescMn, k > 0);
-                tc::commit(b.qs_done);
-            }
-            __syncwarp();
-            ok = mbar_wait_warp(b.z_free, ph, status) && mbar_wait_warp(b.p, ph, status);
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc::mma_ta(tmem + kColO, tmem + kColD1 + 8 * k, desc_mn(V + k * 2048), kIdescMn, 1);
-                tc::commit(b.o_done);
-            }
-            __syncwarp();
+            if (s == 0)
+                ok = mma_chunk<kStates, 0>(p, smem, b, leader, it, c == 0);
+            else if (s == 1)
+                ok = mma_chunk<kStates, 1>(p, smem, b, leader, it, c == 0);
+            else if (n == 3)
+                ok = mma_chunk<kStates, n == 3 ? 2 : 0>(p, smem, b, leader, it, c == 0);
+            s = s + 1 == n ? 0 : s + 1;
         }
     }
     // Every MMA must be complete before tensor memory is released.
-    if (lane == 0) tc::commit(b.done);
+    if (leader) tc::commit(b.done);
     __syncwarp();
-    mbar_wait_warp(b.done, 0, status);
+    wait_phase(b.done, 0, p.a.status);
 }
 
 // Clears the values that are not finite in two 16-byte columns of a slab of
@@ -413,6 +499,32 @@ __device__ __forceinline__ bool clear_not_finite(uint8_t* slab, int chunk, int l
 // Warp ws: key channels 32 (ws % 4) .. + 31, one per lane (the tensor-memory
 // lanes it may access); value channels 64 (ws / 4) .. + 63 of S; of K', the
 // 16 tokens 16 (ws / 4) .. of each 32.
+// 32 of a lane's value channels of a state in global memory ([value][key],
+// stride 128), or zeros.
+__device__ __forceinline__ void load_state(const void* base, bool f32, int64_t at, uint32_t (&x)[32]) {
+    if (!base) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = 0u;
+    } else if (f32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = static_cast<const uint32_t*>(base)[at + i * kHeadDim];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            x[i] = static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + i * kHeadDim]) << 16;
+    }
+}
+__device__ __forceinline__ void store_state(void* base, bool f32, int64_t at, const uint32_t (&x)[32]) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) static_cast<uint32_t*>(base)[at + i * kHeadDim] = x[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            static_cast<__nv_bfloat16*>(base)[at + i * kHeadDim] = __float2bfloat16_rn(__uint_as_float(x[i]));
+    }
+}
+
 template <bool kStates>
 __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int ws, int lane) {
     using M = Smem<kStates>;
@@ -421,29 +533,27 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
     volatile int* flag = reinterpret_cast<volatile int*>(smem + M::kFlag);
     const int half = ws >> 2, key = 32 * (ws & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (ws & 3)) << 16);
+    const uint32_t scol = trow + kColS + 64 * half;
     const uint32_t kbase = (key >> 6) * kSlab + 16 * half * 128 + 2 * (key & 7);
     const uint32_t kchunk = ((key & 63) >> 3) << 4;
     int64_t it = 0;
-    float S[64];
     for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
         const Unit w = unit_at<kStates>(p, u);
         const int64_t at = ((w.n * p.a.H + w.h) * kHeadDim + 64 * half) * kHeadDim + key;
         const int64_t seg_at = (w.slot * kHeadDim + 64 * half) * kHeadDim + key;
-        const void* init = kStates ? nullptr : p.sg.starts ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
-        const int64_t init_at = p.sg.starts ? seg_at : at;
+        const void* init = p.sg.starts ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
         const bool init_f32 = p.sg.starts || p.a.state_f32;
-        const bool skip = kStates ? w.nch == 0 : (w.nch == 0 && !w.last);
-        if (skip) continue;
-        if (!init) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = 0.f;
-        } else if (init_f32) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = static_cast<const float*>(init)[init_at + i * kHeadDim];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                S[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(init)[init_at + i * kHeadDim]);
+        const int64_t init_at = p.sg.starts ? seg_at : at;
+        const bool final = !kStates && w.last && p.a.final_state;
+        if (w.nch == 0) {
+            if (final)
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[32];
+                    load_state(init, init_f32, init_at + 32 * i * kHeadDim, x);
+                    store_state(p.a.final_state, p.a.state_f32, at + 32 * i * kHeadDim, x);
+                }
+            continue;
         }
         float total = 0.f;
         for (int c = 0; c < w.nch; ++c, ++it) {
@@ -452,64 +562,51 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
             uint8_t* K = smem + M::kK + s * kTile;
             uint8_t* V = smem + M::kV + s * kTile;
             const int valid = valid_of(w, c);
-            if (!mbar_wait_warp(&b.full_k[s], st, status) ||
-                !mbar_wait_warp(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status))
+            if (!wait_phase(&b.full_k[s], st, status) ||
+                !wait_phase(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status))
                 return;
             if (valid < kC) {
                 // Rows behind the sequence's end: another sequence's tokens,
                 // or anything.  V's are cleared here, K's below.
-                if (!mbar_wait_warp(&b.full_v[s], st, status)) return;
+                if (!wait_phase(&b.full_v[s], st, status)) return;
                 for (int r = valid + ws; r < kC; r += kStateWarps)
                     if (lane < 16)
                         *reinterpret_cast<uint4*>(V + (lane >> 3) * kSlab + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                if (!kStates && q == 2) {
-                    // The state before this chunk as the B operand of Q' S^T
-                    // (row d: 128 value channels), once the last chunk's
-                    // product has read its own.
-                    if (it > 0 && !mbar_wait_warp(b.qs_done, ph ^ 1u, status)) return;
-                    uint8_t* row = smem + M::kS + half * kSlab + key * 128;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        *reinterpret_cast<uint4*>(row + ((x ^ (key & 7)) << 4)) =
-                            make_uint4(pack_bf16(S[8 * x], S[8 * x + 1]), pack_bf16(S[8 * x + 2], S[8 * x + 3]),
-                                       pack_bf16(S[8 * x + 4], S[8 * x + 5]), pack_bf16(S[8 * x + 6], S[8 * x + 7]));
-                    fence_proxy_async_smem();
-                    arrive_warp(b.s_ready, lane);
-                }
-                // K' of tokens 32 q + 16 half .. + 15: three truncated parts.
+            // K' of tokens 32 q + 16 half .. + 15: three truncated parts.
+            auto form = [&](int q) -> bool {
                 const uint8_t* src = K + kbase + 32 * q * 128;
                 const float4* wp = reinterpret_cast<const float4*>(smem + M::kW + buf * kC * 4) + 8 * q + 4 * half;
+                uint32_t kb[16];
+                float4 w4[4];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    kb[i] = *reinterpret_cast<const uint16_t*>(src + i * 128 + (kchunk ^ ((i & 7) << 4)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w4[i] = wp[i];
+                if (valid < kC) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (32 * q + 16 * half + i >= valid) kb[i] = 0;
+                }
                 uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                    const float4 w4 = wp[i4];
-                    const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-                    uint32_t x0[4], x1[4], x2[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 4 * i4 + r;
-                        uint32_t kb = *reinterpret_cast<const uint16_t*>(src + i * 128 + (kchunk ^ ((i & 7) << 4)));
-                        if (valid < kC && 32 * q + 16 * half + i >= valid) kb = 0;
-                        const float x = __uint_as_float(kb << 16) * wv[r];
-                        x0[r] = __float_as_uint(x);
-                        const float y = x - __uint_as_float(x0[r] & 0xffff0000u);
-                        x1[r] = __float_as_uint(y);
-                        x2[r] = __float_as_uint(y - __uint_as_float(x1[r] & 0xffff0000u));
-                    }
-                    hi[2 * i4] = prmt_hi(x0[0], x0[1]);
-                    hi[2 * i4 + 1] = prmt_hi(x0[2], x0[3]);
-                    mid[2 * i4] = prmt_hi(x1[0], x1[1]);
-                    mid[2 * i4 + 1] = prmt_hi(x1[2], x1[3]);
-                    lo[2 * i4] = prmt_hi(x2[0], x2[1]);
-                    lo[2 * i4 + 1] = prmt_hi(x2[2], x2[3]);
+                for (int i = 0; i < 8; ++i) {
+                    const float w0 = i & 1 ? w4[i >> 1].z : w4[i >> 1].x, w1 = i & 1 ? w4[i >> 1].w : w4[i >> 1].y;
+                    float x0 = __uint_as_float(kb[2 * i] << 16), x1 = __uint_as_float(kb[2 * i + 1] << 16);
+                    mul2v(x0, x1, w0, w1);
+                    const uint32_t a0 = __float_as_uint(x0), a1 = __float_as_uint(x1);
+                    sub2(x0, x1, __uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u));
+                    const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
+                    sub2(x0, x1, __uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
+                    hi[i] = prmt_hi(a0, a1);
+                    mid[i] = prmt_hi(b0, b1);
+                    lo[i] = prmt_hi(__float_as_uint(x0), __float_as_uint(x1));
                 }
                 if (q == 3) stage_release(&b.empty_k[s], lane);
                 const int64_t use = 2 * it + (q >> 1);
-                if (use > 0 && !mbar_wait_warp(&b.kp_empty[q & 1], static_cast<uint32_t>(use - 1) & 1u, status)) return;
+                if (use > 0 && !wait_phase(&b.kp_empty[q & 1], static_cast<uint32_t>(use - 1) & 1u, status)) return false;
                 tc::fence_after_sync();
                 const uint32_t col = trow + kColK + kKBuf * (q & 1) + 8 * half;
                 st_x8(col, hi);
@@ -518,52 +615,85 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
                 tc::wait_st();
                 tc::fence_before_sync();
                 arrive_warp(&b.kp_full[q & 1], lane);
-            }
+                return true;
+            };
+            if (!form(0)) return;
             const float sum = reinterpret_cast<const float*>(smem + M::kG)[buf * kC + kC - 1];
             const float d = exp2f(sum);
             total += sum;
-            if (!mbar_wait_warp(b.z_done, ph, status)) return;
-            tc::fence_after_sync();
-            float chk = 0.f;
+            // The state before this chunk: its BF16 copy as the B operand of
+            // Q' S^T (row d: 128 value channels), once the last chunk's
+            // product has read its own, and the decayed state.
+            if (!kStates && it > 0 && !wait_phase(b.qs_done, ph ^ 1u, status)) return;
+            if (!kStates || c > 0) {
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[32];
+                    if (c == 0) {
+                        load_state(init, init_f32, init_at + 32 * i * kHeadDim, x);
+                    } else {
+                        tc::ld_x32(scol + 32 * i, x);
+                        tc::wait_ld();
+                    }
+                    if (!kStates) {
+                        uint8_t* row = smem + M::kS + half * kSlab + key * 128;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t z[16];
-                ld_x16(trow + kColZ + 64 * half + 16 * x, z);
-                tc::wait_ld();
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                y[r] = pack_bf16(__uint_as_float(x[8 * j + 2 * r]), __uint_as_float(x[8 * j + 2 * r + 1]));
+                            *reinterpret_cast<uint4*>(row + (((4 * i + j) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * d);
+                    tc::st_x32(scol + 32 * i, x);
+                }
+                if (!kStates) fence_proxy_async_smem();
+                tc::wait_st();
+                tc::fence_before_sync();
+            }
+            arrive_warp(b.s_ready, lane);
+#pragma unroll 1
+            for (int q = 1; q < 4; ++q)
+                if (!form(q)) return;
+            arrive_warp(&b.dec_empty[buf], lane);
+            if (!wait_phase(b.z_done, ph, status)) return;
+            tc::fence_after_sync();
+            if (!kStates) {
                 // Each warp watches 16 value channels: a V that is not finite
                 // spoils its channel in every lane.
-                if (!kStates && x == (ws & 3))
+                uint32_t z[16];
+                ld_x16(scol + 16 * (ws & 3), z);
+                tc::wait_ld();
+                float chk = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) chk = fmaf(__uint_as_float(z[i]), 0.f, chk);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * x + i] = fmaf(d, S[16 * x + i], __uint_as_float(z[i]));
-            }
-            if (!kStates) {
+                for (int i = 0; i < 16; ++i) chk = fmaf(__uint_as_float(z[i]), 0.f, chk);
                 if (__any_sync(0xffffffffu, !(chk == 0.f))) {
                     // The flag of a chunk is its number, so none has to be cleared.
                     if (clear_not_finite(V + half * kSlab, 2 * (ws & 3), lane) && lane == 0)
                         flag[buf] = static_cast<int>(it + 1);
                     fence_proxy_async_smem();
+                    __threadfence_block();
                 }
-                __threadfence_block();
+                arrive_warp(b.checked, lane);
             }
-            tc::fence_before_sync();
-            arrive_warp(b.z_free, lane);
-            arrive_warp(&b.dec_empty[buf], lane);
         }
-        if (kStates) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) p.sg.starts[seg_at + i * kHeadDim] = S[i];
-            if (ws == 0 && lane == 0) p.sg.decay[w.slot] = total;
-        } else if (w.last && p.a.final_state) {
-            if (p.a.state_f32) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) static_cast<float*>(p.a.final_state)[at + i * kHeadDim] = S[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    static_cast<__nv_bfloat16*>(p.a.final_state)[at + i * kHeadDim] = __float2bfloat16_rn(S[i]);
+        if (kStates || final) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                uint32_t x[32];
+                tc::ld_x32(scol + 32 * i, x);
+                tc::wait_ld();
+                if (kStates)
+                    store_state(p.sg.starts, true, seg_at + 32 * i * kHeadDim, x);
+                else
+                    store_state(p.a.final_state, p.a.state_f32, at + 32 * i * kHeadDim, x);
             }
+            if (kStates && ws == 0 && lane == 0) p.sg.decay[w.slot] = total;
+            tc::fence_before_sync();
         }
     }
 }
@@ -585,55 +715,60 @@ __device__ __forceinline__ void score_role(const Kernel& p, uint8_t* smem, const
             const int buf = static_cast<int>(it & 1);
             const float* G = reinterpret_cast<const float*>(smem + M::kG) + buf * kC;
             const float4* Cf = reinterpret_cast<const float4*>(smem + M::kCf + buf * 96 * 4);
-            if (!mbar_wait_warp(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status)) return;
+            if (!wait_phase(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status)) return;
             const float gi = G[32 * wp + lane];
-            if (!mbar_wait_warp(b.qk, static_cast<uint32_t>(it & 1), status)) return;
+            if (!wait_phase(b.qk, static_cast<uint32_t>(it & 1), status)) return;
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
+            // A block's columns of P, 16 blk .. + 15, held scores of blocks
+            // already read.
+            auto full = [&](int blk, const uint32_t (&x)[32]) {
+                const float f = scale * ex2(gi - G[32 * blk + 31]);
                 uint32_t pk[16];
-                if (blk <= wp) {
-                    uint32_t x[32];
-                    tc::ld_x32(trow + 32 * blk, x);
-                    if (blk < wp) {
-                        const float f = scale * ex2(gi - G[32 * blk + 31]);
-                        tc::wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 cf = Cf[8 * blk + j];
-                            float y0 = __uint_as_float(x[4 * j]), y1 = __uint_as_float(x[4 * j + 1]);
-                            float y2 = __uint_as_float(x[4 * j + 2]), y3 = __uint_as_float(x[4 * j + 3]);
-                            mul2(y0, y1, f);
-                            mul2(y2, y3, f);
-                            mul2v(y0, y1, cf.x, cf.y);
-                            mul2v(y2, y3, cf.z, cf.w);
-                            pk[2 * j] = pack_bf16(y0, y1);
-                            pk[2 * j + 1] = pack_bf16(y2, y3);
-                        }
-                    } else {
-                        const float4* Gb = reinterpret_cast<const float4*>(G + 32 * blk);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 g4 = Gb[j];
-                            const float gj[4] = {g4.x, g4.y, g4.z, g4.w};
-                            float y[4];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                y[r] = __uint_as_float(x[4 * j + r]) * (scale * ex2(gi - gj[r]));
-                                if (4 * j + r > lane) y[r] = 0.f;
-                            }
-                            pk[2 * j] = pack_bf16(y[0], y[1]);
-                            pk[2 * j + 1] = pack_bf16(y[2], y[3]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = 0u;
+                for (int j = 0; j < 8; ++j) {
+                    const float4 cf = Cf[8 * blk + j];
+                    float y0 = __uint_as_float(x[4 * j]), y1 = __uint_as_float(x[4 * j + 1]);
+                    float y2 = __uint_as_float(x[4 * j + 2]), y3 = __uint_as_float(x[4 * j + 3]);
+                    mul2(y0, y1, f);
+                    mul2(y2, y3, f);
+                    mul2v(y0, y1, cf.x, cf.y);
+                    mul2v(y2, y3, cf.z, cf.w);
+                    pk[2 * j] = pack_bf16(y0, y1);
+                    pk[2 * j + 1] = pack_bf16(y2, y3);
                 }
-                // Columns 16 blk .. + 15 held scores of blocks already read.
                 tc::st_x16(trow + 16 * blk, pk);
+            };
+            uint32_t x[32];
+#pragma unroll 1
+            for (int blk = 0; blk < wp; ++blk) {
+                tc::ld_x32(trow + 32 * blk, x);
+                tc::wait_ld();
+                full(blk, x);
             }
+            tc::ld_x32(trow + 32 * wp, x);
+            uint32_t pk[16];
+            float ex[32];
+            const float4* Gb = reinterpret_cast<const float4*>(G + 32 * wp);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 g4 = Gb[j];
+                ex[4 * j] = scale * ex2(gi - g4.x);
+                ex[4 * j + 1] = scale * ex2(gi - g4.y);
+                ex[4 * j + 2] = scale * ex2(gi - g4.z);
+                ex[4 * j + 3] = scale * ex2(gi - g4.w);
+            }
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float y0 = j > lane ? 0.f : __uint_as_float(x[j]) * ex[j];
+                const float y1 = j + 1 > lane ? 0.f : __uint_as_float(x[j + 1]) * ex[j + 1];
+                pk[j / 2] = pack_bf16(y0, y1);
+            }
+            tc::st_x16(trow + 16 * wp, pk);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+#pragma unroll 1
+            for (int blk = wp + 1; blk < 4; ++blk) tc::st_x16(trow + 16 * blk, pk);
             tc::wait_st();
             tc::fence_before_sync();
             arrive_warp(b.p, lane);
@@ -683,26 +818,31 @@ __device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* 
             const int valid = valid_of(w, c);
             // Q' in place, once D1 has been formed from Q.  The factor goes in
             // as two BF16 parts of one fused multiply-add: one rounding.
-            if (!mbar_wait_warp(&b.dec_full[s], st, status)) return;
+            if (!wait_phase(&b.dec_full[s], st, status)) return;
             const float e = p.a.scale * ex2(reinterpret_cast<const float*>(smem + M::kG)[s * kC + row]);
             arrive_warp(&b.dec_empty[s], lane);
-            if (!mbar_wait_warp(&b.full_q[s], st, status) || !mbar_wait_warp(b.qk, ph, status)) return;
+            if (!wait_phase(&b.full_q[s], st, status) || !wait_phase(b.qk, ph, status)) return;
             const __nv_bfloat16 eh = __float2bfloat16_rn(e);
             const __nv_bfloat162 e1 = __bfloat162bfloat162(eh);
             const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e - __bfloat162float(eh)));
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                uint4* at = reinterpret_cast<uint4*>(Qrow + (x >> 3) * kSlab + (((x & 7) ^ (row & 7)) << 4));
-                uint4 v = *at;
-                __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+            for (int sl = 0; sl < 2; ++sl) {
+                uint4 v[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = __hfma2(h[j], e1, __hmul2(h[j], e2));
-                *at = v;
+                for (int x = 0; x < 8; ++x)
+                    v[x] = *reinterpret_cast<const uint4*>(Qrow + sl * kSlab + ((x ^ (row & 7)) << 4));
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v[x]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = __hfma2(h[j], e1, __hmul2(h[j], e2));
+                    *reinterpret_cast<uint4*>(Qrow + sl * kSlab + ((x ^ (row & 7)) << 4)) = v[x];
+                }
             }
             fence_proxy_async_smem();
             arrive_warp(b.q_scaled, lane);
 
-            if (!mbar_wait_warp(b.o_done, ph, status)) return;
+            if (!wait_phase(b.o_done, ph, status)) return;
             tc::fence_after_sync();
             const bool bad = flag[s] == static_cast<int>(it + 1);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) +
@@ -714,17 +854,14 @@ __device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* 
                 tc::wait_ld();
                 if (bad) {
 #pragma unroll 1
-                    for (int jb = 0; jb <= we; ++jb)
-#pragma unroll 1
-                        for (int j2 = 0; j2 < 16; ++j2) {
-                            uint32_t pp;
-                            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-                                         : "=r"(pp) : "r"(trow + kColD1 + 16 * jb + j2));
-                            tc::wait_ld();
-                            const int j = 32 * jb + 2 * j2;
-                            add_not_finite(x, v0 + j * vstride + 32 * blk, bf16_lo(pp), j <= row && j < valid);
-                            add_not_finite(x, v0 + (j + 1) * vstride + 32 * blk, bf16_hi(pp), j < row && j + 1 < valid);
-                        }
+                    for (int j = 0; j < 32 * (we + 1); j += 2) {
+                        uint32_t pp;
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                                     : "=r"(pp) : "r"(trow + kColD1 + (j >> 1)));
+                        tc::wait_ld();
+                        add_not_finite(x, v0 + j * vstride + 32 * blk, bf16_lo(pp), j <= row && j < valid);
+                        add_not_finite(x, v0 + (j + 1) * vstride + 32 * blk, bf16_hi(pp), j < row && j + 1 < valid);
+                    }
                 }
                 if (blk == 3) {
                     // O and P are read, and V by every product.
@@ -771,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using M = Smem<kStates>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (p.a.valid && !*p.a.valid) return;
-    if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
+    if (smem_u32(smem) != kSmemBase) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
         return;
     }
@@ -796,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(b.qk, 1);
         mbar_init(b.p, 4);
         mbar_init(b.z_done, 1);
-        mbar_init(b.z_free, kStateWarps);
+        mbar_init(b.checked, kStateWarps);
         mbar_init(b.s_ready, kStateWarps);
         mbar_init(b.qs_done, 1);
         mbar_init(b.q_scaled, 4);
