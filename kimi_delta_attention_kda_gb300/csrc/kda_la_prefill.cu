@@ -24,9 +24,9 @@
 // P, Q' and the S operand are rounded to BF16 once each: their error stays in
 // the BF16 output they go to, and S itself is not touched by it.
 //
-// One CTA per SM walks (sequence or segment, head) units.  Warps: 8 state
-// (K' parts, S), 4 score (P), 4 output (Q', O), one each for the loads, the
-// MMA issue and the decay sums.  Tensor memory columns: D1 and P [0, 128),
+// One CTA per SM walks (sequence or segment, head) units.  Warps: 8 key (K'),
+// 8 state (S), 4 score (P), 4 query (Q'), 4 output (O), one each for the
+// loads, the MMA issue and the decay sums.  Tensor memory columns: D1 and P [0, 128),
 // O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32 tokens x 3
 // parts).
 //
@@ -38,7 +38,6 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "kda_common.cuh"
 #include "kda_launch.h"
@@ -48,11 +47,12 @@ namespace kda {
 namespace {
 
 constexpr int kC = kLaChunk;
-constexpr uint32_t kSmemBase = 1024;
 constexpr uint32_t kSlab = 16384;   // 128 rows x 64 BF16, 128-byte swizzle
 constexpr uint32_t kTile = 2 * kSlab;
-constexpr int kStateWarps = 8, kScoreWarp = 8, kOutWarp = 12, kLoadWarp = 16, kMmaWarp = 17, kDecayWarp = 18;
-constexpr int kThreads = 19 * 32;
+// First warp of each role; 8 key, 8 state, 4 score, 4 query and 4 output warps.
+constexpr int kStateWarp = 8, kScoreWarp = 16, kQueryWarp = 20, kOutWarp = 24, kLoadWarp = 28, kMmaWarp = 29, kDecayWarp = 30;
+constexpr int kKeyWarps = 8, kStateWarps = 8;
+constexpr int kThreads = 31 * 32;
 constexpr uint32_t kColD1 = 0, kColO = 128, kColS = 256, kColK = 384, kTmemCols = 512;
 constexpr uint32_t kKBuf = 48, kKPart = 16;   // K' buffer and part, in columns
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,14 +68,14 @@ struct Smem {
     // G (prefix sums), W (exp of the sums behind a token), C (exp of the sum
     // from a token to the end of its block of 32): two buffers each.
     static constexpr uint32_t kG = kMisc, kW = kG + 2 * kC * 4, kCf = kW + 2 * kC * 4, kBars = kCf + 2 * 96 * 4;
-    static constexpr int kNumBars = 4 * kStages + 4 + 18;
+    static constexpr int kNumBars = 6 * kStages + 16;
     static constexpr uint32_t kFlag = kBars + 8 * kNumBars, kTmemPtr = kFlag + 8, kBytes = kTmemPtr + 8;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
 struct Bars {
-    uint64_t *full_k, *full_v, *full_q, *empty_k, *empty_v, *empty_q;   // [stages]
-    uint64_t *qk, *p, *kp_full, *kp_empty, *z_done, *checked, *s_ready, *qs_done, *q_scaled, *o_done, *o_free;
+    uint64_t *full_k, *full_v, *full_q, *empty_k, *empty_v, *empty_q;   // [stages], one after the other
+    uint64_t *qk, *kp_full, *kp_empty, *z_done, *s_ready, *qs_ready, *qs_done, *pv_ready, *o_done;
     uint64_t *dec_full, *dec_empty, *done;
 };
 template <bool kStates>
@@ -83,78 +83,106 @@ __device__ __forceinline__ Bars make_bars(uint8_t* smem) {
     constexpr int n = Smem<kStates>::kStages;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + Smem<kStates>::kBars);
     Bars r;
-    r.full_k = b; b += n;
-    r.full_v = b; b += n;
-    r.empty_k = b; b += n;
-    r.empty_v = b; b += n;
-    r.full_q = b; b += 2;
-    r.empty_q = b; b += 2;
-    r.qk = b++;
-    r.p = b++;
-    r.kp_full = b; b += 2;
-    r.kp_empty = b; b += 2;
-    r.z_done = b++;
-    r.checked = b++;
-    r.s_ready = b++;
-    r.qs_done = b++;
-    r.q_scaled = b++;
-    r.o_done = b++;
-    r.o_free = b++;
-    r.dec_full = b; b += 2;
-    r.dec_empty = b; b += 2;
-    r.done = b++;
+    r.full_k = b;
+    r.full_v = b + n;
+    r.full_q = b + 2 * n;
+    r.empty_k = b + 3 * n;
+    r.empty_v = b + 4 * n;
+    r.empty_q = b + 5 * n;
+    b += 6 * n;
+    r.qk = b;
+    r.kp_full = b + 1;
+    r.kp_empty = b + 3;
+    r.z_done = b + 5;
+    r.s_ready = b + 6;
+    r.qs_ready = b + 7;
+    r.qs_done = b + 8;
+    r.pv_ready = b + 9;
+    r.o_done = b + 10;
+    r.dec_full = b + 11;
+    r.dec_empty = b + 13;
+    r.done = b + 15;
     return r;
 }
 
 struct Kernel {
     LaArgs a;
     LaSegments sg;      // sg.starts null: no segments
-    int64_t units;
+    uint32_t units, heads;
 };
 
 // One (sequence or segment, head).
 struct Unit {
-    int64_t n, h, tok0, len;
-    int64_t slot;       // (segment, head) row of the segments' buffers
+    int n, h, tok0, len;
+    uint32_t slot;      // (segment, head) row of the segments' buffers
     bool last;          // writes the final state
     int nch;
 };
 template <bool kStates>
-__device__ __forceinline__ Unit unit_at(const Kernel& p, int64_t u) {
+__device__ __forceinline__ Unit unit_at(const Kernel& p, uint32_t u) {
     Unit w;
-    const int64_t s = u / p.a.H;
-    w.h = u - s * p.a.H;
+    const uint32_t s = u / p.heads;
+    w.h = u - s * p.heads;
     w.slot = u;
     w.last = true;
     if (!p.sg.starts) {
         w.n = s;
         if (p.a.cu_seqlens) {
-            w.tok0 = p.a.cu_seqlens[s];
-            w.len = p.a.cu_seqlens[s + 1] - w.tok0;
+            w.tok0 = static_cast<int>(p.a.cu_seqlens[s]);
+            w.len = static_cast<int>(p.a.cu_seqlens[s + 1]) - w.tok0;
         } else {
-            w.tok0 = s * p.a.tokens_per_seq;
-            w.len = p.a.tokens_per_seq;
+            w.len = static_cast<int>(p.a.tokens_per_seq);
+            w.tok0 = s * w.len;
         }
     } else if (p.sg.seg_begin) {
-        w.n = p.sg.seg_seq[s];
-        w.tok0 = p.sg.seg_tokens[s];
-        w.len = s < p.sg.seg_begin[p.a.N] ? p.sg.seg_tokens[s + 1] - w.tok0 : 0;
-        w.last = s + 1 == p.sg.seg_begin[w.n + 1];
-        if (w.len == 0) w.last = false;   // padding of the segment table
+        w.n = static_cast<int>(p.sg.seg_seq[s]);
+        w.tok0 = static_cast<int>(p.sg.seg_tokens[s]);
+        w.len = s < p.sg.seg_begin[p.a.N] ? static_cast<int>(p.sg.seg_tokens[s + 1]) - w.tok0 : 0;
+        w.last = s + 1 == p.sg.seg_begin[w.n + 1] && w.len > 0;   // not the table's padding
     } else {
-        w.n = s / p.sg.segs;
-        const int64_t j = s - w.n * p.sg.segs;
-        w.tok0 = w.n * p.a.tokens_per_seq + j * p.sg.seg_tokens_each;
-        w.last = j + 1 == p.sg.segs;
-        w.len = w.last ? p.a.tokens_per_seq - j * p.sg.seg_tokens_each : p.sg.seg_tokens_each;
+        const uint32_t segs = static_cast<uint32_t>(p.sg.segs);
+        const int each = static_cast<int>(p.sg.seg_tokens_each), per = static_cast<int>(p.a.tokens_per_seq);
+        w.n = s / segs;
+        const int j = s - w.n * segs;
+        w.tok0 = w.n * per + j * each;
+        w.last = j + 1 == static_cast<int>(segs);
+        w.len = w.last ? per - j * each : each;
     }
     if (kStates && w.last) w.len = 0;     // nothing follows a sequence's last segment
-    w.nch = static_cast<int>((w.len + kC - 1) / kC);
+    w.nch = (w.len + kC - 1) / kC;
     return w;
 }
-__device__ __forceinline__ int valid_of(const Unit& w, int c) {
-    const int64_t left = w.len - static_cast<int64_t>(c) * kC;
-    return left < kC ? static_cast<int>(left) : kC;
+
+// A chunk's place in the rings: the chunk's number on this CTA, its stage and
+// the parity of the stage's use.
+template <int kStages>
+struct Pos {
+    uint32_t it = 0, st = 0;
+    int s = 0;
+    __device__ __forceinline__ void next() {
+        ++it;
+        if (++s == kStages) {
+            s = 0;
+            st ^= 1u;
+        }
+    }
+    __device__ __forceinline__ uint32_t ph() const { return it & 1u; }            // once a chunk
+    __device__ __forceinline__ uint32_t dec_ph() const { return (it >> 1) & 1u; }   // two buffers
+};
+
+// f(unit, chunk, valid tokens, place) for every chunk of this CTA, until it fails.
+template <bool kStates, class F>
+__device__ __forceinline__ void walk(const Kernel& p, F f) {
+    Pos<Smem<kStates>::kStages> x;
+#pragma unroll 1
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const Unit w = unit_at<kStates>(p, u);
+#pragma unroll 1
+        for (int c = 0; c < w.nch; ++c) {
+            if (!f(w, c, min(kC, w.len - c * kC), x)) return;
+            x.next();
+        }
+    }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -171,14 +199,16 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t x, int32_
 }
 // Shared-memory descriptors as (low word, constant high word): the low word
 // is the start address over 16 and the leading offset, so a step inside a
-// tile is an addition, and an MMA's operands cost the issuing warp one each.
-// K-major operands (128-byte swizzle): 8-row groups 1024 B apart.  Operands
-// whose M or N index is contiguous: rows of 64 elements of it, 8-row groups of
-// K 1024 B apart, the next 64 elements one slab (the leading offset) further.
+// tile is an addition.  K-major operands (128-byte swizzle): 8-row groups
+// 1024 B apart.  Operands whose N index is contiguous: rows of 64 elements of
+// it, 8-row groups of K 1024 B apart, the next 64 elements one slab (the
+// leading offset) further.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (tc::kSwizzle128B << 29);
 constexpr uint32_t kLeadK = 1u << 16, kLeadMn = (kSlab >> 4) << 16;
 __host__ __device__ constexpr uint32_t k_step(int k) { return ((k >> 2) * kSlab + 32 * (k & 3)) >> 4; }   // K-major, 16 elements
 __host__ __device__ constexpr uint32_t mn_step(int k) { return (k * 2048) >> 4; }                        // 16 rows
+constexpr uint32_t kIdesc = tc::idesc_bf16(128, 128);
+constexpr uint32_t kIdescMn = kIdesc | (1u << 16);   // B is MN-major
 template <uint32_t kId>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t acc) {
     asm volatile(
@@ -193,9 +223,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %5, p;\n}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(acc),
         "n"(kDescHi), "n"(kId) : "memory");
 }
-constexpr uint32_t kIdesc = tc::idesc_bf16(128, 128);
-constexpr uint32_t kIdescMn = kIdesc | (1u << 16);   // B is MN-major
-
+__device__ __forceinline__ void ld_x8(uint32_t taddr, uint32_t (&r)[8]) { tc::ld_x8(taddr, r); }
 __device__ __forceinline__ void st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -208,32 +236,23 @@ __device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// Wait, with the whole warp, for a phase of an mbarrier.  A wait that polls
-// takes issue slots from the other warps of its scheduler, so the loop is two
-// instructions a try, with a bound on tries in place of a clock (kTries x 8
-// tries of 20 cycles and more: over a second).
-constexpr uint32_t kTries = 1u << 24;
+
+// Wait, with the whole warp, for a phase of an mbarrier, with a bound on tries
+// in place of a clock (each takes 20 cycles and more: a second or more).  The
+// kernel has many waits, and its roles share an instruction cache, so a wait
+// is a handful of instructions and its failure one call.
+constexpr uint32_t kTries = 1u << 27;
+__device__ __noinline__ void timed_out(int* status) { atomicOr(status, kDevPipeTimeout); }
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
-    uint32_t ok = 0;
-    const uint32_t at = smem_u32(bar);
-#pragma unroll 1
-    for (uint32_t n = 0; n < kTries; ++n) {
-        asm volatile(
-            "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            "D%=:\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok) : "r"(at), "r"(parity) : "memory");
-        if (ok) break;
-    }
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "W%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
+        " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra.uni W%=;\n"
+        "D%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "n"(kTries) : "memory");
     if (__all_sync(0xffffffffu, ok)) return true;
-    if ((threadIdx.x & 31) == 0) atomicOr(status, kDevPipeTimeout);
+    timed_out(status);
     return false;
 }
 __device__ __forceinline__ bool elect_one() {
@@ -251,277 +270,317 @@ template <bool kStates>
 __device__ __forceinline__ void load_role(const Kernel& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap, uint8_t* smem, const Bars& b, int lane) {
     using M = Smem<kStates>;
-    constexpr int n = M::kStages;
-    const int64_t group = p.a.H / p.a.Hk;
-    int64_t it = 0;
-    int issued[3] = {0, 0, 0};   // tiles of K, V, Q under way or done
-    bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const Unit w = unit_at<kStates>(p, u);
-        const int xk = static_cast<int>(w.h / group * kHeadDim), xv = static_cast<int>(w.h * kHeadDim);
-        for (int c = 0; c < w.nch && ok; ++c, ++it) {
-            const int s = static_cast<int>(it % n);
-            const uint32_t ph = static_cast<uint32_t>((it / n) - 1) & 1u;
-            const int y = static_cast<int>(w.tok0 + static_cast<int64_t>(c) * kC);
-            for (int t = 0; t < (kStates ? 2 : 3) && ok; ++t) {
-                uint64_t* empty = t == 0 ? b.empty_k : t == 1 ? b.empty_v : b.empty_q;
-                uint64_t* full = t == 0 ? b.full_k : t == 1 ? b.full_v : b.full_q;
-                if (it >= n) ok = wait_phase(&empty[s], ph, p.a.status);
-                if (!ok) break;
-                if (lane == 0) {
-                    uint8_t* dst = smem + (t == 0 ? M::kK : t == 1 ? M::kV : M::kQ) + s * kTile;
-                    const CUtensorMap* map = t == 0 ? kmap : t == 1 ? vmap : qmap;
-                    const int x = t == 1 ? xv : xk;
-                    mbar_arrive_expect_tx(&full[s], kTile);
-                    tma_load_2d(dst, map, x, y, &full[s]);
-                    tma_load_2d(dst + kSlab, map, x + 64, y, &full[s]);
-                }
-                ++issued[t];
-                __syncwarp();
+    constexpr int n = M::kStages, tiles = kStates ? 2 : 3;
+    const uint32_t group = static_cast<uint32_t>(p.a.H / p.a.Hk);
+    uint32_t issued = 0;   // tiles under way or done, K, V, Q, K, ..
+    walk<kStates>(p, [&](const Unit& w, int c, int, const Pos<n>& x) {
+        const int y = w.tok0 + c * kC;
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            // (The barriers and tiles of K, V and Q follow one another.)
+            if (x.it >= n && !wait_phase(&b.empty_k[t * n + x.s], x.st ^ 1u, p.a.status)) return false;
+            if (lane == 0) {
+                uint64_t* full = &b.full_k[t * n + x.s];
+                uint8_t* dst = smem + (t * n + x.s) * kTile;
+                const CUtensorMap* map = t == 0 ? kmap : t == 1 ? vmap : qmap;
+                const int col = static_cast<int>(t == 1 ? w.h : w.h / group) * kHeadDim;
+                mbar_arrive_expect_tx(full, kTile);
+                tma_load_2d(dst, map, col, y, full);
+                tma_load_2d(dst + kSlab, map, col + 64, y, full);
             }
+            ++issued;
+            __syncwarp();
         }
+        return true;
+    });
+    // No copy may be under way when the CTA ends: the last uses of each stage.
+#pragma unroll 1
+    for (uint32_t i = issued > tiles * n ? issued - tiles * n : 0; i < issued; ++i) {
+        const uint32_t it = i / tiles, t = i % tiles;
+        wait_phase(&b.full_k[t * n + it % n], (it / n) & 1u, p.a.status);
     }
-    // No copy may be under way when the CTA ends.
-    for (int t = 0; t < 3; ++t)
-        for (int s = 0; s < n; ++s)
-            if (issued[t] > s)
-                mbar_wait_bounded(&(t == 0 ? b.full_k : t == 1 ? b.full_v : b.full_q)[s],
-                                  static_cast<uint32_t>((issued[t] - 1 - s) / n) & 1u, p.a.status);
 }
 
 // -------------------------------------------------------------- decay warp
 template <bool kStates>
 __device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const Bars& b, int lane) {
     using M = Smem<kStates>;
-    int64_t it = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const Unit w = unit_at<kStates>(p, u);
-        for (int c = 0; c < w.nch; ++c, ++it) {
-            const int buf = static_cast<int>(it & 1);
-            const int valid = valid_of(w, c);
-            const int64_t tok = w.tok0 + static_cast<int64_t>(c) * kC + 4 * lane;
-            float x[4];
+    walk<kStates>(p, [&](const Unit& w, int c, int valid, const Pos<M::kStages>& at) {
+        const uint32_t buf = at.it & 1u;
+        const float* src = p.a.g + static_cast<int64_t>(w.tok0 + c * kC + 4 * lane) * p.a.g_stride + w.h;
+        float x[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[r] = 0.f;
-                if (4 * lane + r < valid) {
-                    x[r] = p.a.g[(tok + r) * p.a.g_stride + w.h] * kLog2e;
-                    if (x[r] < kMinDecay) x[r] = kMinDecay;   // -inf too; NaN stays
-                }
+        for (int r = 0; r < 4; ++r) {
+            x[r] = 0.f;
+            if (4 * lane + r < valid) {
+                x[r] = src[r * p.a.g_stride] * kLog2e;
+                if (x[r] < kMinDecay) x[r] = kMinDecay;   // -inf too; NaN stays
             }
-            // Prefix and suffix sums, each from its own end.
-            float pre[4], suf[4];
-            pre[0] = x[0];
-            suf[3] = 0.f;
-#pragma unroll
-            for (int r = 1; r < 4; ++r) {
-                pre[r] = pre[r - 1] + x[r];
-                suf[3 - r] = suf[4 - r] + x[4 - r];
-            }
-            float up = pre[3], down = suf[0] + x[0];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up += y;
-                if (lane + o < 32) down += z;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 0.f;
-            if (lane == 31) behind = 0.f;
-            float g[4], wt[4], cf[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) g[r] = before + pre[r];
-            const float ref = __shfl_sync(0xffffffffu, g[3], lane | 7);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                wt[r] = 4 * lane + r < valid ? exp2f(behind + suf[r]) : 0.f;
-                cf[r] = ex2(ref - g[r]);
-            }
-            if (it >= 2 && !wait_phase(&b.dec_empty[buf], static_cast<uint32_t>((it >> 1) - 1) & 1u, p.a.status))
-                return;
-            *reinterpret_cast<float4*>(smem + M::kG + buf * kC * 4 + 16 * lane) = make_float4(g[0], g[1], g[2], g[3]);
-            *reinterpret_cast<float4*>(smem + M::kW + buf * kC * 4 + 16 * lane) = make_float4(wt[0], wt[1], wt[2], wt[3]);
-            if (lane < 24)
-                *reinterpret_cast<float4*>(smem + M::kCf + buf * 96 * 4 + 16 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
-            arrive_warp(&b.dec_full[buf], lane);
         }
-    }
+        // Prefix and suffix sums, each from its own end.
+        float pre[4], suf[4];
+        pre[0] = x[0];
+        suf[3] = 0.f;
+#pragma unroll
+        for (int r = 1; r < 4; ++r) {
+            pre[r] = pre[r - 1] + x[r];
+            suf[3 - r] = suf[4 - r] + x[4 - r];
+        }
+        float up = pre[3], down = suf[0] + x[0];
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
+            if (lane >= o) up += y;
+            if (lane + o < 32) down += z;
+        }
+        float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 0) before = 0.f;
+        if (lane == 31) behind = 0.f;
+        float g[4], wt[4], cf[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) g[r] = before + pre[r];
+        const float ref = __shfl_sync(0xffffffffu, g[3], lane | 7);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            wt[r] = 4 * lane + r < valid ? ex2(behind + suf[r]) : 0.f;
+            cf[r] = ex2(ref - g[r]);
+        }
+        if (at.it >= 2 && !wait_phase(&b.dec_empty[buf], at.dec_ph() ^ 1u, p.a.status)) return false;
+        *reinterpret_cast<float4*>(smem + M::kG + buf * kC * 4 + 16 * lane) = make_float4(g[0], g[1], g[2], g[3]);
+        *reinterpret_cast<float4*>(smem + M::kW + buf * kC * 4 + 16 * lane) = make_float4(wt[0], wt[1], wt[2], wt[3]);
+        if (lane < 24)
+            *reinterpret_cast<float4*>(smem + M::kCf + buf * 96 * 4 + 16 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+        arrive_warp(&b.dec_full[buf], lane);
+        return true;
+    });
 }
 
 // ---------------------------------------------------------------- MMA warp
-// Per chunk: K'^T V of the first 64 tokens, D1, K'^T V of the other 64, Q' S^T,
-// P V.  D1 overwrites the P of the chunk before, whose product is complete by
-// then (the first half runs meanwhile); the CTA's first chunk starts with D1.
-template <bool kStates>
-struct Issue {
-    using M = Smem<kStates>;
-    static constexpr uint32_t kBase = kSmemBase >> 4;
-    template <int s>
-    static __device__ __forceinline__ void scores() {
-        constexpr uint32_t dk = (kBase + ((M::kK + s * kTile) >> 4)) | kLeadK, dq = (kBase + ((M::kQ + s * kTile) >> 4)) | kLeadK;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ss<kIdesc>(kColD1, dq + k_step(k), dk + k_step(k), k > 0);
-    }
-    template <int s, int q>
-    static __device__ __forceinline__ void state(bool fresh) {
-        constexpr uint32_t dv = (kBase + ((M::kV + s * kTile) >> 4)) | kLeadMn;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int part = 0; part < 3; ++part) {
-                const uint32_t a = kColK + kKBuf * (q & 1) + kKPart * part + 8 * t;
-                if (q == 0 && t == 0 && part == 0)
-                    mma_ts<kIdescMn>(kColS, a, dv + mn_step(2 * q + t), fresh ? 0u : 1u);
-                else
-                    mma_ts<kIdescMn>(kColS, a, dv + mn_step(2 * q + t), 1u);
-            }
-    }
-    template <int s>
-    static __device__ __forceinline__ void incoming() {
-        constexpr uint32_t dq = (kBase + ((M::kQ + s * kTile) >> 4)) | kLeadK, ds = (kBase + (M::kS >> 4)) | kLeadMn;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ss<kIdescMn>(kColO, dq + k_step(k), ds + mn_step(k), k > 0);
-    }
-    template <int s>
-    static __device__ __forceinline__ void inside() {
-        constexpr uint32_t dv = (kBase + ((M::kV + s * kTile) >> 4)) | kLeadMn;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts<kIdescMn>(kColO, kColD1 + 8 * k, dv + mn_step(k), 1u);
-    }
-};
-
-template <bool kStates, int s>
-__device__ __forceinline__ bool mma_chunk(const Kernel& p, uint8_t* smem, const Bars& b, bool leader, int64_t it, bool fresh) {
-    using M = Smem<kStates>;
-    using I = Issue<kStates>;
-    constexpr int n = M::kStages;
-    int* status = p.a.status;
-    const volatile int* flag = reinterpret_cast<const volatile int*>(smem + M::kFlag);
-    const uint32_t st = static_cast<uint32_t>(it / n) & 1u, ph = static_cast<uint32_t>(it & 1), pv = ph ^ 1u;
-    auto scores = [&]() {
-        if (!wait_phase(&b.full_k[s], st, status) || !wait_phase(&b.full_q[s], st, status)) return false;
-        if (it > 0) {
-            if (!wait_phase(b.o_done, pv, status)) return false;
-            if (flag[(it - 1) & 1] == static_cast<int>(it) && !wait_phase(b.o_free, pv, status)) return false;   // P still read
-        }
-        tc::fence_after_sync();
-        if (leader) {
-            I::template scores<s>();
-            tc::commit(b.qk);
-            tc::commit(&b.empty_k[s]);
-        }
-        __syncwarp();
-        return true;
-    };
-    auto state = [&](auto qc) {
-        constexpr int q = decltype(qc)::value;
-        if (!wait_phase(&b.kp_full[q & 1], q >> 1, status)) return false;   // two uses a chunk
-        tc::fence_after_sync();
-        if (leader) {
-            I::template state<s, q>(kStates && fresh);
-            tc::commit(&b.kp_empty[q & 1]);
-            if (q == 3) tc::commit(b.z_done);
-            if (kStates && q == 3) tc::commit(&b.empty_v[s]);
-        }
-        __syncwarp();
-        return true;
-    };
-    if (!kStates && it == 0 && !scores()) return false;
-    if (!wait_phase(&b.full_v[s], st, status) || !wait_phase(b.s_ready, ph, status)) return false;
-    if (!state(std::integral_constant<int, 0>()) || !state(std::integral_constant<int, 1>())) return false;
-    if (!kStates && it > 0 && !scores()) return false;
-    if (!state(std::integral_constant<int, 2>()) || !state(std::integral_constant<int, 3>())) return false;
-    if (kStates) return true;
-    if (!wait_phase(b.q_scaled, ph, status) || (it > 0 && !wait_phase(b.o_free, pv, status))) return false;
-    tc::fence_after_sync();
-    if (leader) {
-        I::template incoming<s>();
-        tc::commit(b.qs_done);
-    }
-    __syncwarp();
-    if (!wait_phase(b.checked, ph, status) || !wait_phase(b.p, ph, status)) return false;
-    tc::fence_after_sync();
-    if (leader) {
-        I::template inside<s>();
-        tc::commit(b.o_done);
-    }
-    __syncwarp();
-    return true;
-}
-
+// Per chunk: D1, K'^T V in quarters of 32 tokens, Q' S^T, P V.  D1 overwrites
+// the P of the chunk before, whose product it waits for; P and Q' are formed
+// while K'^T V runs, and the next chunk's state between Q' S^T and its K'^T V.
 template <bool kStates>
 __device__ __forceinline__ void mma_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
-    constexpr int n = Smem<kStates>::kStages;
+    using M = Smem<kStates>;
+    constexpr int n = M::kStages;
+    int* status = p.a.status;
+    const volatile uint32_t* flag = reinterpret_cast<const volatile uint32_t*>(smem + M::kFlag);
     const bool leader = elect_one();
-    int64_t it = 0;
-    int s = 0;
-    bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const Unit w = unit_at<kStates>(p, u);
-        for (int c = 0; c < w.nch && ok; ++c, ++it) {
-            if (s == 0)
-                ok = mma_chunk<kStates, 0>(p, smem, b, leader, it, c == 0);
-            else if (s == 1)
-                ok = mma_chunk<kStates, 1>(p, smem, b, leader, it, c == 0);
-            else if (n == 3)
-                ok = mma_chunk<kStates, n == 3 ? 2 : 0>(p, smem, b, leader, it, c == 0);
-            s = s + 1 == n ? 0 : s + 1;
+    const uint32_t base = (smem_u32(smem) >> 4) & 0x3FFFu, ds = base + (M::kS >> 4) + kLeadMn;
+    walk<kStates>(p, [&](const Unit&, int c, int, const Pos<n>& x) {
+        const uint32_t ph = x.ph(), pv = ph ^ 1u, it = x.it;
+        const uint32_t tile = base + x.s * (kTile >> 4);
+        const uint32_t dk = tile + (M::kK >> 4) + kLeadK, dv = tile + (M::kV >> 4) + kLeadMn, dq = tile + (M::kQ >> 4) + kLeadK;
+        if (!wait_phase(&b.full_k[x.s], x.st, status)) return false;
+        if (!kStates) {
+            if (!wait_phase(&b.full_q[x.s], x.st, status)) return false;
+            if (it > 0) {
+                if (!wait_phase(b.o_done, pv, status)) return false;
+                // P is read once more where V is not finite: until V's stage is released.
+                if (flag[pv] == it && !wait_phase(&b.empty_v[x.s ^ 1], x.s ? x.st : x.st ^ 1u, status)) return false;
+            }
+            tc::fence_after_sync();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_ss<kIdesc>(tmem + kColD1, dq + k_step(k), dk + k_step(k), k > 0);
+                tc::commit(b.qk);
+                tc::commit(&b.empty_k[x.s]);
+            }
+            __syncwarp();
         }
-    }
+        if (!wait_phase(&b.full_v[x.s], x.st, status) || !wait_phase(b.s_ready, ph, status)) return false;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            if (!wait_phase(&b.kp_full[q & 1], q >> 1, status)) return false;   // two uses a chunk
+            tc::fence_after_sync();
+            if (leader) {
+                const uint32_t kp = tmem + kColK + kKBuf * (q & 1), v = dv + q * mn_step(2);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+                        mma_ts<kIdescMn>(tmem + kColS, kp + kKPart * part + 8 * t, v + mn_step(t),
+                                         t + part > 0 ? 1u : static_cast<uint32_t>(!kStates || c + q > 0));
+                tc::commit(&b.kp_empty[q & 1]);
+                if (q == 3) {
+                    tc::commit(b.z_done);
+                    if (kStates) tc::commit(&b.empty_v[x.s]);
+                }
+            }
+            __syncwarp();
+        }
+        if (kStates) return true;
+        if (!wait_phase(b.qs_ready, ph, status)) return false;
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ss<kIdescMn>(tmem + kColO, dq + k_step(k), ds + mn_step(k), k > 0);
+            tc::commit(b.qs_done);
+        }
+        __syncwarp();
+        if (!wait_phase(b.pv_ready, ph, status)) return false;
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ts<kIdescMn>(tmem + kColO, tmem + kColD1 + 8 * k, dv + mn_step(k), 1u);
+            tc::commit(b.o_done);
+        }
+        __syncwarp();
+        return true;
+    });
     // Every MMA must be complete before tensor memory is released.
     if (leader) tc::commit(b.done);
     __syncwarp();
-    wait_phase(b.done, 0, p.a.status);
+    wait_phase(b.done, 0, status);
 }
 
-// Clears the values that are not finite in two 16-byte columns of a slab of
-// V, with one warp; true if there were any.
-__device__ __forceinline__ bool clear_not_finite(uint8_t* slab, int chunk, int lane) {
-    bool any = false;
+// --------------------------------------------------------------- key warps
+// Warp wk: key channels 32 (wk % 4) .. + 31 (the tensor-memory lanes it may
+// access) of the 16 tokens 16 (wk / 4) .. of each 32.  Transposing matrix loads
+// give a thread the same key channel of two neighbouring tokens in a word,
+// which is how the A operand wants them.
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+// 16 lanes x 8 columns: words (lane / 4, lane % 4) of the 8 x 4 blocks (rows
+// 0-7, 8-15) of columns 0-3, then of columns 4-7.
+__device__ __forceinline__ void st_16x8(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <bool kStates>
+__device__ __forceinline__ void key_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wk, int lane) {
+    using M = Smem<kStates>;
+    constexpr int n = M::kStages;
+    int* status = p.a.status;
+    const int half = wk >> 2, kg = 4 * (wk & 3) + (lane >> 3);
+    const uint32_t src0 = smem_u32(smem) + M::kK + (kg >> 3) * kSlab + (16 * half + (lane & 7)) * 128 +
+                          (((kg & 7) ^ (lane & 7)) << 4);
+    const uint32_t dst = tmem + (static_cast<uint32_t>(32 * (wk & 3)) << 16) + kColK + 8 * half;
+    const int tok = 16 * half + 2 * (lane & 3);
+    walk<kStates>(p, [&](const Unit&, int, int valid, const Pos<n>& x) {
+        const uint32_t buf = x.it & 1u;
+        if (!wait_phase(&b.full_k[x.s], x.st, status) || !wait_phase(&b.dec_full[buf], x.dec_ph(), status)) return false;
+        if (valid < kC) {
+            // Rows behind the sequence's end: another sequence's tokens, or
+            // anything.  V's are cleared here, K's below.
+            uint8_t* V = smem + M::kV + x.s * kTile;
+            if (!wait_phase(&b.full_v[x.s], x.st, status)) return false;
 #pragma unroll 1
-    for (int r = lane; r < kC; r += 32)
-#pragma unroll 1
-        for (int x = chunk; x < chunk + 2; ++x) {
-            uint32_t* at = reinterpret_cast<uint32_t*>(slab + r * 128 + ((x ^ (r & 7)) << 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v = at[j];
-                if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-                if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
-                any |= v != at[j];
-                at[j] = v;
-            }
+            for (int r = valid + wk; r < kC; r += kKeyWarps)
+                if (lane < 16)
+                    *reinterpret_cast<uint4*>(V + (lane >> 3) * kSlab + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
         }
-    return __any_sync(0xffffffffu, any);
+        const uint32_t src = src0 + x.s * kTile;
+        const float* W = reinterpret_cast<const float*>(smem + M::kW) + buf * kC + tok;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            // Three truncated parts of k w: the upper halves of k w, of what
+            // is left, and of what is left then.
+            uint32_t part[3][2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t r[4];
+                ldsm_x4_t(r, src + (32 * q + 8 * t) * 128);
+                const float2 w2 = *reinterpret_cast<const float2*>(W + 32 * q + 8 * t);
+                // (Tokens behind the end: k is cleared, w is 0.)
+                const int left = valid - (32 * q + 8 * t + tok);
+                const uint32_t keep = left > 1 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    r[m] &= keep;
+                    float x0 = bf16_lo(r[m]), x1 = bf16_hi(r[m]);
+                    mul2v(x0, x1, w2.x, w2.y);
+                    const uint32_t a0 = __float_as_uint(x0), a1 = __float_as_uint(x1);
+                    sub2(x0, x1, __uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u));
+                    const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
+                    sub2(x0, x1, __uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
+                    part[0][t][m] = prmt_hi(a0, a1);
+                    part[1][t][m] = prmt_hi(b0, b1);
+                    part[2][t][m] = prmt_hi(__float_as_uint(x0), __float_as_uint(x1));
+                }
+            }
+            const uint32_t use = 2 * x.it + (q >> 1);
+            if (use > 0 && !wait_phase(&b.kp_empty[q & 1], (use - 1) & 1u, status)) return false;
+            tc::fence_after_sync();
+            const uint32_t col = dst + kKBuf * (q & 1);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                st_16x8(col + kKPart * i, part[i][0][0], part[i][0][1], part[i][1][0], part[i][1][1]);
+                st_16x8(col + kKPart * i + (16u << 16), part[i][0][2], part[i][0][3], part[i][1][2], part[i][1][3]);
+            }
+            tc::wait_st();
+            tc::fence_before_sync();
+            arrive_warp(&b.kp_full[q & 1], lane);
+        }
+        stage_release(&b.empty_k[x.s], lane);
+        arrive_warp(&b.dec_empty[buf], lane);
+        return true;
+    });
 }
 
 // ------------------------------------------------------------- state warps
 // Warp ws: key channels 32 (ws % 4) .. + 31, one per lane (the tensor-memory
-// lanes it may access); value channels 64 (ws / 4) .. + 63 of S; of K', the
-// 16 tokens 16 (ws / 4) .. of each 32.
-// 32 of a lane's value channels of a state in global memory ([value][key],
-// stride 128), or zeros.
-__device__ __forceinline__ void load_state(const void* base, bool f32, int64_t at, uint32_t (&x)[32]) {
-    if (!base) {
+// lanes it may access); value channels 64 (ws / 4) .. + 63.
+//
+// The paths that run once per unit, or never on finite values, are calls with
+// short loops: they stay out of the instruction cache's way.
+
+// Clears the values that are not finite in two 16-byte columns of a slab of
+// V, with one warp; true if there were any.
+__device__ __noinline__ bool clear_not_finite(uint8_t* slab, int chunk, int lane) {
+    bool any = false;
+#pragma unroll 1
+    for (int r = lane; r < kC; r += 32)
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(slab + r * 128 + (((chunk + (x >> 2)) ^ (r & 7)) << 4)) + (x & 3);
+            uint32_t v = *at;
+            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+            any |= v != *at;
+            *at = v;
+        }
+    return __any_sync(0xffffffffu, any);
+}
+__device__ __forceinline__ float load_elem(const void* base, bool f32, int64_t at) {
+    if (!base) return 0.f;
+    return f32 ? static_cast<const float*>(base)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
+}
+__device__ __forceinline__ void store_elem(void* base, bool f32, int64_t at, float x) {
+    if (f32)
+        static_cast<float*>(base)[at] = x;
+    else
+        static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
+}
+// This thread's 64 value channels of a state in global memory ([value][key]):
+// into tensor memory times d and, in BF16, into its row of the S operand.
+__device__ __noinline__ void state_in(const void* base, bool f32, int64_t at, uint32_t scol, float d, uint8_t* row, int key) {
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        uint32_t x[8], y[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0u;
-    } else if (f32) {
+        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(load_elem(base, f32, at + (8 * j + i) * kHeadDim));
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = static_cast<const uint32_t*>(base)[at + i * kHeadDim];
-    } else {
+        for (int i = 0; i < 4; ++i) y[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        *reinterpret_cast<uint4*>(row + ((j ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            x[i] = static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + i * kHeadDim]) << 16;
+        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * d);
+        st_x8(scol + 8 * j, x);
     }
 }
-__device__ __forceinline__ void store_state(void* base, bool f32, int64_t at, const uint32_t (&x)[32]) {
-    if (f32) {
+// ... and from tensor memory to global memory.
+__device__ __noinline__ void state_out(void* base, bool f32, int64_t at, uint32_t scol) {
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        uint32_t x[8];
+        ld_x8(scol + 8 * j, x);
+        tc::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) static_cast<uint32_t*>(base)[at + i * kHeadDim] = x[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            static_cast<__nv_bfloat16*>(base)[at + i * kHeadDim] = __float2bfloat16_rn(__uint_as_float(x[i]));
+        for (int i = 0; i < 8; ++i) store_elem(base, f32, at + (8 * j + i) * kHeadDim, __uint_as_float(x[i]));
     }
 }
 
@@ -530,136 +589,73 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
-    volatile int* flag = reinterpret_cast<volatile int*>(smem + M::kFlag);
+    volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(smem + M::kFlag);
     const int half = ws >> 2, key = 32 * (ws & 3) + lane;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (ws & 3)) << 16);
-    const uint32_t scol = trow + kColS + 64 * half;
-    const uint32_t kbase = (key >> 6) * kSlab + 16 * half * 128 + 2 * (key & 7);
-    const uint32_t kchunk = ((key & 63) >> 3) << 4;
-    int64_t it = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const uint32_t scol = tmem + (static_cast<uint32_t>(32 * (ws & 3)) << 16) + kColS + 64 * half;
+    uint8_t* row = smem + M::kS + half * kSlab + key * 128;
+    const int64_t lane_at = 64 * half * kHeadDim + key;
+    const void* init = p.sg.starts ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
+    const bool init_f32 = p.sg.starts || p.a.state_f32;
+    Pos<n> x;
+#pragma unroll 1
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
         const Unit w = unit_at<kStates>(p, u);
-        const int64_t at = ((w.n * p.a.H + w.h) * kHeadDim + 64 * half) * kHeadDim + key;
-        const int64_t seg_at = (w.slot * kHeadDim + 64 * half) * kHeadDim + key;
-        const void* init = p.sg.starts ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
-        const bool init_f32 = p.sg.starts || p.a.state_f32;
+        const int64_t at = (static_cast<int64_t>(w.n) * p.a.H + w.h) * (kHeadDim * kHeadDim) + lane_at;
+        const int64_t seg_at = static_cast<int64_t>(w.slot) * (kHeadDim * kHeadDim) + lane_at;
         const int64_t init_at = p.sg.starts ? seg_at : at;
         const bool final = !kStates && w.last && p.a.final_state;
         if (w.nch == 0) {
             if (final)
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t x[32];
-                    load_state(init, init_f32, init_at + 32 * i * kHeadDim, x);
-                    store_state(p.a.final_state, p.a.state_f32, at + 32 * i * kHeadDim, x);
-                }
+                for (int i = 0; i < 64; ++i)
+                    store_elem(p.a.final_state, p.a.state_f32, at + i * kHeadDim, load_elem(init, init_f32, init_at + i * kHeadDim));
             continue;
         }
         float total = 0.f;
-        for (int c = 0; c < w.nch; ++c, ++it) {
-            const int s = static_cast<int>(it % n), buf = static_cast<int>(it & 1);
-            const uint32_t st = static_cast<uint32_t>(it / n) & 1u, ph = static_cast<uint32_t>(it & 1);
-            uint8_t* K = smem + M::kK + s * kTile;
-            uint8_t* V = smem + M::kV + s * kTile;
-            const int valid = valid_of(w, c);
-            if (!wait_phase(&b.full_k[s], st, status) ||
-                !wait_phase(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status))
-                return;
-            if (valid < kC) {
-                // Rows behind the sequence's end: another sequence's tokens,
-                // or anything.  V's are cleared here, K's below.
-                if (!wait_phase(&b.full_v[s], st, status)) return;
-                for (int r = valid + ws; r < kC; r += kStateWarps)
-                    if (lane < 16)
-                        *reinterpret_cast<uint4*>(V + (lane >> 3) * kSlab + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            // K' of tokens 32 q + 16 half .. + 15: three truncated parts.
-            auto form = [&](int q) -> bool {
-                const uint8_t* src = K + kbase + 32 * q * 128;
-                const float4* wp = reinterpret_cast<const float4*>(smem + M::kW + buf * kC * 4) + 8 * q + 4 * half;
-                uint32_t kb[16];
-                float4 w4[4];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    kb[i] = *reinterpret_cast<const uint16_t*>(src + i * 128 + (kchunk ^ ((i & 7) << 4)));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w4[i] = wp[i];
-                if (valid < kC) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (32 * q + 16 * half + i >= valid) kb[i] = 0;
-                }
-                uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float w0 = i & 1 ? w4[i >> 1].z : w4[i >> 1].x, w1 = i & 1 ? w4[i >> 1].w : w4[i >> 1].y;
-                    float x0 = __uint_as_float(kb[2 * i] << 16), x1 = __uint_as_float(kb[2 * i + 1] << 16);
-                    mul2v(x0, x1, w0, w1);
-                    const uint32_t a0 = __float_as_uint(x0), a1 = __float_as_uint(x1);
-                    sub2(x0, x1, __uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u));
-                    const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
-                    sub2(x0, x1, __uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
-                    hi[i] = prmt_hi(a0, a1);
-                    mid[i] = prmt_hi(b0, b1);
-                    lo[i] = prmt_hi(__float_as_uint(x0), __float_as_uint(x1));
-                }
-                if (q == 3) stage_release(&b.empty_k[s], lane);
-                const int64_t use = 2 * it + (q >> 1);
-                if (use > 0 && !wait_phase(&b.kp_empty[q & 1], static_cast<uint32_t>(use - 1) & 1u, status)) return false;
-                tc::fence_after_sync();
-                const uint32_t col = trow + kColK + kKBuf * (q & 1) + 8 * half;
-                st_x8(col, hi);
-                st_x8(col + kKPart, mid);
-                st_x8(col + 2 * kKPart, lo);
-                tc::wait_st();
-                tc::fence_before_sync();
-                arrive_warp(&b.kp_full[q & 1], lane);
-                return true;
-            };
-            if (!form(0)) return;
+#pragma unroll 1
+        for (int c = 0; c < w.nch; ++c, x.next()) {
+            const uint32_t buf = x.it & 1u, ph = x.ph();
+            if (!wait_phase(&b.dec_full[buf], x.dec_ph(), status)) return;
             const float sum = reinterpret_cast<const float*>(smem + M::kG)[buf * kC + kC - 1];
-            const float d = exp2f(sum);
+            arrive_warp(&b.dec_empty[buf], lane);
+            const float d = ex2(sum);
             total += sum;
             // The state before this chunk: its BF16 copy as the B operand of
             // Q' S^T (row d: 128 value channels), once the last chunk's
             // product has read its own, and the decayed state.
-            if (!kStates && it > 0 && !wait_phase(b.qs_done, ph ^ 1u, status)) return;
-            if (!kStates || c > 0) {
-                tc::fence_after_sync();
+            if (!kStates && x.it > 0 && !wait_phase(b.qs_done, ph ^ 1u, status)) return;
+            tc::fence_after_sync();
+            if (c > 0) {
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
-                    uint32_t x[32];
-                    if (c == 0) {
-                        load_state(init, init_f32, init_at + 32 * i * kHeadDim, x);
-                    } else {
-                        tc::ld_x32(scol + 32 * i, x);
-                        tc::wait_ld();
-                    }
-                    if (!kStates) {
-                        uint8_t* row = smem + M::kS + half * kSlab + key * 128;
+                    uint32_t r[32];
+                    tc::ld_x32(scol + 32 * i, r);
+                    tc::wait_ld();
+                    if (!kStates)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t y[4];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                y[r] = pack_bf16(__uint_as_float(x[8 * j + 2 * r]), __uint_as_float(x[8 * j + 2 * r + 1]));
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = pack_bf16(__uint_as_float(r[8 * j + 2 * e]), __uint_as_float(r[8 * j + 2 * e + 1]));
                             *reinterpret_cast<uint4*>(row + (((4 * i + j) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
-                    }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * d);
-                    tc::st_x32(scol + 32 * i, x);
+                    for (int j = 0; j < 32; j += 2) {
+                        float y0 = __uint_as_float(r[j]), y1 = __uint_as_float(r[j + 1]);
+                        mul2(y0, y1, d);
+                        r[j] = __float_as_uint(y0);
+                        r[j + 1] = __float_as_uint(y1);
+                    }
+                    tc::st_x32(scol + 32 * i, r);
                 }
-                if (!kStates) fence_proxy_async_smem();
-                tc::wait_st();
-                tc::fence_before_sync();
+            } else if (!kStates) {
+                state_in(init, init_f32, init_at, scol, d, row, key);
             }
+            if (!kStates) fence_proxy_async_smem();
+            tc::wait_st();
+            tc::fence_before_sync();
             arrive_warp(b.s_ready, lane);
-#pragma unroll 1
-            for (int q = 1; q < 4; ++q)
-                if (!form(q)) return;
-            arrive_warp(&b.dec_empty[buf], lane);
             if (!wait_phase(b.z_done, ph, status)) return;
             tc::fence_after_sync();
             if (!kStates) {
@@ -672,29 +668,22 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
 #pragma unroll
                 for (int i = 0; i < 16; ++i) chk = fmaf(__uint_as_float(z[i]), 0.f, chk);
                 if (__any_sync(0xffffffffu, !(chk == 0.f))) {
-                    // The flag of a chunk is its number, so none has to be cleared.
-                    if (clear_not_finite(V + half * kSlab, 2 * (ws & 3), lane) && lane == 0)
-                        flag[buf] = static_cast<int>(it + 1);
+                    // The flag of a chunk is its number + 1, so none has to be cleared.
+                    if (clear_not_finite(smem + M::kV + x.s * kTile + half * kSlab, 2 * (ws & 3), lane) && lane == 0)
+                        flag[buf] = x.it + 1;
                     fence_proxy_async_smem();
                     __threadfence_block();
                 }
-                arrive_warp(b.checked, lane);
+                arrive_warp(b.pv_ready, lane);
             }
         }
-        if (kStates || final) {
-#pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                uint32_t x[32];
-                tc::ld_x32(scol + 32 * i, x);
-                tc::wait_ld();
-                if (kStates)
-                    store_state(p.sg.starts, true, seg_at + 32 * i * kHeadDim, x);
-                else
-                    store_state(p.a.final_state, p.a.state_f32, at + 32 * i * kHeadDim, x);
-            }
-            if (kStates && ws == 0 && lane == 0) p.sg.decay[w.slot] = total;
-            tc::fence_before_sync();
+        if (kStates) {
+            state_out(p.sg.starts, true, seg_at, scol);
+            if (ws == 0 && lane == 0) p.sg.decay[w.slot] = total;
+        } else if (final) {
+            state_out(p.a.final_state, p.a.state_f32, at, scol);
         }
+        tc::fence_before_sync();
     }
 }
 
@@ -708,196 +697,191 @@ __device__ __forceinline__ void score_role(const Kernel& p, uint8_t* smem, const
     int* status = p.a.status;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wp) << 16) + kColD1;
     const float scale = p.a.scale;
-    int64_t it = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const Unit w = unit_at<false>(p, u);
-        for (int c = 0; c < w.nch; ++c, ++it) {
-            const int buf = static_cast<int>(it & 1);
-            const float* G = reinterpret_cast<const float*>(smem + M::kG) + buf * kC;
-            const float4* Cf = reinterpret_cast<const float4*>(smem + M::kCf + buf * 96 * 4);
-            if (!wait_phase(&b.dec_full[buf], static_cast<uint32_t>(it >> 1) & 1u, status)) return;
-            const float gi = G[32 * wp + lane];
-            if (!wait_phase(b.qk, static_cast<uint32_t>(it & 1), status)) return;
-            tc::fence_after_sync();
-            // A block's columns of P, 16 blk .. + 15, held scores of blocks
-            // already read.
-            auto full = [&](int blk, const uint32_t (&x)[32]) {
-                const float f = scale * ex2(gi - G[32 * blk + 31]);
-                uint32_t pk[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 cf = Cf[8 * blk + j];
-                    float y0 = __uint_as_float(x[4 * j]), y1 = __uint_as_float(x[4 * j + 1]);
-                    float y2 = __uint_as_float(x[4 * j + 2]), y3 = __uint_as_float(x[4 * j + 3]);
-                    mul2(y0, y1, f);
-                    mul2(y2, y3, f);
-                    mul2v(y0, y1, cf.x, cf.y);
-                    mul2v(y2, y3, cf.z, cf.w);
-                    pk[2 * j] = pack_bf16(y0, y1);
-                    pk[2 * j + 1] = pack_bf16(y2, y3);
-                }
-                tc::st_x16(trow + 16 * blk, pk);
-            };
-            uint32_t x[32];
+    walk<false>(p, [&](const Unit&, int, int, const Pos<2>& at) {
+        const uint32_t buf = at.it & 1u;
+        const float* G = reinterpret_cast<const float*>(smem + M::kG) + buf * kC;
+        const float4* Cf = reinterpret_cast<const float4*>(smem + M::kCf + buf * 96 * 4);
+        if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
+        const float gi = G[32 * wp + lane];
+        if (!wait_phase(b.qk, at.ph(), status)) return false;
+        tc::fence_after_sync();
+        // A block's columns of P, 16 blk .. + 15, held scores of blocks read
+        // before it.
+        uint32_t x[32];
 #pragma unroll 1
-            for (int blk = 0; blk < wp; ++blk) {
-                tc::ld_x32(trow + 32 * blk, x);
-                tc::wait_ld();
-                full(blk, x);
-            }
-            tc::ld_x32(trow + 32 * wp, x);
+        for (int blk = 0; blk < wp; ++blk) {
+            tc::ld_x32(trow + 32 * blk, x);
+            const float f = scale * ex2(gi - G[32 * blk + 31]);
+            tc::wait_ld();
             uint32_t pk[16];
-            float ex[32];
-            const float4* Gb = reinterpret_cast<const float4*>(G + 32 * wp);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float4 g4 = Gb[j];
-                ex[4 * j] = scale * ex2(gi - g4.x);
-                ex[4 * j + 1] = scale * ex2(gi - g4.y);
-                ex[4 * j + 2] = scale * ex2(gi - g4.z);
-                ex[4 * j + 3] = scale * ex2(gi - g4.w);
+                const float4 cf = Cf[8 * blk + j];
+                float y0 = __uint_as_float(x[4 * j]), y1 = __uint_as_float(x[4 * j + 1]);
+                float y2 = __uint_as_float(x[4 * j + 2]), y3 = __uint_as_float(x[4 * j + 3]);
+                mul2(y0, y1, f);
+                mul2(y2, y3, f);
+                mul2v(y0, y1, cf.x, cf.y);
+                mul2v(y2, y3, cf.z, cf.w);
+                pk[2 * j] = pack_bf16(y0, y1);
+                pk[2 * j + 1] = pack_bf16(y2, y3);
             }
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const float y0 = j > lane ? 0.f : __uint_as_float(x[j]) * ex[j];
-                const float y1 = j + 1 > lane ? 0.f : __uint_as_float(x[j + 1]) * ex[j + 1];
-                pk[j / 2] = pack_bf16(y0, y1);
-            }
-            tc::st_x16(trow + 16 * wp, pk);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = 0u;
-#pragma unroll 1
-            for (int blk = wp + 1; blk < 4; ++blk) tc::st_x16(trow + 16 * blk, pk);
-            tc::wait_st();
-            tc::fence_before_sync();
-            arrive_warp(b.p, lane);
-            arrive_warp(&b.dec_empty[buf], lane);
+            tc::st_x16(trow + 16 * blk, pk);
         }
-    }
+        const float4* Gb = reinterpret_cast<const float4*>(G + 32 * wp);
+        tc::ld_x32(trow + 32 * wp, x);
+        tc::wait_ld();
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 g4 = Gb[j];
+            const float gj[4] = {g4.x, g4.y, g4.z, g4.w};
+            float y[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                y[r] = 4 * j + r > lane ? 0.f : __uint_as_float(x[4 * j + r]) * (scale * ex2(gi - gj[r]));
+            pk[2 * j] = pack_bf16(y[0], y[1]);
+            pk[2 * j + 1] = pack_bf16(y[2], y[3]);
+        }
+        tc::st_x16(trow + 16 * wp, pk);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = 0u;
+#pragma unroll 1
+        for (int blk = wp + 1; blk < 4; ++blk) tc::st_x16(trow + 16 * blk, pk);
+        tc::wait_st();
+        tc::fence_before_sync();
+        arrive_warp(b.pv_ready, lane);
+        arrive_warp(&b.dec_empty[buf], lane);
+        return true;
+    });
 }
 
-// x[c] += pj v[c] where v[c] is not finite, for 32 channels.
-__device__ __forceinline__ void add_not_finite(uint32_t (&x)[32], const __nv_bfloat16* v, float pj, bool on) {
-    if (!on) return;
+// ------------------------------------------------------------- query warps
+// Warp wq: rows (tokens) 32 wq .. + 31, one per lane.  Q' in place, once D1
+// has been formed from Q.  The factor goes in as two BF16 parts of one fused
+// multiply-add: one rounding.
+__device__ __forceinline__ void query_role(const Kernel& p, uint8_t* smem, const Bars& b, int wq, int lane) {
+    using M = Smem<false>;
+    int* status = p.a.status;
+    const int row = 32 * wq + lane;
+    walk<false>(p, [&](const Unit&, int, int, const Pos<2>& at) {
+        const uint32_t buf = at.it & 1u;
+        uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
+        if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
+        const float e = p.a.scale * ex2(reinterpret_cast<const float*>(smem + M::kG)[buf * kC + row]);
+        arrive_warp(&b.dec_empty[buf], lane);
+        const __nv_bfloat16 eh = __float2bfloat16_rn(e);
+        const __nv_bfloat162 e1 = __bfloat162bfloat162(eh);
+        const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e - __bfloat162float(eh)));
+        if (!wait_phase(&b.full_q[at.s], at.st, status) || !wait_phase(b.qk, at.ph(), status)) return false;
+#pragma unroll 1
+        for (int sl = 0; sl < 2; ++sl, Qrow += kSlab) {
+            uint4 v[8];
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-        const uint4 v4 = reinterpret_cast<const uint4*>(v)[ch];
-        const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+            for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint4*>(Qrow + ((x ^ (row & 7)) << 4));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            uint32_t& o0 = x[8 * ch + 2 * r];
-            uint32_t& o1 = x[8 * ch + 2 * r + 1];
-            if ((vw[r] & 0x7f80u) == 0x7f80u)
-                o0 = __float_as_uint(fmaf(pj, bf16_lo(vw[r]), __uint_as_float(o0)));
-            if ((vw[r] & 0x7f800000u) == 0x7f800000u)
-                o1 = __float_as_uint(fmaf(pj, bf16_hi(vw[r]), __uint_as_float(o1)));
+            for (int x = 0; x < 8; ++x) {
+                __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v[x]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = __hfma2(h[j], e1, __hmul2(h[j], e2));
+                *reinterpret_cast<uint4*>(Qrow + ((x ^ (row & 7)) << 4)) = v[x];
+            }
         }
-    }
+        fence_proxy_async_smem();
+        arrive_warp(b.qs_ready, lane);
+        return true;
+    });
 }
 
 // ------------------------------------------------------------ output warps
 // Warp we: rows (tokens) 32 we .. + 31, one per lane.
+
+// Adds P_ij v_j to this row's O where v_j is not finite, for j <= i.
+// v: the chunk's first token of this head in global memory.
+__device__ __noinline__ void add_not_finite(uint32_t trow, const __nv_bfloat16* v, int64_t vstride, int row, int valid) {
+    const int first = row & ~31;
+#pragma unroll 1
+    for (int col = 0; col < kHeadDim; col += 8) {
+        uint32_t x[8];
+        ld_x8(trow + kColO + col, x);
+        tc::wait_ld();
+#pragma unroll 1
+        for (int j = 0; j < first + 32; ++j) {
+            uint32_t pp;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pp) : "r"(trow + kColD1 + (j >> 1)));
+            tc::wait_ld();
+            if (j <= row && j < valid) {
+                const float pj = j & 1 ? bf16_hi(pp) : bf16_lo(pp);
+                const uint4 v4 = *reinterpret_cast<const uint4*>(v + j * vstride + col);
+                const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if ((vw[r] & 0x7f80u) == 0x7f80u)
+                        x[2 * r] = __float_as_uint(fmaf(pj, bf16_lo(vw[r]), __uint_as_float(x[2 * r])));
+                    if ((vw[r] & 0x7f800000u) == 0x7f800000u)
+                        x[2 * r + 1] = __float_as_uint(fmaf(pj, bf16_hi(vw[r]), __uint_as_float(x[2 * r + 1])));
+                }
+            }
+            __syncwarp();
+        }
+        st_x8(trow + kColO + col, x);
+    }
+    tc::wait_st();
+}
+
 __device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* omap, uint8_t* smem, const Bars& b,
                                             uint32_t tmem, int we, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
-    const volatile int* flag = reinterpret_cast<const volatile int*>(smem + M::kFlag);
+    const volatile uint32_t* flag = reinterpret_cast<const volatile uint32_t*>(smem + M::kFlag);
     const int row = 32 * we + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * we) << 16);
-    int64_t it = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const Unit w = unit_at<false>(p, u);
-        for (int c = 0; c < w.nch; ++c, ++it) {
-            const int s = static_cast<int>(it & 1);   // two stages, two decay buffers
-            const uint32_t st = static_cast<uint32_t>(it >> 1) & 1u, ph = static_cast<uint32_t>(it & 1);
-            uint8_t* Qrow = smem + M::kQ + s * kTile + row * 128;
-            const int64_t vstride = p.a.H * kHeadDim;
-            const __nv_bfloat16* v0 = static_cast<const __nv_bfloat16*>(p.a.v) +
-                                      (w.tok0 + static_cast<int64_t>(c) * kC) * vstride + w.h * kHeadDim;
-            const int valid = valid_of(w, c);
-            // Q' in place, once D1 has been formed from Q.  The factor goes in
-            // as two BF16 parts of one fused multiply-add: one rounding.
-            if (!wait_phase(&b.dec_full[s], st, status)) return;
-            const float e = p.a.scale * ex2(reinterpret_cast<const float*>(smem + M::kG)[s * kC + row]);
-            arrive_warp(&b.dec_empty[s], lane);
-            if (!wait_phase(&b.full_q[s], st, status) || !wait_phase(b.qk, ph, status)) return;
-            const __nv_bfloat16 eh = __float2bfloat16_rn(e);
-            const __nv_bfloat162 e1 = __bfloat162bfloat162(eh);
-            const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e - __bfloat162float(eh)));
-#pragma unroll
-            for (int sl = 0; sl < 2; ++sl) {
-                uint4 v[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    v[x] = *reinterpret_cast<const uint4*>(Qrow + sl * kSlab + ((x ^ (row & 7)) << 4));
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v[x]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = __hfma2(h[j], e1, __hmul2(h[j], e2));
-                    *reinterpret_cast<uint4*>(Qrow + sl * kSlab + ((x ^ (row & 7)) << 4)) = v[x];
-                }
-            }
-            fence_proxy_async_smem();
-            arrive_warp(b.q_scaled, lane);
-
-            if (!wait_phase(b.o_done, ph, status)) return;
-            tc::fence_after_sync();
-            const bool bad = flag[s] == static_cast<int>(it + 1);
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) +
-                                 ((w.tok0 + static_cast<int64_t>(c) * kC + row) * p.a.H + w.h) * kHeadDim;
+    arrive_warp(b.qs_ready, lane);   // O is free for the first chunk
+    walk<false>(p, [&](const Unit& w, int c, int valid, const Pos<2>& at) {
+        uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
+        const int64_t ostride = p.a.H * kHeadDim, o0 = (w.tok0 + c * kC) * ostride + w.h * kHeadDim;
+        if (!wait_phase(b.o_done, at.ph(), status)) return false;
+        tc::fence_after_sync();
+        if (flag[at.it & 1u] == at.it + 1)
+            add_not_finite(trow, static_cast<const __nv_bfloat16*>(p.a.v) + o0, ostride, row, valid);
+        stage_release(&b.empty_v[at.s], lane);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + o0 + row * ostride;
 #pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
-                uint32_t x[32];
-                tc::ld_x32(trow + kColO + 32 * blk, x);
-                tc::wait_ld();
-                if (bad) {
-#pragma unroll 1
-                    for (int j = 0; j < 32 * (we + 1); j += 2) {
-                        uint32_t pp;
-                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-                                     : "=r"(pp) : "r"(trow + kColD1 + (j >> 1)));
-                        tc::wait_ld();
-                        add_not_finite(x, v0 + j * vstride + 32 * blk, bf16_lo(pp), j <= row && j < valid);
-                        add_not_finite(x, v0 + (j + 1) * vstride + 32 * blk, bf16_hi(pp), j < row && j + 1 < valid);
-                    }
-                }
-                if (blk == 3) {
-                    // O and P are read, and V by every product.
-                    tc::fence_before_sync();
-                    arrive_warp(b.o_free, lane);
-                    stage_release(&b.empty_v[s], lane);
-                }
+        for (int blk = 0; blk < 4; ++blk) {
+            uint32_t x[32];
+            tc::ld_x32(trow + kColO + 32 * blk, x);
+            tc::wait_ld();
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t y[4];
+            for (int r = 0; r < 16; ++r) x[r] = pack_bf16(__uint_as_float(x[2 * r]), __uint_as_float(x[2 * r + 1]));
+            if (valid == kC) {   // through Q's stage, which every product has read
+                uint8_t* slab = Qrow + (blk >> 1) * kSlab;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        y[r] = pack_bf16(__uint_as_float(x[8 * ch + 2 * r]), __uint_as_float(x[8 * ch + 2 * r + 1]));
-                    const uint4 v = make_uint4(y[0], y[1], y[2], y[3]);
-                    if (valid == kC)   // through Q's stage, which every product has read
-                        *reinterpret_cast<uint4*>(Qrow + (blk >> 1) * kSlab + (((4 * (blk & 1) + ch) ^ (row & 7)) << 4)) = v;
-                    else if (row < valid)
-                        reinterpret_cast<uint4*>(out)[4 * blk + ch] = v;
-                }
+                for (int ch = 0; ch < 4; ++ch)
+                    *reinterpret_cast<uint4*>(slab + (((4 * (blk & 1) + ch) ^ (row & 7)) << 4)) =
+                        make_uint4(x[4 * ch], x[4 * ch + 1], x[4 * ch + 2], x[4 * ch + 3]);
+            } else if (row < valid) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    reinterpret_cast<uint4*>(out)[4 * blk + ch] = make_uint4(x[4 * ch], x[4 * ch + 1], x[4 * ch + 2], x[4 * ch + 3]);
             }
-            if (valid == kC) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const uint8_t* src = smem + M::kQ + s * kTile + 32 * we * 128;
-                    const int y = static_cast<int>(w.tok0 + static_cast<int64_t>(c) * kC + 32 * we);
-                    const int x = static_cast<int>(w.h * kHeadDim);
-                    tma_store_2d(omap, x, y, src);
-                    tma_store_2d(omap, x + 64, y, src + kSlab);
-                    bulk_commit();
-                    bulk_wait_read_all();
-                }
-            }
-            stage_release(&b.empty_q[s], lane);
         }
-    }
+        tc::fence_before_sync();
+        arrive_warp(b.qs_ready, lane);   // O and P are read
+        if (valid == kC) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                const uint8_t* src = smem + M::kQ + at.s * kTile + 32 * we * 128;
+                const int y = w.tok0 + c * kC + 32 * we, x = w.h * kHeadDim;
+                tma_store_2d(omap, x, y, src);
+                tma_store_2d(omap, x + 64, y, src + kSlab);
+                bulk_commit();
+                bulk_wait_read_all();
+            }
+        }
+        stage_release(&b.empty_q[at.s], lane);
+        return true;
+    });
     if (lane == 0) bulk_wait_all();
 }
 
@@ -908,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using M = Smem<kStates>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (p.a.valid && !*p.a.valid) return;
-    if (smem_u32(smem) != kSmemBase) {   // the tiles' swizzle needs it; shared memory starts so
+    if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
         return;
     }
@@ -919,26 +903,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < M::kStages; ++s) {
             mbar_init(&b.full_k[s], 1);
             mbar_init(&b.full_v[s], 1);
-            mbar_init(&b.empty_k[s], kStates ? kStateWarps : kStateWarps + 1);
+            mbar_init(&b.full_q[s], 1);
+            mbar_init(&b.empty_k[s], kStates ? kKeyWarps : kKeyWarps + 1);
             mbar_init(&b.empty_v[s], kStates ? 1 : 4);
+            mbar_init(&b.empty_q[s], 4);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&b.full_q[s], 1);
-            mbar_init(&b.empty_q[s], 4);
-            mbar_init(&b.kp_full[s], kStateWarps);
+            mbar_init(&b.kp_full[s], kKeyWarps);
             mbar_init(&b.kp_empty[s], 1);
             mbar_init(&b.dec_full[s], 1);
-            mbar_init(&b.dec_empty[s], kStates ? kStateWarps : kStateWarps + 8);
+            mbar_init(&b.dec_empty[s], kKeyWarps + kStateWarps + (kStates ? 0 : 8));
         }
         mbar_init(b.qk, 1);
-        mbar_init(b.p, 4);
         mbar_init(b.z_done, 1);
-        mbar_init(b.checked, kStateWarps);
         mbar_init(b.s_ready, kStateWarps);
+        mbar_init(b.qs_ready, 8);             // query: Q' written; output: the last O read
         mbar_init(b.qs_done, 1);
-        mbar_init(b.q_scaled, 4);
+        mbar_init(b.pv_ready, kStateWarps + 4);   // state: V is finite; score: P written
         mbar_init(b.o_done, 1);
-        mbar_init(b.o_free, 4);
         mbar_init(b.done, 1);
         reinterpret_cast<int*>(smem + M::kFlag)[0] = 0;
         reinterpret_cast<int*>(smem + M::kFlag)[1] = 0;
@@ -953,16 +935,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_ptr;
 
-    if (warp < kStateWarps)
-        state_role<kStates>(p, smem, b, tmem, warp, lane);
+    if (warp < kStateWarp)
+        key_role<kStates>(p, smem, b, tmem, warp, lane);
+    else if (warp < kScoreWarp)
+        state_role<kStates>(p, smem, b, tmem, warp - kStateWarp, lane);
     else if (warp == kLoadWarp)
         load_role<kStates>(p, &qmap, &kmap, &vmap, smem, b, lane);
     else if (warp == kMmaWarp)
         mma_role<kStates>(p, smem, b, tmem, lane);
     else if (warp == kDecayWarp)
         decay_role<kStates>(p, smem, b, lane);
-    else if (!kStates && warp < kOutWarp)
+    else if (!kStates && warp < kQueryWarp)
         score_role(p, smem, b, tmem, warp - kScoreWarp, lane);
+    else if (!kStates && warp < kOutWarp)
+        query_role(p, smem, b, warp - kQueryWarp, lane);
     else if (!kStates)
         output_role(p, &omap, smem, b, tmem, warp - kOutWarp, lane);
 
@@ -1071,8 +1057,11 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     Kernel p;
     p.a = a;
     p.sg = sg;
-    p.units = (sg.starts ? sg.total : a.N) * a.H;
-    if (p.units <= 0) return cudaSuccess;
+    const int64_t units = (sg.starts ? sg.total : a.N) * a.H;
+    if (units <= 0) return cudaSuccess;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.units = static_cast<uint32_t>(units);
+    p.heads = static_cast<uint32_t>(a.H);
     CUtensorMap qm, km, vm, om;
     cudaError_t e;
     if ((e = configure<false>()) != cudaSuccess || (e = configure<true>()) != cudaSuccess) return e;
@@ -1081,7 +1070,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         (e = encode_tokens(&vm, a.v, a.tokens, a.H, kC)) != cudaSuccess ||
         (e = encode_tokens(&om, a.out, a.tokens, a.H, 32)) != cudaSuccess)
         return e;
-    const unsigned grid = static_cast<unsigned>(p.units < sms ? p.units : sms);
+    const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
     if (sg.starts) {
         la_kernel<true><<<grid, kThreads, Smem<true>::kBytes, stream>>>(p, qm, km, vm, om);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
