@@ -302,21 +302,45 @@ __device__ __forceinline__ void load_role(const Kernel& p, const CUtensorMap* qm
 }
 
 // -------------------------------------------------------------- decay warp
+// The decays are single words, a row of heads apart: on a loaded memory
+// system a load takes 3 us and more, so the lines are brought to L2 four
+// chunks ahead and the words one chunk ahead.
 template <bool kStates>
 __device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const Bars& b, int lane) {
     using M = Smem<kStates>;
+    constexpr int kAhead = 4;
+    float next[4] = {0.f, 0.f, 0.f, 0.f};
     walk<kStates>(p, [&](const Unit& w, int c, int valid, const Pos<M::kStages>& at) {
         const uint32_t buf = at.it & 1u;
-        const float* src = p.a.g + static_cast<int64_t>(w.tok0 + c * kC + 4 * lane) * p.a.g_stride + w.h;
+        const int64_t stride = p.a.g_stride;
+        // This lane's four tokens of chunk i: up to `left` of them are there.
+        auto source = [&](int i) { return p.a.g + static_cast<int64_t>(w.tok0 + i * kC + 4 * lane) * stride + w.h; };
+        auto fetch = [&](int i) {
+            const int left = w.len - i * kC - 4 * lane;
+            const float* src = source(i);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) next[r] = r < left ? src[r * stride] : 0.f;
+        };
+        auto prefetch = [&](int i) {
+            const int left = w.len - i * kC - 4 * lane;
+            const float* src = source(i);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < left) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + r * stride));
+        };
+        if (c == 0) {
+            fetch(0);
+#pragma unroll 1
+            for (int i = 1; i < kAhead; ++i) prefetch(i);
+        }
+        prefetch(c + kAhead);
         float x[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            x[r] = 0.f;
-            if (4 * lane + r < valid) {
-                x[r] = src[r * p.a.g_stride] * kLog2e;
-                if (x[r] < kMinDecay) x[r] = kMinDecay;   // -inf too; NaN stays
-            }
+            x[r] = next[r] * kLog2e;
+            if (x[r] < kMinDecay) x[r] = kMinDecay;   // -inf too; NaN stays
         }
+        fetch(c + 1);
         // Prefix and suffix sums, each from its own end.
         float pre[4], suf[4];
         pre[0] = x[0];
