@@ -17,42 +17,57 @@ from ._lib import KdaError
 
 HEAD_DIM = 128
 _SCALE = HEAD_DIM ** -0.5
-_STATE_TYPES = (torch.float32, torch.bfloat16)
 _ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}
+_BF16, _F32 = torch.bfloat16, torch.float32
+_FLOATS = (_F32, _BF16)
+
+# For a single token the checks and the marshalling cost more than the kernel:
+# one expression a tensor, and its message is made only where it fails.
 
 
-def _need(name, t, dtypes, shape):
-    """`t` is a contiguous CUDA tensor of one of `dtypes` with this shape."""
-    if not (t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
+def _bad(t, dtype, shape, dev):
+    """Whether `t` is anything but a contiguous CUDA tensor of this type (or one
+    of these), shape and device."""
+    return (t.get_device() != dev or (t.dtype is not dtype and t.dtype not in _types(dtype))
+            or t.shape != shape or not t.is_contiguous())
+
+
+def _types(dtype):
+    return dtype if type(dtype) is tuple else (dtype,)
+
+
+def _refuse(name, t, dtype, shape, dev):
+    if not t.is_cuda or t.dtype not in _types(dtype) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor"
-                         % (name, " or ".join(str(d) for d in dtypes)))
+                         % (name, " or ".join(str(d) for d in _types(dtype))))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, list(shape), list(t.shape)))
+    raise ValueError("%s must be on the device of the first argument" % name)
 
 
-def _on_current_device(t):
-    if t.get_device() != torch.cuda.current_device():
+def _need(name, t, dtype, shape, dev):
+    if _bad(t, dtype, shape, dev):
+        _refuse(name, t, dtype, shape, dev)
+
+
+def _device(name, t, dtype):
+    """The device of the first argument, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(name, t, dtype, t.shape, dev)
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors must be on the current CUDA device")
+    return dev
 
 
-def _stream(stream):
+def _stream(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-
-
-def _same_device(q, *others):
-    for t in others:
-        if t is not None and t.device != q.device:
-            raise ValueError("all tensors must be on one device")
 
 
 def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_state=None,
@@ -77,69 +92,69 @@ def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_sta
     H = v.shape[2]
     if Hk < 1 or H % Hk:
         raise ValueError("the heads of v must be a multiple of the heads of q")
-    _need("q", q, _BF16, q.shape)
-    _need("k", k, _BF16, q.shape)
-    _need("v", v, _BF16, (B, T, H, HEAD_DIM))
+    dev = _device("q", q, _BF16)
+    _need("q", q, _BF16, q.shape, dev)
+    _need("k", k, _BF16, q.shape, dev)
+    _need("v", v, _BF16, (B, T, H, HEAD_DIM), dev)
     flags = 0
     if g.dim() == 1:
-        _need("g", g, _F32, (H,))
+        _need("g", g, _F32, (H,), dev)
         flags = _lib.FLAG_G_PER_HEAD
     else:
-        _need("g", g, _F32, (B, T, H))
+        _need("g", g, _F32, (B, T, H), dev)
     N = B
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("packed input needs B == 1")
         N = cu_seqlens.numel() - 1
-        _need("cu_seqlens", cu_seqlens, (torch.int64,), (N + 1,))
+        _need("cu_seqlens", cu_seqlens, torch.int64, (N + 1,), dev)
     if init_state is not None:
-        _need("init_state", init_state, _STATE_TYPES, (N, H, HEAD_DIM, HEAD_DIM))
+        _need("init_state", init_state, _FLOATS, (N, H, HEAD_DIM, HEAD_DIM), dev)
         state_dtype = init_state.dtype
     elif final_state is not None:
         state_dtype = final_state.dtype
-    if state_dtype not in _STATE_TYPES:
+    if state_dtype not in _FLOATS:
         raise ValueError("states are torch.float32 or torch.bfloat16")
     if final_state is not None:
-        _need("final_state", final_state, (state_dtype,), (N, H, HEAD_DIM, HEAD_DIM))
+        _need("final_state", final_state, state_dtype, (N, H, HEAD_DIM, HEAD_DIM), dev)
     elif output_final_state:
         final_state = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=state_dtype, device=q.device)
     if out is None:
         out = torch.empty_like(v)
     else:
-        _need("out", out, _BF16, v.shape)
-    _same_device(q, k, v, g, init_state, cu_seqlens, out, final_state)
-    _on_current_device(q)
-    if state_dtype is torch.float32:
+        _need("out", out, _BF16, v.shape, dev)
+    if state_dtype is _F32:
         flags |= _lib.FLAG_STATE_F32
     rc = _lib.load().kda_la_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(init_state), _ptr(out),
                                     _ptr(final_state), N, T, H, Hk, _ptr(cu_seqlens),
-                                    _SCALE if scale is None else scale, flags, _stream(stream))
+                                    _SCALE if scale is None else scale, flags, _stream(stream, dev))
     if rc != 0:
         raise KdaError(rc, "kda_la_prefill")
     return out, final_state
 
 
 def _step_args(q, k, v, state, slots, out):
-    """Checks of q, k, v, state and slots of a single-token step; (N, H, Hk, pool, out)."""
+    """Checks of q, k, v, state and slots of a single-token step;
+    (device, N, H, Hk, pool, out)."""
     if q.dim() != 3 or v.dim() != 3 or q.shape[2] != HEAD_DIM or state.dim() != 4:
         raise ValueError("q and v must be [N, heads, 128], and state [pool, H, 128, 128]")
-    N, Hk, _ = q.shape
+    dev = _device("q", q, _BF16)
+    shape = q.shape
+    N, Hk, _ = shape
     H, pool = v.shape[1], state.shape[0]
-    _need("q", q, _BF16, (N, Hk, HEAD_DIM))
-    _need("k", k, _BF16, (N, Hk, HEAD_DIM))
-    _need("v", v, _BF16, (N, H, HEAD_DIM))
-    _need("state", state, _STATE_TYPES, (pool, H, HEAD_DIM, HEAD_DIM))
+    _need("q", q, _BF16, shape, dev)
+    _need("k", k, _BF16, shape, dev)
+    _need("v", v, _BF16, (N, H, HEAD_DIM), dev)
+    _need("state", state, _FLOATS, (pool, H, HEAD_DIM, HEAD_DIM), dev)
     if slots is not None:
-        _need("slots", slots, (torch.int32,), (N,))
+        _need("slots", slots, torch.int32, (N,), dev)
     elif N > pool:
         raise ValueError("state has fewer rows than there are sequences")
     if out is None:
         out = torch.empty_like(v)
     else:
-        _need("out", out, _BF16, (N, H, HEAD_DIM))
-    _same_device(q, k, v, state, slots, out)
-    _on_current_device(q)
-    return N, H, Hk, pool, out
+        _need("out", out, _BF16, (N, H, HEAD_DIM), dev)
+    return dev, N, H, Hk, pool, out
 
 
 def la_decode(q, k, v, g, state, slots=None, out=None, scale=None, stream=None):
@@ -152,19 +167,18 @@ def la_decode(q, k, v, g, state, slots=None, out=None, scale=None, stream=None):
     row, whose output is zero), or None for rows 0 .. N - 1.  A slot beyond the
     pool is treated as padding and sets ``KDA_DEV_BAD_SLOTS`` (``device_status``).
     """
-    N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
     if Hk < 1 or H % Hk:
         raise ValueError("the heads of v must be a multiple of the heads of q")
     flags = _lib.FLAG_STATE_F32 if state.dtype is torch.float32 else 0
     if g.dim() == 1:
-        _need("g", g, _F32, (H,))
+        _need("g", g, _F32, (H,), dev)
         flags |= _lib.FLAG_G_PER_HEAD
     else:
-        _need("g", g, _F32, (N, H))
-    _same_device(q, g)
+        _need("g", g, _F32, (N, H), dev)
     rc = _lib.load().kda_la_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(slots),
                                    _ptr(out), N, H, Hk, pool, _SCALE if scale is None else scale,
-                                   flags, _stream(stream))
+                                   flags, _stream(stream, dev))
     if rc != 0:
         raise KdaError(rc, "kda_la_decode")
     return out
@@ -179,16 +193,15 @@ def kda_decode(q, k, v, g, beta, state, slots=None, out=None, beta_is_logit=Fals
     such a state, and its fp32 copy keeps long generations from rounding it at
     every token.
     """
-    N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
     if Hk != H:
         raise ValueError("q must have the shape of v")
-    _need("g", g, _F32, (N, H, HEAD_DIM))
-    _need("beta", beta, _BF16, (N, H))
-    _same_device(q, g, beta)
+    _need("g", g, _F32, (N, H, HEAD_DIM), dev)
+    _need("beta", beta, _BF16, (N, H), dev)
     flags = ((_lib.FLAG_STATE_F32 if state.dtype is torch.float32 else 0) |
              (_lib.FLAG_BETA_LOGIT if beta_is_logit else 0))
     rc = _lib.load().kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
-                                _ptr(slots), _ptr(out), N, H, pool, flags, _stream(stream))
+                                _ptr(slots), _ptr(out), N, H, pool, flags, _stream(stream, dev))
     if rc != 0:
         raise KdaError(rc, "kda_decode")
     return out
@@ -209,20 +222,20 @@ def gated_norm(x, weight, gate=None, activation="sigmoid", gate_first=False, eps
     act = _ACTIVATIONS[activation] if gate is not None else 0
     if x.dim() < 1 or x.shape[-1] != HEAD_DIM:
         raise ValueError("x must be [..., 128]")
-    _need("x", x, _BF16, x.shape)
-    _need("weight", weight, _STATE_TYPES, (HEAD_DIM,))
+    dev = _device("x", x, _BF16)
+    shape = x.shape
+    _need("x", x, _BF16, shape, dev)
+    _need("weight", weight, _FLOATS, (HEAD_DIM,), dev)
     if act:
-        _need("gate", gate, _BF16, x.shape)
+        _need("gate", gate, _BF16, shape, dev)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _need("out", out, _BF16, x.shape)
-    _same_device(x, weight, gate, out)
-    _on_current_device(x)
+        _need("out", out, _BF16, shape, dev)
     flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
              (_lib.FLAG_GATE_FIRST if gate_first else 0))
     rc = _lib.load().kda_gated_norm(_ptr(x), _ptr(weight), _ptr(gate) if act else None, _ptr(out),
-                                    x.numel() // HEAD_DIM, act, eps, flags, _stream(stream))
+                                    x.numel() // HEAD_DIM, act, eps, flags, _stream(stream, dev))
     if rc != 0:
         raise KdaError(rc, "kda_gated_norm")
     return out
@@ -243,30 +256,29 @@ def residual_norm(x, residual, weight, post_weight=None, gate=None, scale=1.0, e
     """
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., D]")
-    D = x.shape[-1]
-    _need("x", x, _BF16, x.shape)
-    _need("residual", residual, _STATE_TYPES, x.shape)
-    _need("weight", weight, _STATE_TYPES, (D,))
-    wt = (weight.dtype,)
+    dev = _device("x", x, _BF16)
+    shape = x.shape
+    D = shape[-1]
+    _need("x", x, _BF16, shape, dev)
+    _need("residual", residual, _FLOATS, shape, dev)
+    _need("weight", weight, _FLOATS, (D,), dev)
     if post_weight is not None:
-        _need("post_weight", post_weight, wt, (D,))
+        _need("post_weight", post_weight, weight.dtype, (D,), dev)
     if gate is not None:
-        _need("gate", gate, wt, (D,))
+        _need("gate", gate, weight.dtype, (D,), dev)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _need("out", out, _BF16, x.shape)
+        _need("out", out, _BF16, shape, dev)
     if residual_out is None:
         residual_out = torch.empty_like(residual)
     else:
-        _need("residual_out", residual_out, (residual.dtype,), x.shape)
-    _same_device(x, residual, weight, post_weight, gate, out, residual_out)
-    _on_current_device(x)
+        _need("residual_out", residual_out, residual.dtype, shape, dev)
     flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
              (_lib.FLAG_RESIDUAL_F32 if residual.dtype is torch.float32 else 0))
     rc = _lib.load().kda_residual_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(post_weight),
                                        _ptr(gate), _ptr(out), _ptr(residual_out), x.numel() // D, D,
-                                       scale, eps, flags, _stream(stream))
+                                       scale, eps, flags, _stream(stream, dev))
     if rc != 0:
         raise KdaError(rc, "kda_residual_norm")
     return out, residual_out
