@@ -580,31 +580,42 @@ __device__ __forceinline__ void store_elem(void* base, bool f32, int64_t at, flo
     else
         static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
 }
-// This thread's 64 value channels of a state in global memory ([value][key]):
-// into tensor memory times d and, in BF16, into its row of the S operand.
-__device__ __noinline__ void state_in(const void* base, bool f32, int64_t at, uint32_t scol, float d, uint8_t* row, int key) {
+// This thread's 64 value channels of a state in global memory ([value][key];
+// zeros for none): into tensor memory, and back.  The loads of 32 channels are
+// under way at once: one after the other they took 6 us.
+__device__ __noinline__ void state_in(const void* base, bool f32, int64_t at, uint32_t scol) {
 #pragma unroll 1
-    for (int j = 0; j < 8; ++j) {
-        uint32_t x[8], y[4];
+    for (int i = 0; i < 2; ++i, at += 32 * kHeadDim) {
+        uint32_t x[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(load_elem(base, f32, at + (8 * j + i) * kHeadDim));
+        for (int j = 0; j < 32; ++j) x[j] = 0u;
+        if (base && f32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-        *reinterpret_cast<uint4*>(row + ((j ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int j = 0; j < 32; ++j) x[j] = static_cast<const uint32_t*>(base)[at + j * kHeadDim];
+        } else if (base) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * d);
-        st_x8(scol + 8 * j, x);
+            for (int j = 0; j < 32; ++j) x[j] = static_cast<const uint16_t*>(base)[at + j * kHeadDim];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] <<= 16;
+        }
+        tc::st_x32(scol + 32 * i, x);
     }
+    tc::wait_st();
 }
-// ... and from tensor memory to global memory.
 __device__ __noinline__ void state_out(void* base, bool f32, int64_t at, uint32_t scol) {
 #pragma unroll 1
-    for (int j = 0; j < 8; ++j) {
-        uint32_t x[8];
-        ld_x8(scol + 8 * j, x);
+    for (int i = 0; i < 2; ++i, at += 32 * kHeadDim) {
+        uint32_t x[32];
+        tc::ld_x32(scol + 32 * i, x);
         tc::wait_ld();
+        if (f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store_elem(base, f32, at + (8 * j + i) * kHeadDim, __uint_as_float(x[i]));
+            for (int j = 0; j < 32; ++j) static_cast<uint32_t*>(base)[at + j * kHeadDim] = x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                static_cast<__nv_bfloat16*>(base)[at + j * kHeadDim] = __float2bfloat16_rn(__uint_as_float(x[j]));
+        }
     }
 }
 
@@ -635,6 +646,11 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
                     store_elem(p.a.final_state, p.a.state_f32, at + i * kHeadDim, load_elem(init, init_f32, init_at + i * kHeadDim));
             continue;
         }
+        if (!kStates) {
+            // (The chain over the segments may still be running.)
+            if (p.sg.starts) asm volatile("griddepcontrol.wait;" ::: "memory");
+            state_in(init, init_f32, init_at, scol);
+        }
         float total = 0.f;
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c, x.next()) {
@@ -649,7 +665,7 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
             // product has read its own, and the decayed state.
             if (!kStates && x.it > 0 && !wait_phase(b.qs_done, ph ^ 1u, status)) return;
             tc::fence_after_sync();
-            if (c > 0) {
+            if (!kStates || c > 0) {
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     uint32_t r[32];
@@ -673,8 +689,6 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
                     }
                     tc::st_x32(scol + 32 * i, r);
                 }
-            } else if (!kStates) {
-                state_in(init, init_f32, init_at, scol, d, row, key);
             }
             if (!kStates) fence_proxy_async_smem();
             tc::wait_st();
@@ -911,10 +925,13 @@ __device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* 
 
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
-    la_kernel(const Kernel p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+    la_kernel(const __grid_constant__ Kernel p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
     using M = Smem<kStates>;
     extern __shared__ __align__(1024) uint8_t smem[];
+    // The next kernel may be placed where this one leaves room; what it needs
+    // of this one it waits for.
+    if (p.sg.starts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.a.valid && !*p.a.valid) return;
     if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
@@ -985,17 +1002,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The segments' incoming states: per (sequence, head), S_0 = init and
-// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  A CTA has 1024 of the 16384
-// elements; eight segments are loaded at a time.
-constexpr int kScanThreads = 256, kScanParts = kHeadDim * kHeadDim / (4 * kScanThreads);
-__global__ void __launch_bounds__(kScanThreads) la_scan_kernel(const Kernel p) {
+// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  A CTA has 128 of the 16384
+// elements and takes the segments 128 at a time: each of its eight warps loads
+// up to 16 of them at once, composes them, and starts from what the warps
+// before it compose to.  (One thread per element took the segments' latencies
+// one after the other: 21 us for 128 segments of one head.)
+constexpr int kScanWarps = 8, kScanEach = 16, kScanElems = 128, kScanParts = kHeadDim * kHeadDim / kScanElems;
+__global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_constant__ Kernel p) {
+    __shared__ float4 zsum[kScanWarps][32];
+    __shared__ float dsum[kScanWarps];
+    constexpr int64_t kState = kHeadDim * kHeadDim;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.a.valid && !*p.a.valid) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = blockIdx.x / kScanParts;
     const int64_t n = unit / p.a.H, h = unit - n * p.a.H;
-    const int64_t e = (blockIdx.x % kScanParts) * (4 * kScanThreads) + 4 * threadIdx.x;
+    const int64_t e = (blockIdx.x % kScanParts) * kScanElems + 4 * lane;
     const int64_t s0 = p.sg.seg_begin ? p.sg.seg_begin[n] : n * p.sg.segs;
     const int64_t s1 = p.sg.seg_begin ? p.sg.seg_begin[n + 1] : s0 + p.sg.segs;
-    constexpr int64_t kState = kHeadDim * kHeadDim;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.a.init_state) {
         if (p.a.state_f32) {
@@ -1005,30 +1030,57 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(const Kernel p) {
             s = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
         }
     }
-    if (s0 == s1 && p.a.final_state) {   // an empty sequence
+    if (s0 == s1 && p.a.final_state && warp == 0) {   // an empty sequence
         if (p.a.state_f32)
             *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + unit * kState + e) = s;
         else
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.final_state) + unit * kState + e) =
                 make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
-    for (int64_t j0 = s0; j0 < s1; j0 += 8) {
-        float4 z[8];
-        float d[8];
+    auto step = [](float d, const float4& a, const float4& z) {
+        return make_float4(fmaf(d, a.x, z.x), fmaf(d, a.y, z.y), fmaf(d, a.z, z.z), fmaf(d, a.w, z.w));
+    };
+    for (int64_t base = s0; base < s1; base += kScanWarps * kScanEach) {
+        const int64_t left = s1 - base;
+        const int count = left < kScanWarps * kScanEach ? static_cast<int>(left) : kScanWarps * kScanEach;
+        const int each = (count + kScanWarps - 1) / kScanWarps;
+        const int mine = min(each, max(0, count - warp * each));   // segments of this warp
+        const int64_t first = base + warp * each;
+        float4 z[kScanEach];
+        float d[kScanEach];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j0 + i + 1 < s1) {
-                z[i] = *reinterpret_cast<const float4*>(p.sg.starts + ((j0 + i) * p.a.H + h) * kState + e);
-                d[i] = p.sg.decay[(j0 + i) * p.a.H + h];
+        for (int i = 0; i < kScanEach; ++i) {
+            z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            d[i] = 0.f;
+            if (i < mine && first + i + 1 < s1) {   // (nothing follows the last segment)
+                z[i] = *reinterpret_cast<const float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e);
+                d[i] = p.sg.decay[(first + i) * p.a.H + h];
             }
+        }
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j0 + i < s1) {
-                *reinterpret_cast<float4*>(p.sg.starts + ((j0 + i) * p.a.H + h) * kState + e) = s;
-                if (j0 + i + 1 < s1) {
-                    const float f = exp2f(d[i]);
-                    s = make_float4(fmaf(f, s.x, z[i].x), fmaf(f, s.y, z[i].y), fmaf(f, s.z, z[i].z), fmaf(f, s.w, z[i].w));
-                }
+        for (int i = 0; i < kScanEach; ++i)
+            if (i < mine) {
+                total += d[i];
+                d[i] = ex2(d[i]);
+                sum = step(d[i], sum, z[i]);
+            }
+        __syncthreads();
+        zsum[warp][lane] = sum;
+        if (lane == 0) dsum[warp] = ex2(total);
+        __syncthreads();
+        float4 at = s;
+#pragma unroll 1
+        for (int g = 0; g < kScanWarps; ++g) {
+            if (g == warp) at = s;
+            s = step(dsum[g], s, zsum[g][lane]);
+        }
+#pragma unroll
+        for (int i = 0; i < kScanEach; ++i)
+            if (i < mine) {
+                *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e) = at;
+                at = step(d[i], at, z[i]);
             }
     }
 }
@@ -1095,16 +1147,34 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         (e = encode_tokens(&om, a.out, a.tokens, a.H, 32)) != cudaSuccess)
         return e;
     const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+    // Programmatic dependence: a kernel is launched while the one before it
+    // ends, and waits for it where it reads what that one wrote.
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = &after;
     if (sg.starts) {
-        la_kernel<true><<<grid, kThreads, Smem<true>::kBytes, stream>>>(p, qm, km, vm, om);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        la_scan_kernel<<<static_cast<unsigned>(a.N * a.H * kScanParts), kScanThreads, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Smem<true>::kBytes;
+        cfg.numAttrs = 0;
+        if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.N * a.H * kScanParts));
+        cfg.blockDim = dim3(32 * kScanWarps);
+        cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, la_scan_kernel, p)) != cudaSuccess) return e;
         *launches += 2;
     }
-    la_kernel<false><<<grid, kThreads, Smem<false>::kBytes, stream>>>(p, qm, km, vm, om);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<false>::kBytes;
+    cfg.numAttrs = sg.starts ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, la_kernel<false>, p, qm, km, vm, om)) != cudaSuccess) return e;
     *launches += 1;
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace kda

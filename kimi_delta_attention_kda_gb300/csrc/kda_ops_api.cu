@@ -88,7 +88,7 @@ LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64
         c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
         c.total = c.segs * pl.N;
     }
-    if (c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return LaCut();
+    if (units > 0x7fffffffLL / 128 || c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return LaCut();
     c.bytes = align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
     if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 3 * align256(8 * (c.segs + 1));
     return c;
