@@ -940,6 +940,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Bars b = make_bars<kStates>(smem);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + M::kTmemPtr);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // What the first chunk reads, on its way to L2 while the barriers and the
+    // tensor memory are made ready.
+    if (warp >= kLoadWarp && blockIdx.x < p.units) {
+        const Unit w = unit_at<kStates>(p, blockIdx.x);
+        if (w.nch > 0 && warp == kLoadWarp && lane == 0) {
+            const int kcol = static_cast<int>(w.h / static_cast<uint32_t>(p.a.H / p.a.Hk)) * kHeadDim, vcol = w.h * kHeadDim;
+#pragma unroll 1
+            for (int x = 0; x < kHeadDim; x += 64) {
+                tma_prefetch_l2_2d(&kmap, kcol + x, w.tok0);
+                tma_prefetch_l2_2d(&vmap, vcol + x, w.tok0);
+                if (!kStates) tma_prefetch_l2_2d(&qmap, kcol + x, w.tok0);
+            }
+        } else if (warp == kDecayWarp) {
+#pragma unroll 1
+            for (int r = lane; r < kC && r < w.len; r += 32)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.a.g + (w.tok0 + r) * p.a.g_stride + w.h));
+        }
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < M::kStages; ++s) {
             mbar_init(&b.full_k[s], 1);
@@ -1002,86 +1020,104 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The segments' incoming states: per (sequence, head), S_0 = init and
-// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  A CTA has 128 of the 16384
-// elements and takes the segments 128 at a time: each of its eight warps loads
-// up to 16 of them at once, composes them, and starts from what the warps
-// before it compose to.  (One thread per element took the segments' latencies
-// one after the other: 21 us for 128 segments of one head.)
-constexpr int kScanWarps = 8, kScanEach = 16, kScanElems = 128, kScanParts = kHeadDim * kHeadDim / kScanElems;
+// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  A CTA has 128 kVec of the
+// 16384 elements and takes the segments 8 kEach at a time: each of its eight
+// warps loads up to kEach of them at once, composes them, and starts from what
+// the warps before it compose to.  (One thread per element took the segments'
+// latencies one after the other: 21 us for 128 segments of one head, where
+// this takes 6.)  Few segments (kEach 4): with the registers of kEach 16 the
+// CTAs of 6 heads would need three waves, and the output kernel, which starts
+// when the last scan CTA has, would start with the third (9.4 us for the scan).
+constexpr int kScanWarps = 8;
+__host__ __device__ constexpr int scan_parts(int vec) { return kHeadDim * kHeadDim / (128 * vec); }
+template <int kEach, int kVec>
 __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_constant__ Kernel p) {
-    __shared__ float4 zsum[kScanWarps][32];
+    __shared__ float4 zsum[kScanWarps][kVec][32];
     __shared__ float dsum[kScanWarps];
     constexpr int64_t kState = kHeadDim * kHeadDim;
+    constexpr int kParts = scan_parts(kVec);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.a.valid && !*p.a.valid) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = blockIdx.x / kScanParts;
-    const int64_t n = unit / p.a.H, h = unit - n * p.a.H;
-    const int64_t e = (blockIdx.x % kScanParts) * kScanElems + 4 * lane;
+    const uint32_t unit = blockIdx.x / kParts, n = unit / p.heads, h = unit - n * p.heads;
+    const int64_t e = (blockIdx.x % kParts) * (128 * kVec) + 4 * lane;
     const int64_t s0 = p.sg.seg_begin ? p.sg.seg_begin[n] : n * p.sg.segs;
     const int64_t s1 = p.sg.seg_begin ? p.sg.seg_begin[n + 1] : s0 + p.sg.segs;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.a.init_state) {
-        if (p.a.state_f32) {
-            s = *reinterpret_cast<const float4*>(static_cast<const float*>(p.a.init_state) + unit * kState + e);
-        } else {
-            const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.init_state) + unit * kState + e);
-            s = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+    float4 s[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+        const int64_t at = unit * kState + e + 128 * v;
+        s[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.a.init_state) {
+            if (p.a.state_f32) {
+                s[v] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.a.init_state) + at);
+            } else {
+                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.init_state) + at);
+                s[v] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+            }
         }
-    }
-    if (s0 == s1 && p.a.final_state && warp == 0) {   // an empty sequence
-        if (p.a.state_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + unit * kState + e) = s;
-        else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.final_state) + unit * kState + e) =
-                make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+        if (s0 == s1 && p.a.final_state && warp == 0) {   // an empty sequence
+            if (p.a.state_f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + at) = s[v];
+            else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.final_state) + at) =
+                    make_uint2(pack_bf16(s[v].x, s[v].y), pack_bf16(s[v].z, s[v].w));
+        }
     }
     auto step = [](float d, const float4& a, const float4& z) {
         return make_float4(fmaf(d, a.x, z.x), fmaf(d, a.y, z.y), fmaf(d, a.z, z.z), fmaf(d, a.w, z.w));
     };
-    for (int64_t base = s0; base < s1; base += kScanWarps * kScanEach) {
+    for (int64_t base = s0; base < s1; base += kScanWarps * kEach) {
         const int64_t left = s1 - base;
-        const int count = left < kScanWarps * kScanEach ? static_cast<int>(left) : kScanWarps * kScanEach;
+        const int count = left < kScanWarps * kEach ? static_cast<int>(left) : kScanWarps * kEach;
         const int each = (count + kScanWarps - 1) / kScanWarps;
         const int mine = min(each, max(0, count - warp * each));   // segments of this warp
         const int64_t first = base + warp * each;
-        float4 z[kScanEach];
-        float d[kScanEach];
+        float4 z[kEach][kVec];
+        float d[kEach];
 #pragma unroll
-        for (int i = 0; i < kScanEach; ++i) {
-            z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            d[i] = 0.f;
-            if (i < mine && first + i + 1 < s1) {   // (nothing follows the last segment)
-                z[i] = *reinterpret_cast<const float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e);
-                d[i] = p.sg.decay[(first + i) * p.a.H + h];
-            }
+        for (int i = 0; i < kEach; ++i) {
+            const bool there = i < mine && first + i + 1 < s1;     // (nothing follows the last segment)
+            d[i] = there ? p.sg.decay[(first + i) * p.a.H + h] : 0.f;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+                z[i][v] = there ? *reinterpret_cast<const float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 sum[kVec];
         float total = 0.f;
 #pragma unroll
-        for (int i = 0; i < kScanEach; ++i)
+        for (int v = 0; v < kVec; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
             if (i < mine) {
                 total += d[i];
                 d[i] = ex2(d[i]);
-                sum = step(d[i], sum, z[i]);
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) sum[v] = step(d[i], sum[v], z[i][v]);
             }
         __syncthreads();
-        zsum[warp][lane] = sum;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) zsum[warp][v][lane] = sum[v];
         if (lane == 0) dsum[warp] = ex2(total);
         __syncthreads();
-        float4 at = s;
+        float4 at[kVec];
 #pragma unroll 1
-        for (int g = 0; g < kScanWarps; ++g) {
-            if (g == warp) at = s;
-            s = step(dsum[g], s, zsum[g][lane]);
-        }
+        for (int g = 0; g < kScanWarps; ++g)
 #pragma unroll
-        for (int i = 0; i < kScanEach; ++i)
-            if (i < mine) {
-                *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e) = at;
-                at = step(d[i], at, z[i]);
+            for (int v = 0; v < kVec; ++v) {
+                if (g == warp) at[v] = s[v];
+                s[v] = step(dsum[g], s[v], zsum[g][v][lane]);
             }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i < mine)
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v) = at[v];
+                    at[v] = step(d[i], at[v], z[i][v]);
+                }
     }
 }
 
@@ -1161,11 +1197,13 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         cfg.dynamicSmemBytes = Smem<true>::kBytes;
         cfg.numAttrs = 0;
         if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
-        cfg.gridDim = dim3(static_cast<unsigned>(a.N * a.H * kScanParts));
+        // Segments of a sequence: packed, one can have all but the others'.
+        const bool few = (sg.seg_begin ? sg.total - a.N + 1 : sg.segs) <= 4 * kScanWarps;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.N * a.H * scan_parts(few ? 2 : 1)));
         cfg.blockDim = dim3(32 * kScanWarps);
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, la_scan_kernel, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, few ? la_scan_kernel<4, 2> : la_scan_kernel<16, 1>, p)) != cudaSuccess) return e;
         *launches += 2;
     }
     cfg.gridDim = dim3(grid);
