@@ -110,6 +110,27 @@ struct Kernel {
     LaSegments sg;      // sg.starts null: no segments
     uint32_t units, heads;
 };
+// What this call does: a packed batch's cut is decided on the device.
+struct Work {
+    const LaArgs& a;
+    const LaSegments& sg;
+    uint32_t units, heads;
+    bool cut;           // the units are (segment, head), else (sequence, head)
+    const int32_t* order;   // packed, no cut: the sequences, longest first
+    __device__ __forceinline__ explicit Work(const Kernel& p) : a(p.a), sg(p.sg), units(p.units), heads(p.heads), cut(p.sg.starts), order(nullptr) {
+        if (sg.cut) {
+            cut = *sg.cut != 0;
+            units = static_cast<uint32_t>(cut ? sg.seg_begin[a.N] : a.N) * heads;
+            if (!cut) order = sg.order;
+        }
+    }
+    // The CTA's i-th unit: in rows of the grid's width, where the units come
+    // longest first every other row backwards.
+    __device__ __forceinline__ uint32_t unit(uint32_t i) const {
+        return i * gridDim.x + (order && (i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    }
+    __device__ __forceinline__ uint32_t rows() const { return (units + gridDim.x - 1) / gridDim.x; }
+};
 
 // One (sequence or segment, head).
 struct Unit {
@@ -119,17 +140,17 @@ struct Unit {
     int nch;
 };
 template <bool kStates>
-__device__ __forceinline__ Unit unit_at(const Kernel& p, uint32_t u) {
+__device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
     Unit w;
     const uint32_t s = u / p.heads;
     w.h = u - s * p.heads;
     w.slot = u;
     w.last = true;
-    if (!p.sg.starts) {
-        w.n = s;
+    if (!p.cut) {
+        w.n = p.order ? p.order[s] : s;
         if (p.a.cu_seqlens) {
-            w.tok0 = static_cast<int>(p.a.cu_seqlens[s]);
-            w.len = static_cast<int>(p.a.cu_seqlens[s + 1]) - w.tok0;
+            w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
+            w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
         } else {
             w.len = static_cast<int>(p.a.tokens_per_seq);
             w.tok0 = s * w.len;
@@ -137,8 +158,8 @@ __device__ __forceinline__ Unit unit_at(const Kernel& p, uint32_t u) {
     } else if (p.sg.seg_begin) {
         w.n = static_cast<int>(p.sg.seg_seq[s]);
         w.tok0 = static_cast<int>(p.sg.seg_tokens[s]);
-        w.len = s < p.sg.seg_begin[p.a.N] ? static_cast<int>(p.sg.seg_tokens[s + 1]) - w.tok0 : 0;
-        w.last = s + 1 == p.sg.seg_begin[w.n + 1] && w.len > 0;   // not the table's padding
+        w.len = static_cast<int>(p.sg.seg_tokens[s + 1]) - w.tok0;
+        w.last = s + 1 == p.sg.seg_begin[w.n + 1];
     } else {
         const uint32_t segs = static_cast<uint32_t>(p.sg.segs);
         const int each = static_cast<int>(p.sg.seg_tokens_each), per = static_cast<int>(p.a.tokens_per_seq);
@@ -172,11 +193,12 @@ struct Pos {
 
 // f(unit, chunk, valid tokens, place) for every chunk of this CTA, until it fails.
 template <bool kStates, class F>
-__device__ __forceinline__ void walk(const Kernel& p, F f) {
+__device__ __forceinline__ void walk(const Work& p, F f) {
     Pos<Smem<kStates>::kStages> x;
 #pragma unroll 1
-    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const Unit w = unit_at<kStates>(p, u);
+    for (uint32_t i = 0; i < p.rows(); ++i) {
+        if (p.unit(i) >= p.units) continue;
+        const Unit w = unit_at<kStates>(p, p.unit(i));
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
             if (!f(w, c, min(kC, w.len - c * kC), x)) return;
@@ -267,7 +289,7 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
 
 // --------------------------------------------------------------- load warp
 template <bool kStates>
-__device__ __forceinline__ void load_role(const Kernel& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
+__device__ __forceinline__ void load_role(const Work& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap, uint8_t* smem, const Bars& b, int lane) {
     using M = Smem<kStates>;
     constexpr int n = M::kStages, tiles = kStates ? 2 : 3;
@@ -306,7 +328,7 @@ __device__ __forceinline__ void load_role(const Kernel& p, const CUtensorMap* qm
 // system a load takes 3 us and more, so the lines are brought to L2 four
 // chunks ahead and the words one chunk ahead.
 template <bool kStates>
-__device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const Bars& b, int lane) {
+__device__ __forceinline__ void decay_role(const Work& p, uint8_t* smem, const Bars& b, int lane) {
     using M = Smem<kStates>;
     constexpr int kAhead = 4;
     float next[4] = {0.f, 0.f, 0.f, 0.f};
@@ -384,7 +406,7 @@ __device__ __forceinline__ void decay_role(const Kernel& p, uint8_t* smem, const
 // the P of the chunk before, whose product it waits for; P and Q' are formed
 // while K'^T V runs, and the next chunk's state between Q' S^T and its K'^T V.
 template <bool kStates>
-__device__ __forceinline__ void mma_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
+__device__ __forceinline__ void mma_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
@@ -475,7 +497,7 @@ __device__ __forceinline__ void st_16x8(uint32_t taddr, uint32_t a, uint32_t b, 
 }
 
 template <bool kStates>
-__device__ __forceinline__ void key_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wk, int lane) {
+__device__ __forceinline__ void key_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wk, int lane) {
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
@@ -620,7 +642,7 @@ __device__ __noinline__ void state_out(void* base, bool f32, int64_t at, uint32_
 }
 
 template <bool kStates>
-__device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int ws, int lane) {
+__device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int ws, int lane) {
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
@@ -629,15 +651,16 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
     const uint32_t scol = tmem + (static_cast<uint32_t>(32 * (ws & 3)) << 16) + kColS + 64 * half;
     uint8_t* row = smem + M::kS + half * kSlab + key * 128;
     const int64_t lane_at = 64 * half * kHeadDim + key;
-    const void* init = p.sg.starts ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
-    const bool init_f32 = p.sg.starts || p.a.state_f32;
+    const void* init = p.cut ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
+    const bool init_f32 = p.cut || p.a.state_f32;
     Pos<n> x;
 #pragma unroll 1
-    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const Unit w = unit_at<kStates>(p, u);
+    for (uint32_t row_i = 0; row_i < p.rows(); ++row_i) {
+        if (p.unit(row_i) >= p.units) continue;
+        const Unit w = unit_at<kStates>(p, p.unit(row_i));
         const int64_t at = (static_cast<int64_t>(w.n) * p.a.H + w.h) * (kHeadDim * kHeadDim) + lane_at;
         const int64_t seg_at = static_cast<int64_t>(w.slot) * (kHeadDim * kHeadDim) + lane_at;
-        const int64_t init_at = p.sg.starts ? seg_at : at;
+        const int64_t init_at = p.cut ? seg_at : at;
         const bool final = !kStates && w.last && p.a.final_state;
         if (w.nch == 0) {
             if (final)
@@ -648,7 +671,7 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
         }
         if (!kStates) {
             // (The chain over the segments may still be running.)
-            if (p.sg.starts) asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (p.cut) asm volatile("griddepcontrol.wait;" ::: "memory");
             state_in(init, init_f32, init_at, scol);
         }
         float total = 0.f;
@@ -730,7 +753,7 @@ __device__ __forceinline__ void state_role(const Kernel& p, uint8_t* smem, const
 // before the row's own take exp(G_i - G_j) as a row factor to the end of the
 // block times a column factor from there, both at most 1: one exponential
 // per row and block instead of one per score.
-__device__ __forceinline__ void score_role(const Kernel& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wp, int lane) {
+__device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wp, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wp) << 16) + kColD1;
@@ -798,7 +821,7 @@ __device__ __forceinline__ void score_role(const Kernel& p, uint8_t* smem, const
 // Warp wq: rows (tokens) 32 wq .. + 31, one per lane.  Q' in place, once D1
 // has been formed from Q.  The factor goes in as two BF16 parts of one fused
 // multiply-add: one rounding.
-__device__ __forceinline__ void query_role(const Kernel& p, uint8_t* smem, const Bars& b, int wq, int lane) {
+__device__ __forceinline__ void query_role(const Work& p, uint8_t* smem, const Bars& b, int wq, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
     const int row = 32 * wq + lane;
@@ -867,7 +890,7 @@ __device__ __noinline__ void add_not_finite(uint32_t trow, const __nv_bfloat16* 
     tc::wait_st();
 }
 
-__device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* omap, uint8_t* smem, const Bars& b,
+__device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* omap, uint8_t* smem, const Bars& b,
                                             uint32_t tmem, int we, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
@@ -925,14 +948,25 @@ __device__ __forceinline__ void output_role(const Kernel& p, const CUtensorMap* 
 
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
-    la_kernel(const __grid_constant__ Kernel p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+    la_kernel(const __grid_constant__ Kernel kernel, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
     using M = Smem<kStates>;
     extern __shared__ __align__(1024) uint8_t smem[];
     // The next kernel may be placed where this one leaves room; what it needs
     // of this one it waits for.
-    if (p.sg.starts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (p.a.valid && !*p.a.valid) return;
+    if (kernel.sg.starts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (kernel.sg.cut) asm volatile("griddepcontrol.wait;" ::: "memory");   // the cut is decided before
+    bool valid = !kernel.a.valid || *kernel.a.valid;
+    if (!kernel.a.valid && kernel.a.cu_seqlens) {
+        // A small packed batch checks its offsets here: no kernel before this one.
+        const int64_t* cu = kernel.a.cu_seqlens;
+        bool ok = threadIdx.x > 0 || (cu[0] == 0 && cu[kernel.a.N] == kernel.a.tokens);
+        for (int64_t n = threadIdx.x; n < kernel.a.N; n += kThreads) ok = ok && cu[n] <= cu[n + 1];
+        valid = __syncthreads_and(ok);
+        if (!valid && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(kernel.a.status, kDevBadSeqlens);
+    }
+    const Work p(kernel);
+    if (!valid || (kStates && !p.cut)) return;
     if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
         return;
@@ -1013,6 +1047,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc::fence_before_sync();
     __syncthreads();
+    // (This kernel's end is also the end of the ones before it.)
+    if (!kStates && kernel.sg.starts) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kMmaWarp) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
@@ -1020,104 +1056,239 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The segments' incoming states: per (sequence, head), S_0 = init and
-// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  A CTA has 128 kVec of the
-// 16384 elements and takes the segments 8 kEach at a time: each of its eight
-// warps loads up to kEach of them at once, composes them, and starts from what
-// the warps before it compose to.  (One thread per element took the segments'
-// latencies one after the other: 21 us for 128 segments of one head, where
-// this takes 6.)  Few segments (kEach 4): with the registers of kEach 16 the
+// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  kSplit warps share 128 kVec
+// of the 16384 elements and take the segments kSplit kEach at a time: each warp
+// loads up to kEach of them at once, composes them, and starts from what the
+// warps before it compose to.  Few (sequence, head) units: eight warps a part,
+// or a part's segments come one latency after the other (21 us for 128
+// segments of one head; 6 so).  Many: a warp a part, or the parts do (80 us
+// for 96 units of 5).  kEach 4 for few segments: with the registers of 16 the
 // CTAs of 6 heads would need three waves, and the output kernel, which starts
-// when the last scan CTA has, would start with the third (9.4 us for the scan).
+// when the last scan CTA has, would start with the third.
 constexpr int kScanWarps = 8;
-__host__ __device__ constexpr int scan_parts(int vec) { return kHeadDim * kHeadDim / (128 * vec); }
-template <int kEach, int kVec>
+template <int kSplit, int kEach, int kVec>
 __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_constant__ Kernel p) {
     __shared__ float4 zsum[kScanWarps][kVec][32];
     __shared__ float dsum[kScanWarps];
     constexpr int64_t kState = kHeadDim * kHeadDim;
-    constexpr int kParts = scan_parts(kVec);
+    constexpr uint32_t kParts = kHeadDim * kHeadDim / (128 * kVec), kGroups = kScanWarps / kSplit;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.a.valid && !*p.a.valid) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t unit = blockIdx.x / kParts, n = unit / p.heads, h = unit - n * p.heads;
-    const int64_t e = (blockIdx.x % kParts) * (128 * kVec) + 4 * lane;
-    const int64_t s0 = p.sg.seg_begin ? p.sg.seg_begin[n] : n * p.sg.segs;
-    const int64_t s1 = p.sg.seg_begin ? p.sg.seg_begin[n + 1] : s0 + p.sg.segs;
-    float4 s[kVec];
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-        const int64_t at = unit * kState + e + 128 * v;
-        s[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.a.init_state) {
-            if (p.a.state_f32) {
-                s[v] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.a.init_state) + at);
-            } else {
-                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.init_state) + at);
-                s[v] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
-            }
-        }
-        if (s0 == s1 && p.a.final_state && warp == 0) {   // an empty sequence
-            if (p.a.state_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + at) = s[v];
-            else
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.final_state) + at) =
-                    make_uint2(pack_bf16(s[v].x, s[v].y), pack_bf16(s[v].z, s[v].w));
-        }
-    }
+    if (p.sg.cut && !*p.sg.cut) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, place = warp % kSplit;
+    const uint32_t parts = static_cast<uint32_t>(p.a.N) * p.heads * kParts;
     auto step = [](float d, const float4& a, const float4& z) {
         return make_float4(fmaf(d, a.x, z.x), fmaf(d, a.y, z.y), fmaf(d, a.z, z.z), fmaf(d, a.w, z.w));
     };
-    for (int64_t base = s0; base < s1; base += kScanWarps * kEach) {
-        const int64_t left = s1 - base;
-        const int count = left < kScanWarps * kEach ? static_cast<int>(left) : kScanWarps * kEach;
-        const int each = (count + kScanWarps - 1) / kScanWarps;
-        const int mine = min(each, max(0, count - warp * each));   // segments of this warp
-        const int64_t first = base + warp * each;
-        float4 z[kEach][kVec];
-        float d[kEach];
+    // (kSplit 8: the whole CTA has the same part, so its barriers match.)
+    for (uint32_t part = blockIdx.x * kGroups + warp / kSplit; part < parts; part += gridDim.x * kGroups) {
+        const uint32_t unit = part / kParts, n = unit / p.heads, h = unit - n * p.heads;
+        const int64_t e = (part % kParts) * (128 * kVec) + 4 * lane;
+        const int64_t s0 = p.sg.seg_begin ? p.sg.seg_begin[n] : n * p.sg.segs;
+        const int64_t s1 = p.sg.seg_begin ? p.sg.seg_begin[n + 1] : s0 + p.sg.segs;
+        float4 s[kVec];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const bool there = i < mine && first + i + 1 < s1;     // (nothing follows the last segment)
-            d[i] = there ? p.sg.decay[(first + i) * p.a.H + h] : 0.f;
-#pragma unroll
-            for (int v = 0; v < kVec; ++v)
-                z[i][v] = there ? *reinterpret_cast<const float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float4 sum[kVec];
-        float total = 0.f;
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (i < mine) {
-                total += d[i];
-                d[i] = ex2(d[i]);
-#pragma unroll
-                for (int v = 0; v < kVec; ++v) sum[v] = step(d[i], sum[v], z[i][v]);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) zsum[warp][v][lane] = sum[v];
-        if (lane == 0) dsum[warp] = ex2(total);
-        __syncthreads();
-        float4 at[kVec];
-#pragma unroll 1
-        for (int g = 0; g < kScanWarps; ++g)
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                if (g == warp) at[v] = s[v];
-                s[v] = step(dsum[g], s[v], zsum[g][v][lane]);
-            }
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (i < mine)
-#pragma unroll
-                for (int v = 0; v < kVec; ++v) {
-                    *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v) = at[v];
-                    at[v] = step(d[i], at[v], z[i][v]);
+        for (int v = 0; v < kVec; ++v) {
+            const int64_t at = unit * kState + e + 128 * v;
+            s[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.a.init_state) {
+                if (p.a.state_f32) {
+                    s[v] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.a.init_state) + at);
+                } else {
+                    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.init_state) + at);
+                    s[v] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
                 }
+            }
+            if (s0 == s1 && p.a.final_state && place == 0) {   // an empty sequence
+                if (p.a.state_f32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + at) = s[v];
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.final_state) + at) =
+                        make_uint2(pack_bf16(s[v].x, s[v].y), pack_bf16(s[v].z, s[v].w));
+            }
+        }
+        for (int64_t base = s0; base < s1; base += kSplit * kEach) {
+            const int64_t left = s1 - base;
+            const int count = left < kSplit * kEach ? static_cast<int>(left) : kSplit * kEach;
+            const int each = (count + kSplit - 1) / kSplit;
+            const int mine = min(each, max(0, count - place * each));   // segments of this warp
+            const int64_t first = base + place * each;
+            float4 z[kEach][kVec];
+            float d[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const bool there = i < mine && first + i + 1 < s1;      // (nothing follows the last segment)
+                d[i] = there ? p.sg.decay[(first + i) * p.a.H + h] : 0.f;
+#pragma unroll
+                for (int v = 0; v < kVec; ++v)
+                    z[i][v] = there ? *reinterpret_cast<const float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float4 at[kVec];
+            if (kSplit == 1) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) d[i] = ex2(d[i]);
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) at[v] = s[v];
+            } else {
+                float4 sum[kVec];
+                float total = 0.f;
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (i < mine) {
+                        total += d[i];
+                        d[i] = ex2(d[i]);
+#pragma unroll
+                        for (int v = 0; v < kVec; ++v) sum[v] = step(d[i], sum[v], z[i][v]);
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) zsum[warp][v][lane] = sum[v];
+                if (lane == 0) dsum[warp] = ex2(total);
+                __syncthreads();
+#pragma unroll 1
+                for (int g = 0; g < kSplit; ++g)
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) {
+                        if (g == place) at[v] = s[v];
+                        s[v] = step(dsum[g], s[v], zsum[g][v][lane]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (i < mine)
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) {
+                        *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v) = at[v];
+                        at[v] = step(d[i], at[v], z[i][v]);
+                    }
+            if (kSplit == 1)
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) s[v] = at[v];
+        }
+    }
+}
+
+// A packed batch: checks the offsets' contract (kda_meta.cu) and decides, from
+// the lengths, whether and where to cut.  Without a cut the longest sequence
+// is the least it takes; a cut leaves rows of units of L chunks, each row with
+// its own start (kda_launch.h has the costs).  8 sequences of 33,333 tokens
+// in all, 12 heads, the longest 65 chunks: 180 us uncut, 183 to 266 cut;
+// 20,000 tokens, 16 heads, the longest 154 chunks: 399 uncut, 136 cut into
+// segments of 8.
+constexpr int kCutThreads = 1024;
+__constant__ const int kCutLengths[] = {4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = buf[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__global__ void __launch_bounds__(kCutThreads)
+    la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, int forced, int32_t* valid,
+                  int* status) {
+    __shared__ int64_t buf[32];
+    __shared__ int longest_of[32];
+    __shared__ int length;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int64_t bad = tid == 0 && (cu[0] != 0 || cu[N] != T), chunks = 0;
+    int longest = 0;
+    for (int64_t n = tid; n < N; n += kCutThreads) {
+        const int64_t len = cu[n + 1] - cu[n];
+        if (len < 0 || cu[n] < 0 || cu[n + 1] > T) {
+            bad = 1;
+            continue;
+        }
+        const int c = static_cast<int>((len + kC - 1) / kC);
+        chunks += c;
+        longest = max(longest, c);
+    }
+    bad = block_sum(bad, buf);
+    chunks = block_sum(chunks, buf);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) longest_of[warp] = longest;
+    __syncthreads();
+    if (tid == 0) {
+        *valid = bad ? 0 : 1;
+        if (bad) atomicOr(status, kDevBadSeqlens);
+        for (int i = 0; i < kCutThreads / 32; ++i) longest = max(longest, longest_of[i]);
+        const float all = static_cast<float>(chunks), units = static_cast<float>(H) / sms;
+        float best = kLaChunkUs * fmaxf(static_cast<float>(longest), all * units + 0.5f * longest);
+        int pick = 0;
+        for (int i = 0; i < static_cast<int>(sizeof(kCutLengths) / sizeof(int)); ++i) {
+            const float L = static_cast<float>(kCutLengths[i]);
+            if (kCutLengths[i] >= longest) break;
+            const float rows = ceilf((all / L + 0.5f * N) * units);
+            const float us = kLaCutUs + rows * (L * kLaCutChunkUs + kLaCutRowUs);
+            if (us < best) {
+                best = us;
+                pick = kCutLengths[i];
+            }
+        }
+        if (forced > 0) pick = forced;
+        length = !sg.starts || bad ? 0 : pick;
+        if (sg.starts) *sg.cut = length > 0;
+    }
+    __syncthreads();
+    const int L = length;
+    if (L == 0) {
+        // The sequences by length, longest first (ties by index).
+        if (sg.starts && sg.order && bad == 0)
+            for (int64_t n = tid; n < N; n += kCutThreads) {
+                const int64_t len = cu[n + 1] - cu[n];
+                int rank = 0;
+                for (int64_t m = 0; m < N; ++m) {
+                    const int64_t other = cu[m + 1] - cu[m];
+                    rank += other > len || (other == len && m < n);
+                }
+                sg.order[rank] = static_cast<int32_t>(n);
+            }
+        return;
+    }
+    // The segment table: each sequence's first segment, and each segment's
+    // first token and sequence.
+    int64_t carry = 0;
+    for (int64_t base = 0; base < N; base += kCutThreads) {
+        const int64_t n = base + tid;
+        const int64_t c = n < N ? (cu[n + 1] - cu[n] + kC - 1) / kC : 0, count = (c + L - 1) / L;
+        int64_t x = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) buf[warp] = x;
+        __syncthreads();
+        int64_t before = carry, all = 0;
+        for (int i = 0; i < kCutThreads / 32; ++i) {
+            if (i < warp) before += buf[i];
+            all += buf[i];
+        }
+        const int64_t first = before + x - count;
+        if (n < N) {
+            sg.seg_begin[n] = first;
+            for (int64_t j = 0; j < count; ++j) {
+                sg.seg_tokens[first + j] = cu[n] + j * L * kC;
+                sg.seg_seq[first + j] = n;
+            }
+        }
+        carry += all;
+    }
+    if (tid == 0) {
+        sg.seg_begin[N] = carry;
+        sg.seg_tokens[carry] = T;
     }
 }
 
@@ -1165,6 +1336,13 @@ cudaError_t configure() {
 
 }  // namespace
 
+cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms, const LaSegments& sg,
+                          int64_t forced, int32_t* valid, int* status, cudaStream_t stream) {
+    la_cut_kernel<<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg,
+                                                 static_cast<int>(forced < (1 << 24) ? forced : 1 << 24), valid, status);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream, int* launches) {
     Kernel p;
     p.a = a;
@@ -1195,15 +1373,19 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Smem<true>::kBytes;
-        cfg.numAttrs = 0;
+        cfg.numAttrs = sg.cut ? 1 : 0;
         if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
         // Segments of a sequence: packed, one can have all but the others'.
-        const bool few = (sg.seg_begin ? sg.total - a.N + 1 : sg.segs) <= 4 * kScanWarps;
-        cfg.gridDim = dim3(static_cast<unsigned>(a.N * a.H * scan_parts(few ? 2 : 1)));
+        const bool many = a.N * a.H >= 24, few = (sg.cut ? sg.total - a.N + 1 : sg.segs) <= 4 * kScanWarps;
+        const int64_t parts = a.N * a.H * (many || !few ? 128 : 64), ctas = many ? (parts + kScanWarps - 1) / kScanWarps : parts;
+        const int64_t most = static_cast<int64_t>(sms) * (many ? 4 : few ? 3 : 2);
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
         cfg.blockDim = dim3(32 * kScanWarps);
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, few ? la_scan_kernel<4, 2> : la_scan_kernel<16, 1>, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, many ? la_scan_kernel<1, 8, 1> : few ? la_scan_kernel<8, 4, 2> : la_scan_kernel<8, 16, 1>,
+                                    p)) != cudaSuccess)
+            return e;
         *launches += 2;
     }
     cfg.gridDim = dim3(grid);

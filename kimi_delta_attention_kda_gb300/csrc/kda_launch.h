@@ -210,6 +210,14 @@ struct LaArgs {
     int* status;
 };
 constexpr int kLaChunk = 128;   // tokens of a chunk of kda_la_prefill
+// Costs of kda_la_prefill in microseconds, measured on GB300, for the choice of
+// a cut: a chunk of an uncut chain; with a cut, a chunk's outputs and what it
+// adds, with every SM loading; a further row of units on every SM; the further
+// launches.
+constexpr float kLaChunkUs = 2.7f;
+constexpr float kLaCutChunkUs = 5.0f;
+constexpr float kLaCutRowUs = 8.0f;
+constexpr float kLaCutUs = 18.f;
 // The cut of every sequence into segments of whole chunks (starts null: none).
 struct LaSegments {
     float* starts;             // [total][H][128][128]: what a segment adds, then its incoming state
@@ -217,8 +225,20 @@ struct LaSegments {
     int64_t total;             // segments (packed: a bound)
     int64_t segs;              // fixed layout: segments of each sequence
     int64_t seg_tokens_each;   // fixed layout: tokens of each but the last
-    const int64_t *seg_begin, *seg_tokens, *seg_seq;   // packed: launch_segment_meta's table
+    // Packed: whether there is a cut, each sequence's first segment, and each
+    // segment's first token and sequence, from launch_la_cut.
+    int32_t* cut;
+    int64_t *seg_begin, *seg_tokens, *seg_seq;
+    // Packed, for an uncut batch: its sequences, longest first (or null).
+    int32_t* order;
 };
+constexpr int64_t kMaxLaOrdered = 1024;
+// Packed: the offsets' check (*valid, as launch_varlen_meta) and, with
+// sg.starts, the choice of a cut and its table; forced > 0: segments of that
+// many 128-token chunks.
+cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms,
+                          const LaSegments& sg, int64_t forced, int32_t* valid, int* status,
+                          cudaStream_t stream);
 // Adds the kernels it launches to *launches.
 cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream,
                               int* launches);

@@ -32,7 +32,7 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 struct LaPlan {
     bool packed;
     int64_t N, tokens;
-    int64_t meta_bytes;   // packed: valid flag and chunk offsets of the offsets' check
+    int64_t meta_bytes;   // packed: the verdict on the offsets, and whether there is a cut
 };
 
 int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
@@ -44,21 +44,21 @@ int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
     p->tokens = packed ? T : B * T;
     if (p->tokens >= (int64_t(1) << 31) || p->tokens > kMaxElems / (H * kHeadDim)) return KDA_ERR_SHAPE;
     if (B * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
-    p->meta_bytes = packed ? 256 + align256(8 * (B + 1)) : 0;
+    p->meta_bytes = packed ? 256 : 0;
     return KDA_OK;
 }
 
-// The cut of a call's sequences into segments (see kda_la_prefill).  Costs in
-// microseconds, measured on GB300: a chunk of a chain, of the pass that forms
-// what the segments add, and a step of the chain over the segments; the two
-// further launches.
-constexpr double kChunkUs = 1.8;
-constexpr double kAddChunkUs = 1.2;
-constexpr double kScanStepUs = 0.1;
-constexpr double kCutUs = 8.0;
+// The cut of a call's sequences into segments (see kda_la_prefill).  A packed
+// batch's lengths are on the device, and so is its choice (launch_la_cut): here
+// room is made for the shortest segments it may choose.
+constexpr int64_t kMinCutChunks = 4;    // launch_la_cut's shortest segments
+constexpr int64_t kMinPackedChunks = 16;   // fewer in all: not worth the launches
+// Fixed layout, one unit to an SM: a chunk of both passes (T=8192, H=32 in 4
+// segments of 16 chunks 105 us, H=6 in 22 of 3 37 us).
+constexpr double kLaFixedCutChunkUs = 5.5;
 
 struct LaCut {
-    int64_t chunks = 0;        // chunks of a segment (0: no cut)
+    int64_t chunks = 0;        // chunks of a segment (0: no cut; packed: of the shortest)
     int64_t segs = 0;          // fixed: segments of each sequence; packed: a bound on all
     int64_t total = 0;
     int64_t bytes = 0;         // starts, decays and the packed segment table
@@ -68,29 +68,30 @@ LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64
     LaCut c;
     if (!allowed || pl.tokens <= 0) return c;
     const int64_t units = pl.N * H;
-    // Packed lengths stay on the device: plan on their mean.
-    const double mean = static_cast<double>(pl.tokens) / static_cast<double>(pl.N) / kLaChunk;
-    const int64_t seq_chunks = pl.packed ? static_cast<int64_t>(mean) + 1 : (T + kLaChunk - 1) / kLaChunk;
-    if (forced > 0) {
-        c.chunks = (forced + kLaChunk / 16 - 1) / (kLaChunk / 16);
-    } else {
-        if (2 * units > sms) return c;
-        const int64_t want = sms / units;
-        c.chunks = (seq_chunks + want - 1) / want;
-        const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
-        const double cut = kCutUs + c.chunks * (kChunkUs + kAddChunkUs) + segs * kScanStepUs;
-        if (segs < 2 || cut >= seq_chunks * kChunkUs) return LaCut();
-    }
+    if (forced > 0) c.chunks = (forced + kLaChunk / 16 - 1) / (kLaChunk / 16);
     if (pl.packed) {
+        if (forced <= 0) {
+            if (pl.tokens < kMinPackedChunks * kLaChunk) return c;
+            c.chunks = kMinCutChunks;
+        }
         c.segs = pl.tokens / (c.chunks * kLaChunk) + pl.N;
         c.total = c.segs;
     } else {
+        const int64_t seq_chunks = (T + kLaChunk - 1) / kLaChunk;
+        if (forced <= 0) {
+            if (2 * units > sms) return c;
+            const int64_t want = sms / units;
+            c.chunks = (seq_chunks + want - 1) / want;
+            const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
+            const double cut = kLaCutUs + c.chunks * kLaFixedCutChunkUs;
+            if (segs < 2 || cut >= seq_chunks * kLaChunkUs) return LaCut();
+        }
         c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
         c.total = c.segs * pl.N;
     }
     if (units > 0x7fffffffLL / 128 || c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return LaCut();
     c.bytes = align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
-    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 3 * align256(8 * (c.segs + 1));
+    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 2 * align256(8 * (c.segs + 1)) + align256(4 * pl.N);
     return c;
 }
 
@@ -197,27 +198,23 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
     }
     if (pl.packed) {
         int32_t* valid = reinterpret_cast<int32_t*>(ws);
-        int64_t* cu_chunks = reinterpret_cast<int64_t*>(ws + 256);
-        if (launch_varlen_meta(cu_seqlens, B, T, valid, cu_chunks, nullptr, d.status, stream) != cudaSuccess)
-            rc = KDA_ERR_CUDA;
-        else
-            add_launches(1);
-        if (rc == KDA_OK && cut.chunks > 0) {
-            int64_t* begin = reinterpret_cast<int64_t*>(sg.decay) + align256(cut.total * H * 4) / 8;
-            int64_t* chunk0 = begin + align256(8 * (B + 1)) / 8;
-            int64_t* tokens = chunk0 + align256(8 * (cut.segs + 1)) / 8;
-            int64_t* seq = tokens + align256(8 * (cut.segs + 1)) / 8;
-            if (launch_segment_meta(cu_seqlens, cu_chunks, valid, B, cut.chunks * (kLaChunk / kChunk), cut.segs,
-                                    begin, chunk0, tokens, seq, d.status, stream) != cudaSuccess)
-                rc = KDA_ERR_CUDA;
-            else
-                add_launches(1);
-            sg.seg_begin = begin;
-            sg.seg_tokens = tokens;
-            sg.seg_seq = seq;
+        if (cut.chunks > 0) {
+            sg.cut = valid + 1;
+            sg.seg_begin = reinterpret_cast<int64_t*>(sg.decay) + align256(cut.total * H * 4) / 8;
+            sg.seg_tokens = sg.seg_begin + align256(8 * (B + 1)) / 8;
+            sg.seg_seq = sg.seg_tokens + align256(8 * (cut.segs + 1)) / 8;
+            if (B <= kMaxLaOrdered) sg.order = reinterpret_cast<int32_t*>(sg.seg_seq + align256(8 * (cut.segs + 1)) / 8);
         }
         a.cu_seqlens = cu_seqlens;
-        a.valid = valid;
+        if (cut.chunks == 0 && B <= kMaxLaOrdered) {
+            // The kernel checks the offsets itself.
+        } else if (launch_la_cut(cu_seqlens, B, T, H, d.sms, sg, d.seg_chunks > 0 ? cut.chunks : 0, valid, d.status, stream) !=
+            cudaSuccess)
+            rc = KDA_ERR_CUDA;
+        else {
+            add_launches(1);
+            a.valid = valid;
+        }
     }
     if (rc == KDA_OK) {
         int launches = 0;
