@@ -268,6 +268,7 @@ struct ResidualNormArgs {
     int64_t rows, dim;
     float scale, eps;
     bool weight_f32, residual_f32;
+    int* status;
 };
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, int sms, cudaStream_t stream);
 constexpr int64_t kMaxNormDim = 32768;

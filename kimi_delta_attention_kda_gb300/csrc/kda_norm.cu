@@ -15,16 +15,22 @@
 namespace kda {
 namespace {
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)): 0 and 1 at the infinities, NaN stays.  The hardware's
+// exponential and reciprocal are within 2 units of the last place each; an
+// IEEE division here made the gated norm bound by its arithmetic.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float inv_rms(float mean, float eps) { return rsqrtf(mean + eps); }
 
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+    x[0] = bf16_lo(r.x); x[1] = bf16_hi(r.x); x[2] = bf16_lo(r.y); x[3] = bf16_hi(r.y);
+    x[4] = bf16_lo(r.z); x[5] = bf16_hi(r.z); x[6] = bf16_lo(r.w); x[7] = bf16_hi(r.w);
+}
 // Eight consecutive elements as FP32.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8]);
 template <>
 __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    x[0] = bf16_lo(r.x); x[1] = bf16_hi(r.x); x[2] = bf16_lo(r.y); x[3] = bf16_hi(r.y);
-    x[4] = bf16_lo(r.z); x[5] = bf16_hi(r.z); x[6] = bf16_lo(r.w); x[7] = bf16_hi(r.w);
+    unpack8(*reinterpret_cast<const uint4*>(p), x);
 }
 template <>
 __device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
@@ -56,62 +62,60 @@ __global__ void __launch_bounds__(kGnThreads)
                       __nv_bfloat16* out, int64_t rows, float eps) {
     const int sub = threadIdx.x & 15;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (kGnPass * kRows) + (threadIdx.x >> 4);
-    float a[kRows][8], z[kRows][8], w[8];
+    uint4 xr[kRows], zr[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = row0 + i * kGnPass;
+        xr[i] = zr[i] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-            load8(x + r * kHeadDim + 8 * sub, a[i]);
-            if (kAct != KDA_ACT_NONE) load8(gate + r * kHeadDim + 8 * sub, z[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[i][j] = z[i][j] = 0.f;
+            xr[i] = *reinterpret_cast<const uint4*>(x + r * kHeadDim + 8 * sub);
+            if (kAct != KDA_ACT_NONE) zr[i] = *reinterpret_cast<const uint4*>(gate + r * kHeadDim + 8 * sub);
         }
     }
+    float w[8];
     load8(weight + 8 * sub, w);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+        float a[8], z[8];
+        unpack8(xr[i], a);
+        unpack8(zr[i], z);
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float s = 1.f;
-            if (kAct != KDA_ACT_NONE) s = sigmoid(z[i][j]);
-            if (kAct == KDA_ACT_SILU) s *= z[i][j];
-            z[i][j] = s;
-            if (kFirst) a[i][j] *= s;
-            ss = fmaf(a[i][j], a[i][j], ss);
+            if (kAct != KDA_ACT_NONE) s = sigmoid(z[j]);
+            if (kAct == KDA_ACT_SILU) s *= z[j];
+            z[j] = s;
+            if (kFirst) a[j] *= s;
+            ss = fmaf(a[j], a[j], ss);
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rms = 1.f / sqrtf(ss * (1.f / kHeadDim) + eps);
+        const float rms = inv_rms(ss * (1.f / kHeadDim), eps);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            a[i][j] *= rms * w[j];
-            if (!kFirst) a[i][j] *= z[i][j];
+            a[j] *= rms * w[j];
+            if (!kFirst) a[j] *= z[j];
         }
         const int64_t r = row0 + i * kGnPass;
-        if (r < rows) store8(out + r * kHeadDim + 8 * sub, a[i]);
+        if (r < rows) store8(out + r * kHeadDim + 8 * sub, a);
     }
 }
 
-template <typename W, int kAct, bool kFirst>
+template <typename W, int kAct, bool kFirst, int kRows>
 cudaError_t run_gated(const void* x, const void* weight, const void* gate, void* out, int64_t rows,
                       float eps, cudaStream_t stream) {
-    const auto xp = static_cast<const __nv_bfloat16*>(x);
-    const auto gp = static_cast<const __nv_bfloat16*>(gate);
-    const auto op = static_cast<__nv_bfloat16*>(out);
-    const auto wp = static_cast<const W*>(weight);
-    constexpr int kRows = 2;
     const int64_t blocks = (rows + kGnPass * kRows - 1) / (kGnPass * kRows);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    gated_norm_kernel<W, kAct, kFirst, kRows>
-        <<<static_cast<unsigned>(blocks), kGnThreads, 0, stream>>>(xp, wp, gp, op, rows, eps);
+    gated_norm_kernel<W, kAct, kFirst, kRows><<<static_cast<unsigned>(blocks), kGnThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(x), static_cast<const W*>(weight), static_cast<const __nv_bfloat16*>(gate),
+        static_cast<__nv_bfloat16*>(out), rows, eps);
     return cudaGetLastError();
 }
 
 // ---------------------------------------------------------- residual norm
-// One row per CTA of kThreads threads; a thread holds kGroups groups of kVec
-// consecutive elements (kVec 1: widths that are no multiple of 8).
+// One row per CTA of kThreads threads; a thread holds kGroups groups of eight
+// consecutive elements.
 template <int kThreads>
 __device__ __forceinline__ float block_sum(float x, float* buf) {
 #pragma unroll
@@ -126,22 +130,7 @@ __device__ __forceinline__ float block_sum(float x, float* buf) {
     return y;
 }
 
-template <typename T, int kVec>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[kVec]) {
-    if constexpr (kVec == 8)
-        load8(p, x);
-    else
-        x[0] = to_f32(*p);
-}
-template <typename T, int kVec>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[kVec]) {
-    if constexpr (kVec == 8)
-        store8(p, x);
-    else
-        from_f32(p, x[0]);
-}
-
-template <typename R, typename W, int kVec, int kGroups, int kThreads>
+template <typename R, typename W, int kGroups, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_kernel(ResidualNormArgs p) {
     __shared__ float buf[2][32];
     const int64_t D = p.dim, base = static_cast<int64_t>(blockIdx.x) * D;
@@ -150,88 +139,325 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(ResidualNormArg
     const auto post = static_cast<const W*>(p.post_weight);
     const auto gate = static_cast<const W*>(p.gate);
     const auto weight = static_cast<const W*>(p.weight);
-    float u[kGroups][kVec], r[kGroups][kVec];
+    float u[kGroups][8], r[kGroups][8];
     const float inv_d = 1.f / static_cast<float>(D);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kVec;
+        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) u[i][j] = r[i][j] = 0.f;
+        for (int j = 0; j < 8; ++j) u[i][j] = r[i][j] = 0.f;
         if (at < D) {
-            load_vec<__nv_bfloat16, kVec>(x + at, u[i]);
-            load_vec<R, kVec>(res + at, r[i]);
+            load8(x + at, u[i]);
+            load8(res + at, r[i]);
         }
     }
     if (post) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) ss = fmaf(u[i][j], u[i][j], ss);
-        const float rms = 1.f / sqrtf(block_sum<kThreads>(ss, buf[0]) * inv_d + p.eps);
+            for (int j = 0; j < 8; ++j) ss = fmaf(u[i][j], u[i][j], ss);
+        const float rms = inv_rms(block_sum<kThreads>(ss, buf[0]) * inv_d, p.eps);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kVec;
+            const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
             if (at < D) {
-                float w[kVec];
-                load_vec<W, kVec>(post + at, w);
+                float w[8];
+                load8(post + at, w);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) u[i][j] *= rms * w[j];
+                for (int j = 0; j < 8; ++j) u[i][j] *= rms * w[j];
             }
         }
     }
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kVec;
+        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
         if (at < D) {
             if (gate) {
-                float w[kVec];
-                load_vec<W, kVec>(gate + at, w);
+                float w[8];
+                load8(gate + at, w);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) u[i][j] *= w[j];
+                for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
             }
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 r[i][j] = fmaf(p.scale, u[i][j], r[i][j]);
                 ss = fmaf(r[i][j], r[i][j], ss);
             }
-            store_vec<R, kVec>(static_cast<R*>(p.residual_out) + base + at, r[i]);
+            store8(static_cast<R*>(p.residual_out) + base + at, r[i]);
         }
     }
-    const float rms = 1.f / sqrtf(block_sum<kThreads>(ss, buf[1]) * inv_d + p.eps);
+    const float rms = inv_rms(block_sum<kThreads>(ss, buf[1]) * inv_d, p.eps);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kVec;
+        const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * 8;
         if (at < D) {
-            float w[kVec];
-            load_vec<W, kVec>(weight + at, w);
+            float w[8];
+            load8(weight + at, w);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) r[i][j] *= rms * w[j];
-            store_vec<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(p.out) + base + at, r[i]);
+            for (int j = 0; j < 8; ++j) r[i][j] *= rms * w[j];
+            store8(static_cast<__nv_bfloat16*>(p.out) + base + at, r[i]);
         }
     }
 }
 
-template <typename R, typename W, int kVec, int kGroups, int kThreads>
+// Widths that are no multiple of 8: rows start at any element, so elements go
+// one at a time (kPair: two, where the width is even), and the new residual
+// waits in shared memory for its norm.
+template <typename T, bool kPair>
+__device__ __forceinline__ float2 load_some(const T* p) {
+    if constexpr (!kPair)
+        return make_float2(to_f32(*p), 0.f);
+    else if constexpr (sizeof(T) == 4)
+        return *reinterpret_cast<const float2*>(p);
+    else {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+        return make_float2(bf16_lo(v), bf16_hi(v));
+    }
+}
+template <typename T, bool kPair>
+__device__ __forceinline__ void store_some(T* p, float2 x) {
+    if constexpr (!kPair)
+        from_f32(p, x.x);
+    else if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float2*>(p) = x;
+    else
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(x.x, x.y);
+}
+template <typename R, typename W, bool kPair, int kThreads>
+__global__ void __launch_bounds__(kThreads) residual_norm_odd_kernel(ResidualNormArgs p) {
+    extern __shared__ __align__(16) float row_smem[];
+    __shared__ float buf[2][32];
+    constexpr int kStep = kPair ? 2 : 1;
+    const int D = static_cast<int>(p.dim), t0 = threadIdx.x * kStep;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * D;
+    const auto x = static_cast<const __nv_bfloat16*>(p.x) + base;
+    const auto res = static_cast<const R*>(p.residual) + base;
+    const auto post = static_cast<const W*>(p.post_weight), gate = static_cast<const W*>(p.gate);
+    const float inv_d = 1.f / static_cast<float>(D);
+    float rms = 1.f;
+    if (post) {
+        float ss = 0.f;
+        for (int at = t0; at < D; at += kThreads * kStep) {
+            const float2 v = load_some<__nv_bfloat16, kPair>(x + at);
+            ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+        }
+        rms = inv_rms(block_sum<kThreads>(ss, buf[0]) * inv_d, p.eps);
+    }
+    float ss = 0.f;
+    for (int at = t0; at < D; at += kThreads * kStep) {
+        float2 u = load_some<__nv_bfloat16, kPair>(x + at), r = load_some<R, kPair>(res + at);
+        if (post) {
+            const float2 w = load_some<W, kPair>(post + at);
+            u = make_float2(u.x * rms * w.x, u.y * rms * w.y);
+        }
+        if (gate) {
+            const float2 w = load_some<W, kPair>(gate + at);
+            u = make_float2(u.x * w.x, u.y * w.y);
+        }
+        r = make_float2(fmaf(p.scale, u.x, r.x), fmaf(p.scale, u.y, r.y));
+        ss = fmaf(r.x, r.x, ss);
+        if (kPair) ss = fmaf(r.y, r.y, ss);
+        store_some<float, kPair>(row_smem + at, r);
+        store_some<R, kPair>(static_cast<R*>(p.residual_out) + base + at, r);
+    }
+    rms = inv_rms(block_sum<kThreads>(ss, buf[1]) * inv_d, p.eps);
+    for (int at = t0; at < D; at += kThreads * kStep) {   // (a thread's own elements)
+        const float2 r = load_some<float, kPair>(row_smem + at), w = load_some<W, kPair>(static_cast<const W*>(p.weight) + at);
+        store_some<__nv_bfloat16, kPair>(static_cast<__nv_bfloat16*>(p.out) + base + at,
+                                         make_float2(r.x * rms * w.x, r.y * rms * w.y));
+    }
+}
+
+template <typename R, typename W, bool kPair, int kThreads>
+cudaError_t run_odd(const ResidualNormArgs& p, cudaStream_t stream) {
+    const int bytes = static_cast<int>(p.dim) * 4;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(residual_norm_odd_kernel<R, W, kPair, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kMaxNormDim) * 4);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    residual_norm_odd_kernel<R, W, kPair, kThreads><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Many wide rows: every SM walks over its rows, whose x and residual a bulk
+// copy brings to shared memory two or three rows ahead; a thread keeps the
+// weights of its channels in registers (post weight, gate and scale as one
+// factor: they only ever meet as a product).  Reading the weights again for
+// every row would take as much of L2's bandwidth as the rows take of HBM's.
+constexpr int kStreamStages = 3;
+constexpr int64_t kStreamMinDim = 1024, kStreamMaxDim = 16384, kStreamMinRows = 2;
+constexpr int kStreamSmem = 226 * 1024;
+template <typename R, typename W, int kGroups, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    residual_norm_stream_kernel(ResidualNormArgs p, int stages) {
+    extern __shared__ __align__(16) uint8_t stream_smem[];
+    __shared__ uint64_t full[kStreamStages];
+    __shared__ float red[2][2][32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int D = static_cast<int>(p.dim);
+    const uint32_t xb = D * 2, rb = D * static_cast<uint32_t>(sizeof(R)), stage_bytes = xb + rb;
+    const auto x = static_cast<const uint8_t*>(p.x), res = static_cast<const uint8_t*>(p.residual);
+    auto fetch = [&](int64_t row, int s) {
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_g2s(stream_smem + s * stage_bytes, x + row * xb, xb, &full[s]);
+        bulk_g2s(stream_smem + s * stage_bytes + xb, res + row * rb, rb, &full[s]);
+    };
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+        for (int s = 0; s < stages; ++s) {
+            const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+            if (row < p.rows) fetch(row, s);
+        }
+    }
+    float fac[kGroups][8], wt[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int at = (i * kThreads + tid) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            fac[i][j] = p.scale;
+            wt[i][j] = 0.f;
+        }
+        if (at < D) {
+            float v[8];
+            load8(static_cast<const W*>(p.weight) + at, wt[i]);
+            if (p.post_weight) {
+                load8(static_cast<const W*>(p.post_weight) + at, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) fac[i][j] *= v[j];
+            }
+            if (p.gate) {
+                load8(static_cast<const W*>(p.gate) + at, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) fac[i][j] *= v[j];
+            }
+        }
+    }
+    const float inv_d = 1.f / static_cast<float>(D);
+    __syncthreads();
+    auto sum_all = [&](float v, float* buf) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) buf[warp] = v;
+        __syncthreads();
+        float y = lane < kThreads / 32 ? buf[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        return y;
+    };
+    int s = 0;
+    uint32_t phase = 0;
+    int odd = 0;   // the sums' buffers alternate from row to row
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        if (!mbar_wait_bounded(&full[s], phase, p.status)) return;
+        const auto xs = reinterpret_cast<const __nv_bfloat16*>(stream_smem + s * stage_bytes);
+        const auto rs = reinterpret_cast<const R*>(stream_smem + s * stage_bytes + xb);
+        float rms = 1.f;
+        if (p.post_weight) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int at = (i * kThreads + tid) * 8;
+                if (at < D) {
+                    float v[8];
+                    load8(xs + at, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+                }
+            }
+            rms = inv_rms(sum_all(ss, red[odd][0]) * inv_d, p.eps);
+        }
+        float r[kGroups][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int at = (i * kThreads + tid) * 8;
+            if (at < D) {
+                float v[8];
+                load8(xs + at, v);
+                load8(rs + at, r[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    r[i][j] = fmaf(v[j] * rms, fac[i][j], r[i][j]);
+                    ss = fmaf(r[i][j], r[i][j], ss);
+                }
+                store8(static_cast<R*>(p.residual_out) + row * D + at, r[i]);
+            }
+        }
+        fence_proxy_async_smem();   // this stage is read; a copy may follow the barrier
+        rms = inv_rms(sum_all(ss, red[odd][1]) * inv_d, p.eps);
+        const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
+        if (tid == 0 && next < p.rows) fetch(next, s);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int at = (i * kThreads + tid) * 8;
+            if (at < D) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[i][j] *= rms * wt[i][j];
+                store8(static_cast<__nv_bfloat16*>(p.out) + row * D + at, r[i]);
+            }
+        }
+        odd ^= 1;
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+template <typename R, typename W, int kGroups, int kThreads>
+cudaError_t run_stream(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
+    const int row = static_cast<int>(p.dim) * (2 + static_cast<int>(sizeof(R))), room = kStreamSmem / (1024 / kThreads);
+    const int stages = row * kStreamStages <= room ? kStreamStages : room / row;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(residual_norm_stream_kernel<R, W, kGroups, kThreads>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    const int64_t ctas = static_cast<int64_t>(sms) * (1024 / kThreads);
+    residual_norm_stream_kernel<R, W, kGroups, kThreads>
+        <<<static_cast<unsigned>(p.rows < ctas ? p.rows : ctas), kThreads, stages * row, stream>>>(p, stages);
+    return cudaGetLastError();
+}
+
+template <typename R, typename W, int kGroups, int kThreads>
 cudaError_t run_residual(const ResidualNormArgs& p, cudaStream_t stream) {
-    residual_norm_kernel<R, W, kVec, kGroups, kThreads>
+    residual_norm_kernel<R, W, kGroups, kThreads>
         <<<static_cast<unsigned>(p.rows), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename R, typename W>
-cudaError_t pick_residual(const ResidualNormArgs& p, cudaStream_t stream) {
+cudaError_t pick_residual(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
     const int64_t D = p.dim;
-    if (D % 8 == 0) {
-        if (D <= 1024) return run_residual<R, W, 8, 1, 128>(p, stream);
-        if (D <= 4096) return run_residual<R, W, 8, 2, 256>(p, stream);
-        if (D <= 12288) return run_residual<R, W, 8, 3, 512>(p, stream);
-        return run_residual<R, W, 8, 4, 1024>(p, stream);
+    if (D % 8 == 0 && D > kStreamMinDim && D <= kStreamMaxDim && p.rows >= kStreamMinRows * sms) {
+        if (D <= 2048) return run_stream<R, W, 1, 256>(p, sms, stream);
+        if (D <= 4096) return run_stream<R, W, 1, 512>(p, sms, stream);
+        if (D <= 8192) return run_stream<R, W, 1, 1024>(p, sms, stream);
+        if (D <= 12288) return run_stream<R, W, 2, 768>(p, sms, stream);
+        return run_stream<R, W, 2, 1024>(p, sms, stream);
     }
-    if (D <= 512) return run_residual<R, W, 1, 4, 128>(p, stream);
-    if (D <= 4096) return run_residual<R, W, 1, 8, 512>(p, stream);
-    return run_residual<R, W, 1, 32, 1024>(p, stream);
+    if (D % 8 == 0) {
+        if (D <= 1024) return run_residual<R, W, 1, 128>(p, stream);
+        if (D <= 4096) return run_residual<R, W, 2, 256>(p, stream);
+        if (D <= 12288) return run_residual<R, W, 3, 512>(p, stream);
+        return run_residual<R, W, 4, 1024>(p, stream);
+    }
+    if (D % 2 == 0) return D <= 2048 ? run_odd<R, W, true, 128>(p, stream) : run_odd<R, W, true, 512>(p, stream);
+    return D <= 1024 ? run_odd<R, W, false, 128>(p, stream) : run_odd<R, W, false, 512>(p, stream);
 }
 
 }  // namespace
@@ -240,9 +466,10 @@ cudaError_t launch_gated_norm(const void* x, const void* weight, const void* gat
                               int64_t rows, int activation, bool gate_first, bool weight_f32,
                               float eps, cudaStream_t stream) {
     if (rows <= 0) return cudaSuccess;
-#define KDA_GN(ACT, FIRST)                                                                     \
-    return weight_f32 ? run_gated<float, ACT, FIRST>(x, weight, gate, out, rows, eps, stream)  \
-                      : run_gated<__nv_bfloat16, ACT, FIRST>(x, weight, gate, out, rows, eps, stream)
+    constexpr int kRows = 4;
+#define KDA_GN(ACT, FIRST)                                                                            \
+    return weight_f32 ? run_gated<float, ACT, FIRST, kRows>(x, weight, gate, out, rows, eps, stream)  \
+                      : run_gated<__nv_bfloat16, ACT, FIRST, kRows>(x, weight, gate, out, rows, eps, stream)
     if (activation == KDA_ACT_SIGMOID) {
         if (gate_first) KDA_GN(KDA_ACT_SIGMOID, true);
         KDA_GN(KDA_ACT_SIGMOID, false);
@@ -256,14 +483,13 @@ cudaError_t launch_gated_norm(const void* x, const void* weight, const void* gat
 }
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
-    (void)sms;
     if (p.rows <= 0) return cudaSuccess;
     if (p.rows > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.residual_f32)
-        return p.weight_f32 ? pick_residual<float, float>(p, stream)
-                            : pick_residual<float, __nv_bfloat16>(p, stream);
-    return p.weight_f32 ? pick_residual<__nv_bfloat16, float>(p, stream)
-                        : pick_residual<__nv_bfloat16, __nv_bfloat16>(p, stream);
+        return p.weight_f32 ? pick_residual<float, float>(p, sms, stream)
+                            : pick_residual<float, __nv_bfloat16>(p, sms, stream);
+    return p.weight_f32 ? pick_residual<__nv_bfloat16, float>(p, sms, stream)
+                        : pick_residual<__nv_bfloat16, __nv_bfloat16>(p, sms, stream);
 }
 
 }  // namespace kda

@@ -319,7 +319,7 @@ extern "C" int kda_residual_norm(const void* x, const void* residual, const void
     if (!(eps >= 0.f)) return KDA_ERR_ARG;
     if (rows < 0 || rows > 0x7fffffffLL || dim < 1 || dim > kMaxNormDim) return KDA_ERR_SHAPE;
     ResidualNormArgs a = {x, residual, weight, post_weight, gate, out, residual_out, rows, dim, scale, eps,
-                          (flags & KDA_FLAG_WEIGHT_F32) != 0, (flags & KDA_FLAG_RESIDUAL_F32) != 0};
+                          (flags & KDA_FLAG_WEIGHT_F32) != 0, (flags & KDA_FLAG_RESIDUAL_F32) != 0, nullptr};
     if (rows > 0) {
         if (!x || !residual || !weight || !out || !residual_out) return KDA_ERR_NULL;
         for (const void* p : {x, residual, weight, post_weight, gate, static_cast<const void*>(out),
@@ -335,6 +335,7 @@ extern "C" int kda_residual_norm(const void* x, const void* residual, const void
     DeviceView d;
     int rc = device_view(&d);
     if (rc != KDA_OK || rows == 0) return rc;
+    a.status = d.status;
     if (launch_residual_norm(a, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return KDA_ERR_CUDA;
