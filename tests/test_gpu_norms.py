@@ -125,6 +125,22 @@ def test_residual_rows(kda, rows):
     check_residual(kda, r(rows, 136).bfloat16(), r(rows, 136), r(136), r(136), None, 0.5)
 
 
+@pytest.mark.parametrize("rows,dim", [(304, 1032), (700, 2048), (333, 2056), (500, 4096), (310, 4104), (460, 8192),
+                                      (305, 12288), (304, 12296), (310, 16384), (400, 4100), (400, 2047)])
+@pytest.mark.parametrize("rt", TYPES)
+@pytest.mark.parametrize("wt", TYPES)
+def test_residual_many_rows(kda, rows, dim, rt, wt):
+    """Enough rows for every SM to walk over several."""
+    r = gen(rows + dim)
+    x, res, w, post, gate = r(rows, dim).bfloat16(), r(rows, dim).to(rt), r(dim).to(wt), r(dim).to(wt), r(dim).to(wt)
+    check_residual(kda, x, res, w, post, gate, 0.7)
+    check_residual(kda, x, res, w)
+    dev = [t.cuda() for t in (x, res, w)]
+    want = kda.residual_norm(*dev)
+    got = kda.residual_norm(*dev, out=dev[0], residual_out=dev[1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_residual_zero_rows_and_eps(kda):
     x, r, w = torch.zeros(3, 256).bfloat16(), torch.zeros(3, 256), torch.ones(256)
     out, res = check_residual(kda, x, r, w, w, w)
