@@ -12,23 +12,24 @@
 // to FP32 even where G and G_j are large.
 //
 // As products of 128 x 128 tiles (i, j tokens; c value, d key channels):
-//     D1[i][j] = Q K^T              Q, K from shared memory
-//     P[i][j]  = scale exp(G_i - G_j) D1, causal, BF16, in tensor memory
-//     O[i][c]  = Q' S^T + P V       Q' = scale exp(G_i) Q (BF16), S^T BF16 in shared memory
-//     S^T[d][c] <- exp(G) S^T + K'^T V   K'^T[d][j] = exp(G - G_j) k_jd, in tensor memory
+//     D1[i][j]  = Q K^T
+//     P[i][j]   = 2^n_i exp(-G_j) D1, causal, BF16, in tensor memory
+//     O[i][c]   = scale f_i (Q' S^T + P V)   Q' = 2^n_i Q, S^T BF16 in shared memory
+//     S^T[d][c] <- exp(G) S^T + K'^T V       K'^T[d][j] = exp(G - G_j) k_jd, in tensor memory
+// with exp(G_i) = 2^n_i f_i and 1 <= f_i < 2: Q' has the bits of Q.
 // S^T is FP32 in tensor memory: the state warps read it, write its BF16 copy
 // to shared memory and exp(G) S^T back, and K'^T V accumulates on that.
 // K' is split by truncation into three BF16 parts whose sum is the FP32
 // value, so the state is accurate to FP32: with two parts (16 bits) the final
 // state was off by 2e-6 of its norm, against 1e-7 for FP32 arithmetic.
-// P, Q' and the S operand are rounded to BF16 once each: their error stays in
-// the BF16 output they go to, and S itself is not touched by it.
+// P and the S operand are rounded to BF16 once each: their error stays in the
+// BF16 output they go to, and S itself is not touched by it.
 //
 // One CTA per SM walks (sequence or segment, head) units.  Warps: 8 key (K'),
 // 8 state (S), 4 score (P), 4 query (Q'), 4 output (O), one each for the
-// loads, the MMA issue and the decay sums.  Tensor memory columns: D1 and P [0, 128),
-// O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32 tokens x 3
-// parts).
+// loads, the MMA issue and the decay sums.  Tensor memory columns: D1 and P
+// [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32
+// tokens x 3 parts).
 //
 // A value that is not finite must not reach earlier tokens of its chunk: a
 // zero of P times an infinite V is NaN.  S^T shows it (its whole column is
@@ -114,20 +115,21 @@ struct Kernel {
 struct Work {
     const LaArgs& a;
     const LaSegments& sg;
-    uint32_t units, heads;
+    const uint32_t& heads;
+    uint32_t units;
     bool cut;           // the units are (segment, head), else (sequence, head)
-    const int32_t* order;   // packed, no cut: the sequences, longest first
-    __device__ __forceinline__ explicit Work(const Kernel& p) : a(p.a), sg(p.sg), units(p.units), heads(p.heads), cut(p.sg.starts), order(nullptr) {
+    __device__ __forceinline__ explicit Work(const Kernel& p) : a(p.a), sg(p.sg), heads(p.heads), units(p.units), cut(p.sg.starts) {
         if (sg.cut) {
             cut = *sg.cut != 0;
             units = static_cast<uint32_t>(cut ? sg.seg_begin[a.N] : a.N) * heads;
-            if (!cut) order = sg.order;
         }
     }
+    // Of an uncut packed batch: its sequences, longest first (or null).
+    __device__ __forceinline__ const int32_t* order() const { return cut ? nullptr : sg.order; }
     // The CTA's i-th unit: in rows of the grid's width, where the units come
     // longest first every other row backwards.
     __device__ __forceinline__ uint32_t unit(uint32_t i) const {
-        return i * gridDim.x + (order && (i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        return i * gridDim.x + ((i & 1) && order() ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     }
     __device__ __forceinline__ uint32_t rows() const { return (units + gridDim.x - 1) / gridDim.x; }
 };
@@ -147,7 +149,7 @@ __device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
     w.slot = u;
     w.last = true;
     if (!p.cut) {
-        w.n = p.order ? p.order[s] : s;
+        w.n = p.order() ? p.order()[s] : s;
         if (p.a.cu_seqlens) {
             w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
             w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
@@ -750,20 +752,19 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
 
 // ------------------------------------------------------------- score warps
 // Warp wp: rows (tokens) 32 wp .. + 31, one per lane.  Blocks of 32 columns
-// before the row's own take exp(G_i - G_j) as a row factor to the end of the
+// before the row's own take 2^n_i exp(-G_j) as a row factor to the end of the
 // block times a column factor from there, both at most 1: one exponential
 // per row and block instead of one per score.
 __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wp, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wp) << 16) + kColD1;
-    const float scale = p.a.scale;
     walk<false>(p, [&](const Unit&, int, int, const Pos<2>& at) {
         const uint32_t buf = at.it & 1u;
         const float* G = reinterpret_cast<const float*>(smem + M::kG) + buf * kC;
         const float4* Cf = reinterpret_cast<const float4*>(smem + M::kCf + buf * 96 * 4);
         if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
-        const float gi = G[32 * wp + lane];
+        const float gi = floorf(G[32 * wp + lane]);   // n_i
         if (!wait_phase(b.qk, at.ph(), status)) return false;
         tc::fence_after_sync();
         // A block's columns of P, 16 blk .. + 15, held scores of blocks read
@@ -772,7 +773,7 @@ __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const B
 #pragma unroll 1
         for (int blk = 0; blk < wp; ++blk) {
             tc::ld_x32(trow + 32 * blk, x);
-            const float f = scale * ex2(gi - G[32 * blk + 31]);
+            const float f = ex2(gi - G[32 * blk + 31]);
             tc::wait_ld();
             uint32_t pk[16];
 #pragma unroll
@@ -800,7 +801,7 @@ __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const B
             float y[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                y[r] = 4 * j + r > lane ? 0.f : __uint_as_float(x[4 * j + r]) * (scale * ex2(gi - gj[r]));
+                y[r] = 4 * j + r > lane ? 0.f : __uint_as_float(x[4 * j + r]) * ex2(gi - gj[r]);
             pk[2 * j] = pack_bf16(y[0], y[1]);
             pk[2 * j + 1] = pack_bf16(y[2], y[3]);
         }
@@ -819,8 +820,7 @@ __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const B
 
 // ------------------------------------------------------------- query warps
 // Warp wq: rows (tokens) 32 wq .. + 31, one per lane.  Q' in place, once D1
-// has been formed from Q.  The factor goes in as two BF16 parts of one fused
-// multiply-add: one rounding.
+// has been formed from Q.
 __device__ __forceinline__ void query_role(const Work& p, uint8_t* smem, const Bars& b, int wq, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
@@ -829,11 +829,9 @@ __device__ __forceinline__ void query_role(const Work& p, uint8_t* smem, const B
         const uint32_t buf = at.it & 1u;
         uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
         if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
-        const float e = p.a.scale * ex2(reinterpret_cast<const float*>(smem + M::kG)[buf * kC + row]);
+        const float e = ex2(floorf(reinterpret_cast<const float*>(smem + M::kG)[buf * kC + row]));   // 2^n_i
         arrive_warp(&b.dec_empty[buf], lane);
-        const __nv_bfloat16 eh = __float2bfloat16_rn(e);
-        const __nv_bfloat162 e1 = __bfloat162bfloat162(eh);
-        const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e - __bfloat162float(eh)));
+        const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e));
         if (!wait_phase(&b.full_q[at.s], at.st, status) || !wait_phase(b.qk, at.ph(), status)) return false;
 #pragma unroll 1
         for (int sl = 0; sl < 2; ++sl, Qrow += kSlab) {
@@ -844,7 +842,7 @@ __device__ __forceinline__ void query_role(const Work& p, uint8_t* smem, const B
             for (int x = 0; x < 8; ++x) {
                 __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v[x]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = __hfma2(h[j], e1, __hmul2(h[j], e2));
+                for (int j = 0; j < 4; ++j) h[j] = __hmul2(h[j], e2);
                 *reinterpret_cast<uint4*>(Qrow + ((x ^ (row & 7)) << 4)) = v[x];
             }
         }
@@ -900,20 +898,29 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
     arrive_warp(b.qs_ready, lane);   // O is free for the first chunk
     walk<false>(p, [&](const Unit& w, int c, int valid, const Pos<2>& at) {
         uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
-        const int64_t ostride = p.a.H * kHeadDim, o0 = (w.tok0 + c * kC) * ostride + w.h * kHeadDim;
+        // The chunk's first token of this head, in V and the output.
+        auto first = [&]() { return (w.tok0 + c * kC) * p.a.H * kHeadDim + w.h * kHeadDim; };
+        const uint32_t buf = at.it & 1u;
+        if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
+        const float gi = reinterpret_cast<const float*>(smem + M::kG)[buf * kC + row];
+        arrive_warp(&b.dec_empty[buf], lane);
+        const float f = p.a.scale * ex2(gi - floorf(gi));
         if (!wait_phase(b.o_done, at.ph(), status)) return false;
         tc::fence_after_sync();
         if (flag[at.it & 1u] == at.it + 1)
-            add_not_finite(trow, static_cast<const __nv_bfloat16*>(p.a.v) + o0, ostride, row, valid);
+            add_not_finite(trow, static_cast<const __nv_bfloat16*>(p.a.v) + first(), p.a.H * kHeadDim, row, valid);
         stage_release(&b.empty_v[at.s], lane);
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + o0 + row * ostride;
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
             uint32_t x[32];
             tc::ld_x32(trow + kColO + 32 * blk, x);
             tc::wait_ld();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = pack_bf16(__uint_as_float(x[2 * r]), __uint_as_float(x[2 * r + 1]));
+            for (int r = 0; r < 16; ++r) {
+                float y0 = __uint_as_float(x[2 * r]), y1 = __uint_as_float(x[2 * r + 1]);
+                mul2(y0, y1, f);
+                x[r] = pack_bf16(y0, y1);
+            }
             if (valid == kC) {   // through Q's stage, which every product has read
                 uint8_t* slab = Qrow + (blk >> 1) * kSlab;
 #pragma unroll
@@ -921,9 +928,9 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
                     *reinterpret_cast<uint4*>(slab + (((4 * (blk & 1) + ch) ^ (row & 7)) << 4)) =
                         make_uint4(x[4 * ch], x[4 * ch + 1], x[4 * ch + 2], x[4 * ch + 3]);
             } else if (row < valid) {
+                uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + first() + row * p.a.H * kHeadDim) + 4 * blk;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    reinterpret_cast<uint4*>(out)[4 * blk + ch] = make_uint4(x[4 * ch], x[4 * ch + 1], x[4 * ch + 2], x[4 * ch + 3]);
+                for (int ch = 0; ch < 4; ++ch) out[ch] = make_uint4(x[4 * ch], x[4 * ch + 1], x[4 * ch + 2], x[4 * ch + 3]);
             }
         }
         tc::fence_before_sync();
@@ -1005,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.kp_full[s], kKeyWarps);
             mbar_init(&b.kp_empty[s], 1);
             mbar_init(&b.dec_full[s], 1);
-            mbar_init(&b.dec_empty[s], kKeyWarps + kStateWarps + (kStates ? 0 : 8));
+            mbar_init(&b.dec_empty[s], kKeyWarps + kStateWarps + (kStates ? 0 : 12));
         }
         mbar_init(b.qk, 1);
         mbar_init(b.z_done, 1);
