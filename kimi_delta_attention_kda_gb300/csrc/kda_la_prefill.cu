@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The next kernel may be placed where this one leaves room; what it needs
     // of this one it waits for.
     if (kernel.sg.starts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (kernel.sg.cut) asm volatile("griddepcontrol.wait;" ::: "memory");   // the cut is decided before
+    if (kernel.a.valid) asm volatile("griddepcontrol.wait;" ::: "memory");   // the cut is decided before
     bool valid = !kernel.a.valid || *kernel.a.valid;
     if (!kernel.a.valid && kernel.a.cu_seqlens) {
         // A small packed batch checks its offsets here: no kernel before this one.
@@ -1202,7 +1202,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* buf) {
 }
 
 __global__ void __launch_bounds__(kCutThreads)
-    la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, int forced, int32_t* valid,
+    la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, bool forced, int32_t* valid,
                   int* status) {
     __shared__ int64_t buf[32];
     __shared__ int longest_of[32];
@@ -1230,11 +1230,13 @@ __global__ void __launch_bounds__(kCutThreads)
         *valid = bad ? 0 : 1;
         if (bad) atomicOr(status, kDevBadSeqlens);
         for (int i = 0; i < kCutThreads / 32; ++i) longest = max(longest, longest_of[i]);
+        const int shortest = static_cast<int>(sg.seg_tokens_each / kC);
         const float all = static_cast<float>(chunks), units = static_cast<float>(H) / sms;
         float best = kLaChunkUs * fmaxf(static_cast<float>(longest), all * units + 0.5f * longest);
         int pick = 0;
         for (int i = 0; i < static_cast<int>(sizeof(kCutLengths) / sizeof(int)); ++i) {
             const float L = static_cast<float>(kCutLengths[i]);
+            if (kCutLengths[i] < shortest) continue;
             if (kCutLengths[i] >= longest) break;
             const float rows = ceilf((all / L + 0.5f * N) * units);
             const float us = kLaCutUs + rows * (L * kLaCutChunkUs + kLaCutRowUs);
@@ -1243,7 +1245,7 @@ __global__ void __launch_bounds__(kCutThreads)
                 pick = kCutLengths[i];
             }
         }
-        if (forced > 0) pick = forced;
+        if (forced) pick = shortest;
         length = !sg.starts || bad ? 0 : pick;
         if (sg.starts) *sg.cut = length > 0;
     }
@@ -1251,7 +1253,7 @@ __global__ void __launch_bounds__(kCutThreads)
     const int L = length;
     if (L == 0) {
         // The sequences by length, longest first (ties by index).
-        if (sg.starts && sg.order && bad == 0)
+        if (sg.order && bad == 0)
             for (int64_t n = tid; n < N; n += kCutThreads) {
                 const int64_t len = cu[n + 1] - cu[n];
                 int rank = 0;
@@ -1344,9 +1346,8 @@ cudaError_t configure() {
 }  // namespace
 
 cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms, const LaSegments& sg,
-                          int64_t forced, int32_t* valid, int* status, cudaStream_t stream) {
-    la_cut_kernel<<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg,
-                                                 static_cast<int>(forced < (1 << 24) ? forced : 1 << 24), valid, status);
+                          bool forced, int32_t* valid, int* status, cudaStream_t stream) {
+    la_cut_kernel<<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg, forced, valid, status);
     return cudaGetLastError();
 }
 
@@ -1380,7 +1381,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Smem<true>::kBytes;
-        cfg.numAttrs = sg.cut ? 1 : 0;
+        cfg.numAttrs = a.valid ? 1 : 0;
         if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
         // Segments of a sequence: packed, one can have all but the others'.
         const bool many = a.N * a.H >= 24, few = (sg.cut ? sg.total - a.N + 1 : sg.segs) <= 4 * kScanWarps;
@@ -1398,7 +1399,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Smem<false>::kBytes;
-    cfg.numAttrs = sg.starts ? 1 : 0;
+    cfg.numAttrs = sg.starts || a.valid ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, la_kernel<false>, p, qm, km, vm, om)) != cudaSuccess) return e;
     *launches += 1;
     return cudaSuccess;

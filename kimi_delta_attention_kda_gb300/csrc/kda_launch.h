@@ -224,7 +224,7 @@ struct LaSegments {
     float* decay;              // [total][H]: its decay in base 2
     int64_t total;             // segments (packed: a bound)
     int64_t segs;              // fixed layout: segments of each sequence
-    int64_t seg_tokens_each;   // fixed layout: tokens of each but the last
+    int64_t seg_tokens_each;   // tokens of each but a sequence's last (packed: of the shortest choice)
     // Packed: whether there is a cut, each sequence's first segment, and each
     // segment's first token and sequence, from launch_la_cut.
     int32_t* cut;
@@ -234,10 +234,10 @@ struct LaSegments {
 };
 constexpr int64_t kMaxLaOrdered = 1024;
 // Packed: the offsets' check (*valid, as launch_varlen_meta) and, with
-// sg.starts, the choice of a cut and its table; forced > 0: segments of that
-// many 128-token chunks.
+// sg.starts, the choice of a cut and its table (forced: segments of
+// sg.seg_tokens_each tokens); without a cut, sg.order if it is there.
 cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms,
-                          const LaSegments& sg, int64_t forced, int32_t* valid, int* status,
+                          const LaSegments& sg, bool forced, int32_t* valid, int* status,
                           cudaStream_t stream);
 // Adds the kernels it launches to *launches.
 cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream,

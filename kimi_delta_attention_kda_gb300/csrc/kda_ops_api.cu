@@ -50,8 +50,10 @@ int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
 
 // The cut of a call's sequences into segments (see kda_la_prefill).  A packed
 // batch's lengths are on the device, and so is its choice (launch_la_cut): here
-// room is made for the shortest segments it may choose.
-constexpr int64_t kMinCutChunks = 4;    // launch_la_cut's shortest segments
+// room is made for the shortest segments it may choose.  Those are longer where
+// 4 chunks would leave more than 16 rows of units: finer ones balance nothing
+// more, and each segment's state takes 64 KB per head.
+constexpr int64_t kMinCutChunks = 4, kMaxCutChunks = 64, kMaxCutRows = 16;
 constexpr int64_t kMinPackedChunks = 16;   // fewer in all: not worth the launches
 // Fixed layout, one unit to an SM: a chunk of both passes (T=8192, H=32 in 4
 // segments of 16 chunks 105 us, H=6 in 22 of 3 37 us).
@@ -61,37 +63,50 @@ struct LaCut {
     int64_t chunks = 0;        // chunks of a segment (0: no cut; packed: of the shortest)
     int64_t segs = 0;          // fixed: segments of each sequence; packed: a bound on all
     int64_t total = 0;
-    int64_t bytes = 0;         // starts, decays and the packed segment table
+    bool order = false;        // packed: an uncut batch's sequences go longest first
+    int64_t bytes = 0;         // starts, decays, the packed segment table and the order
 };
 
 LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64_t forced) {
-    LaCut c;
-    if (!allowed || pl.tokens <= 0) return c;
+    LaCut c, none;
+    if (pl.tokens <= 0) return c;
     const int64_t units = pl.N * H;
-    if (forced > 0) c.chunks = (forced + kLaChunk / 16 - 1) / (kLaChunk / 16);
+    if (pl.packed && pl.N > 1 && pl.N <= kMaxLaOrdered && units > sms && pl.tokens >= kMinPackedChunks * kLaChunk) {
+        c.order = none.order = true;
+        c.bytes = none.bytes = align256(4 * pl.N);
+    }
+    if (!allowed) return none;
+    if (forced > 0) {
+        c.chunks = (forced + kLaChunk / 16 - 1) / (kLaChunk / 16);
+        if (c.chunks > (1 << 23)) c.chunks = 1 << 23;   // 2^30 tokens
+    }
     if (pl.packed) {
         if (forced <= 0) {
-            if (pl.tokens < kMinPackedChunks * kLaChunk) return c;
+            // (A cut costs every SM its part of the chunks; without one, one
+            // sequence is the most that a batch can wait for.)
+            const double part = static_cast<double>(H) / sms, uncut = part + 0.5 > 1. ? part + 0.5 : 1.;
+            if (pl.tokens < kMinPackedChunks * kLaChunk || kLaCutChunkUs * part >= kLaChunkUs * uncut) return none;
             c.chunks = kMinCutChunks;
+            while (c.chunks < kMaxCutChunks && pl.tokens / (c.chunks * kLaChunk) * H > kMaxCutRows * sms) c.chunks *= 2;
         }
         c.segs = pl.tokens / (c.chunks * kLaChunk) + pl.N;
         c.total = c.segs;
     } else {
         const int64_t seq_chunks = (T + kLaChunk - 1) / kLaChunk;
         if (forced <= 0) {
-            if (2 * units > sms) return c;
+            if (2 * units > sms) return none;
             const int64_t want = sms / units;
             c.chunks = (seq_chunks + want - 1) / want;
             const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
             const double cut = kLaCutUs + c.chunks * kLaFixedCutChunkUs;
-            if (segs < 2 || cut >= seq_chunks * kLaChunkUs) return LaCut();
+            if (segs < 2 || cut >= seq_chunks * kLaChunkUs) return none;
         }
         c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
         c.total = c.segs * pl.N;
     }
-    if (units > 0x7fffffffLL / 128 || c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return LaCut();
-    c.bytes = align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
-    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 2 * align256(8 * (c.segs + 1)) + align256(4 * pl.N);
+    if (units > 0x7fffffffLL / 128 || c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return none;
+    c.bytes += align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
+    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 2 * align256(8 * (c.segs + 1));
     return c;
 }
 
@@ -189,9 +204,15 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
         return KDA_ERR_CUDA;
     }
     LaSegments sg = {};
+    uint8_t* at = ws + pl.meta_bytes;
+    auto take = [&at](int64_t bytes) {
+        uint8_t* p = at;
+        at += align256(bytes);
+        return p;
+    };
     if (cut.chunks > 0) {
-        sg.starts = reinterpret_cast<float*>(ws + pl.meta_bytes);
-        sg.decay = sg.starts + align256(cut.total * H * kStateElems * 4) / 4;
+        sg.starts = reinterpret_cast<float*>(take(cut.total * H * kStateElems * 4));
+        sg.decay = reinterpret_cast<float*>(take(cut.total * H * 4));
         sg.total = cut.total;
         sg.segs = cut.segs;
         sg.seg_tokens_each = cut.chunks * kLaChunk;
@@ -200,20 +221,20 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
         int32_t* valid = reinterpret_cast<int32_t*>(ws);
         if (cut.chunks > 0) {
             sg.cut = valid + 1;
-            sg.seg_begin = reinterpret_cast<int64_t*>(sg.decay) + align256(cut.total * H * 4) / 8;
-            sg.seg_tokens = sg.seg_begin + align256(8 * (B + 1)) / 8;
-            sg.seg_seq = sg.seg_tokens + align256(8 * (cut.segs + 1)) / 8;
-            if (B <= kMaxLaOrdered) sg.order = reinterpret_cast<int32_t*>(sg.seg_seq + align256(8 * (cut.segs + 1)) / 8);
+            sg.seg_begin = reinterpret_cast<int64_t*>(take(8 * (B + 1)));
+            sg.seg_tokens = reinterpret_cast<int64_t*>(take(8 * (cut.segs + 1)));
+            sg.seg_seq = reinterpret_cast<int64_t*>(take(8 * (cut.segs + 1)));
         }
+        if (cut.order) sg.order = reinterpret_cast<int32_t*>(take(4 * B));
         a.cu_seqlens = cu_seqlens;
-        if (cut.chunks == 0 && B <= kMaxLaOrdered) {
-            // The kernel checks the offsets itself.
-        } else if (launch_la_cut(cu_seqlens, B, T, H, d.sms, sg, d.seg_chunks > 0 ? cut.chunks : 0, valid, d.status, stream) !=
-            cudaSuccess)
-            rc = KDA_ERR_CUDA;
-        else {
-            add_launches(1);
-            a.valid = valid;
+        // With nothing to decide, and few offsets, the prefill kernel checks them itself.
+        if (cut.chunks > 0 || cut.order || B > kMaxLaOrdered) {
+            if (launch_la_cut(cu_seqlens, B, T, H, d.sms, sg, d.seg_chunks > 0, valid, d.status, stream) != cudaSuccess) {
+                rc = KDA_ERR_CUDA;
+            } else {
+                add_launches(1);
+                a.valid = valid;
+            }
         }
     }
     if (rc == KDA_OK) {

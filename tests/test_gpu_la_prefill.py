@@ -251,6 +251,91 @@ def test_graph_and_determinism(kda, B, T, H, cu):
     assert kda.device_status() == 0
 
 
+def heads(x, hs, Hk, H):
+    """The inputs of heads hs alone."""
+    ks = [h // (H // Hk) for h in hs]
+    return {"q": x["q"][:, :, ks], "k": x["k"][:, :, ks], "v": x["v"][:, :, hs],
+            "g": x["g"][hs] if x["g"].dim() == 1 else x["g"][:, :, hs]}
+
+
+def check_heads(kda, d, init, cu, hs, Hk, H):
+    """The whole call, compared on some heads."""
+    out, fin = run(kda, d, init, cu)
+    sub = heads(d, hs, Hk, H)
+    o, f, oa, fa = ref.la_tokens(sub["q"], sub["k"], sub["v"], sub["g"], None if init is None else init[:, hs], cu)
+    half = ref.HALF_BF16 if fin.dtype == torch.bfloat16 else 0.0
+    ref.assert_close(out[:, :, hs], o, ref.HALF_BF16 * o.abs() + 2.1 * ref.HALF_BF16 * oa, "out")
+    ref.assert_close(fin[:, hs], f, 2.0 ** -14 * fa + half * f.abs(), "final state")
+
+
+def offsets(lengths):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lengths", [[40, 0, 5000, 70, 300], [5000], [2500, 1, 2500], [0, 4097, 0]])
+def test_packed_cut_on_the_device(kda, lengths, dtype):
+    """One long sequence among short ones, few heads: cut by the plan itself."""
+    cu = offsets(lengths)
+    d, rnd = inputs(1, cu[-1], 2, 1, seed=len(lengths), low=-0.02)
+    check(kda, d, init=rnd(len(lengths), 2, D, D).to(dtype), cu=cu)
+    check(kda, d, cu=cu, state_dtype=dtype)
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 8), (96, 32)])
+def test_packed_longest_first(kda, H, Hk):
+    """More units than SMs: the sequences go by their lengths; zeros and ties."""
+    lengths = [(37 * i) % 151 for i in range(40)] + [0, 0, 150, 150] if H == 8 else [700, 0, 20, 900, 20, 600]
+    cu = offsets(lengths)
+    d, rnd = inputs(1, cu[-1], H, Hk, seed=H, low=-0.05)
+    check_heads(kda, d, rnd(len(lengths), H, D, D), cu, [0, 5, H - 1], Hk, H)
+
+
+@pytest.mark.parametrize("top", [2, 6])
+def test_packed_many_sequences(kda, top):
+    """More sequences than one block has threads, most of them short or empty."""
+    lengths = [(7 * i) % top for i in range(1100)]
+    cu = offsets(lengths)
+    d, rnd = inputs(1, cu[-1], 2, seed=top)
+    check(kda, d, init=rnd(len(lengths), 2, D, D), cu=cu)
+
+
+@pytest.mark.parametrize("B,T,H,Hk,seg,cu", [
+    (2, 900, 12, 4, 24, None),                      # many units: one warp a part of the scan
+    (1, 1100, 24, 24, 8, [0, 700, 700, 1100]),
+    (1, 4500, 1, 1, 8, None),                       # many segments of few units
+    (1, 4500, 2, 1, 8, [0, 4400, 4500]),
+])
+def test_segment_scans(kda, B, T, H, Hk, seg, cu):
+    kda.set_segments(True, seg)
+    try:
+        d, rnd = inputs(B, T, H, Hk, seed=T, low=-0.03)
+        init = rnd(len(cu) - 1 if cu else B, H, D, D)
+        hs = sorted({0, H // 2, H - 1})
+        check_heads(kda, d, init, cu, hs, Hk, H)
+        check_heads(kda, d, init.bfloat16(), cu, hs, Hk, H)
+    finally:
+        kda.set_segments(True, 0)
+
+
+@pytest.mark.parametrize("H", [2, 96])
+def test_bad_offsets_of_larger_batches_touch_nothing(kda, H):
+    d, _ = inputs(1, 2500, H, seed=43)
+    dev = {key: x.cuda() for key, x in d.items()}
+    many = [min(n, 2500) for n in range(0, 4400, 4)]
+    many[600] = many[602] + 1
+    for cu in ([0, 1500, 1000, 2500], [0, 1000, 2499], [-1, 1000, 2500], [0, 1 << 40, 2500], many):
+        out = torch.full_like(dev["v"], 7)
+        fin = torch.full((len(cu) - 1, H, D, D), 7.0, device="cuda")
+        kda.la_prefill(dev["q"], dev["k"], dev["v"], dev["g"], cu_seqlens=torch.tensor(cu, device="cuda"),
+                       out=out, final_state=fin)
+        assert kda.device_status() == 1
+        assert (out == 7).all() and (fin == 7).all()
+
+
 @pytest.mark.slow
 def test_many_heads_long(kda):
     """More chains than SMs, and chunks enough for every buffer to be reused."""

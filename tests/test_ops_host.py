@@ -2,6 +2,8 @@
 are turned away on the host, before any CUDA call.  Addresses passed here are
 never dereferenced."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -51,7 +53,6 @@ def test_la_prefill(lib):
 
 
 def test_la_queries(lib):
-    import ctypes
     n = ctypes.c_int64(0)
     assert lib.kda_la_plan_segments(1, 16, 0, 0, ctypes.byref(n)) == -2
     assert lib.kda_la_plan_segments(1, 16, 1, 0, None) == -1
@@ -151,3 +152,18 @@ def test_python_refuses_host_tensors_and_shapes():
         ops.gated_norm(t(2, 64), t(64), t(2, 64))
     with pytest.raises(ValueError, match="x must be a contiguous"):
         ops.residual_norm(t(2, 64), t(2, 64), t(64))
+
+
+def test_packed_workspace_stays_small(lib):
+    """Room for a cut only where one can be worth it, and for few states."""
+    def need(N, T, H):
+        n = ctypes.c_int64()
+        assert lib.kda_la_workspace_bytes(N, T, H, 1, ctypes.byref(n)) == 0
+        return n.value
+    state = 128 * 128 * 4
+    assert need(4, 2000, 8) == 256                        # nothing to decide
+    assert need(8, 1 << 20, 128) <= 1024                  # a cut never pays: the order alone
+    for H in (1, 6, 12, 32, 64):
+        for T in (4096, 33333, 1 << 17, 1 << 20):
+            segments = max(16 * 152 / H, T / (64 * 128)) + 8
+            assert need(8, T, H) <= segments * H * state * 1.01 + 65536, (H, T)
