@@ -70,6 +70,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(shape, dtype, dev, stream):
+    """A new tensor in the memory of the stream that the call runs on: a block
+    that another stream has just freed may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    handle = _stream(stream, dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream(dev)):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
 def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_state=None,
                output_final_state=True, state_dtype=torch.float32, scale=None, stream=None):
     """Linear attention with one decay per head and token over whole prompts;
@@ -118,9 +128,9 @@ def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_sta
     if final_state is not None:
         _need("final_state", final_state, state_dtype, (N, H, HEAD_DIM, HEAD_DIM), dev)
     elif output_final_state:
-        final_state = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=state_dtype, device=q.device)
+        final_state = _new((N, H, HEAD_DIM, HEAD_DIM), state_dtype, dev, stream)
     if out is None:
-        out = torch.empty_like(v)
+        out = _new(v.shape, _BF16, dev, stream)
     else:
         _need("out", out, _BF16, v.shape, dev)
     if state_dtype is _F32:
@@ -133,7 +143,7 @@ def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_sta
     return out, final_state
 
 
-def _step_args(q, k, v, state, slots, out):
+def _step_args(q, k, v, state, slots, out, stream):
     """Checks of q, k, v, state and slots of a single-token step;
     (device, N, H, Hk, pool, out)."""
     if q.dim() != 3 or v.dim() != 3 or q.shape[2] != HEAD_DIM or state.dim() != 4:
@@ -151,7 +161,7 @@ def _step_args(q, k, v, state, slots, out):
     elif N > pool:
         raise ValueError("state has fewer rows than there are sequences")
     if out is None:
-        out = torch.empty_like(v)
+        out = _new(v.shape, _BF16, dev, stream)
     else:
         _need("out", out, _BF16, (N, H, HEAD_DIM), dev)
     return dev, N, H, Hk, pool, out
@@ -167,7 +177,7 @@ def la_decode(q, k, v, g, state, slots=None, out=None, scale=None, stream=None):
     row, whose output is zero), or None for rows 0 .. N - 1.  A slot beyond the
     pool is treated as padding and sets ``KDA_DEV_BAD_SLOTS`` (``device_status``).
     """
-    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out, stream)
     if Hk < 1 or H % Hk:
         raise ValueError("the heads of v must be a multiple of the heads of q")
     flags = _lib.FLAG_STATE_F32 if state.dtype is torch.float32 else 0
@@ -193,7 +203,7 @@ def kda_decode(q, k, v, g, beta, state, slots=None, out=None, beta_is_logit=Fals
     such a state, and its fp32 copy keeps long generations from rounding it at
     every token.
     """
-    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out)
+    dev, N, H, Hk, pool, out = _step_args(q, k, v, state, slots, out, stream)
     if Hk != H:
         raise ValueError("q must have the shape of v")
     _need("g", g, _F32, (N, H, HEAD_DIM), dev)
@@ -229,7 +239,7 @@ def gated_norm(x, weight, gate=None, activation="sigmoid", gate_first=False, eps
     if act:
         _need("gate", gate, _BF16, shape, dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(shape, _BF16, dev, stream)
     else:
         _need("out", out, _BF16, shape, dev)
     flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
@@ -267,11 +277,11 @@ def residual_norm(x, residual, weight, post_weight=None, gate=None, scale=1.0, e
     if gate is not None:
         _need("gate", gate, weight.dtype, (D,), dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(shape, _BF16, dev, stream)
     else:
         _need("out", out, _BF16, shape, dev)
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _new(shape, residual.dtype, dev, stream)
     else:
         _need("residual_out", residual_out, residual.dtype, shape, dev)
     flags = ((_lib.FLAG_WEIGHT_F32 if weight.dtype is torch.float32 else 0) |
