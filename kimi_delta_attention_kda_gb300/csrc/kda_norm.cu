@@ -6,8 +6,13 @@
 //     u = x or x / sqrt(mean(x^2) + eps) * w_post,  r' = r + scale gate u,
 //     y = r' / sqrt(mean(r'^2) + eps) * w.
 // Both are bound by HBM: every element is read once and written once, and a
-// row stays in registers between its sums and its outputs.  Sums and all
-// arithmetic are FP32; outputs are rounded once.
+// row stays in registers (or shared memory) between its sums and its outputs.
+// Sums and all arithmetic are FP32; outputs are rounded once.
+//
+// Measured on GB300, L2 flushed: gated norm of 8192 x 96 rows 92 us, 6.55 TB/s
+// (floor at 6.80 TB/s, the rate of a plain copy of 2 GB: 89); residual norm of
+// 8192 x 12288, FP32 residual and three weights 209 us, 5.8 TB/s (floor 178; a
+// plain copy of as many bytes 196), BF16 residual 133 us, 6.1 TB/s.
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
@@ -45,10 +50,36 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
+// kVec consecutive elements: 8, or 2 or 1 where rows start at any element.
+template <int kVec, typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[kVec]) {
+    if constexpr (kVec == 8) {
+        load8(p, x);
+    } else if constexpr (kVec == 1) {
+        x[0] = static_cast<float>(*p);
+    } else if constexpr (sizeof(T) == 4) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+        x[0] = bf16_lo(v);
+        x[1] = bf16_hi(v);
+    }
+}
+template <int kVec, typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[kVec]) {
+    if constexpr (kVec == 8)
+        store8(p, x);
+    else if constexpr (kVec == 1)
+        from_f32(p, x[0]);
+    else if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+    else
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(x[0], x[1]);
+}
 
 // ------------------------------------------------------------- gated norm
 // 16 lanes share a row, 8 channels (16 bytes) each; a thread has kRows rows,
@@ -202,35 +233,104 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(ResidualNormArg
     }
 }
 
-// Widths that are no multiple of 8: rows start at any element, so elements go
-// one at a time (kPair: two, where the width is even), and the new residual
-// waits in shared memory for its norm.
-template <typename T, bool kPair>
-__device__ __forceinline__ float2 load_some(const T* p) {
-    if constexpr (!kPair)
-        return make_float2(to_f32(*p), 0.f);
-    else if constexpr (sizeof(T) == 4)
-        return *reinterpret_cast<const float2*>(p);
-    else {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-        return make_float2(bf16_lo(v), bf16_hi(v));
+// Narrow rows: kLanes lanes a row and kGroups vectors a lane, all loaded before
+// the first sum; no barrier.  65536 rows of 128, FP32 residual: 25 us, against 60
+// with a CTA of 128 threads a row; of 512 68 and 82, of 768 107 and 103: up to 512.
+constexpr int kRowsThreads = 256;
+constexpr int64_t kRowsMaxDim = 512;
+template <typename R, typename W, int kVec, int kGroups, int kLanes>
+__global__ void __launch_bounds__(kRowsThreads) residual_norm_rows_kernel(ResidualNormArgs p) {
+    const int D = static_cast<int>(p.dim), lane = threadIdx.x % kLanes;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / kLanes) + threadIdx.x / kLanes, base = row * D;
+    const int end = row < p.rows ? D : 0;
+    const auto x = static_cast<const __nv_bfloat16*>(p.x) + base;
+    const auto res = static_cast<const R*>(p.residual) + base;
+    const auto post = static_cast<const W*>(p.post_weight), gate = static_cast<const W*>(p.gate);
+    float u[kGroups][kVec], r[kGroups][kVec];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int at = (i * kLanes + lane) * kVec;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) u[i][j] = r[i][j] = 0.f;
+        if (at < end) {
+            load_vec<kVec>(x + at, u[i]);
+            load_vec<kVec>(res + at, r[i]);
+        }
+    }
+    auto sum_row = [](float v) {
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    const float inv_d = 1.f / static_cast<float>(D);
+    float ss = 0.f;
+    if (post) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) ss = fmaf(u[i][j], u[i][j], ss);
+        const float rms = inv_rms(sum_row(ss) * inv_d, p.eps);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int at = (i * kLanes + lane) * kVec;
+            if (at < end) {
+                float w[kVec];
+                load_vec<kVec>(post + at, w);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) u[i][j] *= rms * w[j];
+            }
+        }
+        ss = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int at = (i * kLanes + lane) * kVec;
+        if (at < end) {
+            if (gate) {
+                float w[kVec];
+                load_vec<kVec>(gate + at, w);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) u[i][j] *= w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                r[i][j] = fmaf(p.scale, u[i][j], r[i][j]);
+                ss = fmaf(r[i][j], r[i][j], ss);
+            }
+            store_vec<kVec>(static_cast<R*>(p.residual_out) + base + at, r[i]);
+        }
+    }
+    const float rms = inv_rms(sum_row(ss) * inv_d, p.eps);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int at = (i * kLanes + lane) * kVec;
+        if (at < end) {
+            float w[kVec];
+            load_vec<kVec>(static_cast<const W*>(p.weight) + at, w);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) r[i][j] *= rms * w[j];
+            store_vec<kVec>(static_cast<__nv_bfloat16*>(p.out) + base + at, r[i]);
+        }
     }
 }
-template <typename T, bool kPair>
-__device__ __forceinline__ void store_some(T* p, float2 x) {
-    if constexpr (!kPair)
-        from_f32(p, x.x);
-    else if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float2*>(p) = x;
-    else
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16(x.x, x.y);
+
+template <typename R, typename W, int kVec, int kGroups, int kLanes>
+cudaError_t run_rows(const ResidualNormArgs& p, cudaStream_t stream) {
+    constexpr int64_t each = kRowsThreads / kLanes;
+    residual_norm_rows_kernel<R, W, kVec, kGroups, kLanes>
+        <<<static_cast<unsigned>((p.rows + each - 1) / each), kRowsThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
-template <typename R, typename W, bool kPair, int kThreads>
+
+// Wide rows of a width that is no multiple of 8, for which the streaming
+// kernel has too few rows or too little room: one row per CTA, its new
+// residual in shared memory until its norm is known.  Elements (pairs, where the
+// width is even) one at a time: 300 rows of 5001 take 16 us, launch and latency.
+template <typename R, typename W, int kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads) residual_norm_odd_kernel(ResidualNormArgs p) {
     extern __shared__ __align__(16) float row_smem[];
     __shared__ float buf[2][32];
-    constexpr int kStep = kPair ? 2 : 1;
-    const int D = static_cast<int>(p.dim), t0 = threadIdx.x * kStep;
+    const int D = static_cast<int>(p.dim), t0 = threadIdx.x * kVec;
     const int64_t base = static_cast<int64_t>(blockIdx.x) * D;
     const auto x = static_cast<const __nv_bfloat16*>(p.x) + base;
     const auto res = static_cast<const R*>(p.residual) + base;
@@ -239,38 +339,49 @@ __global__ void __launch_bounds__(kThreads) residual_norm_odd_kernel(ResidualNor
     float rms = 1.f;
     if (post) {
         float ss = 0.f;
-        for (int at = t0; at < D; at += kThreads * kStep) {
-            const float2 v = load_some<__nv_bfloat16, kPair>(x + at);
-            ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+        for (int at = t0; at < D; at += kThreads * kVec) {
+            float v[kVec];
+            load_vec<kVec>(x + at, v);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) ss = fmaf(v[j], v[j], ss);
         }
         rms = inv_rms(block_sum<kThreads>(ss, buf[0]) * inv_d, p.eps);
     }
     float ss = 0.f;
-    for (int at = t0; at < D; at += kThreads * kStep) {
-        float2 u = load_some<__nv_bfloat16, kPair>(x + at), r = load_some<R, kPair>(res + at);
+    for (int at = t0; at < D; at += kThreads * kVec) {
+        float u[kVec], r[kVec], w[kVec];
+        load_vec<kVec>(x + at, u);
+        load_vec<kVec>(res + at, r);
         if (post) {
-            const float2 w = load_some<W, kPair>(post + at);
-            u = make_float2(u.x * rms * w.x, u.y * rms * w.y);
+            load_vec<kVec>(post + at, w);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) u[j] *= rms * w[j];
         }
         if (gate) {
-            const float2 w = load_some<W, kPair>(gate + at);
-            u = make_float2(u.x * w.x, u.y * w.y);
+            load_vec<kVec>(gate + at, w);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) u[j] *= w[j];
         }
-        r = make_float2(fmaf(p.scale, u.x, r.x), fmaf(p.scale, u.y, r.y));
-        ss = fmaf(r.x, r.x, ss);
-        if (kPair) ss = fmaf(r.y, r.y, ss);
-        store_some<float, kPair>(row_smem + at, r);
-        store_some<R, kPair>(static_cast<R*>(p.residual_out) + base + at, r);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            r[j] = fmaf(p.scale, u[j], r[j]);
+            ss = fmaf(r[j], r[j], ss);
+        }
+        store_vec<kVec>(row_smem + at, r);
+        store_vec<kVec>(static_cast<R*>(p.residual_out) + base + at, r);
     }
     rms = inv_rms(block_sum<kThreads>(ss, buf[1]) * inv_d, p.eps);
-    for (int at = t0; at < D; at += kThreads * kStep) {   // (a thread's own elements)
-        const float2 r = load_some<float, kPair>(row_smem + at), w = load_some<W, kPair>(static_cast<const W*>(p.weight) + at);
-        store_some<__nv_bfloat16, kPair>(static_cast<__nv_bfloat16*>(p.out) + base + at,
-                                         make_float2(r.x * rms * w.x, r.y * rms * w.y));
+    for (int at = t0; at < D; at += kThreads * kVec) {   // (a thread's own elements)
+        float r[kVec], w[kVec];
+        load_vec<kVec>(row_smem + at, r);
+        load_vec<kVec>(static_cast<const W*>(p.weight) + at, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) r[j] *= rms * w[j];
+        store_vec<kVec>(static_cast<__nv_bfloat16*>(p.out) + base + at, r);
     }
 }
 
-template <typename R, typename W, bool kPair, int kThreads>
+template <typename R, typename W, int kVec, int kThreads>
 cudaError_t run_odd(const ResidualNormArgs& p, cudaStream_t stream) {
     const int bytes = static_cast<int>(p.dim) * 4;
     static bool configured[64] = {};
@@ -278,12 +389,12 @@ cudaError_t run_odd(const ResidualNormArgs& p, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(residual_norm_odd_kernel<R, W, kPair, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(residual_norm_odd_kernel<R, W, kVec, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kMaxNormDim) * 4);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    residual_norm_odd_kernel<R, W, kPair, kThreads><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
+    residual_norm_odd_kernel<R, W, kVec, kThreads><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -291,11 +402,38 @@ cudaError_t run_odd(const ResidualNormArgs& p, cudaStream_t stream) {
 // copy brings to shared memory two or three rows ahead; a thread keeps the
 // weights of its channels in registers (post weight, gate and scale as one
 // factor: they only ever meet as a product).  Reading the weights again for
-// every row would take as much of L2's bandwidth as the rows take of HBM's.
+// every row would take as much of L2's bandwidth as the rows take of HBM's: a
+// CTA a row takes 336 us for 8192 x 12288 with an FP32 residual, this 209 (768
+// threads; 1024 206, but 144 against 133 with a BF16 residual).  Rows of a width
+// that is no multiple of 8 gain more, because shared memory has no need of their
+// alignment: 8192 x 12281 213 against 343 us, 65536 x 777 111 against 195.  Up to
+// 1024, multiples of 8 are as well served by a CTA a row (65536 x 768: 103, 105).
 constexpr int kStreamStages = 3;
-constexpr int64_t kStreamMinDim = 1024, kStreamMaxDim = 16384, kStreamMinRows = 2;
+constexpr int64_t kStreamMaxDim = 16384, kStreamMinRows = 2;
 constexpr int kStreamSmem = 226 * 1024;
-template <typename R, typename W, int kGroups, int kThreads>
+// A row that does not start on 16 bytes is copied from the boundary before it to
+// the one behind it, and read in shared memory at its offset.
+template <typename R, int kVec>
+__host__ __device__ constexpr uint32_t stream_x_bytes(uint32_t D) { return kVec == 8 ? 2 * D : (2 * D + 30) & ~15u; }
+template <typename R, int kVec>
+__host__ __device__ constexpr uint32_t stream_stage_bytes(uint32_t D) {
+    constexpr uint32_t n = sizeof(R);
+    return stream_x_bytes<R, kVec>(D) + (kVec == 8 ? n * D : (n * D + 30) & ~15u);
+}
+// The span of row `row` that a bulk copy brings, [lo, up): where the tensor
+// ends between two boundaries, up to the one before, and the rest is copied here.
+__device__ __forceinline__ void stream_span(const uint8_t* base, uint8_t* dst, int64_t row, int64_t rows, uint32_t row_bytes,
+                                            int64_t* lo, int64_t* up) {
+    const int64_t at = row * row_bytes, end = at + row_bytes;
+    *lo = at & ~int64_t(15);
+    *up = (end + 15) & ~int64_t(15);
+    if (*up > rows * row_bytes) {
+        *up = end & ~int64_t(15);
+        for (int64_t b = *up; b < end; b += 2)
+            *reinterpret_cast<uint16_t*>(dst + (b - *lo)) = *reinterpret_cast<const uint16_t*>(base + b);
+    }
+}
+template <typename R, typename W, int kVec, int kGroups, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     residual_norm_stream_kernel(ResidualNormArgs p, int stages) {
     extern __shared__ __align__(16) uint8_t stream_smem[];
@@ -303,12 +441,24 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     __shared__ float red[2][2][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int D = static_cast<int>(p.dim);
-    const uint32_t xb = D * 2, rb = D * static_cast<uint32_t>(sizeof(R)), stage_bytes = xb + rb;
+    const uint32_t xb = D * 2, rb = D * static_cast<uint32_t>(sizeof(R));
+    const uint32_t xs_bytes = stream_x_bytes<R, kVec>(D), stage_bytes = stream_stage_bytes<R, kVec>(D);
     const auto x = static_cast<const uint8_t*>(p.x), res = static_cast<const uint8_t*>(p.residual);
     auto fetch = [&](int64_t row, int s) {
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
-        bulk_g2s(stream_smem + s * stage_bytes, x + row * xb, xb, &full[s]);
-        bulk_g2s(stream_smem + s * stage_bytes + xb, res + row * rb, rb, &full[s]);
+        uint8_t* dst = stream_smem + s * stage_bytes;
+        if constexpr (kVec == 8) {
+            mbar_arrive_expect_tx(&full[s], xb + rb);
+            bulk_g2s(dst, x + row * xb, xb, &full[s]);
+            bulk_g2s(dst + xs_bytes, res + row * rb, rb, &full[s]);
+        } else {
+            int64_t xlo, xup, rlo, rup;
+            stream_span(x, dst, row, p.rows, xb, &xlo, &xup);
+            stream_span(res, dst + xs_bytes, row, p.rows, rb, &rlo, &rup);
+            const uint32_t xn = static_cast<uint32_t>(xup - xlo), rn = static_cast<uint32_t>(rup - rlo);
+            mbar_arrive_expect_tx(&full[s], xn + rn);
+            bulk_g2s(dst, x + xlo, xn, &full[s]);
+            bulk_g2s(dst + xs_bytes, res + rlo, rn, &full[s]);
+        }
     };
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -318,27 +468,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             if (row < p.rows) fetch(row, s);
         }
     }
-    float fac[kGroups][8], wt[kGroups][8];
+    float fac[kGroups][kVec], wt[kGroups][kVec];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const int at = (i * kThreads + tid) * 8;
+        const int at = (i * kThreads + tid) * kVec;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kVec; ++j) {
             fac[i][j] = p.scale;
             wt[i][j] = 0.f;
         }
         if (at < D) {
-            float v[8];
-            load8(static_cast<const W*>(p.weight) + at, wt[i]);
+            float v[kVec];
+            load_vec<kVec>(static_cast<const W*>(p.weight) + at, wt[i]);
             if (p.post_weight) {
-                load8(static_cast<const W*>(p.post_weight) + at, v);
+                load_vec<kVec>(static_cast<const W*>(p.post_weight) + at, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) fac[i][j] *= v[j];
+                for (int j = 0; j < kVec; ++j) fac[i][j] *= v[j];
             }
             if (p.gate) {
-                load8(static_cast<const W*>(p.gate) + at, v);
+                load_vec<kVec>(static_cast<const W*>(p.gate) + at, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) fac[i][j] *= v[j];
+                for (int j = 0; j < kVec; ++j) fac[i][j] *= v[j];
             }
         }
     }
@@ -359,37 +509,37 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     int odd = 0;   // the sums' buffers alternate from row to row
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         if (!mbar_wait_bounded(&full[s], phase, p.status)) return;
-        const auto xs = reinterpret_cast<const __nv_bfloat16*>(stream_smem + s * stage_bytes);
-        const auto rs = reinterpret_cast<const R*>(stream_smem + s * stage_bytes + xb);
+        const auto xs = reinterpret_cast<const __nv_bfloat16*>(stream_smem + s * stage_bytes + (kVec == 8 ? 0 : row * xb & 15));
+        const auto rs = reinterpret_cast<const R*>(stream_smem + s * stage_bytes + xs_bytes + (kVec == 8 ? 0 : row * rb & 15));
         float rms = 1.f;
         if (p.post_weight) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const int at = (i * kThreads + tid) * 8;
+                const int at = (i * kThreads + tid) * kVec;
                 if (at < D) {
-                    float v[8];
-                    load8(xs + at, v);
+                    float v[kVec];
+                    load_vec<kVec>(xs + at, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+                    for (int j = 0; j < kVec; ++j) ss = fmaf(v[j], v[j], ss);
                 }
             }
             rms = inv_rms(sum_all(ss, red[odd][0]) * inv_d, p.eps);
         }
-        float r[kGroups][8], ss = 0.f;
+        float r[kGroups][kVec], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int at = (i * kThreads + tid) * 8;
+            const int at = (i * kThreads + tid) * kVec;
             if (at < D) {
-                float v[8];
-                load8(xs + at, v);
-                load8(rs + at, r[i]);
+                float v[kVec];
+                load_vec<kVec>(xs + at, v);
+                load_vec<kVec>(rs + at, r[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kVec; ++j) {
                     r[i][j] = fmaf(v[j] * rms, fac[i][j], r[i][j]);
                     ss = fmaf(r[i][j], r[i][j], ss);
                 }
-                store8(static_cast<R*>(p.residual_out) + row * D + at, r[i]);
+                store_vec<kVec>(static_cast<R*>(p.residual_out) + row * D + at, r[i]);
             }
         }
         fence_proxy_async_smem();   // this stage is read; a copy may follow the barrier
@@ -398,11 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         if (tid == 0 && next < p.rows) fetch(next, s);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int at = (i * kThreads + tid) * 8;
+            const int at = (i * kThreads + tid) * kVec;
             if (at < D) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[i][j] *= rms * wt[i][j];
-                store8(static_cast<__nv_bfloat16*>(p.out) + row * D + at, r[i]);
+                for (int j = 0; j < kVec; ++j) r[i][j] *= rms * wt[i][j];
+                store_vec<kVec>(static_cast<__nv_bfloat16*>(p.out) + row * D + at, r[i]);
             }
         }
         odd ^= 1;
@@ -413,22 +563,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
 }
 
-template <typename R, typename W, int kGroups, int kThreads>
+template <typename R, typename W, int kVec, int kGroups, int kThreads>
 cudaError_t run_stream(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
-    const int row = static_cast<int>(p.dim) * (2 + static_cast<int>(sizeof(R))), room = kStreamSmem / (1024 / kThreads);
+    const int row = static_cast<int>(stream_stage_bytes<R, kVec>(static_cast<uint32_t>(p.dim))), room = kStreamSmem / (1024 / kThreads);
     const int stages = row * kStreamStages <= room ? kStreamStages : room / row;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(residual_norm_stream_kernel<R, W, kGroups, kThreads>,
+        e = cudaFuncSetAttribute(residual_norm_stream_kernel<R, W, kVec, kGroups, kThreads>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
     const int64_t ctas = static_cast<int64_t>(sms) * (1024 / kThreads);
-    residual_norm_stream_kernel<R, W, kGroups, kThreads>
+    residual_norm_stream_kernel<R, W, kVec, kGroups, kThreads>
         <<<static_cast<unsigned>(p.rows < ctas ? p.rows : ctas), kThreads, stages * row, stream>>>(p, stages);
     return cudaGetLastError();
 }
@@ -440,24 +590,42 @@ cudaError_t run_residual(const ResidualNormArgs& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <typename R, typename W, int kVec>
+cudaError_t pick_stream(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
+    constexpr int n = 8 / kVec;   // vectors in eight elements
+    if constexpr (kVec != 8)
+        if (p.dim <= 1024) return run_stream<R, W, kVec, n, 128>(p, sms, stream);
+    if (p.dim <= 2048) return run_stream<R, W, kVec, n, 256>(p, sms, stream);
+    if (p.dim <= 4096) return run_stream<R, W, kVec, n, 512>(p, sms, stream);
+    if (p.dim <= 8192) return run_stream<R, W, kVec, n, 1024>(p, sms, stream);
+    if (p.dim <= 12288) return run_stream<R, W, kVec, 2 * n, 768>(p, sms, stream);
+    return run_stream<R, W, kVec, 2 * n, 1024>(p, sms, stream);
+}
+template <typename R, typename W, int kVec>
+cudaError_t pick_rows(const ResidualNormArgs& p, cudaStream_t stream) {
+    constexpr int n = 8 / kVec;
+    if (p.dim <= 64) return run_rows<R, W, kVec, n, 8>(p, stream);
+    if (p.dim <= 256) return run_rows<R, W, kVec, n, 32>(p, stream);
+    if constexpr (kVec != 8)
+        if (p.dim > 512) return run_rows<R, W, kVec, 4 * n, 32>(p, stream);
+    return run_rows<R, W, kVec, 2 * n, 32>(p, stream);
+}
 template <typename R, typename W>
 cudaError_t pick_residual(const ResidualNormArgs& p, int sms, cudaStream_t stream) {
     const int64_t D = p.dim;
-    if (D % 8 == 0 && D > kStreamMinDim && D <= kStreamMaxDim && p.rows >= kStreamMinRows * sms) {
-        if (D <= 2048) return run_stream<R, W, 1, 256>(p, sms, stream);
-        if (D <= 4096) return run_stream<R, W, 1, 512>(p, sms, stream);
-        if (D <= 8192) return run_stream<R, W, 1, 1024>(p, sms, stream);
-        if (D <= 12288) return run_stream<R, W, 2, 768>(p, sms, stream);
-        return run_stream<R, W, 2, 1024>(p, sms, stream);
-    }
-    if (D % 8 == 0) {
-        if (D <= 1024) return run_residual<R, W, 1, 128>(p, stream);
-        if (D <= 4096) return run_residual<R, W, 2, 256>(p, stream);
-        if (D <= 12288) return run_residual<R, W, 3, 512>(p, stream);
-        return run_residual<R, W, 4, 1024>(p, stream);
-    }
-    if (D % 2 == 0) return D <= 2048 ? run_odd<R, W, true, 128>(p, stream) : run_odd<R, W, true, 512>(p, stream);
-    return D <= 1024 ? run_odd<R, W, false, 128>(p, stream) : run_odd<R, W, false, 512>(p, stream);
+    const int vec = D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1;
+    const bool walk = D > kRowsMaxDim && D <= kStreamMaxDim && p.rows >= kStreamMinRows * sms;
+    if (vec == 8 && D > kRowsMaxDim && D <= 1024) return run_residual<R, W, 1, 128>(p, stream);
+    if (D <= kRowsMaxDim || (D <= 1024 && !walk))
+        return vec == 8 ? pick_rows<R, W, 8>(p, stream) : vec == 2 ? pick_rows<R, W, 2>(p, stream) : pick_rows<R, W, 1>(p, stream);
+    if (walk)
+        return vec == 8 ? pick_stream<R, W, 8>(p, sms, stream)
+                        : vec == 2 ? pick_stream<R, W, 2>(p, sms, stream) : pick_stream<R, W, 1>(p, sms, stream);
+    if (vec == 2) return run_odd<R, W, 2, 512>(p, stream);
+    if (vec == 1) return run_odd<R, W, 1, 512>(p, stream);
+    if (D <= 4096) return run_residual<R, W, 2, 256>(p, stream);
+    if (D <= 12288) return run_residual<R, W, 3, 512>(p, stream);
+    return run_residual<R, W, 4, 1024>(p, stream);
 }
 
 }  // namespace

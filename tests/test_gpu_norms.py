@@ -141,6 +141,22 @@ def test_residual_many_rows(kda, rows, dim, rt, wt):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("rows,dim", [(304, 1025), (333, 1026), (311, 4099), (305, 8191), (306, 12289), (304, 16383),
+                                      (310, 12282), (1000, 1), (777, 13), (2049, 63), (513, 64), (300, 65), (300, 72),
+                                      (300, 255), (301, 257), (300, 512), (333, 770), (300, 1001), (77, 1023)])
+@pytest.mark.parametrize("rt", TYPES)
+def test_residual_odd_and_narrow_rows(kda, rows, dim, rt):
+    """Rows that start at any element, and several rows a warp; in place too."""
+    r = gen(rows + dim)
+    wt = rt
+    x, res, w, post, gate = r(rows, dim).bfloat16(), r(rows, dim).to(rt), r(dim).to(wt), r(dim).to(wt), r(dim).to(wt)
+    want = check_residual(kda, x, res, w, post, gate, 0.7)
+    check_residual(kda, x, res, w)
+    dev = [t.cuda() for t in (x, res, w, post, gate)]
+    got = kda.residual_norm(*dev, scale=0.7, out=dev[0], residual_out=dev[1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_residual_zero_rows_and_eps(kda):
     x, r, w = torch.zeros(3, 256).bfloat16(), torch.zeros(3, 256), torch.ones(256)
     out, res = check_residual(kda, x, r, w, w, w)
