@@ -111,17 +111,31 @@ struct Kernel {
     LaSegments sg;      // sg.starts null: no segments
     uint32_t units, heads;
 };
-// What this call does: a packed batch's cut is decided on the device.
+// What a CTA does: units of (sequence, head), every grid's width one; of
+// (segment, head) for a fixed layout's cut; and for a packed batch's, decided on
+// the device, the parts of its span, for one head.
 struct Work {
     const LaArgs& a;
     const LaSegments& sg;
     const uint32_t& heads;
-    uint32_t units;
-    bool cut;           // the units are (segment, head), else (sequence, head)
-    __device__ __forceinline__ explicit Work(const Kernel& p) : a(p.a), sg(p.sg), heads(p.heads), units(p.units), cut(p.sg.starts) {
+    uint32_t base, step, end;
+    bool cut;
+    __device__ __forceinline__ Work(const Kernel& p, bool states)
+        : a(p.a), sg(p.sg), heads(p.heads), base(0), step(gridDim.x), end(p.units), cut(p.sg.starts) {
         if (sg.cut) {
             cut = *sg.cut != 0;
-            units = static_cast<uint32_t>(cut ? sg.seg_begin[a.N] : a.N) * heads;
+            end = static_cast<uint32_t>(a.N) * heads;
+            if (cut) {
+                const uint32_t s = blockIdx.x / heads;
+                step = 1;
+                base = end = 0;
+                if (s < sg.spans) {
+                    base = sg.first[s];
+                    end = sg.first[s + 1];
+                    // Only a span's last part can go on in the next.
+                    if (states && base < end) base = end - 1;
+                }
+            }
         }
     }
     // Of an uncut packed batch: its sequences, longest first (or null).
@@ -129,49 +143,59 @@ struct Work {
     // The CTA's i-th unit: in rows of the grid's width, where the units come
     // longest first every other row backwards.
     __device__ __forceinline__ uint32_t unit(uint32_t i) const {
-        return i * gridDim.x + ((i & 1) && order() ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const uint32_t at = step > 1 ? blockIdx.x : 0;
+        return base + i * step + ((i & 1) && order() ? step - 1 - at : at);
     }
-    __device__ __forceinline__ uint32_t rows() const { return (units + gridDim.x - 1) / gridDim.x; }
+    __device__ __forceinline__ uint32_t rows() const { return (end - base + step - 1) / step; }
 };
 
 // One (sequence or segment, head).
 struct Unit {
     int n, h, tok0, len;
-    uint32_t slot;      // (segment, head) row of the segments' buffers
+    uint32_t slot;      // (span, head) row of the spans' buffers
+    bool mid;           // goes on from the span before
     bool last;          // writes the final state
     int nch;
 };
 template <bool kStates>
 __device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
     Unit w;
-    const uint32_t s = u / p.heads;
-    w.h = u - s * p.heads;
-    w.slot = u;
-    w.last = true;
-    if (!p.cut) {
-        w.n = p.order() ? p.order()[s] : s;
-        if (p.a.cu_seqlens) {
-            w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
-            w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
-        } else {
-            w.len = static_cast<int>(p.a.tokens_per_seq);
-            w.tok0 = s * w.len;
-        }
-    } else if (p.sg.seg_begin) {
-        w.n = static_cast<int>(p.sg.seg_seq[s]);
-        w.tok0 = static_cast<int>(p.sg.seg_tokens[s]);
-        w.len = static_cast<int>(p.sg.seg_tokens[s + 1]) - w.tok0;
-        w.last = s + 1 == p.sg.seg_begin[w.n + 1];
+    if (p.cut && p.sg.cut) {
+        const int4 part = p.sg.part[u];
+        w.n = part.x;
+        w.h = blockIdx.x % p.heads;
+        w.tok0 = part.y;
+        w.len = part.z;
+        w.slot = blockIdx.x;
+        w.mid = part.w & kLaMid;
+        w.last = part.w & kLaLast;
     } else {
-        const uint32_t segs = static_cast<uint32_t>(p.sg.segs);
-        const int each = static_cast<int>(p.sg.seg_tokens_each), per = static_cast<int>(p.a.tokens_per_seq);
-        w.n = s / segs;
-        const int j = s - w.n * segs;
-        w.tok0 = w.n * per + j * each;
-        w.last = j + 1 == static_cast<int>(segs);
-        w.len = w.last ? per - j * each : each;
+        const uint32_t s = u / p.heads;
+        w.h = u - s * p.heads;
+        w.slot = u;
+        w.mid = false;
+        w.last = true;
+        if (p.cut) {
+            const uint32_t segs = static_cast<uint32_t>(p.sg.segs);
+            const int each = static_cast<int>(p.sg.seg_tokens_each), per = static_cast<int>(p.a.tokens_per_seq);
+            w.n = s / segs;
+            const int j = s - w.n * segs;
+            w.tok0 = w.n * per + j * each;
+            w.mid = j > 0;
+            w.last = j + 1 == static_cast<int>(segs);
+            w.len = w.last ? per - j * each : each;
+        } else {
+            w.n = p.order() ? p.order()[s] : s;
+            if (p.a.cu_seqlens) {
+                w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
+                w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
+            } else {
+                w.len = static_cast<int>(p.a.tokens_per_seq);
+                w.tok0 = s * w.len;
+            }
+        }
     }
-    if (kStates && w.last) w.len = 0;     // nothing follows a sequence's last segment
+    if (kStates && w.last) w.len = 0;     // nothing of the sequence follows
     w.nch = (w.len + kC - 1) / kC;
     return w;
 }
@@ -199,7 +223,7 @@ __device__ __forceinline__ void walk(const Work& p, F f) {
     Pos<Smem<kStates>::kStages> x;
 #pragma unroll 1
     for (uint32_t i = 0; i < p.rows(); ++i) {
-        if (p.unit(i) >= p.units) continue;
+        if (p.unit(i) >= p.end) continue;
         const Unit w = unit_at<kStates>(p, p.unit(i));
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
@@ -653,16 +677,19 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
     const uint32_t scol = tmem + (static_cast<uint32_t>(32 * (ws & 3)) << 16) + kColS + 64 * half;
     uint8_t* row = smem + M::kS + half * kSlab + key * 128;
     const int64_t lane_at = 64 * half * kHeadDim + key;
-    const void* init = p.cut ? static_cast<const void*>(p.sg.starts) : p.a.init_state;
-    const bool init_f32 = p.cut || p.a.state_f32;
     Pos<n> x;
 #pragma unroll 1
     for (uint32_t row_i = 0; row_i < p.rows(); ++row_i) {
-        if (p.unit(row_i) >= p.units) continue;
+        if (p.unit(row_i) >= p.end) continue;
         const Unit w = unit_at<kStates>(p, p.unit(row_i));
         const int64_t at = (static_cast<int64_t>(w.n) * p.a.H + w.h) * (kHeadDim * kHeadDim) + lane_at;
         const int64_t seg_at = static_cast<int64_t>(w.slot) * (kHeadDim * kHeadDim) + lane_at;
-        const int64_t init_at = p.cut ? seg_at : at;
+        // (Where final states overwrite the initial ones, a sequence's last part
+        // may be done before its first has begun.)
+        const bool scanned = w.mid || (p.sg.inits && !w.last);
+        const void* init = w.mid ? static_cast<const void*>(p.sg.starts) : scanned ? p.sg.inits : p.a.init_state;
+        const bool init_f32 = scanned || p.a.state_f32;
+        const int64_t init_at = w.mid ? seg_at : at;
         const bool final = !kStates && w.last && p.a.final_state;
         if (w.nch == 0) {
             if (final)
@@ -672,8 +699,8 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
             continue;
         }
         if (!kStates) {
-            // (The chain over the segments may still be running.)
-            if (p.cut) asm volatile("griddepcontrol.wait;" ::: "memory");
+            // (The chain over the spans may still be running.)
+            if (scanned) asm volatile("griddepcontrol.wait;" ::: "memory");
             state_in(init, init_f32, init_at, scol);
         }
         float total = 0.f;
@@ -741,8 +768,9 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
             }
         }
         if (kStates) {
-            state_out(p.sg.starts, true, seg_at, scol);
-            if (ws == 0 && lane == 0) p.sg.decay[w.slot] = total;
+            // (For the next span of this head.)
+            state_out(p.sg.starts, true, seg_at + static_cast<int64_t>(p.heads) * (kHeadDim * kHeadDim), scol);
+            if (ws == 0 && lane == 0) p.sg.decay[w.slot + p.heads] = total;
         } else if (final) {
             state_out(p.a.final_state, p.a.state_f32, at, scol);
         }
@@ -972,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         valid = __syncthreads_and(ok);
         if (!valid && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(kernel.a.status, kDevBadSeqlens);
     }
-    const Work p(kernel);
+    const Work p(kernel, kStates);
     if (!valid || (kStates && !p.cut)) return;
     if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
@@ -983,8 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // What the first chunk reads, on its way to L2 while the barriers and the
     // tensor memory are made ready.
-    if (warp >= kLoadWarp && blockIdx.x < p.units) {
-        const Unit w = unit_at<kStates>(p, blockIdx.x);
+    if (warp >= kLoadWarp && p.rows() > 0 && p.unit(0) < p.end) {
+        const Unit w = unit_at<kStates>(p, p.unit(0));
         if (w.nch > 0 && warp == kLoadWarp && lane == 0) {
             const int kcol = static_cast<int>(w.h / static_cast<uint32_t>(p.a.H / p.a.Hk)) * kHeadDim, vcol = w.h * kHeadDim;
 #pragma unroll 1
@@ -1062,8 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The segments' incoming states: per (sequence, head), S_0 = init and
-// S_{j+1} = exp(D_j) S_j + Z_j, in place over Z.  kSplit warps share 128 kVec
+// The spans' incoming states: per (sequence, head), from S = init over the spans
+// that it goes on in, S <- exp(D) S + Z, in place over Z.  kSplit warps share 128 kVec
 // of the 16384 elements and take the segments kSplit kEach at a time: each warp
 // loads up to kEach of them at once, composes them, and starts from what the
 // warps before it compose to.  Few (sequence, head) units: eight warps a part,
@@ -1092,8 +1120,13 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
     for (uint32_t part = blockIdx.x * kGroups + warp / kSplit; part < parts; part += gridDim.x * kGroups) {
         const uint32_t unit = part / kParts, n = unit / p.heads, h = unit - n * p.heads;
         const int64_t e = (part % kParts) * (128 * kVec) + 4 * lane;
-        const int64_t s0 = p.sg.seg_begin ? p.sg.seg_begin[n] : n * p.sg.segs;
-        const int64_t s1 = p.sg.seg_begin ? p.sg.seg_begin[n + 1] : s0 + p.sg.segs;
+        int64_t s0 = n * p.sg.segs + 1, s1 = s0 + p.sg.segs - 1;
+        if (p.sg.inner) {
+            const int2 in = p.sg.inner[n];
+            s0 = in.x;
+            s1 = in.y;
+        }
+        if (s0 >= 0 && s0 >= s1) continue;   // the sequence is within one span
         float4 s[kVec];
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
@@ -1107,7 +1140,8 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
                     s[v] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
                 }
             }
-            if (s0 == s1 && p.a.final_state && place == 0) {   // an empty sequence
+            if (p.sg.inits && place == 0) *reinterpret_cast<float4*>(p.sg.inits + at) = s[v];
+            if (s0 < 0 && p.a.final_state && place == 0) {   // an empty sequence
                 if (p.a.state_f32)
                     *reinterpret_cast<float4*>(static_cast<float*>(p.a.final_state) + at) = s[v];
                 else
@@ -1125,7 +1159,7 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
             float d[kEach];
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const bool there = i < mine && first + i + 1 < s1;      // (nothing follows the last segment)
+                const bool there = i < mine;
                 d[i] = there ? p.sg.decay[(first + i) * p.a.H + h] : 0.f;
 #pragma unroll
                 for (int v = 0; v < kVec; ++v)
@@ -1169,8 +1203,8 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
                 if (i < mine)
 #pragma unroll
                     for (int v = 0; v < kVec; ++v) {
-                        *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v) = at[v];
                         at[v] = step(d[i], at[v], z[i][v]);
+                        *reinterpret_cast<float4*>(p.sg.starts + ((first + i) * p.a.H + h) * kState + e + 128 * v) = at[v];
                     }
             if (kSplit == 1)
 #pragma unroll
@@ -1180,14 +1214,10 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
 }
 
 // A packed batch: checks the offsets' contract (kda_meta.cu) and decides, from
-// the lengths, whether and where to cut.  Without a cut the longest sequence
-// is the least it takes; a cut leaves rows of units of L chunks, each row with
-// its own start (kda_launch.h has the costs).  8 sequences of 33,333 tokens
-// in all, 12 heads, the longest 65 chunks: 180 us uncut, 183 to 266 cut;
-// 20,000 tokens, 16 heads, the longest 154 chunks: 399 uncut, 136 cut into
-// segments of 8.
+// the lengths, whether to cut.  Without a cut the longest sequence is the least
+// it takes; with one, every SM has a span of W chunks, and takes kLaCutChunkUs
+// for each (kda_launch.h has the costs).
 constexpr int kCutThreads = 1024;
-__constant__ const int kCutLengths[] = {4, 6, 8, 12, 16, 24, 32, 48, 64};
 
 __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* buf) {
 #pragma unroll
@@ -1202,7 +1232,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* buf) {
 }
 
 __global__ void __launch_bounds__(kCutThreads)
-    la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, bool forced, int32_t* valid,
+    la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, int forced, int32_t* valid,
                   int* status) {
     __shared__ int64_t buf[32];
     __shared__ int longest_of[32];
@@ -1230,28 +1260,16 @@ __global__ void __launch_bounds__(kCutThreads)
         *valid = bad ? 0 : 1;
         if (bad) atomicOr(status, kDevBadSeqlens);
         for (int i = 0; i < kCutThreads / 32; ++i) longest = max(longest, longest_of[i]);
-        const int shortest = static_cast<int>(sg.seg_tokens_each / kC);
-        const float all = static_cast<float>(chunks), units = static_cast<float>(H) / sms;
-        float best = kLaChunkUs * fmaxf(static_cast<float>(longest), all * units + 0.5f * longest);
-        int pick = 0;
-        for (int i = 0; i < static_cast<int>(sizeof(kCutLengths) / sizeof(int)); ++i) {
-            const float L = static_cast<float>(kCutLengths[i]);
-            if (kCutLengths[i] < shortest) continue;
-            if (kCutLengths[i] >= longest) break;
-            const float rows = ceilf((all / L + 0.5f * N) * units);
-            const float us = kLaCutUs + rows * (L * kLaCutChunkUs + kLaCutRowUs);
-            if (us < best) {
-                best = us;
-                pick = kCutLengths[i];
-            }
-        }
-        if (forced) pick = shortest;
-        length = !sg.starts || bad ? 0 : pick;
+        const float all = static_cast<float>(chunks);
+        const float uncut = kLaChunkUs * fmaxf(static_cast<float>(longest), all * H / sms + 0.5f * longest);
+        const int64_t width = sg.starts ? (chunks + sg.spans - 1) / sg.spans : 0;
+        const bool pays = kLaCutUs + static_cast<float>(width) * kLaCutChunkUs < uncut;
+        length = !sg.starts || bad || chunks == 0 ? 0 : forced > 0 ? forced : pays ? static_cast<int>(width) : 0;
         if (sg.starts) *sg.cut = length > 0;
     }
     __syncthreads();
-    const int L = length;
-    if (L == 0) {
+    const int W = length;
+    if (W == 0) {
         // The sequences by length, longest first (ties by index).
         if (sg.order && bad == 0)
             for (int64_t n = tid; n < N; n += kCutThreads) {
@@ -1265,13 +1283,14 @@ __global__ void __launch_bounds__(kCutThreads)
             }
         return;
     }
-    // The segment table: each sequence's first segment, and each segment's
-    // first token and sequence.
-    int64_t carry = 0;
+    // The sequences' chunks lie one after the other, cut every W chunks.  Every
+    // cut and every sequence that is not empty begins a part, in this order: a
+    // cut first where both are at one place (its part is empty then).
+    int64_t carry = 0;   // chunks, and in the upper half sequences, before
     for (int64_t base = 0; base < N; base += kCutThreads) {
         const int64_t n = base + tid;
-        const int64_t c = n < N ? (cu[n + 1] - cu[n] + kC - 1) / kC : 0, count = (c + L - 1) / L;
-        int64_t x = count;
+        const int64_t len = n < N ? cu[n + 1] - cu[n] : 0, count = (len + kC - 1) / kC, own = count | (len > 0 ? int64_t(1) << 32 : 0);
+        int64_t x = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -1285,20 +1304,34 @@ __global__ void __launch_bounds__(kCutThreads)
             if (i < warp) before += buf[i];
             all += buf[i];
         }
-        const int64_t first = before + x - count;
+        before += x - own;
         if (n < N) {
-            sg.seg_begin[n] = first;
-            for (int64_t j = 0; j < count; ++j) {
-                sg.seg_tokens[first + j] = cu[n] + j * L * kC;
-                sg.seg_seq[first + j] = n;
+            const int rank = static_cast<int>(before >> 32), x0 = static_cast<int>(before), x1 = x0 + static_cast<int>(count);
+            const int s0 = x0 / W, first = static_cast<int>(cu[n]);
+            sg.inner[n] = make_int2(-1, -1);
+            if (count > 0) {
+                auto part = [&](int from, int s) {      // of span s, from chunk `from`
+                    const int to = min(x1, (s + 1) * W), skip = (from - x0) * kC;
+                    const int tokens = min(static_cast<int>(len) - skip, (to - from) * kC);
+                    return make_int4(static_cast<int>(n), first + skip, tokens, (from > x0 ? kLaMid : 0) | (to == x1 ? kLaLast : 0));
+                };
+                if (s0 * W == x0) {
+                    sg.first[s0] = s0 + rank;
+                    sg.part[s0 + rank] = make_int4(static_cast<int>(n), first, 0, kLaMid);
+                }
+                sg.part[s0 + rank + 1] = part(x0, s0);
+                int s = s0 + 1;
+                for (; s * W < x1; ++s) {
+                    sg.first[s] = s + rank + 1;
+                    sg.part[s + rank + 1] = part(s * W, s);
+                }
+                sg.inner[n] = make_int2(s0 + 1, s);
             }
         }
         carry += all;
     }
-    if (tid == 0) {
-        sg.seg_begin[N] = carry;
-        sg.seg_tokens[carry] = T;
-    }
+    const int parted = static_cast<int>((static_cast<int>(carry) + W - 1) / W);
+    for (int s = parted + tid; s <= sg.spans; s += kCutThreads) sg.first[s] = parted + static_cast<int>(carry >> 32);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1346,7 +1379,7 @@ cudaError_t configure() {
 }  // namespace
 
 cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms, const LaSegments& sg,
-                          bool forced, int32_t* valid, int* status, cudaStream_t stream) {
+                          int forced, int32_t* valid, int* status, cudaStream_t stream) {
     la_cut_kernel<<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg, forced, valid, status);
     return cudaGetLastError();
 }
@@ -1355,9 +1388,11 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     Kernel p;
     p.a = a;
     p.sg = sg;
-    const int64_t units = (sg.starts ? sg.total : a.N) * a.H;
+    const int64_t spans = sg.starts ? sg.spans * a.H : 0;
+    // A packed batch's units or, cut, spans: one of the two comes to nothing.
+    const int64_t units = sg.starts && !sg.cut ? spans : a.N * a.H;
     if (units <= 0) return cudaSuccess;
-    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (units > 0x7fffffffLL || spans > 0x7fffffffLL) return cudaErrorInvalidValue;
     p.units = static_cast<uint32_t>(units);
     p.heads = static_cast<uint32_t>(a.H);
     CUtensorMap qm, km, vm, om;
@@ -1368,7 +1403,8 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         (e = encode_tokens(&vm, a.v, a.tokens, a.H, kC)) != cudaSuccess ||
         (e = encode_tokens(&om, a.out, a.tokens, a.H, 32)) != cudaSuccess)
         return e;
-    const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+    int64_t grid = units < sms ? units : sms;
+    if (sg.cut && grid < spans) grid = spans;
     // Programmatic dependence: a kernel is launched while the one before it
     // ends, and waits for it where it reads what that one wrote.
     cudaLaunchAttribute after;
@@ -1378,13 +1414,12 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     cfg.stream = stream;
     cfg.attrs = &after;
     if (sg.starts) {
-        cfg.gridDim = dim3(grid);
+        cfg.gridDim = dim3(static_cast<unsigned>(sg.cut ? spans : grid));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Smem<true>::kBytes;
         cfg.numAttrs = a.valid ? 1 : 0;
         if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
-        // Segments of a sequence: packed, one can have all but the others'.
-        const bool many = a.N * a.H >= 24, few = (sg.cut ? sg.total - a.N + 1 : sg.segs) <= 4 * kScanWarps;
+        const bool many = a.N * a.H >= 24, few = (sg.cut ? sg.spans : sg.segs) <= 4 * kScanWarps;
         const int64_t parts = a.N * a.H * (many || !few ? 128 : 64), ctas = many ? (parts + kScanWarps - 1) / kScanWarps : parts;
         const int64_t most = static_cast<int64_t>(sms) * (many ? 4 : few ? 3 : 2);
         cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
@@ -1396,7 +1431,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
             return e;
         *launches += 2;
     }
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Smem<false>::kBytes;
     cfg.numAttrs = sg.starts || a.valid ? 1 : 0;

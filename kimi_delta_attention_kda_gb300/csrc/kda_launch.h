@@ -212,32 +212,39 @@ struct LaArgs {
 constexpr int kLaChunk = 128;   // tokens of a chunk of kda_la_prefill
 // Costs of kda_la_prefill in microseconds, measured on GB300, for the choice of
 // a cut: a chunk of an uncut chain; with a cut, a chunk's outputs and what it
-// adds, with every SM loading; a further row of units on every SM; the further
-// launches.
+// adds, with every SM loading; the further launches and states.
 constexpr float kLaChunkUs = 2.7f;
 constexpr float kLaCutChunkUs = 5.0f;
-constexpr float kLaCutRowUs = 8.0f;
-constexpr float kLaCutUs = 18.f;
-// The cut of every sequence into segments of whole chunks (starts null: none).
+constexpr float kLaCutUs = 26.f;
+// A cut into spans of whole chunks, the same for every head (starts null: none).
+// Fixed layout: a span is a part of a sequence, all but each sequence's last of
+// seg_tokens_each tokens.  Packed: the sequences' chunks lie one after the other
+// and a span is so many of them, ends of sequences among them.
 struct LaSegments {
-    float* starts;             // [total][H][128][128]: what a segment adds, then its incoming state
-    float* decay;              // [total][H]: its decay in base 2
-    int64_t total;             // segments (packed: a bound)
-    int64_t segs;              // fixed layout: segments of each sequence
-    int64_t seg_tokens_each;   // tokens of each but a sequence's last (packed: of the shortest choice)
-    // Packed: whether there is a cut, each sequence's first segment, and each
-    // segment's first token and sequence, from launch_la_cut.
+    float* starts;             // [spans][H][128][128]: what the span before adds, then the state its first tokens meet
+    float* decay;              // [spans][H]: the decay over the span before, in base 2
+    float* inits;              // [N][H][128][128], or null: copies of initial states that final ones overwrite
+    int64_t spans;             // (packed: the most there can be)
+    int64_t segs;              // fixed layout: spans of each sequence
+    int64_t seg_tokens_each;
+    // Packed, from launch_la_cut: whether there is a cut; each span's first part
+    // (spans + 1); the parts, a sequence's tokens within a span; and each
+    // sequence's spans that it does not begin, first and end.
     int32_t* cut;
-    int64_t *seg_begin, *seg_tokens, *seg_seq;
+    int32_t* first;
+    int4* part;                // sequence, first token, tokens, kLaMid and kLaLast
+    int2* inner;               // (-1, -1) for an empty sequence
     // Packed, for an uncut batch: its sequences, longest first (or null).
     int32_t* order;
 };
+constexpr int kLaMid = 1;      // the part goes on from the span before
+constexpr int kLaLast = 2;     // the sequence ends with the part
 constexpr int64_t kMaxLaOrdered = 1024;
 // Packed: the offsets' check (*valid, as launch_varlen_meta) and, with
-// sg.starts, the choice of a cut and its table (forced: segments of
-// sg.seg_tokens_each tokens); without a cut, sg.order if it is there.
+// sg.starts, the choice of a cut and its tables (forced > 0: into spans of that
+// many chunks); without a cut, sg.order if it is there.
 cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms,
-                          const LaSegments& sg, bool forced, int32_t* valid, int* status,
+                          const LaSegments& sg, int forced, int32_t* valid, int* status,
                           cudaStream_t stream);
 // Adds the kernels it launches to *launches.
 cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream,

@@ -48,23 +48,20 @@ int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
     return KDA_OK;
 }
 
-// The cut of a call's sequences into segments (see kda_la_prefill).  A packed
-// batch's lengths are on the device, and so is its choice (launch_la_cut): here
-// room is made for the shortest segments it may choose.  Those are longer where
-// 4 chunks would leave more than 16 rows of units: finer ones balance nothing
-// more, and each segment's state takes 64 KB per head.
-constexpr int64_t kMinCutChunks = 4, kMaxCutChunks = 64, kMaxCutRows = 16;
+// The cut of a call's sequences into spans (see kda_la_prefill).  A packed
+// batch's lengths are on the device, and so is its choice (launch_la_cut).
 constexpr int64_t kMinPackedChunks = 16;   // fewer in all: not worth the launches
-// Fixed layout, one unit to an SM: a chunk of both passes (T=8192, H=32 in 4
-// segments of 16 chunks 105 us, H=6 in 22 of 3 37 us).
-constexpr double kLaFixedCutChunkUs = 5.5;
+// Fixed layout, one span of a head to an SM: a chunk of both passes (T=8192,
+// H=32 in 4 segments of 16 chunks 105 us, H=6 in 22 of 3 37 us), and the rest.
+constexpr double kLaFixedCutChunkUs = 5.5, kLaFixedCutUs = 18;
 
 struct LaCut {
-    int64_t chunks = 0;        // chunks of a segment (0: no cut; packed: of the shortest)
-    int64_t segs = 0;          // fixed: segments of each sequence; packed: a bound on all
-    int64_t total = 0;
+    int64_t chunks = 0;        // chunks of a span (packed: when forced)
+    int64_t segs = 0;          // fixed: spans of each sequence
+    int64_t spans = 0;         // in all (0: no cut; packed: the most there can be)
     bool order = false;        // packed: an uncut batch's sequences go longest first
-    int64_t bytes = 0;         // starts, decays, the packed segment table and the order
+    int64_t init_bytes = 0;    // when final states overwrite initial ones (not in bytes)
+    int64_t bytes = 0;         // states, decays, the packed tables and the order
 };
 
 LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64_t forced) {
@@ -81,16 +78,16 @@ LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64
         if (c.chunks > (1 << 23)) c.chunks = 1 << 23;   // 2^30 tokens
     }
     if (pl.packed) {
-        if (forced <= 0) {
+        if (forced > 0) {
+            c.spans = (pl.tokens / kLaChunk + pl.N) / c.chunks + 1;
+        } else {
             // (A cut costs every SM its part of the chunks; without one, one
             // sequence is the most that a batch can wait for.)
+            c.spans = sms / H;
             const double part = static_cast<double>(H) / sms, uncut = part + 0.5 > 1. ? part + 0.5 : 1.;
-            if (pl.tokens < kMinPackedChunks * kLaChunk || kLaCutChunkUs * part >= kLaChunkUs * uncut) return none;
-            c.chunks = kMinCutChunks;
-            while (c.chunks < kMaxCutChunks && pl.tokens / (c.chunks * kLaChunk) * H > kMaxCutRows * sms) c.chunks *= 2;
+            if (pl.tokens < kMinPackedChunks * kLaChunk || c.spans < 2 || kLaCutChunkUs >= kLaChunkUs * uncut * c.spans)
+                return none;
         }
-        c.segs = pl.tokens / (c.chunks * kLaChunk) + pl.N;
-        c.total = c.segs;
     } else {
         const int64_t seq_chunks = (T + kLaChunk - 1) / kLaChunk;
         if (forced <= 0) {
@@ -98,15 +95,16 @@ LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64
             const int64_t want = sms / units;
             c.chunks = (seq_chunks + want - 1) / want;
             const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
-            const double cut = kLaCutUs + c.chunks * kLaFixedCutChunkUs;
+            const double cut = kLaFixedCutUs + c.chunks * kLaFixedCutChunkUs;
             if (segs < 2 || cut >= seq_chunks * kLaChunkUs) return none;
         }
         c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
-        c.total = c.segs * pl.N;
+        c.spans = c.segs * pl.N;
     }
-    if (units > 0x7fffffffLL / 128 || c.total * H > 0x7fffffffLL || c.total > kMaxElems / (H * kStateElems * 4)) return none;
-    c.bytes += align256(c.total * H * kStateElems * 4) + align256(c.total * H * 4);
-    if (pl.packed) c.bytes += align256(8 * (pl.N + 1)) + 2 * align256(8 * (c.segs + 1));
+    if (units > 0x7fffffffLL / 128 || c.spans > 0x7fffffffLL / H || c.spans > kMaxElems / (H * kStateElems * 4)) return none;
+    c.init_bytes = units * kStateElems * 4;
+    c.bytes += align256(c.spans * H * kStateElems * 4) + align256(c.spans * H * 4);
+    if (pl.packed) c.bytes += align256(16 * (pl.N + c.spans)) + align256(4 * (c.spans + 1)) + align256(8 * pl.N);
     return c;
 }
 
@@ -197,9 +195,10 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
     a.status = d.status;
     const LaCut cut = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks);
     uint8_t* ws = nullptr;
-    if (pl.meta_bytes + cut.bytes > 0 &&
-        cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), static_cast<size_t>(pl.meta_bytes + cut.bytes),
-                                d.pool, stream) != cudaSuccess) {
+    const bool in_place = init_state && init_state == final_state;
+    const int64_t ws_bytes = pl.meta_bytes + cut.bytes + (in_place ? cut.init_bytes : 0);
+    if (ws_bytes > 0 &&
+        cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), static_cast<size_t>(ws_bytes), d.pool, stream) != cudaSuccess) {
         cudaGetLastError();
         return KDA_ERR_CUDA;
     }
@@ -210,26 +209,28 @@ extern "C" int kda_la_prefill(const void* q, const void* k, const void* v, const
         at += align256(bytes);
         return p;
     };
-    if (cut.chunks > 0) {
-        sg.starts = reinterpret_cast<float*>(take(cut.total * H * kStateElems * 4));
-        sg.decay = reinterpret_cast<float*>(take(cut.total * H * 4));
-        sg.total = cut.total;
+    if (cut.spans > 0) {
+        sg.starts = reinterpret_cast<float*>(take(cut.spans * H * kStateElems * 4));
+        sg.decay = reinterpret_cast<float*>(take(cut.spans * H * 4));
+        if (in_place) sg.inits = reinterpret_cast<float*>(take(cut.init_bytes));
+        sg.spans = cut.spans;
         sg.segs = cut.segs;
         sg.seg_tokens_each = cut.chunks * kLaChunk;
     }
     if (pl.packed) {
         int32_t* valid = reinterpret_cast<int32_t*>(ws);
-        if (cut.chunks > 0) {
+        if (cut.spans > 0) {
             sg.cut = valid + 1;
-            sg.seg_begin = reinterpret_cast<int64_t*>(take(8 * (B + 1)));
-            sg.seg_tokens = reinterpret_cast<int64_t*>(take(8 * (cut.segs + 1)));
-            sg.seg_seq = reinterpret_cast<int64_t*>(take(8 * (cut.segs + 1)));
+            sg.part = reinterpret_cast<int4*>(take(16 * (B + cut.spans)));
+            sg.first = reinterpret_cast<int32_t*>(take(4 * (cut.spans + 1)));
+            sg.inner = reinterpret_cast<int2*>(take(8 * B));
         }
         if (cut.order) sg.order = reinterpret_cast<int32_t*>(take(4 * B));
         a.cu_seqlens = cu_seqlens;
         // With nothing to decide, and few offsets, the prefill kernel checks them itself.
-        if (cut.chunks > 0 || cut.order || B > kMaxLaOrdered) {
-            if (launch_la_cut(cu_seqlens, B, T, H, d.sms, sg, d.seg_chunks > 0, valid, d.status, stream) != cudaSuccess) {
+        if (cut.spans > 0 || cut.order || B > kMaxLaOrdered) {
+            if (launch_la_cut(cu_seqlens, B, T, H, d.sms, sg, static_cast<int>(cut.chunks), valid, d.status, stream) !=
+                cudaSuccess) {
                 rc = KDA_ERR_CUDA;
             } else {
                 add_launches(1);
@@ -255,7 +256,8 @@ extern "C" int kda_la_plan_segments(int64_t B, int64_t T, int64_t H, int packed,
     DeviceView d;
     rc = device_view(&d);
     if (rc != KDA_OK) return rc;
-    *segs = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks).segs;
+    const LaCut cut = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks);
+    *segs = pl.packed ? cut.spans : cut.segs;
     return KDA_OK;
 }
 
@@ -270,7 +272,8 @@ extern "C" int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packe
         d.sms = 152;
         segment_settings(&d.segments, &d.seg_chunks);
     }
-    *bytes = pl.meta_bytes + cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks).bytes;
+    const LaCut cut = cut_la(pl, T, H, d.sms, d.segments, d.seg_chunks);
+    *bytes = pl.meta_bytes + cut.bytes + cut.init_bytes;
     return KDA_OK;
 }
 

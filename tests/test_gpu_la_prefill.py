@@ -186,6 +186,26 @@ def test_state_in_place_and_no_final(kda):
     assert f3 is None and torch.equal(o3.cpu(), out)
 
 
+@pytest.mark.parametrize("seg", [0, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cu", [None, [0, 40, 40, 5040, 5110]])
+def test_state_in_place_with_segments(kda, cu, dtype, seg):
+    T = 5110 if cu else 4100
+    d, rnd = inputs(1, T, 4, 2, seed=47, low=-0.02)
+    init = rnd(len(cu) - 1 if cu else 1, 4, D, D).to(dtype)
+    dev = {key: x.cuda() for key, x in d.items()}
+    kda.set_segments(True, seg)
+    try:
+        out, fin = run(kda, d, init, cu)
+        for _ in range(3):
+            st = init.cuda()
+            o2, _ = kda.la_prefill(dev["q"], dev["k"], dev["v"], dev["g"], init_state=st, final_state=st,
+                                   cu_seqlens=None if cu is None else torch.tensor(cu, device="cuda"))
+            assert torch.equal(st.cpu(), fin) and torch.equal(o2.cpu(), out)
+    finally:
+        kda.set_segments(True, 0)
+
+
 def test_no_tokens(kda):
     init = torch.randn(2, 3, D, D)
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
