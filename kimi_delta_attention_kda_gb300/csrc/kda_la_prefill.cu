@@ -1217,21 +1217,23 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
 // the lengths, whether to cut.  Without a cut the longest sequence is the least
 // it takes; with one, every SM has a span of W chunks, and takes kLaCutChunkUs
 // for each (kda_launch.h has the costs).
-constexpr int kCutThreads = 1024;
+constexpr int kCutThreads = 1024, kCutThreadsFew = 128;   // few: up to 128 sequences
 
+template <int kThreads>
 __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* buf) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = buf[threadIdx.x & 31];
+    x = (threadIdx.x & 31) < kThreads / 32 ? buf[threadIdx.x & 31] : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-__global__ void __launch_bounds__(kCutThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
     la_cut_kernel(const int64_t* cu, int64_t N, int64_t T, int64_t H, int sms, LaSegments sg, int forced, int32_t* valid,
                   int* status) {
     __shared__ int64_t buf[32];
@@ -1241,7 +1243,7 @@ __global__ void __launch_bounds__(kCutThreads)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t bad = tid == 0 && (cu[0] != 0 || cu[N] != T), chunks = 0;
     int longest = 0;
-    for (int64_t n = tid; n < N; n += kCutThreads) {
+    for (int64_t n = tid; n < N; n += kThreads) {
         const int64_t len = cu[n + 1] - cu[n];
         if (len < 0 || cu[n] < 0 || cu[n + 1] > T) {
             bad = 1;
@@ -1251,15 +1253,15 @@ __global__ void __launch_bounds__(kCutThreads)
         chunks += c;
         longest = max(longest, c);
     }
-    bad = block_sum(bad, buf);
-    chunks = block_sum(chunks, buf);
+    bad = block_sum<kThreads>(bad, buf);
+    chunks = block_sum<kThreads>(chunks, buf);
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) longest_of[warp] = longest;
     __syncthreads();
     if (tid == 0) {
         *valid = bad ? 0 : 1;
         if (bad) atomicOr(status, kDevBadSeqlens);
-        for (int i = 0; i < kCutThreads / 32; ++i) longest = max(longest, longest_of[i]);
+        for (int i = 0; i < kThreads / 32; ++i) longest = max(longest, longest_of[i]);
         const float all = static_cast<float>(chunks);
         const float uncut = kLaChunkUs * fmaxf(static_cast<float>(longest), all * H / sms + 0.5f * longest);
         const int64_t width = sg.starts ? (chunks + sg.spans - 1) / sg.spans : 0;
@@ -1272,7 +1274,7 @@ __global__ void __launch_bounds__(kCutThreads)
     if (W == 0) {
         // The sequences by length, longest first (ties by index).
         if (sg.order && bad == 0)
-            for (int64_t n = tid; n < N; n += kCutThreads) {
+            for (int64_t n = tid; n < N; n += kThreads) {
                 const int64_t len = cu[n + 1] - cu[n];
                 int rank = 0;
                 for (int64_t m = 0; m < N; ++m) {
@@ -1287,7 +1289,7 @@ __global__ void __launch_bounds__(kCutThreads)
     // cut and every sequence that is not empty begins a part, in this order: a
     // cut first where both are at one place (its part is empty then).
     int64_t carry = 0;   // chunks, and in the upper half sequences, before
-    for (int64_t base = 0; base < N; base += kCutThreads) {
+    for (int64_t base = 0; base < N; base += kThreads) {
         const int64_t n = base + tid;
         const int64_t len = n < N ? cu[n + 1] - cu[n] : 0, count = (len + kC - 1) / kC, own = count | (len > 0 ? int64_t(1) << 32 : 0);
         int64_t x = own;
@@ -1300,7 +1302,7 @@ __global__ void __launch_bounds__(kCutThreads)
         if (lane == 31) buf[warp] = x;
         __syncthreads();
         int64_t before = carry, all = 0;
-        for (int i = 0; i < kCutThreads / 32; ++i) {
+        for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += buf[i];
             all += buf[i];
         }
@@ -1331,7 +1333,7 @@ __global__ void __launch_bounds__(kCutThreads)
         carry += all;
     }
     const int parted = static_cast<int>((static_cast<int>(carry) + W - 1) / W);
-    for (int s = parted + tid; s <= sg.spans; s += kCutThreads) sg.first[s] = parted + static_cast<int>(carry >> 32);
+    for (int s = parted + tid; s <= sg.spans; s += kThreads) sg.first[s] = parted + static_cast<int>(carry >> 32);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1380,7 +1382,10 @@ cudaError_t configure() {
 
 cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tokens, int64_t H, int sms, const LaSegments& sg,
                           int forced, int32_t* valid, int* status, cudaStream_t stream) {
-    la_cut_kernel<<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg, forced, valid, status);
+    if (n_seqs <= kCutThreadsFew)
+        la_cut_kernel<kCutThreadsFew><<<1, kCutThreadsFew, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg, forced, valid, status);
+    else
+        la_cut_kernel<kCutThreads><<<1, kCutThreads, 0, stream>>>(cu_seqlens, n_seqs, tokens, H, sms, sg, forced, valid, status);
     return cudaGetLastError();
 }
 
