@@ -25,7 +25,8 @@
 // P and the S operand are rounded to BF16 once each: their error stays in the
 // BF16 output they go to, and S itself is not touched by it.
 //
-// One CTA per SM walks (sequence or segment, head) units.  Warps: 8 key (K'),
+// One CTA per SM walks its units, a sequence's tokens or a part of them for one
+// head.  Warps: 8 key (K'),
 // 8 state (S), 4 score (P), 4 query (Q'), 4 output (O), one each for the
 // loads, the MMA issue and the decay sums.  Tensor memory columns: D1 and P
 // [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32
@@ -113,18 +114,20 @@ struct Kernel {
 };
 // What a CTA does: units of (sequence, head), every grid's width one; of
 // (segment, head) for a fixed layout's cut; and for a packed batch's, decided on
-// the device, the parts of its span, for one head.
+// the device, the parts of its span, for one head.  The layout is a constant:
+// with both in one kernel every role's code is longer, and a chunk slower by 1%.
+template <bool kStates_, bool kPacked_>
 struct Work {
+    static constexpr bool kStates = kStates_, kPacked = kPacked_;
     const LaArgs& a;
     const LaSegments& sg;
     const uint32_t& heads;
     uint32_t base, step, end;
     bool cut;
-    __device__ __forceinline__ Work(const Kernel& p, bool states)
+    __device__ __forceinline__ explicit Work(const Kernel& p)
         : a(p.a), sg(p.sg), heads(p.heads), base(0), step(gridDim.x), end(p.units), cut(p.sg.starts) {
-        if (sg.cut) {
-            cut = *sg.cut != 0;
-            end = static_cast<uint32_t>(a.N) * heads;
+        if (kPacked) {
+            cut = sg.cut && *sg.cut != 0;
             if (cut) {
                 const uint32_t s = blockIdx.x / heads;
                 step = 1;
@@ -133,17 +136,17 @@ struct Work {
                     base = sg.first[s];
                     end = sg.first[s + 1];
                     // Only a span's last part can go on in the next.
-                    if (states && base < end) base = end - 1;
+                    if (kStates && base < end) base = end - 1;
                 }
             }
         }
     }
     // Of an uncut packed batch: its sequences, longest first (or null).
-    __device__ __forceinline__ const int32_t* order() const { return cut ? nullptr : sg.order; }
+    __device__ __forceinline__ const int32_t* order() const { return !kPacked || cut ? nullptr : sg.order; }
     // The CTA's i-th unit: in rows of the grid's width, where the units come
     // longest first every other row backwards.
     __device__ __forceinline__ uint32_t unit(uint32_t i) const {
-        const uint32_t at = step > 1 ? blockIdx.x : 0;
+        const uint32_t at = !kPacked || step > 1 ? blockIdx.x : 0;
         return base + i * step + ((i & 1) && order() ? step - 1 - at : at);
     }
     __device__ __forceinline__ uint32_t rows() const { return (end - base + step - 1) / step; }
@@ -157,10 +160,10 @@ struct Unit {
     bool last;          // writes the final state
     int nch;
 };
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
     Unit w;
-    if (p.cut && p.sg.cut) {
+    if (Work::kPacked && p.cut) {
         const int4 part = p.sg.part[u];
         w.n = part.x;
         w.h = blockIdx.x % p.heads;
@@ -175,7 +178,11 @@ __device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
         w.slot = u;
         w.mid = false;
         w.last = true;
-        if (p.cut) {
+        if (Work::kPacked) {
+            w.n = p.order() ? p.order()[s] : s;
+            w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
+            w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
+        } else if (p.cut) {
             const uint32_t segs = static_cast<uint32_t>(p.sg.segs);
             const int each = static_cast<int>(p.sg.seg_tokens_each), per = static_cast<int>(p.a.tokens_per_seq);
             w.n = s / segs;
@@ -185,46 +192,44 @@ __device__ __forceinline__ Unit unit_at(const Work& p, uint32_t u) {
             w.last = j + 1 == static_cast<int>(segs);
             w.len = w.last ? per - j * each : each;
         } else {
-            w.n = p.order() ? p.order()[s] : s;
-            if (p.a.cu_seqlens) {
-                w.tok0 = static_cast<int>(p.a.cu_seqlens[w.n]);
-                w.len = static_cast<int>(p.a.cu_seqlens[w.n + 1]) - w.tok0;
-            } else {
-                w.len = static_cast<int>(p.a.tokens_per_seq);
-                w.tok0 = s * w.len;
-            }
+            w.n = s;
+            w.len = static_cast<int>(p.a.tokens_per_seq);
+            w.tok0 = s * w.len;
         }
     }
-    if (kStates && w.last) w.len = 0;     // nothing of the sequence follows
+    if (Work::kStates && w.last) w.len = 0;     // nothing of the sequence follows
     w.nch = (w.len + kC - 1) / kC;
     return w;
 }
 
 // A chunk's place in the rings: the chunk's number on this CTA, its stage and
 // the parity of the stage's use.
+// (With two stages both are bits of the number: fewer registers to keep.)
 template <int kStages>
 struct Pos {
-    uint32_t it = 0, st = 0;
-    int s = 0;
+    uint32_t it = 0, st_ = 0;
+    int s_ = 0;
     __device__ __forceinline__ void next() {
         ++it;
-        if (++s == kStages) {
-            s = 0;
-            st ^= 1u;
+        if (kStages != 2 && ++s_ == kStages) {
+            s_ = 0;
+            st_ ^= 1u;
         }
     }
+    __device__ __forceinline__ int s() const { return kStages == 2 ? static_cast<int>(it & 1u) : s_; }
+    __device__ __forceinline__ uint32_t st() const { return kStages == 2 ? (it >> 1) & 1u : st_; }
     __device__ __forceinline__ uint32_t ph() const { return it & 1u; }            // once a chunk
     __device__ __forceinline__ uint32_t dec_ph() const { return (it >> 1) & 1u; }   // two buffers
 };
 
 // f(unit, chunk, valid tokens, place) for every chunk of this CTA, until it fails.
-template <bool kStates, class F>
+template <class Work, class F>
 __device__ __forceinline__ void walk(const Work& p, F f) {
-    Pos<Smem<kStates>::kStages> x;
+    Pos<Smem<Work::kStates>::kStages> x;
 #pragma unroll 1
     for (uint32_t i = 0; i < p.rows(); ++i) {
         if (p.unit(i) >= p.end) continue;
-        const Unit w = unit_at<kStates>(p, p.unit(i));
+        const Unit w = unit_at(p, p.unit(i));
 #pragma unroll 1
         for (int c = 0; c < w.nch; ++c) {
             if (!f(w, c, min(kC, w.len - c * kC), x)) return;
@@ -314,22 +319,23 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
 }
 
 // --------------------------------------------------------------- load warp
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ void load_role(const Work& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap, uint8_t* smem, const Bars& b, int lane) {
+    constexpr bool kStates = Work::kStates;
     using M = Smem<kStates>;
     constexpr int n = M::kStages, tiles = kStates ? 2 : 3;
     const uint32_t group = static_cast<uint32_t>(p.a.H / p.a.Hk);
     uint32_t issued = 0;   // tiles under way or done, K, V, Q, K, ..
-    walk<kStates>(p, [&](const Unit& w, int c, int, const Pos<n>& x) {
+    walk(p, [&](const Unit& w, int c, int, const Pos<n>& x) {
         const int y = w.tok0 + c * kC;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             // (The barriers and tiles of K, V and Q follow one another.)
-            if (x.it >= n && !wait_phase(&b.empty_k[t * n + x.s], x.st ^ 1u, p.a.status)) return false;
+            if (x.it >= n && !wait_phase(&b.empty_k[t * n + x.s()], x.st() ^ 1u, p.a.status)) return false;
             if (lane == 0) {
-                uint64_t* full = &b.full_k[t * n + x.s];
-                uint8_t* dst = smem + (t * n + x.s) * kTile;
+                uint64_t* full = &b.full_k[t * n + x.s()];
+                uint8_t* dst = smem + (t * n + x.s()) * kTile;
                 const CUtensorMap* map = t == 0 ? kmap : t == 1 ? vmap : qmap;
                 const int col = static_cast<int>(t == 1 ? w.h : w.h / group) * kHeadDim;
                 mbar_arrive_expect_tx(full, kTile);
@@ -353,12 +359,13 @@ __device__ __forceinline__ void load_role(const Work& p, const CUtensorMap* qmap
 // The decays are single words, a row of heads apart: on a loaded memory
 // system a load takes 3 us and more, so the lines are brought to L2 four
 // chunks ahead and the words one chunk ahead.
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ void decay_role(const Work& p, uint8_t* smem, const Bars& b, int lane) {
+    constexpr bool kStates = Work::kStates;
     using M = Smem<kStates>;
     constexpr int kAhead = 4;
     float next[4] = {0.f, 0.f, 0.f, 0.f};
-    walk<kStates>(p, [&](const Unit& w, int c, int valid, const Pos<M::kStages>& at) {
+    walk(p, [&](const Unit& w, int c, int valid, const Pos<M::kStages>& at) {
         const uint32_t buf = at.it & 1u;
         const int64_t stride = p.a.g_stride;
         // This lane's four tokens of chunk i: up to `left` of them are there.
@@ -431,36 +438,37 @@ __device__ __forceinline__ void decay_role(const Work& p, uint8_t* smem, const B
 // Per chunk: D1, K'^T V in quarters of 32 tokens, Q' S^T, P V.  D1 overwrites
 // the P of the chunk before, whose product it waits for; P and Q' are formed
 // while K'^T V runs, and the next chunk's state between Q' S^T and its K'^T V.
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ void mma_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int lane) {
+    constexpr bool kStates = Work::kStates;
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
     const volatile uint32_t* flag = reinterpret_cast<const volatile uint32_t*>(smem + M::kFlag);
     const bool leader = elect_one();
     const uint32_t base = (smem_u32(smem) >> 4) & 0x3FFFu, ds = base + (M::kS >> 4) + kLeadMn;
-    walk<kStates>(p, [&](const Unit&, int c, int, const Pos<n>& x) {
+    walk(p, [&](const Unit&, int c, int, const Pos<n>& x) {
         const uint32_t ph = x.ph(), pv = ph ^ 1u, it = x.it;
-        const uint32_t tile = base + x.s * (kTile >> 4);
+        const uint32_t tile = base + x.s() * (kTile >> 4);
         const uint32_t dk = tile + (M::kK >> 4) + kLeadK, dv = tile + (M::kV >> 4) + kLeadMn, dq = tile + (M::kQ >> 4) + kLeadK;
-        if (!wait_phase(&b.full_k[x.s], x.st, status)) return false;
+        if (!wait_phase(&b.full_k[x.s()], x.st(), status)) return false;
         if (!kStates) {
-            if (!wait_phase(&b.full_q[x.s], x.st, status)) return false;
+            if (!wait_phase(&b.full_q[x.s()], x.st(), status)) return false;
             if (it > 0) {
                 if (!wait_phase(b.o_done, pv, status)) return false;
                 // P is read once more where V is not finite: until V's stage is released.
-                if (flag[pv] == it && !wait_phase(&b.empty_v[x.s ^ 1], x.s ? x.st : x.st ^ 1u, status)) return false;
+                if (flag[pv] == it && !wait_phase(&b.empty_v[x.s() ^ 1], x.s() ? x.st() : x.st() ^ 1u, status)) return false;
             }
             tc::fence_after_sync();
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ss<kIdesc>(tmem + kColD1, dq + k_step(k), dk + k_step(k), k > 0);
                 tc::commit(b.qk);
-                tc::commit(&b.empty_k[x.s]);
+                tc::commit(&b.empty_k[x.s()]);
             }
             __syncwarp();
         }
-        if (!wait_phase(&b.full_v[x.s], x.st, status) || !wait_phase(b.s_ready, ph, status)) return false;
+        if (!wait_phase(&b.full_v[x.s()], x.st(), status) || !wait_phase(b.s_ready, ph, status)) return false;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             if (!wait_phase(&b.kp_full[q & 1], q >> 1, status)) return false;   // two uses a chunk
@@ -476,7 +484,7 @@ __device__ __forceinline__ void mma_role(const Work& p, uint8_t* smem, const Bar
                 tc::commit(&b.kp_empty[q & 1]);
                 if (q == 3) {
                     tc::commit(b.z_done);
-                    if (kStates) tc::commit(&b.empty_v[x.s]);
+                    if (kStates) tc::commit(&b.empty_v[x.s()]);
                 }
             }
             __syncwarp();
@@ -522,8 +530,9 @@ __device__ __forceinline__ void st_16x8(uint32_t taddr, uint32_t a, uint32_t b, 
                  ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ void key_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wk, int lane) {
+    constexpr bool kStates = Work::kStates;
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
@@ -532,21 +541,21 @@ __device__ __forceinline__ void key_role(const Work& p, uint8_t* smem, const Bar
                           (((kg & 7) ^ (lane & 7)) << 4);
     const uint32_t dst = tmem + (static_cast<uint32_t>(32 * (wk & 3)) << 16) + kColK + 8 * half;
     const int tok = 16 * half + 2 * (lane & 3);
-    walk<kStates>(p, [&](const Unit&, int, int valid, const Pos<n>& x) {
+    walk(p, [&](const Unit&, int, int valid, const Pos<n>& x) {
         const uint32_t buf = x.it & 1u;
-        if (!wait_phase(&b.full_k[x.s], x.st, status) || !wait_phase(&b.dec_full[buf], x.dec_ph(), status)) return false;
+        if (!wait_phase(&b.full_k[x.s()], x.st(), status) || !wait_phase(&b.dec_full[buf], x.dec_ph(), status)) return false;
         if (valid < kC) {
             // Rows behind the sequence's end: another sequence's tokens, or
             // anything.  V's are cleared here, K's below.
-            uint8_t* V = smem + M::kV + x.s * kTile;
-            if (!wait_phase(&b.full_v[x.s], x.st, status)) return false;
+            uint8_t* V = smem + M::kV + x.s() * kTile;
+            if (!wait_phase(&b.full_v[x.s()], x.st(), status)) return false;
 #pragma unroll 1
             for (int r = valid + wk; r < kC; r += kKeyWarps)
                 if (lane < 16)
                     *reinterpret_cast<uint4*>(V + (lane >> 3) * kSlab + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
         }
-        const uint32_t src = src0 + x.s * kTile;
+        const uint32_t src = src0 + x.s() * kTile;
         const float* W = reinterpret_cast<const float*>(smem + M::kW) + buf * kC + tok;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -588,7 +597,7 @@ __device__ __forceinline__ void key_role(const Work& p, uint8_t* smem, const Bar
             tc::fence_before_sync();
             arrive_warp(&b.kp_full[q & 1], lane);
         }
-        stage_release(&b.empty_k[x.s], lane);
+        stage_release(&b.empty_k[x.s()], lane);
         arrive_warp(&b.dec_empty[buf], lane);
         return true;
     });
@@ -667,8 +676,9 @@ __device__ __noinline__ void state_out(void* base, bool f32, int64_t at, uint32_
     }
 }
 
-template <bool kStates>
+template <class Work>
 __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int ws, int lane) {
+    constexpr bool kStates = Work::kStates;
     using M = Smem<kStates>;
     constexpr int n = M::kStages;
     int* status = p.a.status;
@@ -681,27 +691,29 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
 #pragma unroll 1
     for (uint32_t row_i = 0; row_i < p.rows(); ++row_i) {
         if (p.unit(row_i) >= p.end) continue;
-        const Unit w = unit_at<kStates>(p, p.unit(row_i));
-        const int64_t at = (static_cast<int64_t>(w.n) * p.a.H + w.h) * (kHeadDim * kHeadDim) + lane_at;
-        const int64_t seg_at = static_cast<int64_t>(w.slot) * (kHeadDim * kHeadDim) + lane_at;
-        // (Where final states overwrite the initial ones, a sequence's last part
-        // may be done before its first has begun.)
-        const bool scanned = w.mid || (p.sg.inits && !w.last);
-        const void* init = w.mid ? static_cast<const void*>(p.sg.starts) : scanned ? p.sg.inits : p.a.init_state;
-        const bool init_f32 = scanned || p.a.state_f32;
-        const int64_t init_at = w.mid ? seg_at : at;
-        const bool final = !kStates && w.last && p.a.final_state;
+        const Unit w = unit_at(p, p.unit(row_i));
+        // (Offsets are formed where they are used: held over the chunks they cost
+        // spilled registers.)
+        auto own_at = [&] { return (static_cast<int64_t>(w.n) * p.a.H + w.h) * (kHeadDim * kHeadDim) + lane_at; };
+        auto slot_at = [&](uint32_t slot) { return static_cast<int64_t>(slot) * (kHeadDim * kHeadDim) + lane_at; };
         if (w.nch == 0) {
-            if (final)
+            if (!kStates && w.last && p.a.final_state)
 #pragma unroll 1
                 for (int i = 0; i < 64; ++i)
-                    store_elem(p.a.final_state, p.a.state_f32, at + i * kHeadDim, load_elem(init, init_f32, init_at + i * kHeadDim));
+                    store_elem(p.a.final_state, p.a.state_f32, own_at() + i * kHeadDim,
+                               load_elem(p.a.init_state, p.a.state_f32, own_at() + i * kHeadDim));
             continue;
         }
         if (!kStates) {
+            // (Where final states overwrite the initial ones, a sequence's last
+            // part may be done before its first has begun.)
+            const bool copied = p.sg.inits && !w.last;
             // (The chain over the spans may still be running.)
-            if (scanned) asm volatile("griddepcontrol.wait;" ::: "memory");
-            state_in(init, init_f32, init_at, scol);
+            if (w.mid || copied) asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (w.mid)
+                state_in(p.sg.starts, true, slot_at(w.slot), scol);
+            else
+                state_in(copied ? p.sg.inits : p.a.init_state, copied || p.a.state_f32, own_at(), scol);
         }
         float total = 0.f;
 #pragma unroll 1
@@ -759,7 +771,7 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
                 for (int i = 0; i < 16; ++i) chk = fmaf(__uint_as_float(z[i]), 0.f, chk);
                 if (__any_sync(0xffffffffu, !(chk == 0.f))) {
                     // The flag of a chunk is its number + 1, so none has to be cleared.
-                    if (clear_not_finite(smem + M::kV + x.s * kTile + half * kSlab, 2 * (ws & 3), lane) && lane == 0)
+                    if (clear_not_finite(smem + M::kV + x.s() * kTile + half * kSlab, 2 * (ws & 3), lane) && lane == 0)
                         flag[buf] = x.it + 1;
                     fence_proxy_async_smem();
                     __threadfence_block();
@@ -769,10 +781,10 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
         }
         if (kStates) {
             // (For the next span of this head.)
-            state_out(p.sg.starts, true, seg_at + static_cast<int64_t>(p.heads) * (kHeadDim * kHeadDim), scol);
+            state_out(p.sg.starts, true, slot_at(w.slot + p.heads), scol);
             if (ws == 0 && lane == 0) p.sg.decay[w.slot + p.heads] = total;
-        } else if (final) {
-            state_out(p.a.final_state, p.a.state_f32, at, scol);
+        } else if (w.last && p.a.final_state) {
+            state_out(p.a.final_state, p.a.state_f32, own_at(), scol);
         }
         tc::fence_before_sync();
     }
@@ -783,11 +795,12 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
 // before the row's own take 2^n_i exp(-G_j) as a row factor to the end of the
 // block times a column factor from there, both at most 1: one exponential
 // per row and block instead of one per score.
+template <class Work>
 __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const Bars& b, uint32_t tmem, int wp, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wp) << 16) + kColD1;
-    walk<false>(p, [&](const Unit&, int, int, const Pos<2>& at) {
+    walk(p, [&](const Unit&, int, int, const Pos<2>& at) {
         const uint32_t buf = at.it & 1u;
         const float* G = reinterpret_cast<const float*>(smem + M::kG) + buf * kC;
         const float4* Cf = reinterpret_cast<const float4*>(smem + M::kCf + buf * 96 * 4);
@@ -849,18 +862,19 @@ __device__ __forceinline__ void score_role(const Work& p, uint8_t* smem, const B
 // ------------------------------------------------------------- query warps
 // Warp wq: rows (tokens) 32 wq .. + 31, one per lane.  Q' in place, once D1
 // has been formed from Q.
+template <class Work>
 __device__ __forceinline__ void query_role(const Work& p, uint8_t* smem, const Bars& b, int wq, int lane) {
     using M = Smem<false>;
     int* status = p.a.status;
     const int row = 32 * wq + lane;
-    walk<false>(p, [&](const Unit&, int, int, const Pos<2>& at) {
+    walk(p, [&](const Unit&, int, int, const Pos<2>& at) {
         const uint32_t buf = at.it & 1u;
-        uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
+        uint8_t* Qrow = smem + M::kQ + at.s() * kTile + row * 128;
         if (!wait_phase(&b.dec_full[buf], at.dec_ph(), status)) return false;
         const float e = ex2(floorf(reinterpret_cast<const float*>(smem + M::kG)[buf * kC + row]));   // 2^n_i
         arrive_warp(&b.dec_empty[buf], lane);
         const __nv_bfloat162 e2 = __bfloat162bfloat162(__float2bfloat16_rn(e));
-        if (!wait_phase(&b.full_q[at.s], at.st, status) || !wait_phase(b.qk, at.ph(), status)) return false;
+        if (!wait_phase(&b.full_q[at.s()], at.st(), status) || !wait_phase(b.qk, at.ph(), status)) return false;
 #pragma unroll 1
         for (int sl = 0; sl < 2; ++sl, Qrow += kSlab) {
             uint4 v[8];
@@ -916,6 +930,7 @@ __device__ __noinline__ void add_not_finite(uint32_t trow, const __nv_bfloat16* 
     tc::wait_st();
 }
 
+template <class Work>
 __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* omap, uint8_t* smem, const Bars& b,
                                             uint32_t tmem, int we, int lane) {
     using M = Smem<false>;
@@ -924,8 +939,8 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
     const int row = 32 * we + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * we) << 16);
     arrive_warp(b.qs_ready, lane);   // O is free for the first chunk
-    walk<false>(p, [&](const Unit& w, int c, int valid, const Pos<2>& at) {
-        uint8_t* Qrow = smem + M::kQ + at.s * kTile + row * 128;
+    walk(p, [&](const Unit& w, int c, int valid, const Pos<2>& at) {
+        uint8_t* Qrow = smem + M::kQ + at.s() * kTile + row * 128;
         // The chunk's first token of this head, in V and the output.
         auto first = [&]() { return (w.tok0 + c * kC) * p.a.H * kHeadDim + w.h * kHeadDim; };
         const uint32_t buf = at.it & 1u;
@@ -937,7 +952,7 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
         tc::fence_after_sync();
         if (flag[at.it & 1u] == at.it + 1)
             add_not_finite(trow, static_cast<const __nv_bfloat16*>(p.a.v) + first(), p.a.H * kHeadDim, row, valid);
-        stage_release(&b.empty_v[at.s], lane);
+        stage_release(&b.empty_v[at.s()], lane);
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
             uint32_t x[32];
@@ -967,7 +982,7 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                const uint8_t* src = smem + M::kQ + at.s * kTile + 32 * we * 128;
+                const uint8_t* src = smem + M::kQ + at.s() * kTile + 32 * we * 128;
                 const int y = w.tok0 + c * kC + 32 * we, x = w.h * kHeadDim;
                 tma_store_2d(omap, x, y, src);
                 tma_store_2d(omap, x + 64, y, src + kSlab);
@@ -975,13 +990,13 @@ __device__ __forceinline__ void output_role(const Work& p, const CUtensorMap* om
                 bulk_wait_read_all();
             }
         }
-        stage_release(&b.empty_q[at.s], lane);
+        stage_release(&b.empty_q[at.s()], lane);
         return true;
     });
     if (lane == 0) bulk_wait_all();
 }
 
-template <bool kStates>
+template <bool kStates, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 1)
     la_kernel(const __grid_constant__ Kernel kernel, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
@@ -990,9 +1005,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The next kernel may be placed where this one leaves room; what it needs
     // of this one it waits for.
     if (kernel.sg.starts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (kernel.a.valid) asm volatile("griddepcontrol.wait;" ::: "memory");   // the cut is decided before
-    bool valid = !kernel.a.valid || *kernel.a.valid;
-    if (!kernel.a.valid && kernel.a.cu_seqlens) {
+    if (kPacked && kernel.a.valid) asm volatile("griddepcontrol.wait;" ::: "memory");   // the cut is decided before
+    bool valid = !kPacked || !kernel.a.valid || *kernel.a.valid;
+    if (kPacked && !kernel.a.valid) {
         // A small packed batch checks its offsets here: no kernel before this one.
         const int64_t* cu = kernel.a.cu_seqlens;
         bool ok = threadIdx.x > 0 || (cu[0] == 0 && cu[kernel.a.N] == kernel.a.tokens);
@@ -1000,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         valid = __syncthreads_and(ok);
         if (!valid && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(kernel.a.status, kDevBadSeqlens);
     }
-    const Work p(kernel, kStates);
+    const Work<kStates, kPacked> p(kernel);
     if (!valid || (kStates && !p.cut)) return;
     if (smem_u32(smem) & 1023u) {   // the tiles' swizzle needs it; shared memory starts so
         if (threadIdx.x == 0) atomicOr(p.a.status, kDevPipeTimeout);
@@ -1012,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What the first chunk reads, on its way to L2 while the barriers and the
     // tensor memory are made ready.
     if (warp >= kLoadWarp && p.rows() > 0 && p.unit(0) < p.end) {
-        const Unit w = unit_at<kStates>(p, p.unit(0));
+        const Unit w = unit_at(p, p.unit(0));
         if (w.nch > 0 && warp == kLoadWarp && lane == 0) {
             const int kcol = static_cast<int>(w.h / static_cast<uint32_t>(p.a.H / p.a.Hk)) * kHeadDim, vcol = w.h * kHeadDim;
 #pragma unroll 1
@@ -1064,21 +1079,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_ptr;
 
     if (warp < kStateWarp)
-        key_role<kStates>(p, smem, b, tmem, warp, lane);
+        key_role(p, smem, b, tmem, warp, lane);
     else if (warp < kScoreWarp)
-        state_role<kStates>(p, smem, b, tmem, warp - kStateWarp, lane);
+        state_role(p, smem, b, tmem, warp - kStateWarp, lane);
     else if (warp == kLoadWarp)
-        load_role<kStates>(p, &qmap, &kmap, &vmap, smem, b, lane);
+        load_role(p, &qmap, &kmap, &vmap, smem, b, lane);
     else if (warp == kMmaWarp)
-        mma_role<kStates>(p, smem, b, tmem, lane);
+        mma_role(p, smem, b, tmem, lane);
     else if (warp == kDecayWarp)
-        decay_role<kStates>(p, smem, b, lane);
-    else if (!kStates && warp < kQueryWarp)
-        score_role(p, smem, b, tmem, warp - kScoreWarp, lane);
-    else if (!kStates && warp < kOutWarp)
-        query_role(p, smem, b, warp - kQueryWarp, lane);
-    else if (!kStates)
-        output_role(p, &omap, smem, b, tmem, warp - kOutWarp, lane);
+        decay_role(p, smem, b, lane);
+    else if constexpr (!kStates) {
+        if (warp < kQueryWarp)
+            score_role(p, smem, b, tmem, warp - kScoreWarp, lane);
+        else if (warp < kOutWarp)
+            query_role(p, smem, b, warp - kQueryWarp, lane);
+        else
+            output_role(p, &omap, smem, b, tmem, warp - kOutWarp, lane);
+    }
 
     tc::fence_before_sync();
     __syncthreads();
@@ -1366,13 +1383,13 @@ cudaError_t encode_tokens(CUtensorMap* map, const void* base, int64_t tokens, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool kStates>
+template <bool kStates, bool kPacked>
 cudaError_t configure() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static bool configured[64] = {};
     if (configured[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(la_kernel<kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(la_kernel<kStates, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Smem<kStates>::kBytes));
     if (e == cudaSuccess) configured[dev] = true;
     return e;
@@ -1389,7 +1406,8 @@ cudaError_t launch_la_cut(const int64_t* cu_seqlens, int64_t n_seqs, int64_t tok
     return cudaGetLastError();
 }
 
-cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream, int* launches) {
+template <bool kPacked>
+static cudaError_t launch(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream, int* launches) {
     Kernel p;
     p.a = a;
     p.sg = sg;
@@ -1402,7 +1420,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     p.heads = static_cast<uint32_t>(a.H);
     CUtensorMap qm, km, vm, om;
     cudaError_t e;
-    if ((e = configure<false>()) != cudaSuccess || (e = configure<true>()) != cudaSuccess) return e;
+    if ((e = configure<false, kPacked>()) != cudaSuccess || (e = configure<true, kPacked>()) != cudaSuccess) return e;
     if ((e = encode_tokens(&qm, a.q, a.tokens, a.Hk, kC)) != cudaSuccess ||
         (e = encode_tokens(&km, a.k, a.tokens, a.Hk, kC)) != cudaSuccess ||
         (e = encode_tokens(&vm, a.v, a.tokens, a.H, kC)) != cudaSuccess ||
@@ -1423,7 +1441,7 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Smem<true>::kBytes;
         cfg.numAttrs = a.valid ? 1 : 0;
-        if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true>, p, qm, km, vm, om)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, la_kernel<true, kPacked>, p, qm, km, vm, om)) != cudaSuccess) return e;
         const bool many = a.N * a.H >= 24, few = (sg.cut ? sg.spans : sg.segs) <= 4 * kScanWarps;
         const int64_t parts = a.N * a.H * (many || !few ? 128 : 64), ctas = many ? (parts + kScanWarps - 1) / kScanWarps : parts;
         const int64_t most = static_cast<int64_t>(sms) * (many ? 4 : few ? 3 : 2);
@@ -1440,9 +1458,13 @@ cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cu
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Smem<false>::kBytes;
     cfg.numAttrs = sg.starts || a.valid ? 1 : 0;
-    if ((e = cudaLaunchKernelEx(&cfg, la_kernel<false>, p, qm, km, vm, om)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, la_kernel<false, kPacked>, p, qm, km, vm, om)) != cudaSuccess) return e;
     *launches += 1;
     return cudaSuccess;
+}
+
+cudaError_t launch_la_prefill(const LaArgs& a, const LaSegments& sg, int sms, cudaStream_t stream, int* launches) {
+    return a.cu_seqlens ? launch<true>(a, sg, sms, stream, launches) : launch<false>(a, sg, sms, stream, launches);
 }
 
 }  // namespace kda
