@@ -16,14 +16,22 @@
 // 16-byte loads that cover 128 contiguous bytes, so a row's sums take three
 // shuffles; a warp has four rows at a time.  All arithmetic is FP32; a BF16
 // state is rounded once per step, when it is stored.
+//
+// Four CTAs share a (sequence, head), 32 rows each.  Where there are enough to
+// fill the SMs, two warps take four rows a lane group: the state's loads are all
+// under way before the first sum, and a lane group's exponentials and norms
+// serve four rows.  Else eight warps take one each, which is sooner done.
+// Measured on GB300, L2 flushed, 64 sequences x 96 heads (floors at the 6.80 TB/s
+// of a plain copy): FP32 state la_decode 121 us, kda_decode 123 (floor 118.5,
+// 119), BF16 65 and 75 (59.3, 60); one CTA of eight warps for all 128 rows took
+// 83 for the last, because fewer, larger CTAs start and end together.  6 states:
+// 6.1 us with one row a lane group, 8.2 with four.
 #include "kda_common.cuh"
 #include "kda_launch.h"
 
 namespace kda {
 namespace {
 
-constexpr int kStepThreads = 256;
-constexpr int kPassRows = 32;   // rows of a CTA's eight warps at a time
 constexpr int kPer = 16;        // key channels of a lane
 
 struct StepParams {
@@ -130,10 +138,11 @@ __device__ __forceinline__ float dot(const float (&x)[kPer], const float (&y)[kP
     return s0 + s1;
 }
 
-// One CTA: kPasses x 32 value rows of one (sequence, head).
-template <bool kDelta, bool kF32, int kPasses>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(StepParams p) {
+// One CTA: kPasses times kThreads / 8 value rows of one (sequence, head).
+template <bool kDelta, bool kF32, int kPasses, int kThreads>
+__global__ void __launch_bounds__(kThreads) step_kernel(StepParams p) {
     const StepArgs& a = p.a;
+    constexpr int kPassRows = kThreads / 8;
     constexpr int kParts = kHeadDim / (kPassRows * kPasses);
     const int64_t unit = blockIdx.x / kParts;
     const int part = static_cast<int>(blockIdx.x % kParts);
@@ -210,10 +219,11 @@ template <bool kDelta, bool kF32>
 cudaError_t launch(const StepParams& p, int sms, cudaStream_t stream) {
     const int64_t units = p.a.N * p.a.H;
     if (units * 4 > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned ctas = static_cast<unsigned>(units * 4);
     if (units >= sms)
-        step_kernel<kDelta, kF32, 4><<<static_cast<unsigned>(units), kStepThreads, 0, stream>>>(p);
+        step_kernel<kDelta, kF32, 4, 64><<<ctas, 64, 0, stream>>>(p);
     else
-        step_kernel<kDelta, kF32, 1><<<static_cast<unsigned>(units * 4), kStepThreads, 0, stream>>>(p);
+        step_kernel<kDelta, kF32, 1, 256><<<ctas, 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
