@@ -435,12 +435,19 @@ int64_t kda_noalloc_scratch_bytes(void);
  * rules, limits and the T = 0 rule are those of kda_prefill (g: 4 bytes).
  * The state is held in FP32 throughout; a NaN or an infinity in a token
  * reaches no earlier token and no other sequence.
- * When there are too few (sequence, head) chains to fill the GPU, each
- * sequence is cut into segments of whole 128-token chunks: one launch forms
- * the state each segment adds, one chains them, and one forms the outputs
- * from the segments' incoming states.  kda_set_segments governs this too
- * (off: never; a forced length is rounded up to whole 128-token chunks).
- * Scratch comes from the library's stream-ordered pool.
+ * When there are too few (sequence, head) chains to fill the GPU, the tokens
+ * are cut into spans of whole 128-token chunks: one launch forms the state each
+ * span adds, one chains them, and one forms the outputs from the spans'
+ * incoming states.  In the fixed layout each sequence is cut into equal
+ * segments.  A packed batch's lengths are known on the device alone, and a
+ * launch there decides: its sequences' chunks, one after the other, are cut into
+ * one span an SM (and head) where that is sooner done than its longest sequence;
+ * else, when there are more (sequence, head) units than SMs, the longest
+ * sequences go first.  kda_set_segments governs this too (off: no cut; a forced
+ * length is rounded up to whole 128-token chunks).  Equal calls give equal bits.
+ * Scratch comes from the library's stream-ordered pool: with a cut, an FP32 state
+ * for each span and head, and copies of the initial states where final_state
+ * is init_state.
  */
 int kda_la_prefill(const void* q, const void* k, const void* v, const float* g,
                    const void* init_state, void* out, void* final_state, int64_t B, int64_t T,
@@ -502,8 +509,9 @@ int kda_residual_norm(const void* x, const void* residual, const void* weight,
 
 /*
  * Segments per sequence kda_la_prefill would use for a call of this shape
- * (packed: a bound on all segments; 0: none), and the bytes of scratch it
- * takes at most (HOST out).  As kda_plan_segments and kda_workspace_bytes.
+ * (packed: the most spans it may cut the batch into; 0: no cut), and the bytes
+ * of scratch it takes at most (HOST out).  As kda_plan_segments and
+ * kda_workspace_bytes.
  */
 int kda_la_plan_segments(int64_t B, int64_t T, int64_t H, int packed, int64_t* segs);
 int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packed, int64_t* bytes);

@@ -291,7 +291,8 @@ def noalloc_scratch_bytes() -> int:
 
 
 def la_plan_segments(B: int, T: int, H: int, packed: bool) -> int:
-    """Segments per sequence la_prefill uses for this shape (0: one chain per sequence)."""
+    """Segments per sequence la_prefill uses for this shape (packed: the most
+    spans it may cut the batch into); 0: no cut."""
     out = ctypes.c_int64(0)
     _check(load().kda_la_plan_segments(int(B), int(T), int(H), 1 if packed else 0,
                                        ctypes.byref(out)), "kda_la_plan_segments")
