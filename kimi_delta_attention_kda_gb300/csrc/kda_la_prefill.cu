@@ -26,11 +26,15 @@
 // BF16 output they go to, and S itself is not touched by it.
 //
 // One CTA per SM walks its units, a sequence's tokens or a part of them for one
-// head.  Warps: 8 key (K'),
-// 8 state (S), 4 score (P), 4 query (Q'), 4 output (O), one each for the
-// loads, the MMA issue and the decay sums.  Tensor memory columns: D1 and P
-// [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two buffers of 32
-// tokens x 3 parts).
+// head.  Warps: 8 key (K'), 8 state (S), 4 score (P), 4 query (Q'), 4 output
+// (O), one each for the loads, the MMA issue and the decay sums.  Tensor memory
+// columns: D1 and P [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two
+// buffers of 32 tokens x 3 parts).
+//
+// Measured on GB300 (T = 8192, L2 flushed): a chain takes 2.65 us a chunk, of
+// which the six products' MMA time is 1.6; with 152 heads, every SM loading,
+// HBM's 2.9 us a chunk bind (207 us, floor 188 at a plain copy's 6.80 TB/s); 96
+// heads 184, floor 119; 6 heads 37, cut into spans, floor 7.6.
 //
 // A value that is not finite must not reach earlier tokens of its chunk: a
 // zero of P times an infinite V is NaN.  S^T shows it (its whole column is
@@ -109,10 +113,10 @@ __device__ __forceinline__ Bars make_bars(uint8_t* smem) {
 
 struct Kernel {
     LaArgs a;
-    LaSegments sg;      // sg.starts null: no segments
+    LaSegments sg;      // sg.starts null: no cut
     uint32_t units, heads;
 };
-// What a CTA does: units of (sequence, head), every grid's width one; of
+// What a CTA does: units of (sequence, head), one every grid's width; of
 // (segment, head) for a fixed layout's cut; and for a packed batch's, decided on
 // the device, the parts of its span, for one head.  The layout is a constant:
 // with both in one kernel every role's code is longer, and a chunk slower by 1%.
@@ -152,7 +156,7 @@ struct Work {
     __device__ __forceinline__ uint32_t rows() const { return (end - base + step - 1) / step; }
 };
 
-// One (sequence or segment, head).
+// One (sequence or part of one, head).
 struct Unit {
     int n, h, tok0, len;
     uint32_t slot;      // (span, head) row of the spans' buffers
@@ -1108,15 +1112,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The spans' incoming states: per (sequence, head), from S = init over the spans
-// that it goes on in, S <- exp(D) S + Z, in place over Z.  kSplit warps share 128 kVec
-// of the 16384 elements and take the segments kSplit kEach at a time: each warp
-// loads up to kEach of them at once, composes them, and starts from what the
-// warps before it compose to.  Few (sequence, head) units: eight warps a part,
-// or a part's segments come one latency after the other (21 us for 128
-// segments of one head; 6 so).  Many: a warp a part, or the parts do (80 us
-// for 96 units of 5).  kEach 4 for few segments: with the registers of 16 the
-// CTAs of 6 heads would need three waves, and the output kernel, which starts
-// when the last scan CTA has, would start with the third.
+// that it goes on in, S <- exp(D) S + Z, in place over Z.  kSplit warps share
+// 128 kVec of the 16384 elements and take the spans kSplit kEach at a time: each
+// warp loads up to kEach of them at once, composes them, and starts from what
+// the warps before it compose to.  Few (sequence, head) units: eight warps a
+// part, or a part's spans come one latency after the other (21 us for 128 spans
+// of one head; 6 so).  Many: a warp a part, or the parts do (80 us for 96 units
+// of 5).  kEach 4 for few spans: with the registers of 16 the CTAs of 6 heads
+// would need three waves, and the output kernel, which starts when the last scan
+// CTA has, would start with the third.
 constexpr int kScanWarps = 8;
 template <int kSplit, int kEach, int kVec>
 __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_constant__ Kernel p) {
@@ -1170,7 +1174,7 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
             const int64_t left = s1 - base;
             const int count = left < kSplit * kEach ? static_cast<int>(left) : kSplit * kEach;
             const int each = (count + kSplit - 1) / kSplit;
-            const int mine = min(each, max(0, count - place * each));   // segments of this warp
+            const int mine = min(each, max(0, count - place * each));   // spans of this warp
             const int64_t first = base + place * each;
             float4 z[kEach][kVec];
             float d[kEach];
@@ -1233,7 +1237,9 @@ __global__ void __launch_bounds__(32 * kScanWarps) la_scan_kernel(const __grid_c
 // A packed batch: checks the offsets' contract (kda_meta.cu) and decides, from
 // the lengths, whether to cut.  Without a cut the longest sequence is the least
 // it takes; with one, every SM has a span of W chunks, and takes kLaCutChunkUs
-// for each (kda_launch.h has the costs).
+// for each (kda_launch.h has the costs).  8 sequences of 33,333 tokens, 12 heads:
+// the longest 65 chunks, 178 us uncut and 134 cut; all 33, 100 and 130.  20,000
+// tokens, 16 heads, the longest 154 chunks: 405 and 119.
 constexpr int kCutThreads = 1024, kCutThreadsFew = 128;   // few: up to 128 sequences
 
 template <int kThreads>
