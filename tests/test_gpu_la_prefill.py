@@ -138,6 +138,18 @@ def test_decay_extremes(kda, value, seg):
         kda.set_segments(True, 0)
 
 
+@pytest.mark.parametrize("size", [1e-6, 1e4])
+@pytest.mark.parametrize("low", [-0.02, -0.6, -1.2, -20.0])
+def test_large_and_small_values(kda, size, low):
+    """Decays of a chunk from next to none to many powers of two: the bounds are
+    relative to the values."""
+    d, rnd = inputs(1, 390, 3, 1, seed=53, low=low)
+    d["g"][:, :, 2] = low                          # the same at every token
+    for key in ("q", "k", "v"):
+        d[key] = (d[key].float() * size).bfloat16()
+    check(kda, d, init=rnd(1, 3, D, D) * size * size)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("where", ["q", "k", "v", "g"])
 def test_not_finite(kda, where, bad):
