@@ -8,11 +8,13 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
+TORCH_PATH = os.path.join(_HERE, "_kda_torch.so")
 
 KDA_OK = 0
 KDA_DEV_BAD_SEQLENS = 1
@@ -21,6 +23,7 @@ KDA_DEV_BAD_SLOTS = 8
 
 _lock = threading.Lock()
 _lib = None
+_torch_module = None
 
 
 class KdaError(RuntimeError):
@@ -288,6 +291,26 @@ def prefill_noalloc_raw(q, k, v, g, beta, init_state, out, final_state, B, T, H,
 
 def noalloc_scratch_bytes() -> int:
     return int(load().kda_noalloc_scratch_bytes())
+
+
+def load_torch_module():
+    """The module of ``csrc/kda_torch.cpp``, bound to the library's entry points."""
+    global _torch_module
+    lib = load()
+    with _lock:
+        if _torch_module is None:
+            if not os.path.exists(TORCH_PATH):
+                raise RuntimeError("_kda_torch.so is not built (run kimi_delta_attention_kda_gb300.build"
+                                   ".build() or __graft_entry__.build())")
+            import torch  # noqa: F401  (the module's libraries)
+            spec = importlib.util.spec_from_file_location("_kda_torch", TORCH_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+                lib.kda_la_prefill, lib.kda_la_decode, lib.kda_decode, lib.kda_gated_norm,
+                lib.kda_residual_norm)))
+            _torch_module = module
+    return _torch_module
 
 
 def la_plan_segments(B: int, T: int, H: int, packed: bool) -> int:

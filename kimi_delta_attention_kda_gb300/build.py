@@ -3,21 +3,26 @@
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
 the objects are linked into ``kimi_delta_attention_kda_gb300/libkda.so``
 (CUDA runtime linked statically, so the library needs only the driver).
+``csrc/kda_torch.cpp``, the operators' calls on PyTorch tensors, becomes the
+module ``_kda_torch.so`` beside it, built against the installed PyTorch.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libkda.so")
+TORCH_PATH = os.path.join(HERE, "_kda_torch.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
@@ -46,8 +51,22 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_command(target):
+    """The compiler's command for ``csrc/kda_torch.cpp``."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch not found")
+    torch_dir = spec.submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + ["-I" + d for d in include] +
+            ["-L" + os.path.join(torch_dir, "lib"), os.path.join(CSRC, "kda_torch.cpp"),
+             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", target])
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link ``libkda.so``; returns its path."""
+    """Compile and link ``libkda.so`` and ``_kda_torch.so``; returns the former's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()
@@ -62,6 +81,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    torch_tmp = TORCH_PATH + ".tmp.%d" % os.getpid()
+    torch_src = os.path.join(CSRC, "kda_torch.cpp")
+    torch_stale = force or _stale(TORCH_PATH, [torch_src] + hdrs)
+    if torch_stale:
+        jobs.append(_torch_command(torch_tmp))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -72,9 +97,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                failed.append(cmd[-3])
+                failed.append(next(arg for arg in cmd if arg.startswith(CSRC)))
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("the compiler failed for: " + ", ".join(failed))
+    if torch_stale:
+        os.replace(torch_tmp, TORCH_PATH)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp.%d" % os.getpid()
         cmd = [nvcc()] + ARCH_FLAGS + ["-shared", "-o", tmp] + objs
