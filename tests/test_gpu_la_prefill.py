@@ -368,6 +368,49 @@ def test_bad_offsets_of_larger_batches_touch_nothing(kda, H):
         assert (out == 7).all() and (fin == 7).all()
 
 
+@pytest.mark.parametrize("T,cu", [(77, None), (700, [0, 100, 700]), (4100, None), (4200, [0, 4100, 4200])])
+def test_calls_in_a_row(kda, T, cu):
+    """Each call reads what the one before it wrote, without a pause between
+    them, eagerly and in a graph behind a copy and a fill."""
+    d, _ = inputs(1, T, 4, seed=59, low=-0.05)
+    dev = {key: x.cuda() for key, x in d.items()}
+    cu_t = None if cu is None else torch.tensor(cu, device="cuda")
+    st = torch.zeros(1 if cu is None else len(cu) - 1, 4, D, D, device="cuda")
+    bufs = [torch.empty_like(dev["v"]) for _ in range(3)]
+    src = torch.empty_like(dev["q"])
+
+    def chain(pause):
+        src.copy_(dev["q"])
+        st.zero_()
+        x = src
+        for i in range(8):
+            out = bufs[i % 3]
+            # (Outputs of a size that stays: the scale undoes their growth.)
+            kda.la_prefill(x, dev["k"], x, dev["g"], init_state=st, final_state=st, cu_seqlens=cu_t, out=out,
+                           scale=2.0 ** -10)
+            if pause:
+                torch.cuda.synchronize()
+            x = out
+        return x
+
+    want, state = chain(True).clone(), st.clone()
+    assert torch.isfinite(want).all()
+    for _ in range(5):
+        got = chain(False)
+        assert torch.equal(got, want) and torch.equal(st, state)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = chain(False)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(st, state)
+    assert kda.device_status() == 0
+
+
 @pytest.mark.slow
 def test_many_heads_long(kda):
     """More chains than SMs, and chunks enough for every buffer to be reused."""
