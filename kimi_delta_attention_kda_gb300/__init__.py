@@ -2,9 +2,9 @@
 
 The operation runs in ``libkda.so`` (CUDA kernels for sm_103a behind the C ABI
 of ``include/kda.h``), and so do the operators around it: single-token steps,
-linear attention with a decay per head, and norms (``ops.py``).  This package only builds that library and marshals
-PyTorch tensors into its entry points; PyTorch provides device memory and
-streams.  There is no CPU path.
+linear attention with a decay per head, and norms (``ops.py``).  This package
+only builds that library and marshals PyTorch tensors into its entry points;
+PyTorch provides device memory and streams.  There is no CPU path.
 """
 
 from __future__ import annotations

@@ -34,10 +34,11 @@
 // columns: D1 and P [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two
 // buffers of 32 tokens x 3 parts).
 //
-// Measured on GB300 (T = 8192, L2 flushed): a chain takes 2.65 us a chunk, of
-// which the six products' MMA time is 1.6; with 152 heads, every SM loading,
-// HBM's 2.9 us a chunk bind (207 us, floor 188 at a plain copy's 6.80 TB/s); 96
-// heads 184, floor 119; 6 heads 37, cut into spans, floor 7.6.
+// Measured on GB300 (T = 8192, L2 flushed): a chain takes 2.55 us a chunk, of
+// which the six products' MMA time is 1.6, and in which shared memory moves 480
+// KB, four fifths of its rate.  With 152 heads, every SM loading, HBM's 2.9 us a chunk bind
+// (205 us, floor 188 at a plain copy's 6.80 TB/s); 96 heads 179, floor 119; 6
+// heads 37, cut into spans, floor 7.6.
 //
 // A value that is not finite must not reach earlier tokens of its chunk: a
 // zero of P times an infinite V is NaN.  S^T shows it (its whole column is
