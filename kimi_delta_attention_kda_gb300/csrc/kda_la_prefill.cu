@@ -719,8 +719,6 @@ __device__ __forceinline__ void state_role(const Work& p, uint8_t* smem, const B
             // (Where final states overwrite the initial ones, a sequence's last
             // part may be done before its first has begun.)
             const bool copied = p.sg.inits && !w.last;
-            // (The chain over the spans may still be running.)
-            if (w.mid || copied) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (w.mid)
                 state_in(p.sg.starts, true, slot_at(w.slot), scol);
             else
@@ -1014,10 +1012,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
     using M = Smem<kStates>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    // The next kernel may be placed where this one leaves room; it waits for
-    // this one's end before it reads or writes.  The output kernel of a cut call
-    // waits only where it needs the spans' states: the kernels before it let it
-    // come when what the stream has before the call is done.
+    // The next kernel may be placed where this one leaves room.  Every kernel of
+    // a call waits for the end of the one before it ahead of its first read or
+    // write of global memory: only that wait makes the writes of the kernels
+    // before visible to it, a launch let come early does not.
     if (!kStates) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (kPacked) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the offsets; the cut is decided before
@@ -1094,8 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_ptr;
-    // The first kernel of a call: what the stream has before it.
-    if (!kPacked && (kStates || !kernel.sg.starts)) {
+    if (!kPacked) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (kStates) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
@@ -1121,8 +1118,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc::fence_before_sync();
     __syncthreads();
-    // (This kernel's end is also the end of the ones before it.)
-    if (!kStates && kernel.sg.starts) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kMmaWarp) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
