@@ -52,6 +52,7 @@
 #include "kda_common.cuh"
 #include "kda_launch.h"
 #include "kda_tcgen05.cuh"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace {
@@ -301,24 +302,6 @@ __device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-// Wait, with the whole warp, for a phase of an mbarrier, with a bound on tries
-// in place of a clock (each takes 20 cycles and more: a second or more).  The
-// kernel has many waits, and its roles share an instruction cache, so a wait
-// is a handful of instructions and its failure one call.
-constexpr uint32_t kTries = 1u << 27;
-__device__ __noinline__ void timed_out(int* status) { atomicOr(status, kDevPipeTimeout); }
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-        "W%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D%=;\n"
-        " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra.uni W%=;\n"
-        "D%=:\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "n"(kTries) : "memory");
-    if (__all_sync(0xffffffffu, ok)) return true;
-    timed_out(status);
-    return false;
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -362,7 +345,7 @@ __device__ __forceinline__ void load_role(const Work& p, const CUtensorMap* qmap
 #pragma unroll 1
     for (uint32_t i = issued > tiles * n ? issued - tiles * n : 0; i < issued; ++i) {
         const uint32_t it = i / tiles, t = i % tiles;
-        wait_phase(&b.full_k[t * n + it % n], (it / n) & 1u, p.a.status);
+        if (!wait_phase(&b.full_k[t * n + it % n], (it / n) & 1u, p.a.status)) break;
     }
 }
 

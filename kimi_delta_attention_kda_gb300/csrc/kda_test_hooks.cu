@@ -4,13 +4,14 @@
 // Compiled only into the test library libkda_testhooks.so, with
 // KDA_TEST_HOOKS defined and KDA_WAIT_BOUND_CYCLES = 10^5 (about 50 us), never
 // into libkda.so.  Each hook launches one CTA that uses the waits of the real
-// kernels (kda_common.cuh) on a ring nobody completes or a ready flag nobody
-// sets.  A wait that runs out sets kDevPipeTimeout and returns; the kernel
+// kernels (kda_common.cuh, kda_wait.cuh) on a ring or a barrier nobody completes
+// or a ready flag nobody sets.  A wait that runs out sets kDevPipeTimeout and returns; the kernel
 // then leaves with nothing in flight, and the context stays usable.  Nothing
 // here faults or hangs: every wait is bounded, every copy stays inside the
 // caller's buffer and the CTA's shared memory.
 #ifdef KDA_TEST_HOOKS
 #include "kda_common.cuh"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace {
@@ -63,6 +64,28 @@ __global__ void unset_flag_kernel(const uint32_t* flags, int* status, int* out) 
     if (threadIdx.x == 0) out[2] = ok ? 0 : 1;
 }
 
+// The wait of the linear-attention kernels: warp 0 on a barrier that warp 2
+// completes (out[0] = 1: it ended), warp 1 on one that nobody does (out[1] = 1:
+// it ran out; out[2]: after so many cycles).
+__global__ void __launch_bounds__(96, 1) stalled_phase_kernel(int* status, int* out) {
+    __shared__ uint64_t bars[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 2) {
+        mbar_init(&bars[threadIdx.x], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (warp == 2) {
+        if (lane == 0) mbar_arrive(&bars[0]);
+        return;
+    }
+    const long long t0 = clock64();
+    const bool ok = wait_phase(&bars[warp], 0, status);
+    const long long t = clock64() - t0;
+    if (lane == 0) out[warp] = ok == (warp == 0);
+    if (lane == 0 && warp == 1) out[2] = static_cast<int>(t < 0x7fffffff ? t : 0x7fffffff);
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -76,6 +99,12 @@ extern "C" int kda_test_wait_bounds(const void* src, const uint32_t* flags, int*
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     stalled_ring_kernel<<<1, 96, 0, stream>>>(static_cast<const uint8_t*>(src), 3, status, out);
     unset_flag_kernel<<<1, 32, 0, stream>>>(flags, status, out);
+    return static_cast<int>(cudaGetLastError());
+}
+
+// wait_phase's hook on `stream` (status a device int, out 3 device ints).
+extern "C" int kda_test_wait_phase(int* status, int* out, void* stream_ptr) {
+    stalled_phase_kernel<<<1, 96, 0, static_cast<cudaStream_t>(stream_ptr)>>>(status, out);
     return static_cast<int>(cudaGetLastError());
 }
 
