@@ -16,6 +16,7 @@
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace {
@@ -508,7 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     uint32_t phase = 0;
     int odd = 0;   // the sums' buffers alternate from row to row
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        if (!mbar_wait_bounded(&full[s], phase, p.status)) return;
+        if (!mbar_wait_warp(&full[s], phase, p.status)) {
+            // Warp 0 starts the copies, so none follows: none may be under way
+            // when the CTA ends.
+            const int64_t after = (p.rows - row + gridDim.x - 1) / gridDim.x;
+            if (warp == 0) drain_ring(full, stages, s, phase, static_cast<int>(after < stages ? after : stages), p.status);
+            return;
+        }
         const auto xs = reinterpret_cast<const __nv_bfloat16*>(stream_smem + s * stage_bytes + (kVec == 8 ? 0 : row * xb & 15));
         const auto rs = reinterpret_cast<const R*>(stream_smem + s * stage_bytes + xs_bytes + (kVec == 8 ? 0 : row * rb & 15));
         float rms = 1.f;

@@ -86,6 +86,39 @@ __global__ void __launch_bounds__(96, 1) stalled_phase_kernel(int* status, int* 
     if (lane == 0 && warp == 1) out[2] = static_cast<int>(t < 0x7fffffff ? t : 0x7fffffff);
 }
 
+// One warp leaves a ring of three stages early, at its second one: the first of
+// `filled` copies of 1 KB went to stage 1, the next to stages 2 and 0, which has
+// its second phase by then.  drain_ring waits for `left` copies; out[0] = 1 if
+// all came, and then out[1] = whether their bytes are those of src.
+__global__ void __launch_bounds__(32, 1) left_ring_kernel(const uint8_t* src, int filled, int left, int* status, int* out) {
+    __shared__ __align__(128) uint8_t ring[3][kRingStageBytes];
+    __shared__ uint64_t full[3];
+    const int lane = threadIdx.x;
+    auto fetch = [&](int s, int from) {
+        mbar_arrive_expect_tx(&full[s], kRingStageBytes);
+        bulk_g2s(ring[s], src + from * kRingStageBytes, kRingStageBytes, &full[s]);
+    };
+    if (lane == 0) {
+        for (int s = 0; s < 3; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+        fetch(0, 0);
+    }
+    __syncwarp();
+    if (!mbar_wait_warp(&full[0], 0, status)) return;   // stage 0's first phase
+    if (lane == 0)
+        for (int i = 0; i < filled && i < 3; ++i) fetch((1 + i) % 3, i);
+    __syncwarp();
+    const bool all = drain_ring(full, 3, 1, 0, left, status);
+    bool same = all;
+    for (int i = 0; all && i < left && i < filled; ++i)
+        for (uint32_t b = lane; b < kRingStageBytes; b += 32) same = same && ring[(1 + i) % 3][b] == src[i * kRingStageBytes + b];
+    same = __all_sync(0xffffffffu, same);
+    if (lane == 0) {
+        out[0] = all;
+        out[1] = same;
+    }
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -99,6 +132,16 @@ extern "C" int kda_test_wait_bounds(const void* src, const uint32_t* flags, int*
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     stalled_ring_kernel<<<1, 96, 0, stream>>>(static_cast<const uint8_t*>(src), 3, status, out);
     unset_flag_kernel<<<1, 32, 0, stream>>>(flags, status, out);
+    return static_cast<int>(cudaGetLastError());
+}
+
+// drain_ring's hook on `stream`: src as for kda_test_wait_bounds, filled and left
+// up to 3 (filled <= left: the kernel leaves nothing under way), status a device
+// int, out 2 device ints.
+extern "C" int kda_test_left_ring(const void* src, int filled, int left, int* status, int* out, void* stream_ptr) {
+    if (filled < 0 || left < filled || left > 3) return static_cast<int>(cudaErrorInvalidValue);
+    left_ring_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream_ptr)>>>(static_cast<const uint8_t*>(src), filled, left,
+                                                                          status, out);
     return static_cast<int>(cudaGetLastError());
 }
 

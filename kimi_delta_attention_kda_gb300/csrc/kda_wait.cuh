@@ -1,5 +1,6 @@
-// kda_wait.cuh -- the wait of kernels with many roles on mbarriers (sm_103a):
-// bounded in time, in a handful of instructions where it is used.
+// kda_wait.cuh -- waits on mbarriers beside those of kda_common.cuh (sm_103a):
+// that of kernels with many roles, bounded in time, in a handful of instructions
+// where it is used; and what a ring of copies is left with when a wait ran out.
 #pragma once
 
 #include "kda_common.cuh"
@@ -14,7 +15,7 @@ constexpr long long kTryCycles = 8000;
 constexpr uint32_t kWaitTries = static_cast<uint32_t>(kWaitBoundCycles / kTryCycles);
 static_assert(kWaitTries > 0 && kWaitBoundCycles / kTryCycles < 1LL << 31, "tries of a wait");
 
-__device__ __noinline__ void timed_out(int* status) { atomicOr(status, kDevPipeTimeout); }
+static __device__ __noinline__ void timed_out(int* status) { atomicOr(status, kDevPipeTimeout); }
 
 // Wait, with the whole warp, for a phase of an mbarrier, for kWaitBoundCycles
 // (about 2 s) at most.  The bound is a number of tries: the roles of a kernel
@@ -32,6 +33,20 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* 
     if (ok) return true;
     timed_out(status);
     return false;
+}
+
+// Before a CTA leaves a ring of `stages` copies early, with one warp: waits for
+// the `left` copies under way from stage s on (phase `parity` there, the other
+// one behind the ring's end).  False if one does not come.
+__device__ __forceinline__ bool drain_ring(uint64_t* full, int stages, int s, uint32_t parity, int left, int* status) {
+    for (int i = 0; i < left; ++i) {
+        if (!mbar_wait_warp(&full[s], parity, status)) return false;
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+    return true;
 }
 
 }  // namespace kda
