@@ -87,6 +87,12 @@ bool number(PyObject* o, double* x) {
     *x = PyFloat_AsDouble(o);
     return *x != -1.0 || !PyErr_Occurred();
 }
+// An argument's truth value, before anything runs: taking it may raise.
+bool truth(PyObject* o, bool* x) {
+    const int r = PyObject_IsTrue(o);
+    *x = r > 0;
+    return r >= 0;
+}
 bool counted(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments expected", want);
     return n == want;
@@ -122,7 +128,8 @@ PyObject* la_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         N = cu->numel() - 1;
         c.need(cu, at::kLong, {N + 1});
     }
-    bool f32 = PyObject_IsTrue(a[9]) != 0;
+    bool f32, want_final;
+    if (!truth(a[9], &f32) || !truth(a[8], &want_final)) return nullptr;
     const int64_t shape[] = {N, H, kDim, kDim};
     if (a[4] != Py_None) {
         c.need_float(init, shape);
@@ -139,7 +146,7 @@ PyObject* la_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[11], c.dev, &stream) || !number(a[10], &scale)) return nullptr;
     at::Tensor new_out, new_fin;
     if (!out) out = &(new_out = fresh(*v));
-    const bool want_final = fin || PyObject_IsTrue(a[8]);
+    want_final = want_final || fin;
     if (!fin && want_final) fin = &(new_fin = at::empty(shape, q->options().dtype(f32 ? kF32 : kBF16)));
     const int rc = la_prefill_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(init), ptr(out), ptr(fin), N, T,
                                  H, Hk, static_cast<const int64_t*>(ptr(cu)), static_cast<float>(scale),
@@ -213,12 +220,13 @@ PyObject* kda_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c.need(beta, kBF16, {N, H});
     if (!c.ok) Py_RETURN_NONE;
     void* stream;
-    if (!stream_of(a[9], c.dev, &stream)) return nullptr;
+    bool logit;
+    if (!stream_of(a[9], c.dev, &stream) || !truth(a[8], &logit)) return nullptr;
     at::Tensor made;
     if (!out) out = &(made = fresh(*v));
     return result(decode_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(beta), ptr(state),
                             static_cast<const int32_t*>(ptr(slots)), ptr(out), N, H, state->size(0),
-                            (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (PyObject_IsTrue(a[8]) ? KDA_FLAG_BETA_LOGIT : 0u), stream),
+                            (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (logit ? KDA_FLAG_BETA_LOGIT : 0u), stream),
                   a[7], made);
     END_HANDLE_TH_ERRORS
 }
@@ -239,13 +247,13 @@ PyObject* gated_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!c.ok) Py_RETURN_NONE;
     void* stream;
     double eps;
-    if (!stream_of(a[7], c.dev, &stream) || !number(a[5], &eps)) return nullptr;
+    bool first;
+    if (!stream_of(a[7], c.dev, &stream) || !number(a[5], &eps) || !truth(a[4], &first)) return nullptr;
     at::Tensor made;
     if (!out) out = &(made = fresh(*x));
     return result(gated_norm_fn(ptr(x), ptr(weight), act ? ptr(gate) : nullptr, ptr(out), x->numel() / kDim,
                                 static_cast<int>(act), static_cast<float>(eps),
-                                (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (PyObject_IsTrue(a[4]) ? KDA_FLAG_GATE_FIRST : 0u),
-                                stream),
+                                (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (first ? KDA_FLAG_GATE_FIRST : 0u), stream),
                   a[6], made);
     END_HANDLE_TH_ERRORS
 }

@@ -2,9 +2,9 @@
 zero in BF16.
 
 Bounds: one rounding to BF16 (2^-8 of the value; 2^-134 where it is subnormal);
-the sigmoid of z < 0 is exp(z), off by 2^-16 at -95, over 1 + exp(z), and an FP32 number below 2^-126 from z = -87.3 on, whose last bit
-is 2^-150 / exp(-95) = 2^-12.9 of it at z = -95; sums over a row and all else
-stay below 2^-14."""
+the sigmoid of z < 0 is exp(z), off by 2^-16 at -95, over 1 + exp(z), and an
+FP32 number below 2^-126 from z = -87.3 on, whose rounding is 2^-150 / exp(-95) =
+2^-12.9 of it at z = -95; sums over a row and all else stay below 2^-14."""
 
 import pytest
 import torch
