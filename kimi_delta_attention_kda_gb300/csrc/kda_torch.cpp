@@ -97,6 +97,24 @@ bool counted(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments expected", want);
     return n == want;
 }
+// Other Python threads run while new outputs are allocated and the library is
+// called: either may wait for the GPU (a pool that grows, a full launch queue,
+// a device's set-up at its first call).  Nothing of Python is touched meanwhile.
+class Released {
+public:
+    Released() : state_(PyEval_SaveThread()) {}
+    ~Released() { PyEval_RestoreThread(state_); }
+    Released(const Released&) = delete;
+    Released& operator=(const Released&) = delete;
+
+private:
+    PyThreadState* state_;
+};
+template <class F>
+int released(F f) {
+    Released r;
+    return f();
+}
 at::Tensor fresh(const at::Tensor& like) { return at::empty(like.sizes(), like.options()); }
 
 PyObject* result(int rc, PyObject* given, const at::Tensor& out) {
@@ -145,12 +163,14 @@ PyObject* la_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     double scale;
     if (!stream_of(a[11], c.dev, &stream) || !number(a[10], &scale)) return nullptr;
     at::Tensor new_out, new_fin;
-    if (!out) out = &(new_out = fresh(*v));
     want_final = want_final || fin;
-    if (!fin && want_final) fin = &(new_fin = at::empty(shape, q->options().dtype(f32 ? kF32 : kBF16)));
-    const int rc = la_prefill_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(init), ptr(out), ptr(fin), N, T,
-                                 H, Hk, static_cast<const int64_t*>(ptr(cu)), static_cast<float>(scale),
-                                 (f32 ? KDA_FLAG_STATE_F32 : 0u) | (g->dim() == 1 ? KDA_FLAG_G_PER_HEAD : 0u), stream);
+    const int rc = released([&] {
+        if (!out) out = &(new_out = fresh(*v));
+        if (!fin && want_final) fin = &(new_fin = at::empty(shape, q->options().dtype(f32 ? kF32 : kBF16)));
+        return la_prefill_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(init), ptr(out), ptr(fin), N, T, H,
+                             Hk, static_cast<const int64_t*>(ptr(cu)), static_cast<float>(scale),
+                             (f32 ? KDA_FLAG_STATE_F32 : 0u) | (g->dim() == 1 ? KDA_FLAG_G_PER_HEAD : 0u), stream);
+    });
     if (rc != KDA_OK) return PyLong_FromLong(rc);
     PyObject* o = result(rc, a[6], new_out);
     PyObject* f = !want_final ? Py_NewRef(Py_None) : result(rc, a[7], new_fin);
@@ -197,12 +217,14 @@ PyObject* la_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     double scale;
     if (!stream_of(a[8], c.dev, &stream) || !number(a[7], &scale)) return nullptr;
     at::Tensor made;
-    if (!out) out = &(made = fresh(*v));
-    return result(la_decode_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(state),
-                               static_cast<const int32_t*>(ptr(slots)), ptr(out), N, H, q->size(1), state->size(0),
-                               static_cast<float>(scale),
-                               (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (g->dim() == 1 ? KDA_FLAG_G_PER_HEAD : 0u), stream),
-                  a[6], made);
+    const int rc = released([&] {
+        if (!out) out = &(made = fresh(*v));
+        return la_decode_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(state),
+                            static_cast<const int32_t*>(ptr(slots)), ptr(out), N, H, q->size(1), state->size(0),
+                            static_cast<float>(scale),
+                            (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (g->dim() == 1 ? KDA_FLAG_G_PER_HEAD : 0u), stream);
+    });
+    return result(rc, a[6], made);
     END_HANDLE_TH_ERRORS
 }
 
@@ -223,11 +245,13 @@ PyObject* kda_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bool logit;
     if (!stream_of(a[9], c.dev, &stream) || !truth(a[8], &logit)) return nullptr;
     at::Tensor made;
-    if (!out) out = &(made = fresh(*v));
-    return result(decode_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(beta), ptr(state),
-                            static_cast<const int32_t*>(ptr(slots)), ptr(out), N, H, state->size(0),
-                            (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (logit ? KDA_FLAG_BETA_LOGIT : 0u), stream),
-                  a[7], made);
+    const int rc = released([&] {
+        if (!out) out = &(made = fresh(*v));
+        return decode_fn(ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(g)), ptr(beta), ptr(state),
+                         static_cast<const int32_t*>(ptr(slots)), ptr(out), N, H, state->size(0),
+                         (fp32(state) ? KDA_FLAG_STATE_F32 : 0u) | (logit ? KDA_FLAG_BETA_LOGIT : 0u), stream);
+    });
+    return result(rc, a[7], made);
     END_HANDLE_TH_ERRORS
 }
 
@@ -250,11 +274,13 @@ PyObject* gated_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bool first;
     if (!stream_of(a[7], c.dev, &stream) || !number(a[5], &eps) || !truth(a[4], &first)) return nullptr;
     at::Tensor made;
-    if (!out) out = &(made = fresh(*x));
-    return result(gated_norm_fn(ptr(x), ptr(weight), act ? ptr(gate) : nullptr, ptr(out), x->numel() / kDim,
-                                static_cast<int>(act), static_cast<float>(eps),
-                                (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (first ? KDA_FLAG_GATE_FIRST : 0u), stream),
-                  a[6], made);
+    const int rc = released([&] {
+        if (!out) out = &(made = fresh(*x));
+        return gated_norm_fn(ptr(x), ptr(weight), act ? ptr(gate) : nullptr, ptr(out), x->numel() / kDim, static_cast<int>(act),
+                             static_cast<float>(eps),
+                             (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (first ? KDA_FLAG_GATE_FIRST : 0u), stream);
+    });
+    return result(rc, a[6], made);
     END_HANDLE_TH_ERRORS
 }
 
@@ -281,12 +307,14 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     double scale, eps;
     if (!stream_of(a[9], c.dev, &stream) || !number(a[5], &scale) || !number(a[6], &eps)) return nullptr;
     at::Tensor made, rmade;
-    if (!out) out = &(made = fresh(*x));
-    if (!rout) rout = &(rmade = fresh(*residual));
-    const int rc = residual_norm_fn(ptr(x), ptr(residual), ptr(weight), ptr(post), ptr(gate), ptr(out), ptr(rout),
-                                    x->numel() / D, D, static_cast<float>(scale), static_cast<float>(eps),
-                                    (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (fp32(residual) ? KDA_FLAG_RESIDUAL_F32 : 0u),
-                                    stream);
+    const int rc = released([&] {
+        if (!out) out = &(made = fresh(*x));
+        if (!rout) rout = &(rmade = fresh(*residual));
+        return residual_norm_fn(ptr(x), ptr(residual), ptr(weight), ptr(post), ptr(gate), ptr(out), ptr(rout), x->numel() / D, D,
+                                static_cast<float>(scale), static_cast<float>(eps),
+                                (fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u) | (fp32(residual) ? KDA_FLAG_RESIDUAL_F32 : 0u),
+                                stream);
+    });
     if (rc != KDA_OK) return PyLong_FromLong(rc);
     PyObject* o = result(rc, a[7], made);
     PyObject* r = result(rc, a[8], rmade);
