@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
 the objects are linked into ``kimi_delta_attention_kda_gb300/libkda.so``
 (CUDA runtime linked statically, so the library needs only the driver).
 ``csrc/kda_torch.cpp``, the operators' calls on PyTorch tensors, becomes the
-module ``_kda_torch.so`` beside it, built against the installed PyTorch.
+module ``_kda_torch.so`` beside it, built against the installed PyTorch.  The
+library does not need it: without a PyTorch for CUDA it is left out.
 """
 
 from __future__ import annotations
@@ -51,12 +52,17 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _torch_command(target):
-    """The compiler's command for ``csrc/kda_torch.cpp``."""
+def _torch_dir():
+    """The installed PyTorch's folder, or None without one that has CUDA."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("PyTorch not found")
-    torch_dir = spec.submodule_search_locations[0]
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    path = spec.submodule_search_locations[0]
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
+def _torch_command(torch_dir, target):
+    """The compiler's command for ``csrc/kda_torch.cpp``."""
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -66,7 +72,8 @@ def _torch_command(target):
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link ``libkda.so`` and ``_kda_torch.so``; returns the former's path."""
+    """Compile and link ``libkda.so`` and ``_kda_torch.so``; returns the former's path.
+    A module that does not compile is an error only once the library is linked."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()
@@ -83,25 +90,29 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     torch_tmp = TORCH_PATH + ".tmp.%d" % os.getpid()
     torch_src = os.path.join(CSRC, "kda_torch.cpp")
-    torch_stale = force or _stale(TORCH_PATH, [torch_src] + hdrs)
-    if torch_stale:
-        jobs.append(_torch_command(torch_tmp))
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        sys.stderr.write("no PyTorch for CUDA: _kda_torch.so is not built, libkda.so does without\n")
+    torch_job = None
+    if torch_dir is not None and (force or _stale(TORCH_PATH, [torch_src] + hdrs)):
+        torch_job = _torch_command(torch_dir, torch_tmp)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
     failed = []
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
-        for cmd, r in ex.map(run, jobs):
+    torch_failed = False
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        for cmd, r in ex.map(run, jobs + ([torch_job] if torch_job else [])):
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if r.returncode != 0:
-                failed.append(next(arg for arg in cmd if arg.startswith(CSRC)))
+            if r.returncode != 0 and cmd is torch_job:
+                torch_failed = True
+            elif r.returncode != 0:
+                failed.append(cmd[cmd.index("-c") + 1])
     if failed:
         raise RuntimeError("the compiler failed for: " + ", ".join(failed))
-    if torch_stale:
-        os.replace(torch_tmp, TORCH_PATH)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp.%d" % os.getpid()
         cmd = [nvcc()] + ARCH_FLAGS + ["-shared", "-o", tmp] + objs
@@ -109,6 +120,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB_PATH)
+    if torch_failed:
+        raise RuntimeError("libkda.so is built, but the compiler failed for: " + torch_src)
+    if torch_job:
+        os.replace(torch_tmp, TORCH_PATH)
     return LIB_PATH
 
 
