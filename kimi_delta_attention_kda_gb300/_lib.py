@@ -302,6 +302,10 @@ def load_torch_module():
             if not os.path.exists(TORCH_PATH):
                 raise RuntimeError("_kda_torch.so is not built (run kimi_delta_attention_kda_gb300.build"
                                    ".build() or __graft_entry__.build())")
+            from . import build
+            if (build.torch_note() or {}).get("abi") != build.torch_abi():
+                raise RuntimeError("_kda_torch.so was built for another PyTorch or Python (run "
+                                   "kimi_delta_attention_kda_gb300.build.build())")
             import torch  # noqa: F401  (the module's libraries)
             spec = importlib.util.spec_from_file_location("_kda_torch", TORCH_PATH)
             module = importlib.util.module_from_spec(spec)

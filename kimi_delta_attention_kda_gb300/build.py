@@ -5,7 +5,9 @@ the objects are linked into ``kimi_delta_attention_kda_gb300/libkda.so``
 (CUDA runtime linked statically, so the library needs only the driver).
 ``csrc/kda_torch.cpp``, the operators' calls on PyTorch tensors, becomes the
 module ``_kda_torch.so`` beside it, built against the installed PyTorch.  The
-library does not need it: without a PyTorch for CUDA it is left out.
+library does not need it: without a PyTorch for CUDA it is left out.  A note
+beside the module says which PyTorch and Python it was built for: it is built
+again for others, and not loaded with them.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import importlib.util
+import json
 import os
 import shutil
 import subprocess
@@ -24,6 +27,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libkda.so")
 TORCH_PATH = os.path.join(HERE, "_kda_torch.so")
+TORCH_NOTE = os.path.join(BUILD_DIR, "kda_torch.json")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
@@ -71,6 +75,26 @@ def _torch_command(torch_dir, target):
              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", target])
 
 
+def torch_abi():
+    """What ``_kda_torch.so`` is built against: the installed PyTorch's version
+    file as it is (the version, the commit, CUDA's version) and Python's ABI."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return None
+    with open(os.path.join(torch_dir, "version.py")) as fh:
+        return {"torch": fh.read(), "python": sysconfig.get_config_var("SOABI")}
+
+
+def torch_note():
+    """The note of the module that is there: ``torch_abi()`` and the compiler's
+    command, or None."""
+    try:
+        with open(TORCH_NOTE) as fh:
+            return json.load(fh)
+    except (OSError, ValueError):
+        return None
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link ``libkda.so`` and ``_kda_torch.so``; returns the former's path.
     A module that does not compile is an error only once the library is linked."""
@@ -94,8 +118,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if torch_dir is None:
         sys.stderr.write("no PyTorch for CUDA: _kda_torch.so is not built, libkda.so does without\n")
     torch_job = None
-    if torch_dir is not None and (force or _stale(TORCH_PATH, [torch_src] + hdrs)):
-        torch_job = _torch_command(torch_dir, torch_tmp)
+    if torch_dir is not None:
+        # (The package's own path is left out: it may be reached by several.)
+        note = {"abi": torch_abi(), "command": [x.replace(HERE, "") for x in _torch_command(torch_dir, TORCH_PATH)]}
+        if force or _stale(TORCH_PATH, [torch_src] + hdrs) or torch_note() != note:
+            torch_job = _torch_command(torch_dir, torch_tmp)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -123,7 +150,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if torch_failed:
         raise RuntimeError("libkda.so is built, but the compiler failed for: " + torch_src)
     if torch_job:
+        # (Between the two there is a module without its note: it is not loaded.)
+        if os.path.exists(TORCH_NOTE):
+            os.remove(TORCH_NOTE)
         os.replace(torch_tmp, TORCH_PATH)
+        with open(TORCH_NOTE + ".tmp", "w") as fh:
+            json.dump(note, fh)
+        os.replace(TORCH_NOTE + ".tmp", TORCH_NOTE)
     return LIB_PATH
 
 

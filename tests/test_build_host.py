@@ -1,7 +1,9 @@
 """What the build does beside compiling (no GPU needed): the library and the
-module of the calls on PyTorch tensors do not wait for each other."""
+module of the calls on PyTorch tensors do not wait for each other, and the module
+is only used with the PyTorch that it was built against."""
 
 import importlib.util
+import json
 import os
 
 import pytest
@@ -53,4 +55,42 @@ def test_operators_name_the_missing_module(elsewhere, monkeypatch):
     monkeypatch.setattr(_lib, "_torch_module", None)
     monkeypatch.setattr(_lib, "TORCH_PATH", str(elsewhere / "not_there.so"))
     with pytest.raises(RuntimeError, match="not built"):
+        _lib.load_torch_module()
+
+
+def test_another_pytorch_means_another_module(elsewhere, monkeypatch):
+    monkeypatch.setattr(build, "TORCH_NOTE", str(elsewhere / "note.json"))
+    compiled = []
+
+    def command(torch_dir, target):
+        # A stand-in for the compiler, which takes 20 seconds.
+        compiled.append(target)
+        return ["cp", os.path.join(build.CSRC, "kda_torch.cpp"), target] if ".tmp." in target else ["as", "before"]
+
+    monkeypatch.setattr(build, "_torch_command", command)
+    path = build.TORCH_PATH
+
+    def builds():
+        before = len([x for x in compiled if x != path])
+        build.build()
+        return len([x for x in compiled if x != path]) - before
+
+    assert builds() == 1 and builds() == 0
+    abi = build.torch_abi()
+    assert "version" in abi["torch"] and json.load(open(build.TORCH_NOTE))["abi"] == abi
+    for other in ({"torch": "__version__ = '0'"}, {"python": "cpython-99"}):
+        monkeypatch.setattr(build, "torch_abi", lambda other=other: dict(abi, **other))
+        assert builds() == 1 and builds() == 0
+    os.remove(build.TORCH_NOTE)
+    assert builds() == 1 and builds() == 0
+
+
+@pytest.mark.parametrize("note", [None, {}, {"abi": {"torch": "__version__ = '0'", "python": "cpython-99"}}])
+def test_a_module_for_another_pytorch_is_not_loaded(elsewhere, monkeypatch, note):
+    from kimi_delta_attention_kda_gb300 import _lib
+    monkeypatch.setattr(_lib, "_torch_module", None)
+    monkeypatch.setattr(build, "TORCH_NOTE", str(elsewhere / "note.json"))
+    if note is not None:
+        (elsewhere / "note.json").write_text(json.dumps(note))
+    with pytest.raises(RuntimeError, match="another PyTorch"):
         _lib.load_torch_module()
