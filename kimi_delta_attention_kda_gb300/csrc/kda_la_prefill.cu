@@ -23,10 +23,12 @@
 // S^T is FP32 in tensor memory: the state warps read it, write its BF16 copy
 // to shared memory and exp(G) S^T back, and K'^T V accumulates on that.
 // K' is split by truncation into three BF16 parts whose sum is the FP32
-// value, so the state is accurate to FP32: with two parts (16 bits) the final
-// state was off by 2e-6 of its norm, against 1e-7 for FP32 arithmetic.
+// value, so the state is accurate to FP32: final states are off by 2e-7 to 3e-7 of
+// their norm; with two parts (16 bits) a key is short of 2^-17 to 2^-16 of itself,
+// always to one side, and states of random keys would be off by 1e-5.
 // P and the S operand are rounded to BF16 once each: their error stays in the
-// BF16 output they go to, and S itself is not touched by it.
+// BF16 output they go to, which is off by 2.4e-3 of its norm where its own
+// rounding alone is 1.7e-3, and S itself is not touched by it.
 //
 // One CTA per SM walks its units, a sequence's tokens or a part of them for one
 // head.  Warps: 8 key (K'), 8 state (S), 4 score (P), 4 query (Q'), 4 output
