@@ -433,8 +433,14 @@ int64_t kda_noalloc_scratch_bytes(void);
  *   final_state : the same type, or NULL (not written); may be init_state
  * Fixed and packed layouts, cu_seqlens, empty sequences, alignment, overlap
  * rules, limits and the T = 0 rule are those of kda_prefill (g: 4 bytes).
- * The state is held in FP32 throughout; a NaN or an infinity in a token
- * reaches no earlier token and no other sequence.
+ * The state is held in FP32 throughout (final states are off by 3e-7 of their
+ * norm); a NaN or an infinity in a token reaches no earlier token and no other
+ * sequence.  On the way to out, the decayed scores (q . k) exp(..) and a copy of
+ * the state before each 128 tokens are operands of the tensor cores, rounded to
+ * BF16 once each: out is off by 2.4e-3 of its norm, where its own rounding alone
+ * is 1.7e-3.  Range: out is formed with a factor of up to 2^48 that its token's
+ * decay then takes away, so where the tokens of a chunk of 128 decay, values of
+ * out / scale above 2^79 (6e23) may come out infinite.
  * When there are too few (sequence, head) chains to fill the GPU, the tokens
  * are cut into spans of whole 128-token chunks: one launch forms the state each
  * span adds, one chains them, and one forms the outputs from the spans'

@@ -90,6 +90,10 @@ def la_prefill(q, k, v, g, init_state=None, cu_seqlens=None, out=None, final_sta
     (then ``B == 1``).  ``final_state`` may be ``init_state``; a new one takes
     the type of ``init_state``, or ``state_dtype`` without one.  ``scale``
     defaults to 1/sqrt(128).
+
+    The state is held in FP32; ``out`` takes one rounding to BF16 of the decayed
+    scores and one of the state before each 128 tokens besides its own (2.4e-3 of
+    its norm in all), and may be infinite where ``out / scale`` is above 2^79.
     """
     if stream is not None:
         _check_prefill(q, k, v, g, init_state, cu_seqlens, out, final_state, state_dtype)
