@@ -163,11 +163,6 @@ def prefill_checkpointed_raw(q, k, v, g, beta, init_state, out, final_state, B, 
 
 
 FLAG_BETA_LOGIT = 1
-FLAG_STATE_F32 = 2
-FLAG_G_PER_HEAD = 4
-FLAG_WEIGHT_F32 = 8
-FLAG_GATE_FIRST = 16
-FLAG_RESIDUAL_F32 = 32
 
 
 def prefill_ex_raw(q, k, v, g, beta, init_state, out, final_state, B, T, H, cu_seqlens, flags,
