@@ -51,9 +51,13 @@ int plan_la(int64_t B, int64_t T, int64_t H, bool packed, LaPlan* p) {
 // The cut of a call's sequences into spans (see kda_la_prefill).  A packed
 // batch's lengths are on the device, and so is its choice (launch_la_cut).
 constexpr int64_t kMinPackedChunks = 16;   // fewer in all: not worth the launches
-// Fixed layout, one span of a head to an SM: a chunk of both passes (T=8192,
-// H=32 in 4 segments of 16 chunks 105 us, H=6 in 22 of 3 37 us), and the rest.
-constexpr double kLaFixedCutChunkUs = 5.5, kLaFixedCutUs = 18;
+// Fixed layout, one span of a head to an SM, in microseconds a call among others:
+// an uncut chain takes 5 and 2.4 a chunk (8 chunks 23, 16 42, 64 151 to 161, 128
+// 313), a cut call 15 and 4.5 for each chunk of a span, in both passes (spans of 1
+// chunk 15 to 24, of 3 28, 16 86, 22 114, 32 157 to 165, 64 297 to 313; more heads
+// take longer).  So 8 chunks of 2 heads are cut (23 against 16), 4 are not (14
+// against 15), nor 64 of 76 heads (161 against 165).
+constexpr double kLaFixedChunkUs = 2.4, kLaFixedCutChunkUs = 4.5, kLaFixedCutUs = 10;
 
 struct LaCut {
     int64_t chunks = 0;        // chunks of a span (packed: when forced)
@@ -96,7 +100,7 @@ LaCut cut_la(const LaPlan& pl, int64_t T, int64_t H, int sms, int allowed, int64
             c.chunks = (seq_chunks + want - 1) / want;
             const int64_t segs = (seq_chunks + c.chunks - 1) / c.chunks;
             const double cut = kLaFixedCutUs + c.chunks * kLaFixedCutChunkUs;
-            if (segs < 2 || cut >= seq_chunks * kLaChunkUs) return none;
+            if (segs < 2 || cut >= seq_chunks * kLaFixedChunkUs) return none;
         }
         c.segs = (seq_chunks + c.chunks - 1) / c.chunks;
         c.spans = c.segs * pl.N;

@@ -41,3 +41,11 @@ def test_one_state_an_sm(need, N, H, packed):
 def test_a_cut_takes_its_states(need):
     """The bound above is not loose: T = 8192, 6 heads in 22 spans of 3 chunks each."""
     assert need(1, 8192, 6, False) == 22 * 6 * STATE + 3 * 256 + 6 * STATE
+
+
+@pytest.mark.parametrize("T,H,cut", [(77, 6, False), (512, 2, False), (1024, 2, True), (1024, 12, True), (2048, 48, True),
+                                     (8192, 6, True), (8192, 48, True), (8192, 76, False), (8192, 96, False),
+                                     (16384, 64, True)])
+def test_cut_where_it_was_measured_to_pay(need, T, H, cut):
+    """Fixed layout, one sequence: on either side of the planner's costs."""
+    assert (need(1, T, H, False) > 0) == cut
