@@ -77,3 +77,60 @@ def test_inputs_rewritten_just_before(kda, B, T, H, cu, last):
         torch.cuda.synchronize()
         assert same(got)
     assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("capture", [False, True])
+@pytest.mark.parametrize("T,cu", [(700, None), (4100, None), (900, [0, 500, 500, 900]), (4200, [0, 4100, 4200])])
+def test_inputs_from_another_stream(kda, T, cu, capture):
+    """A call behind an earlier call of the library and a wait for an event of
+    another stream, whose late copies are its inputs: the early launch must not
+    pass the event."""
+    H, N = 4, 1 if cu is None else len(cu) - 1
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    src = {"q": normal(1, T, H, D).bfloat16(), "k": normal(1, T, H, D).bfloat16(), "v": normal(1, T, H, D).bfloat16(),
+           "g": -0.05 * torch.rand((1, T, H), generator=gen, device="cuda"), "init": normal(N, H, D, D)}
+    cu_t = None if cu is None else torch.tensor(cu, device="cuda")
+    at = {key: torch.zeros_like(x) for key, x in src.items()}
+    big = normal(4096, 4096)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def call(x):
+        return kda.la_prefill(x["q"], x["k"], x["v"], x["g"], init_state=x["init"], cu_seqlens=cu_t)
+
+    def run():
+        for x in at.values():
+            x.zero_()
+        call(at)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y = big
+            for _ in range(12):
+                y = y @ big
+            for key in at:
+                at[key].copy_(src[key])
+        call(src)
+        torch.cuda.current_stream().wait_stream(side)
+        return call(at)
+
+    want = call(src)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        got = run()
+    torch.cuda.synchronize()
+    if capture:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            got = run()
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        if capture:
+            graph.replay()
+        else:
+            torch.cuda.synchronize()
+            with torch.cuda.stream(main):
+                got = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert kda.device_status() == 0
