@@ -36,11 +36,14 @@
 // columns: D1 and P [0, 128), O [128, 256), S^T [256, 384), K' [384, 480) (two
 // buffers of 32 tokens x 3 parts).
 //
-// Measured on GB300 (T = 8192, L2 flushed): a chain takes 2.55 us a chunk, of
-// which the six products' MMA time is 1.6, and in which shared memory moves 480
-// KB, four fifths of its rate.  With 152 heads, every SM loading, HBM's 2.9 us a chunk bind
-// (205 us, floor 188 at a plain copy's 6.80 TB/s); 96 heads 179, floor 119; 6
-// heads 37, cut into spans, floor 7.6.
+// Measured on GB300 (T = 8192; a call among others, and from a flushed L2): an
+// uncut chain takes 2.35 us a chunk with one head (151 us), 2.6 with 96 (168, 175;
+// floor 119 at a plain copy's 6.80 TB/s), of which the six products' MMA time is
+// 1.6, and in which shared memory moves 480 KB, four fifths of its rate.  With 152
+// heads, every SM loading, HBM's 2.9 us a chunk bind (199, 204 to 216; floor 188).
+// 6 heads, cut into spans: 28, 37; floor 7.6.  The output kernels spill a little
+// at their 64 registers: 28 bytes stored and 84 loaded in the fixed layout, 60 and
+// 172 in the packed one.
 //
 // A value that is not finite must not reach earlier tokens of its chunk: a
 // zero of P times an infinite V is NaN.  S^T shows it (its whole column is

@@ -9,10 +9,14 @@
 // row stays in registers (or shared memory) between its sums and its outputs.
 // Sums and all arithmetic are FP32; outputs are rounded once.
 //
-// Measured on GB300, L2 flushed: gated norm of 8192 x 96 rows 92 us, 6.55 TB/s
-// (floor at 6.80 TB/s, the rate of a plain copy of 2 GB: 89); residual norm of
-// 8192 x 12288, FP32 residual and three weights 209 us, 5.8 TB/s (floor 178; a
-// plain copy of as many bytes 196), BF16 residual 133 us, 6.1 TB/s.
+// Measured on GB300, floors at 6.80 TB/s, the rate of a plain copy of 2 GB: gated
+// norm of 8192 x 96 rows 86 to 88 us among other calls (part of the last call's
+// output is still in L2 then), 94 from a flushed L2, 6.4 TB/s (floor 89); residual
+// norm of 8192 x 12288, FP32 residual and three weights 206 to 213 us either way,
+// 5.8 TB/s (floor 178; a plain copy of as many bytes 196), BF16 residual 136 to 140,
+// 5.8 TB/s (floor 119).  Rows above 16384 go one to a CTA, at 64 FP32 values a
+// thread and 64 registers, spilled: 2048 x 18432 140 us (floor 67), x 32768 229
+// (119).
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
