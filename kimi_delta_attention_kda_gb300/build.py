@@ -13,6 +13,7 @@ again for others, and not loaded with them.
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import glob
 import importlib.util
 import json
@@ -151,12 +152,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         raise RuntimeError("libkda.so is built, but the compiler failed for: " + torch_src)
     if torch_job:
         # (Between the two there is a module without its note: it is not loaded.)
-        if os.path.exists(TORCH_NOTE):
+        with contextlib.suppress(FileNotFoundError):
             os.remove(TORCH_NOTE)
         os.replace(torch_tmp, TORCH_PATH)
-        with open(TORCH_NOTE + ".tmp", "w") as fh:
+        tmp = TORCH_NOTE + ".tmp.%d" % os.getpid()
+        with open(tmp, "w") as fh:
             json.dump(note, fh)
-        os.replace(TORCH_NOTE + ".tmp", TORCH_NOTE)
+        os.replace(tmp, TORCH_NOTE)
     return LIB_PATH
 
 
