@@ -433,7 +433,7 @@ int64_t kda_noalloc_scratch_bytes(void);
  *   final_state : the same type, or NULL (not written); may be init_state
  * Fixed and packed layouts, cu_seqlens, empty sequences, alignment, overlap
  * rules, limits and the T = 0 rule are those of kda_prefill (g: 4 bytes).
- * The state is held in FP32 throughout (final states are off by 3e-7 of their
+ * The state is held in FP32 throughout (final states are off by 4e-7 of their
  * norm); a NaN or an infinity in a token reaches no earlier token and no other
  * sequence.  On the way to out, the decayed scores (q . k) exp(..) and a copy of
  * the state before each 128 tokens are operands of the tensor cores, rounded to

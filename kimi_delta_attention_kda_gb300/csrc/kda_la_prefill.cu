@@ -23,7 +23,7 @@
 // S^T is FP32 in tensor memory: the state warps read it, write its BF16 copy
 // to shared memory and exp(G) S^T back, and K'^T V accumulates on that.
 // K' is split by truncation into three BF16 parts whose sum is the FP32
-// value, so the state is accurate to FP32: final states are off by 2e-7 to 3e-7 of
+// value, so the state is accurate to FP32: final states are off by 2e-7 to 4e-7 of
 // their norm; with two parts (16 bits) a key is short of 2^-17 to 2^-16 of itself,
 // always to one side, and states of random keys would be off by 1e-5.
 // P and the S operand are rounded to BF16 once each: their error stays in the
