@@ -51,6 +51,9 @@ extern "C" {
 #define KDA_FLAG_WEIGHT_F32 8u    /* norm weights (and a channel gate) are FP32 (BF16 without it) */
 #define KDA_FLAG_GATE_FIRST 16u   /* the gate multiplies before the norm */
 #define KDA_FLAG_RESIDUAL_F32 32u /* the residual stream is FP32 (BF16 without it) */
+#define KDA_FLAG_DT_F32 64u       /* step sizes are FP32 (BF16 without it) */
+#define KDA_FLAG_BC_F32 128u      /* the scan's B and C are FP32 (BF16 without it) */
+#define KDA_FLAG_DT_SOFTPLUS 256u /* step sizes pass through a softplus */
 
 /* Activations of kda_gated_norm. */
 #define KDA_ACT_NONE 0
@@ -521,6 +524,104 @@ int kda_residual_norm(const void* x, const void* residual, const void* weight,
  */
 int kda_la_plan_segments(int64_t B, int64_t T, int64_t H, int packed, int64_t* segs);
 int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packed, int64_t* bytes);
+
+/*
+ * The short causal convolution in front of a mixer, for each channel on its own
+ * and over whole prompts:
+ *     y[t][d] = act(bias[d] + sum_{j < W} weight[d][j] x[t - W + 1 + j][d])
+ * where the W - 1 rows before a sequence's first are its initial state.
+ *
+ *   x           : BF16, a row of D channels for each token, rows ldx elements apart
+ *                 (ldx >= D: a part of a wider projection's output; 2-byte aligned).
+ *                 Fixed layout: the B sequences' rows one after the other, T each
+ *   out         : BF16 [tokens, D], contiguous
+ *   weight      : [D, W], W = 2 .. 4; bias: [D] or NULL; BF16, or FP32 (KDA_FLAG_WEIGHT_F32)
+ *   init_state  : BF16 [N, W - 1, D], oldest first, or NULL for zeros
+ *   final_state : BF16 [N, W - 1, D] or NULL (not written): the last W - 1 inputs,
+ *                 the initial state's among them where a sequence is shorter; may
+ *                 be init_state (then the call takes a copy of it as scratch)
+ *   activation  : KDA_ACT_NONE or KDA_ACT_SILU
+ * Packed layout, cu_seqlens, empty sequences, the T = 0 rule (weight is still
+ * needed) and the limit on tokens are those of kda_prefill.  Alignment: 16 bytes
+ * but for x and cu_seqlens (8).  out may overlap no input; it and final_state no
+ * input and not each other.  FP32 inside, one rounding of out.  Rows and
+ * channels in multiples of 8 (ldx, D, and x on 16 bytes) are read fastest.
+ */
+int kda_conv_prefill(const void* x, int64_t ldx, const void* weight, const void* bias,
+                     const void* init_state, void* out, void* final_state, int64_t B, int64_t T,
+                     int64_t D, int W, const int64_t* cu_seqlens, int activation, uint32_t flags,
+                     void* stream);
+
+/*
+ * One token per sequence of the same operation, on a pool of states: x [N, D]
+ * (rows ldx apart), out [N, D], state BF16 [pool, W - 1, D], updated in place
+ * (its rows move up by one and x becomes the last); slots as kda_la_decode.
+ */
+int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* bias, void* state,
+                    const int32_t* slots, void* out, int64_t N, int64_t D, int W, int64_t pool,
+                    int activation, uint32_t flags, void* stream);
+
+/*
+ * The selective state space scan over whole prompts: a linear recurrence whose
+ * decay differs in every channel d and state n = 0 .. nstate - 1,
+ *     s = softplus(dt[t][d] + dt_bias[d])        (without KDA_FLAG_DT_SOFTPLUS: the sum)
+ *     h[d][n] <- exp(s A[d][n]) h[d][n] + s x[t][d] B[t][g][n]
+ *     y = sum_n C[t][g][n] h[d][n] + D[d] x[t][d],   out[t][d] = y silu(z[t][d])
+ * with g = d / (dim / groups), the channel's group.
+ *
+ *   x, z        : BF16, a row of dim channels for each token; z may be NULL (no gate)
+ *   dt          : BF16 or FP32 (KDA_FLAG_DT_F32), a row of dim for each token
+ *   Bm, Cm      : BF16 or FP32 (KDA_FLAG_BC_F32), a row of [groups, nstate] for each token
+ *   ldx, lddt, ldb, ldc, ldz : elements between rows, at least a row's width
+ *   A           : FP32 [dim, nstate], contiguous, finite; D, dt_bias: FP32 [dim] or NULL
+ *   out         : BF16 [tokens, dim], contiguous
+ *   init_state  : [N, dim, nstate] or NULL for zeros; BF16, or FP32 with KDA_FLAG_STATE_F32
+ *   final_state : the same type, or NULL (not written); may be init_state
+ *   nstate      : 1 .. 64 (multiples of 16 waste nothing); groups divides dim
+ * Fixed and packed layouts, cu_seqlens, empty sequences, the T = 0 rule (A is
+ * still needed) and the limit on tokens are those of kda_prefill.  Alignment: A, out
+ * and the states 16 bytes, cu_seqlens 8, the rest an element's size (rows on 16
+ * bytes and channels of a group in multiples of 8 are read fastest).
+ * out and final_state may overlap no input and not each other.
+ * The states and all sums are FP32; on the way to out each state is cut to TF32
+ * (2^-10 of a product at most) before its product with C, and out is rounded
+ * once.  A NaN or an infinity in a token reaches no earlier token, no other
+ * channel (but through B and C, its group's) and no other sequence.
+ * When there are too few channels to fill the GPU the tokens are cut into
+ * spans: one launch forms the state each span ends with, one the outputs from
+ * what the spans before leave.  kda_set_segments governs this (off: no cut; a
+ * forced length is rounded up to whole 32 tokens).  Equal calls give equal
+ * bits.  Scratch comes from the library's stream-ordered pool: with a cut an
+ * FP32 state for each span and channel, and a copy of the initial states where
+ * final_state is init_state.
+ */
+int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A,
+                    const void* Bm, int64_t ldb, const void* Cm, int64_t ldc, const float* D,
+                    const void* z, int64_t ldz, const float* dt_bias, const void* init_state,
+                    void* out, void* final_state, int64_t B, int64_t T, int64_t dim,
+                    int64_t groups, int64_t nstate, const int64_t* cu_seqlens, uint32_t flags,
+                    void* stream);
+
+/*
+ * One token per sequence of the same operation, on a pool of states: rows are
+ * the sequences' tokens, state [pool, dim, nstate] (BF16 or FP32 as above) is updated in
+ * place, slots as kda_la_decode.
+ */
+int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A,
+                   const void* Bm, int64_t ldb, const void* Cm, int64_t ldc, const float* D,
+                   const void* z, int64_t ldz, const float* dt_bias, void* state,
+                   const int32_t* slots, void* out, int64_t N, int64_t dim, int64_t groups,
+                   int64_t nstate, int64_t pool, uint32_t flags, void* stream);
+
+/*
+ * Spans kda_ssm_prefill cuts each sequence of a call of this shape into
+ * (packed: the whole batch; 0: no cut), and the bytes of scratch it takes at
+ * most (HOST out).  As kda_plan_segments and kda_workspace_bytes.
+ */
+int kda_ssm_plan_segments(int64_t B, int64_t T, int64_t dim, int64_t groups, int64_t nstate,
+                          int packed, int64_t* segs);
+int kda_ssm_workspace_bytes(int64_t B, int64_t T, int64_t dim, int64_t groups, int64_t nstate,
+                            int packed, int64_t* bytes);
 
 #ifdef __cplusplus
 }

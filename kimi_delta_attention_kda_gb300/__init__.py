@@ -2,7 +2,8 @@
 
 The operation runs in ``libkda.so`` (CUDA kernels for sm_103a behind the C ABI
 of ``include/kda.h``), and so do the operators around it: single-token steps,
-linear attention with a decay per head, and norms (``ops.py``).  This package
+linear attention with a decay per head, the selective state space scan, the
+short causal convolution, and norms (``ops.py``).  This package
 only builds that library and marshals PyTorch tensors into its entry points;
 PyTorch provides device memory and streams.  There is no CPU path.
 """
@@ -13,7 +14,7 @@ from . import _lib
 from ._lib import (KdaError, auto_split, device_status, la_plan_segments, la_workspace_bytes,
                    packet_bytes, plan_fused,
                    plan_long_split, plan_segments, set_engine, set_fusion, set_segments,
-                   set_split, workspace_bytes)
+                   set_split, ssm_plan_segments, ssm_workspace_bytes, workspace_bytes)
 
 HEAD_DIM = 128
 
@@ -21,9 +22,11 @@ __all__ = ["kda_prefill", "kda_prefill_host", "prep_only", "KdaError", "device_s
            "set_fusion", "plan_fused", "plan_long_split", "set_segments", "plan_segments",
            "auto_split",
            "workspace_bytes", "packet_bytes", "HEAD_DIM", "la_prefill", "la_decode", "kda_decode",
-           "gated_norm", "residual_norm", "la_plan_segments", "la_workspace_bytes"]
+           "gated_norm", "residual_norm", "la_plan_segments", "la_workspace_bytes", "conv_prefill",
+           "conv_decode", "ssm_prefill", "ssm_decode", "ssm_plan_segments", "ssm_workspace_bytes"]
 
-_OPS = ("la_prefill", "la_decode", "kda_decode", "gated_norm", "residual_norm")
+_OPS = ("la_prefill", "la_decode", "kda_decode", "gated_norm", "residual_norm", "conv_prefill",
+        "conv_decode", "ssm_prefill", "ssm_decode")
 
 
 def __getattr__(name):

@@ -104,8 +104,17 @@ def load():
         lib.kda_residual_norm.argtypes = [P] * 7 + [I64, I64, F, F, U32, P]
         lib.kda_la_plan_segments.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
         lib.kda_la_workspace_bytes.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
+        lib.kda_conv_prefill.argtypes = [P, I64] + [P] * 5 + [I64] * 3 + [I, P, I, U32, P]
+        lib.kda_conv_decode.argtypes = [P, I64] + [P] * 5 + [I64] * 2 + [I, I64, I, U32, P]
+        ssm = [P, I64, P, I64, P, P, I64, P, I64, P, P, I64] + [P] * 4
+        lib.kda_ssm_prefill.argtypes = ssm + [I64] * 5 + [P, U32, P]
+        lib.kda_ssm_decode.argtypes = ssm + [I64] * 5 + [U32, P]
+        lib.kda_ssm_plan_segments.argtypes = [I64] * 5 + [I, ctypes.POINTER(I64)]
+        lib.kda_ssm_workspace_bytes.argtypes = [I64] * 5 + [I, ctypes.POINTER(I64)]
         for fn in (lib.kda_la_prefill, lib.kda_la_decode, lib.kda_decode, lib.kda_gated_norm,
-                   lib.kda_residual_norm, lib.kda_la_plan_segments, lib.kda_la_workspace_bytes):
+                   lib.kda_residual_norm, lib.kda_la_plan_segments, lib.kda_la_workspace_bytes,
+                   lib.kda_conv_prefill, lib.kda_conv_decode, lib.kda_ssm_prefill,
+                   lib.kda_ssm_decode, lib.kda_ssm_plan_segments, lib.kda_ssm_workspace_bytes):
             fn.restype = I
         _lib = lib
         return lib
@@ -308,6 +317,9 @@ def load_torch_module():
             module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
                 lib.kda_la_prefill, lib.kda_la_decode, lib.kda_decode, lib.kda_gated_norm,
                 lib.kda_residual_norm)))
+            module.bind_scan(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+                lib.kda_conv_prefill, lib.kda_conv_decode, lib.kda_ssm_prefill,
+                lib.kda_ssm_decode)))
             _torch_module = module
     return _torch_module
 
@@ -325,4 +337,22 @@ def la_workspace_bytes(B: int, T: int, H: int, packed: bool) -> int:
     out = ctypes.c_int64(0)
     _check(load().kda_la_workspace_bytes(int(B), int(T), int(H), 1 if packed else 0,
                                          ctypes.byref(out)), "kda_la_workspace_bytes")
+    return int(out.value)
+
+
+def ssm_plan_segments(B: int, T: int, dim: int, groups: int, nstate: int, packed: bool) -> int:
+    """Spans ssm_prefill cuts each sequence of this shape into (packed: the
+    whole batch); 0: no cut."""
+    out = ctypes.c_int64(0)
+    _check(load().kda_ssm_plan_segments(int(B), int(T), int(dim), int(groups), int(nstate),
+                                        1 if packed else 0, ctypes.byref(out)),
+           "kda_ssm_plan_segments")
+    return int(out.value)
+
+
+def ssm_workspace_bytes(B: int, T: int, dim: int, groups: int, nstate: int, packed: bool) -> int:
+    out = ctypes.c_int64(0)
+    _check(load().kda_ssm_workspace_bytes(int(B), int(T), int(dim), int(groups), int(nstate),
+                                          1 if packed else 0, ctypes.byref(out)),
+           "kda_ssm_workspace_bytes")
     return int(out.value)

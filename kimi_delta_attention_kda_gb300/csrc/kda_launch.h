@@ -282,6 +282,56 @@ struct ResidualNormArgs {
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, int sms, cudaStream_t stream);
 constexpr int64_t kMaxNormDim = 32768;
 
+// The short causal convolution.  Rows of x lie ldx elements apart.
+struct ConvArgs {
+    const void *x, *weight, *bias, *init_state;
+    void *state;               // decode: the pool
+    const int32_t* slots;      // decode
+    void *out, *final_state;
+    int64_t ldx, N, rows, tokens, tokens_per_seq;   // rows: of x; tokens_per_seq: fixed layout only
+    int64_t D, pool;
+    int W;
+    const int64_t* cu_seqlens;           // packed only
+    const int32_t* valid;                // packed only: a verdict on the offsets, or null
+    bool silu, weight_f32;
+    int* status;
+    int64_t run_tokens, runs, runs_per_seq;   // (set by the launch)
+};
+cudaError_t launch_conv_prefill(const ConvArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_conv_decode(const ConvArgs& a, int sms, cudaStream_t stream);
+
+// The selective state space scan.  Rows of x, dt, B, C and z lie ldx .. elements apart.
+struct SsmArgs {
+    const void *x, *dt, *B, *C, *z;
+    int64_t ldx, lddt, ldb, ldc, ldz;
+    const float *A, *D, *dt_bias;
+    const void* init_state;
+    void* state;               // decode: the pool
+    const int32_t* slots;      // decode
+    void *out, *final_state;
+    int64_t N, tokens, tokens_per_seq;   // tokens_per_seq: fixed layout only
+    int64_t dim, groups, nstate, pool;
+    const int64_t* cu_seqlens;           // packed only
+    const int32_t* valid;                // packed only: a verdict on the offsets, or null
+    // Spans of span_tokens tokens: of each sequence in the fixed layout, of the
+    // whole batch in the packed one.  More than one: the state each ends with
+    // ([spans][dim][16, 32 or 64]) and its sum of dt ([spans][dim]).
+    int64_t spans, spans_per_seq, span_tokens;
+    float *span_states, *span_steps;
+    int64_t tiles, tiles_per_group;      // of kSsmChannels channels
+    bool dt_f32, bc_f32, state_f32, softplus;
+    bool vec, vec_bc;                    // (set by the launch)
+    int* status;
+};
+constexpr int kSsmTile = 32;
+constexpr int kSsmChannels = 32;
+constexpr int64_t kSsmMaxState = 64;
+// Adds the kernels it launches to *launches.
+cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches);
+cudaError_t launch_ssm_decode(const SsmArgs& a, int sms, cudaStream_t stream);
+// Up to this many offsets every CTA checks them itself.
+constexpr int64_t kMaxSelfChecked = 1024;
+
 // Per-device status word and the split kda_prefill picks for `units`
 // (sequence x head) recurrences, for entry points outside kda_api.cu.
 int device_context(int** status, int64_t units, int* nsplit);

@@ -145,6 +145,131 @@ int run_step(StepArgs& a, bool delta, void* stream) {
     return KDA_OK;
 }
 
+// Rows of `width` elements that lie `ld` apart, as a range of memory.
+int64_t rows_bytes(int64_t rows, int64_t ld, int64_t width, int64_t size) { return rows > 0 ? ((rows - 1) * ld + width) * size : 0; }
+bool rows_fit(int64_t rows, int64_t ld, int64_t width) {
+    return width <= kMaxElems && (rows < 2 || (ld >= width && ld <= kMaxElems && rows <= kMaxElems / ld));
+}
+
+// Scratch of a call from the library's stream-ordered pool, given back in stream order.
+struct Scratch {
+    uint8_t* p = nullptr;
+    int64_t used = 0;
+    cudaStream_t stream = nullptr;
+    ~Scratch() {
+        if (p) cudaFreeAsync(p, stream);
+    }
+    bool take(int64_t bytes, cudaMemPool_t pool, cudaStream_t s) {
+        stream = s;
+        if (bytes <= 0) return true;
+        if (cudaMallocFromPoolAsync(reinterpret_cast<void**>(&p), static_cast<size_t>(bytes), pool, s) == cudaSuccess) return true;
+        cudaGetLastError();
+        p = nullptr;
+        return false;
+    }
+    uint8_t* part(int64_t bytes) {
+        uint8_t* at = p + used;
+        used += align256(bytes);
+        return at;
+    }
+};
+// The offsets' check ahead of the kernels that read them, where there are many.
+int check_offsets(const int64_t* cu, int64_t N, int64_t tokens, const DeviceView& d, int32_t* valid, cudaStream_t stream) {
+    if (launch_la_cut(cu, N, tokens, 1, d.sms, LaSegments{}, 0, valid, d.status, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    add_launches(1);
+    return KDA_OK;
+}
+
+// Tokens of N sequences, fixed (T each) or packed (T in all).
+int count_tokens(int64_t N, int64_t T, bool packed, int64_t* tokens) {
+    if (N < 1 || T < 0 || N > 0x7fffffffLL || T >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
+    *tokens = packed ? T : N * T;
+    return *tokens < (int64_t(1) << 31) ? KDA_OK : KDA_ERR_SHAPE;
+}
+
+int check_conv(const ConvArgs& a, int activation) {
+    if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_ARG;
+    if (a.D < 1 || a.D > kMaxElems / 8 || a.W < 2 || a.W > 4) return KDA_ERR_SHAPE;
+    return rows_fit(a.rows, a.ldx, a.D) && a.rows <= kMaxElems / a.D ? KDA_OK : KDA_ERR_SHAPE;
+}
+
+// The cut of a call of the scan (see kda_ssm_prefill).
+struct SsmCut {
+    int64_t tiles_per_group, tiles;
+    int64_t spans = 0, spans_per_seq = 1, span_tokens = 0;
+    int64_t state_bytes = 0, step_bytes = 0;   // of the spans' states, with more than one
+    int64_t init_bytes = 0;                    // a copy of initial states that final ones overwrite
+    bool cut() const { return state_bytes > 0; }
+    int64_t bytes() const { return align256(state_bytes) + align256(step_bytes); }
+};
+
+// A span for every quarter of an SM, of at least kSsmMinSpan tokens.
+constexpr int64_t kSsmMinSpan = 4 * kSsmTile;
+
+int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, bool packed, bool state_f32, int sms,
+             int allowed, int64_t forced, int64_t* tokens, SsmCut* c) {
+    int rc = count_tokens(N, T, packed, tokens);
+    if (rc != KDA_OK) return rc;
+    if (dim < 1 || groups < 1 || dim % groups || nstate < 1 || nstate > kSsmMaxState) return KDA_ERR_SHAPE;
+    const int64_t wide = nstate <= 16 ? 16 : nstate <= 32 ? 32 : 64;
+    if (dim > 0x7fffffffLL || N > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
+    c->tiles_per_group = (dim / groups + kSsmChannels - 1) / kSsmChannels;
+    c->tiles = c->tiles_per_group * groups;
+    const int64_t chains = packed ? 1 : N;        // that go on for `length` tokens
+    const int64_t length = packed ? *tokens : T;
+    c->span_tokens = length > 0 ? length : 1;
+    if (allowed && length > 0) {
+        if (forced > 0) {
+            c->span_tokens = forced > length / 16 ? length : (16 * forced + kSsmTile - 1) / kSsmTile * kSsmTile;
+        } else if (4 * c->tiles * chains < 5 * sms && length >= 2 * kSsmMinSpan) {
+            const int64_t want = 4 * static_cast<int64_t>(sms) / (c->tiles * chains);
+            c->span_tokens = ((length + want - 1) / want + kSsmTile - 1) / kSsmTile * kSsmTile;
+            if (c->span_tokens < kSsmMinSpan) c->span_tokens = kSsmMinSpan;
+        }
+    }
+    c->spans_per_seq = length > 0 ? (length + c->span_tokens - 1) / c->span_tokens : 1;
+    c->spans = c->spans_per_seq * chains;
+    if (c->spans > 0x7fffffffLL / c->tiles) return KDA_ERR_SHAPE;
+    if (c->spans_per_seq > 1) {
+        if (c->spans > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
+        c->state_bytes = c->spans * dim * wide * 4;
+        c->step_bytes = c->spans * dim * 4;
+        c->init_bytes = N * dim * nstate * (state_f32 ? 4 : 2);
+    }
+    return KDA_OK;
+}
+
+// What both forms of the scan read, for `rows` tokens, and where they write.
+int check_ssm(const SsmArgs& a, int64_t rows, const Span& read_write, const Span& also_read) {
+    const int64_t dt = a.dt_f32 ? 4 : 2, bc = a.bc_f32 ? 4 : 2, w = a.groups * a.nstate;
+    if (rows <= 0) return KDA_OK;
+    if (!a.x || !a.dt || !a.A || !a.B || !a.C || !a.out) return KDA_ERR_NULL;
+    if (!aligned(a.x, 2) || !aligned(a.dt, dt) || !aligned(a.A, 16) || !aligned(a.B, bc) || !aligned(a.C, bc) ||
+        !aligned(a.D, 4) || !aligned(a.z, 2) || !aligned(a.dt_bias, 4) || !aligned(a.out, 16))
+        return KDA_ERR_ALIGN;
+    const Span out(a.out, rows * a.dim * 2);
+    const Span in[] = {Span(a.x, rows_bytes(rows, a.ldx, a.dim, 2)), Span(a.dt, rows_bytes(rows, a.lddt, a.dim, dt)),
+                       Span(a.B, rows_bytes(rows, a.ldb, w, bc)), Span(a.C, rows_bytes(rows, a.ldc, w, bc)),
+                       Span(a.z, rows_bytes(rows, a.ldz, a.dim, 2)), Span(a.A, a.dim * a.nstate * 4), Span(a.D, a.dim * 4),
+                       Span(a.dt_bias, a.dim * 4), also_read};
+    return meets_any(out, in) || meets_any(read_write, in) || out.meets(read_write) ? KDA_ERR_OVERLAP : KDA_OK;
+}
+bool ssm_rows_fit(const SsmArgs& a, int64_t rows) {
+    const int64_t w = a.groups * a.nstate;
+    return rows <= kMaxElems / a.dim && rows_fit(rows, a.ldx, a.dim) && rows_fit(rows, a.lddt, a.dim) && rows_fit(rows, a.ldb, w) &&
+           rows_fit(rows, a.ldc, w) && (!a.z || rows_fit(rows, a.ldz, a.dim));
+}
+constexpr uint32_t kSsmFlags = KDA_FLAG_STATE_F32 | KDA_FLAG_DT_F32 | KDA_FLAG_BC_F32 | KDA_FLAG_DT_SOFTPLUS;
+void ssm_flags(SsmArgs* a, uint32_t flags) {
+    a->state_f32 = (flags & KDA_FLAG_STATE_F32) != 0;
+    a->dt_f32 = (flags & KDA_FLAG_DT_F32) != 0;
+    a->bc_f32 = (flags & KDA_FLAG_BC_F32) != 0;
+    a->softplus = (flags & KDA_FLAG_DT_SOFTPLUS) != 0;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -370,4 +495,280 @@ extern "C" int kda_residual_norm(const void* x, const void* residual, const void
     }
     add_launches(1);
     return KDA_OK;
+}
+
+extern "C" int kda_conv_prefill(const void* x, int64_t ldx, const void* weight, const void* bias, const void* init_state,
+                                void* out, void* final_state, int64_t B, int64_t T, int64_t D, int W,
+                                const int64_t* cu_seqlens, int activation, uint32_t flags, void* stream_ptr) {
+    reset_launches();
+    if (flags & ~KDA_FLAG_WEIGHT_F32) return KDA_ERR_ARG;
+    ConvArgs a = {};
+    int rc = count_tokens(B, T, cu_seqlens != nullptr, &a.tokens);
+    if (rc != KDA_OK) return rc;
+    a.x = x;
+    a.ldx = ldx;
+    a.weight = weight;
+    a.bias = bias;
+    a.init_state = init_state;
+    a.out = out;
+    a.final_state = final_state;
+    a.N = B;
+    a.rows = a.tokens;
+    a.tokens_per_seq = T;
+    a.D = D;
+    a.W = W;
+    a.cu_seqlens = cu_seqlens;
+    a.silu = activation == KDA_ACT_SILU;
+    a.weight_f32 = (flags & KDA_FLAG_WEIGHT_F32) != 0;
+    if ((rc = check_conv(a, activation)) != KDA_OK) return rc;
+    if (B > kMaxElems / (8 * D)) return KDA_ERR_SHAPE;
+    // (The filter is read without tokens too, by the threads that write the states.)
+    if (!weight || (a.tokens > 0 && (!x || !out))) return KDA_ERR_NULL;
+    if (!aligned(x, 2) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(init_state, 16) || !aligned(out, 16) ||
+        !aligned(final_state, 16) || !aligned(cu_seqlens, 8))
+        return KDA_ERR_ALIGN;
+    const int64_t state = B * (W - 1) * D * 2, wb = a.weight_f32 ? 4 : 2;
+    const Span so(out, a.tokens * D * 2), sf(final_state, state), si(init_state, state);
+    const Span in[] = {Span(x, rows_bytes(a.tokens, ldx, D, 2)), Span(weight, D * W * wb), Span(bias, D * wb),
+                       Span(cu_seqlens, 8 * (B + 1))};
+    if (meets_any(so, in) || meets_any(sf, in) || so.meets(sf) || so.meets(si) || (final_state != init_state && sf.meets(si)))
+        return KDA_ERR_OVERLAP;
+    DeviceView d;
+    if ((rc = device_view(&d)) != KDA_OK) return rc;
+    a.status = d.status;
+    const auto stream = static_cast<cudaStream_t>(stream_ptr);
+    const bool many = cu_seqlens && B > kMaxSelfChecked, in_place = init_state && init_state == final_state;
+    Scratch ws;
+    if (!ws.take((many ? 256 : 0) + (in_place ? align256(state) : 0), d.pool, stream)) return KDA_ERR_CUDA;
+    if (many) {
+        const auto valid = reinterpret_cast<int32_t*>(ws.part(256));
+        if ((rc = check_offsets(cu_seqlens, B, a.tokens, d, valid, stream)) != KDA_OK) return rc;
+        a.valid = valid;
+    }
+    if (in_place) {   // one thread ends a sequence while another begins it
+        void* copy = ws.part(state);
+        if (cudaMemcpyAsync(copy, init_state, static_cast<size_t>(state), cudaMemcpyDeviceToDevice, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return KDA_ERR_CUDA;
+        }
+        a.init_state = copy;
+    }
+    if (launch_conv_prefill(a, d.sms, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    add_launches(1);
+    return KDA_OK;
+}
+
+extern "C" int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* bias, void* state,
+                               const int32_t* slots, void* out, int64_t N, int64_t D, int W, int64_t pool,
+                               int activation, uint32_t flags, void* stream) {
+    reset_launches();
+    if (flags & ~KDA_FLAG_WEIGHT_F32) return KDA_ERR_ARG;
+    ConvArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.weight = weight;
+    a.bias = bias;
+    a.state = state;
+    a.slots = slots;
+    a.out = out;
+    a.N = a.rows = N;
+    a.D = D;
+    a.W = W;
+    a.pool = pool;
+    a.silu = activation == KDA_ACT_SILU;
+    a.weight_f32 = (flags & KDA_FLAG_WEIGHT_F32) != 0;
+    if (N < 0 || N > 0x7fffffffLL || pool < 0) return KDA_ERR_SHAPE;
+    int rc = check_conv(a, activation);
+    if (rc != KDA_OK) return rc;
+    if (pool > kMaxElems / (8 * D) || (!slots && N > pool)) return KDA_ERR_SHAPE;
+    if (N > 0) {
+        if (!x || !weight || !out || (pool > 0 && !state)) return KDA_ERR_NULL;
+        if (!aligned(x, 2) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(state, 16) || !aligned(out, 16) ||
+            !aligned(slots, 4))
+            return KDA_ERR_ALIGN;
+        const int64_t wb = a.weight_f32 ? 4 : 2;
+        const Span so(out, N * D * 2), ss(state, pool * (W - 1) * D * 2);
+        const Span in[] = {Span(x, rows_bytes(N, ldx, D, 2)), Span(weight, D * W * wb), Span(bias, D * wb), Span(slots, 4 * N)};
+        if (meets_any(so, in) || meets_any(ss, in) || so.meets(ss)) return KDA_ERR_OVERLAP;
+    }
+    DeviceView d;
+    rc = device_view(&d);
+    if (rc != KDA_OK || N == 0) return rc;
+    a.status = d.status;
+    if (launch_conv_decode(a, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    add_launches(1);
+    return KDA_OK;
+}
+
+extern "C" int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A, const void* Bm,
+                               int64_t ldb, const void* Cm, int64_t ldc, const float* D, const void* z, int64_t ldz,
+                               const float* dt_bias, const void* init_state, void* out, void* final_state, int64_t B,
+                               int64_t T, int64_t dim, int64_t groups, int64_t nstate, const int64_t* cu_seqlens,
+                               uint32_t flags, void* stream_ptr) {
+    reset_launches();
+    if (flags & ~kSsmFlags) return KDA_ERR_ARG;
+    SsmArgs a = {};
+    ssm_flags(&a, flags);
+    SsmCut cut;
+    int64_t tokens = 0;
+    // (The sizes' check; the device's plan follows.)
+    int rc = plan_ssm(B, T, dim, groups, nstate, cu_seqlens != nullptr, a.state_f32, 1, 0, 0, &tokens, &cut);
+    if (rc != KDA_OK) return rc;
+    a.x = x;
+    a.ldx = ldx;
+    a.dt = dt;
+    a.lddt = lddt;
+    a.A = A;
+    a.B = Bm;
+    a.ldb = ldb;
+    a.C = Cm;
+    a.ldc = ldc;
+    a.D = D;
+    a.z = z;
+    a.ldz = ldz;
+    a.dt_bias = dt_bias;
+    a.init_state = init_state;
+    a.out = out;
+    a.final_state = final_state;
+    a.N = B;
+    a.tokens = tokens;
+    a.tokens_per_seq = T;
+    a.dim = dim;
+    a.groups = groups;
+    a.nstate = nstate;
+    a.cu_seqlens = cu_seqlens;
+    if (!ssm_rows_fit(a, tokens)) return KDA_ERR_SHAPE;
+    // (The rates are read without tokens too.)
+    if (!A) return KDA_ERR_NULL;
+    if (!aligned(A, 16) || !aligned(init_state, 16) || !aligned(final_state, 16) || !aligned(cu_seqlens, 8)) return KDA_ERR_ALIGN;
+    const int64_t state = B * dim * nstate * (a.state_f32 ? 4 : 2);
+    const Span sf(final_state, state), si(init_state, state), cu(cu_seqlens, 8 * (B + 1));
+    if ((rc = check_ssm(a, tokens, sf, cu)) != KDA_OK) return rc;
+    if ((final_state != init_state && sf.meets(si)) || sf.meets(cu) || (tokens > 0 && Span(out, tokens * dim * 2).meets(si)))
+        return KDA_ERR_OVERLAP;
+    DeviceView d;
+    if ((rc = device_view(&d)) != KDA_OK) return rc;
+    a.status = d.status;
+    if ((rc = plan_ssm(B, T, dim, groups, nstate, cu_seqlens != nullptr, a.state_f32, d.sms, d.segments, d.seg_chunks, &tokens,
+                       &cut)) != KDA_OK)
+        return rc;
+    a.spans = cut.spans;
+    a.spans_per_seq = cut.spans_per_seq;
+    a.span_tokens = cut.span_tokens;
+    a.tiles = cut.tiles;
+    a.tiles_per_group = cut.tiles_per_group;
+    const auto stream = static_cast<cudaStream_t>(stream_ptr);
+    const bool many = cu_seqlens && B > kMaxSelfChecked, copied = cut.cut() && init_state && init_state == final_state;
+    Scratch ws;
+    if (!ws.take((many ? 256 : 0) + cut.bytes() + (copied ? align256(state) : 0), d.pool, stream)) return KDA_ERR_CUDA;
+    if (many) {
+        const auto valid = reinterpret_cast<int32_t*>(ws.part(256));
+        if ((rc = check_offsets(cu_seqlens, B, tokens, d, valid, stream)) != KDA_OK) return rc;
+        a.valid = valid;
+    }
+    if (cut.cut()) {
+        a.span_states = reinterpret_cast<float*>(ws.part(cut.state_bytes));
+        a.span_steps = reinterpret_cast<float*>(ws.part(cut.step_bytes));
+    }
+    if (copied) {   // one CTA ends a sequence while another begins it
+        void* copy = ws.part(state);
+        if (cudaMemcpyAsync(copy, init_state, static_cast<size_t>(state), cudaMemcpyDeviceToDevice, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return KDA_ERR_CUDA;
+        }
+        a.init_state = copy;
+    }
+    int launches = 0;
+    const cudaError_t e = launch_ssm_prefill(a, stream, &launches);
+    add_launches(launches);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
+extern "C" int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A, const void* Bm,
+                              int64_t ldb, const void* Cm, int64_t ldc, const float* D, const void* z, int64_t ldz,
+                              const float* dt_bias, void* state, const int32_t* slots, void* out, int64_t N, int64_t dim,
+                              int64_t groups, int64_t nstate, int64_t pool, uint32_t flags, void* stream) {
+    reset_launches();
+    if (flags & ~kSsmFlags) return KDA_ERR_ARG;
+    if (N < 0 || N > 0x7fffffffLL || pool < 0 || dim < 1 || dim > 0x7fffffffLL || groups < 1 || dim % groups || nstate < 1 ||
+        nstate > kSsmMaxState || pool > kMaxElems / (dim * nstate * 4) || (!slots && N > pool))
+        return KDA_ERR_SHAPE;
+    SsmArgs a = {};
+    ssm_flags(&a, flags);
+    a.x = x;
+    a.ldx = ldx;
+    a.dt = dt;
+    a.lddt = lddt;
+    a.A = A;
+    a.B = Bm;
+    a.ldb = ldb;
+    a.C = Cm;
+    a.ldc = ldc;
+    a.D = D;
+    a.z = z;
+    a.ldz = ldz;
+    a.dt_bias = dt_bias;
+    a.state = state;
+    a.slots = slots;
+    a.out = out;
+    a.N = a.tokens = N;
+    a.dim = dim;
+    a.groups = groups;
+    a.nstate = nstate;
+    a.pool = pool;
+    if (!ssm_rows_fit(a, N)) return KDA_ERR_SHAPE;
+    if (N > 0 && pool > 0 && !state) return KDA_ERR_NULL;
+    if (!aligned(state, 16) || !aligned(slots, 4)) return KDA_ERR_ALIGN;
+    int rc = check_ssm(a, N, Span(state, pool * dim * nstate * (a.state_f32 ? 4 : 2)), Span(slots, 4 * N));
+    if (rc != KDA_OK) return rc;
+    DeviceView d;
+    rc = device_view(&d);
+    if (rc != KDA_OK || N == 0) return rc;
+    a.status = d.status;
+    if (launch_ssm_decode(a, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    add_launches(1);
+    return KDA_OK;
+}
+
+extern "C" int kda_ssm_plan_segments(int64_t B, int64_t T, int64_t dim, int64_t groups, int64_t nstate, int packed,
+                                     int64_t* segs) {
+    if (!segs) return KDA_ERR_NULL;
+    SsmCut cut;
+    int64_t tokens;
+    int rc = plan_ssm(B, T, dim, groups, nstate, packed != 0, true, 1, 0, 0, &tokens, &cut);
+    if (rc != KDA_OK) return rc;
+    DeviceView d;
+    if ((rc = device_view(&d)) != KDA_OK) return rc;
+    rc = plan_ssm(B, T, dim, groups, nstate, packed != 0, true, d.sms, d.segments, d.seg_chunks, &tokens, &cut);
+    if (rc == KDA_OK) *segs = cut.cut() ? cut.spans_per_seq : 0;
+    return rc;
+}
+
+extern "C" int kda_ssm_workspace_bytes(int64_t B, int64_t T, int64_t dim, int64_t groups, int64_t nstate, int packed,
+                                       int64_t* bytes) {
+    if (!bytes) return KDA_ERR_NULL;
+    // As planned on the current device (on a 152-SM device when there is none).
+    DeviceView d;
+    if (device_view(&d) != KDA_OK) {
+        d.sms = 152;
+        segment_settings(&d.segments, &d.seg_chunks);
+    }
+    SsmCut cut;
+    int64_t tokens;
+    const int rc = plan_ssm(B, T, dim, groups, nstate, packed != 0, true, d.sms, d.segments, d.seg_chunks, &tokens, &cut);
+    if (rc == KDA_OK) *bytes = (packed && B > kMaxSelfChecked ? 256 : 0) + cut.bytes() + align256(cut.init_bytes);
+    return rc;
 }

@@ -41,6 +41,28 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// The convolution's and the scan's, in this order from bind_scan().
+decltype(&kda_conv_prefill) conv_prefill_fn = nullptr;
+decltype(&kda_conv_decode) conv_decode_fn = nullptr;
+decltype(&kda_ssm_prefill) ssm_prefill_fn = nullptr;
+decltype(&kda_ssm_decode) ssm_decode_fn = nullptr;
+
+PyObject* bind_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 4) return PyErr_Format(PyExc_TypeError, "four addresses expected");
+    void* p[4];
+    for (int i = 0; i < 4; ++i)
+        if (!(p[i] = PyLong_AsVoidPtr(a[i]))) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "null address");
+    conv_prefill_fn = reinterpret_cast<decltype(conv_prefill_fn)>(p[0]);
+    conv_decode_fn = reinterpret_cast<decltype(conv_decode_fn)>(p[1]);
+    ssm_prefill_fn = reinterpret_cast<decltype(ssm_prefill_fn)>(p[2]);
+    ssm_decode_fn = reinterpret_cast<decltype(ssm_decode_fn)>(p[3]);
+    Py_RETURN_NONE;
+}
+bool bound(const void* fn) {
+    if (!fn) PyErr_SetString(PyExc_RuntimeError, "the module is not bound to the library");
+    return fn;
+}
+
 // A tensor argument; null for None and for anything else.
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 void* ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
@@ -60,6 +82,38 @@ struct Args {
     // FP32 or BF16.
     void need_float(const at::Tensor* t, at::IntArrayRef shape) {
         if (ok && t) need(t, t->scalar_type() == kF32 ? kF32 : kBF16, shape);
+        want(t);
+    }
+    // A contiguous row of the last `inner` sizes for each token, where the sizes
+    // before are tokens; rows lie *ld elements apart, a row's width at least.
+    void need_rows(const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, int inner, int64_t* ld) {
+        ok = ok && t && t->is_cuda() && t->get_device() == dev && t->scalar_type() == type && t->sizes() == shape;
+        if (!ok) return;
+        const int dims = static_cast<int>(shape.size()), lead = dims - inner;
+        int64_t width = 1, rows = 1, step = 0;
+        if (t->numel() == 0) {   // no element has an address
+            for (int i = lead; i < dims; ++i) width *= shape[i];
+            *ld = width;
+            return;
+        }
+        for (int i = dims - 1; i >= lead; --i) {
+            ok = ok && (shape[i] == 1 || t->stride(i) == width);
+            width *= shape[i];
+        }
+        for (int i = lead - 1; i >= 0; --i) {
+            if (shape[i] == 1) continue;
+            if (rows == 1)
+                step = t->stride(i);
+            else
+                ok = ok && t->stride(i) == rows * step;
+            rows *= shape[i];
+        }
+        *ld = rows > 1 ? step : width;
+        ok = ok && *ld >= width;
+    }
+    // The same, BF16 or FP32.
+    void need_rows_float(const at::Tensor* t, at::IntArrayRef shape, int inner, int64_t* ld) {
+        if (ok && t) need_rows(t, t->scalar_type() == kF32 ? kF32 : kBF16, shape, inner, ld);
         want(t);
     }
     // None, or as need().
@@ -121,6 +175,13 @@ PyObject* result(int rc, PyObject* given, const at::Tensor& out) {
     if (rc != KDA_OK) return PyLong_FromLong(rc);
     return given != Py_None ? Py_NewRef(given) : THPVariable_Wrap(out);
 }
+// A tuple of two results, which it takes over.
+PyObject* two(PyObject* x, PyObject* y) {
+    PyObject* both = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return both;
+}
 
 // q, k, v, g, init_state, cu_seqlens, out, final_state, want_final, state_fp32, scale, stream
 PyObject* la_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -172,12 +233,7 @@ PyObject* la_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              (f32 ? KDA_FLAG_STATE_F32 : 0u) | (g->dim() == 1 ? KDA_FLAG_G_PER_HEAD : 0u), stream);
     });
     if (rc != KDA_OK) return PyLong_FromLong(rc);
-    PyObject* o = result(rc, a[6], new_out);
-    PyObject* f = !want_final ? Py_NewRef(Py_None) : result(rc, a[7], new_fin);
-    PyObject* both = o && f ? PyTuple_Pack(2, o, f) : nullptr;
-    Py_XDECREF(o);
-    Py_XDECREF(f);
-    return both;
+    return two(result(rc, a[6], new_out), !want_final ? Py_NewRef(Py_None) : result(rc, a[7], new_fin));
     END_HANDLE_TH_ERRORS
 }
 
@@ -316,12 +372,195 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 stream);
     });
     if (rc != KDA_OK) return PyLong_FromLong(rc);
-    PyObject* o = result(rc, a[7], made);
-    PyObject* r = result(rc, a[8], rmade);
-    PyObject* both = o && r ? PyTuple_Pack(2, o, r) : nullptr;
-    Py_XDECREF(o);
-    Py_XDECREF(r);
-    return both;
+    return two(result(rc, a[7], made), result(rc, a[8], rmade));
+    END_HANDLE_TH_ERRORS
+}
+
+// x, weight, bias, init_state, cu_seqlens, silu, out, final_state, want_final, stream
+PyObject* conv_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!counted(n, 10) || !bound(reinterpret_cast<void*>(conv_prefill_fn))) return nullptr;
+    const at::Tensor *x = tensor(a[0]), *weight = tensor(a[1]), *bias = tensor(a[2]), *init = tensor(a[3]), *cu = tensor(a[4]),
+                     *out = tensor(a[6]), *fin = tensor(a[7]);
+    Args c(x);
+    if (!c.dims(x, 3) || !c.dims(weight, 2)) Py_RETURN_NONE;
+    const int64_t B = x->size(0), T = x->size(1), D = x->size(2), W = weight->size(1);
+    int64_t ldx = 0;
+    c.want(W >= 2 && W <= 4);
+    c.need_rows(x, kBF16, {B, T, D}, 1, &ldx);
+    c.need_float(weight, {D, W});
+    if (!c.ok) Py_RETURN_NONE;
+    c.may(a[2], bias, weight->scalar_type(), {D});
+    int64_t N = B;
+    if (a[4] != Py_None) {
+        c.want(cu && B == 1 && cu->numel() > 0);
+        if (!c.ok) Py_RETURN_NONE;
+        N = cu->numel() - 1;
+        c.need(cu, at::kLong, {N + 1});
+    }
+    const int64_t shape[] = {N, W - 1, D};
+    c.may(a[3], init, kBF16, shape);
+    c.may(a[6], out, kBF16, x->sizes());
+    c.may(a[7], fin, kBF16, shape);
+    if (!c.ok) Py_RETURN_NONE;
+    void* stream;
+    bool silu, want_final;
+    if (!truth(a[5], &silu) || !truth(a[8], &want_final) || !stream_of(a[9], c.dev, &stream)) return nullptr;
+    at::Tensor new_out, new_fin;
+    want_final = want_final || fin;
+    const int rc = released([&] {
+        if (!out) out = &(new_out = at::empty(x->sizes(), x->options()));
+        if (!fin && want_final) fin = &(new_fin = at::empty(shape, x->options()));
+        return conv_prefill_fn(ptr(x), ldx, ptr(weight), ptr(bias), ptr(init), ptr(out), ptr(fin), N, T, D, static_cast<int>(W),
+                               static_cast<const int64_t*>(ptr(cu)), silu ? KDA_ACT_SILU : KDA_ACT_NONE,
+                               fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u, stream);
+    });
+    if (rc != KDA_OK) return PyLong_FromLong(rc);
+    return two(result(rc, a[6], new_out), !want_final ? Py_NewRef(Py_None) : result(rc, a[7], new_fin));
+    END_HANDLE_TH_ERRORS
+}
+
+// x, weight, state, bias, slots, silu, out, stream
+PyObject* conv_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!counted(n, 8) || !bound(reinterpret_cast<void*>(conv_decode_fn))) return nullptr;
+    const at::Tensor *x = tensor(a[0]), *weight = tensor(a[1]), *state = tensor(a[2]), *bias = tensor(a[3]),
+                     *slots = tensor(a[4]), *out = tensor(a[6]);
+    Args c(x);
+    if (!c.dims(x, 2) || !c.dims(weight, 2) || !c.dims(state, 3)) Py_RETURN_NONE;
+    const int64_t N = x->size(0), D = x->size(1), W = weight->size(1), pool = state->size(0);
+    int64_t ldx = 0;
+    c.want(W >= 2 && W <= 4);
+    c.need_rows(x, kBF16, {N, D}, 1, &ldx);
+    c.need_float(weight, {D, W});
+    c.need(state, kBF16, {pool, W - 1, D});
+    if (!c.ok) Py_RETURN_NONE;
+    c.may(a[3], bias, weight->scalar_type(), {D});
+    if (a[4] == Py_None)
+        c.want(N <= pool);
+    else
+        c.need(slots, at::kInt, {N});
+    c.may(a[6], out, kBF16, x->sizes());
+    if (!c.ok) Py_RETURN_NONE;
+    void* stream;
+    bool silu;
+    if (!truth(a[5], &silu) || !stream_of(a[7], c.dev, &stream)) return nullptr;
+    at::Tensor made;
+    const int rc = released([&] {
+        if (!out) out = &(made = at::empty(x->sizes(), x->options()));
+        return conv_decode_fn(ptr(x), ldx, ptr(weight), ptr(bias), ptr(state), static_cast<const int32_t*>(ptr(slots)), ptr(out),
+                              N, D, static_cast<int>(W), pool, silu ? KDA_ACT_SILU : KDA_ACT_NONE,
+                              fp32(weight) ? KDA_FLAG_WEIGHT_F32 : 0u, stream);
+    });
+    return result(rc, a[6], made);
+    END_HANDLE_TH_ERRORS
+}
+
+// What both forms of the scan read: x, dt, A, B, C, D, z, dt_bias, of `lead` tokens.
+struct Scan {
+    const at::Tensor *x, *dt, *A, *B, *C, *D, *z, *bias;
+    int64_t dim = 0, groups = 0, S = 0, ldx = 0, lddt = 0, ldb = 0, ldc = 0, ldz = 0;
+    Scan(Args& c, PyObject* const* a, int tokens_dims)
+        : x(tensor(a[0])), dt(tensor(a[1])), A(tensor(a[2])), B(tensor(a[3])), C(tensor(a[4])), D(tensor(a[5])),
+          z(tensor(a[6])), bias(tensor(a[7])) {
+        const int64_t d = tokens_dims;
+        if (!c.dims(x, d + 1) || !c.dims(A, 2) || !c.dims(B, d + 2)) return;
+        dim = x->size(d);
+        groups = B->size(d);
+        S = A->size(1);
+        c.want(groups > 0 && dim % groups == 0 && S > 0 && S <= 64);
+        c.need_rows(x, kBF16, x->sizes(), 1, &ldx);
+        c.need_rows_float(dt, x->sizes(), 1, &lddt);
+        c.need(A, kF32, {dim, S});
+        if (!c.ok) return;
+        at::DimVector keys(x->sizes().begin(), x->sizes().end() - 1);
+        keys.push_back(groups);
+        keys.push_back(S);
+        c.need_rows_float(B, keys, 2, &ldb);
+        if (c.ok) c.need_rows(C, B->scalar_type(), keys, 2, &ldc);
+        c.may(a[5], D, kF32, {dim});
+        if (a[6] != Py_None) c.need_rows(z, kBF16, x->sizes(), 1, &ldz);
+        c.may(a[7], bias, kF32, {dim});
+    }
+    uint32_t flags(bool state_f32, bool softplus) const {
+        return (state_f32 ? KDA_FLAG_STATE_F32 : 0u) | (fp32(dt) ? KDA_FLAG_DT_F32 : 0u) | (fp32(B) ? KDA_FLAG_BC_F32 : 0u) |
+               (softplus ? KDA_FLAG_DT_SOFTPLUS : 0u);
+    }
+    static const float* f(const at::Tensor* t) { return static_cast<const float*>(ptr(t)); }
+};
+
+// x, dt, A, B, C, D, z, dt_bias, dt_softplus, init_state, cu_seqlens, out, final_state, want_final, state_fp32, stream
+PyObject* ssm_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!counted(n, 16) || !bound(reinterpret_cast<void*>(ssm_prefill_fn))) return nullptr;
+    Args c(tensor(a[0]));
+    const Scan s(c, a, 2);
+    if (!c.ok) Py_RETURN_NONE;
+    const at::Tensor *init = tensor(a[9]), *cu = tensor(a[10]), *out = tensor(a[11]), *fin = tensor(a[12]);
+    const int64_t B = s.x->size(0), T = s.x->size(1);
+    int64_t N = B;
+    if (a[10] != Py_None) {
+        c.want(cu && B == 1 && cu->numel() > 0);
+        if (!c.ok) Py_RETURN_NONE;
+        N = cu->numel() - 1;
+        c.need(cu, at::kLong, {N + 1});
+    }
+    bool softplus, f32, want_final;
+    if (!truth(a[8], &softplus) || !truth(a[14], &f32) || !truth(a[13], &want_final)) return nullptr;
+    const int64_t shape[] = {N, s.dim, s.S};
+    if (a[9] != Py_None) {
+        c.need_float(init, shape);
+        f32 = fp32(init);
+    } else if (a[12] != Py_None) {
+        c.need_float(fin, shape);
+        f32 = fp32(fin);
+    }
+    c.may(a[12], fin, f32 ? kF32 : kBF16, shape);
+    c.may(a[11], out, kBF16, s.x->sizes());
+    if (!c.ok) Py_RETURN_NONE;
+    void* stream;
+    if (!stream_of(a[15], c.dev, &stream)) return nullptr;
+    at::Tensor new_out, new_fin;
+    want_final = want_final || fin;
+    const int rc = released([&] {
+        if (!out) out = &(new_out = at::empty(s.x->sizes(), s.x->options()));
+        if (!fin && want_final) fin = &(new_fin = at::empty(shape, s.x->options().dtype(f32 ? kF32 : kBF16)));
+        return ssm_prefill_fn(ptr(s.x), s.ldx, ptr(s.dt), s.lddt, Scan::f(s.A), ptr(s.B), s.ldb, ptr(s.C), s.ldc, Scan::f(s.D),
+                              ptr(s.z), s.ldz, Scan::f(s.bias), ptr(init), ptr(out), ptr(fin), N, T, s.dim, s.groups, s.S,
+                              static_cast<const int64_t*>(ptr(cu)), s.flags(f32, softplus), stream);
+    });
+    if (rc != KDA_OK) return PyLong_FromLong(rc);
+    return two(result(rc, a[11], new_out), !want_final ? Py_NewRef(Py_None) : result(rc, a[12], new_fin));
+    END_HANDLE_TH_ERRORS
+}
+
+// x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, slots, out, stream
+PyObject* ssm_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!counted(n, 13) || !bound(reinterpret_cast<void*>(ssm_decode_fn))) return nullptr;
+    Args c(tensor(a[0]));
+    const Scan s(c, a, 1);
+    const at::Tensor *state = tensor(a[9]), *slots = tensor(a[10]), *out = tensor(a[11]);
+    if (!c.dims(state, 3)) Py_RETURN_NONE;
+    const int64_t N = s.x->size(0), pool = state->size(0);
+    c.need_float(state, {pool, s.dim, s.S});
+    if (a[10] == Py_None)
+        c.want(N <= pool);
+    else
+        c.need(slots, at::kInt, {N});
+    c.may(a[11], out, kBF16, s.x->sizes());
+    if (!c.ok) Py_RETURN_NONE;
+    void* stream;
+    bool softplus;
+    if (!truth(a[8], &softplus) || !stream_of(a[12], c.dev, &stream)) return nullptr;
+    at::Tensor made;
+    const int rc = released([&] {
+        if (!out) out = &(made = at::empty(s.x->sizes(), s.x->options()));
+        return ssm_decode_fn(ptr(s.x), s.ldx, ptr(s.dt), s.lddt, Scan::f(s.A), ptr(s.B), s.ldb, ptr(s.C), s.ldc, Scan::f(s.D),
+                             ptr(s.z), s.ldz, Scan::f(s.bias), ptr(state), static_cast<const int32_t*>(ptr(slots)), ptr(out), N,
+                             s.dim, s.groups, s.S, pool, s.flags(fp32(state), softplus), stream);
+    });
+    return result(rc, a[11], made);
     END_HANDLE_TH_ERRORS
 }
 
@@ -330,6 +569,11 @@ PyCFunction method(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_ca
 
 PyMethodDef methods[] = {
     {"bind", method(bind), METH_FASTCALL, nullptr},
+    {"bind_scan", method(bind_scan), METH_FASTCALL, nullptr},
+    {"conv_prefill", method(conv_prefill), METH_FASTCALL, nullptr},
+    {"conv_decode", method(conv_decode), METH_FASTCALL, nullptr},
+    {"ssm_prefill", method(ssm_prefill), METH_FASTCALL, nullptr},
+    {"ssm_decode", method(ssm_decode), METH_FASTCALL, nullptr},
     {"la_prefill", method(la_prefill), METH_FASTCALL, nullptr},
     {"la_decode", method(la_decode), METH_FASTCALL, nullptr},
     {"kda_decode", method(kda_step), METH_FASTCALL, nullptr},
