@@ -21,75 +21,89 @@ namespace {
 constexpr int kConvThreads = 256;
 constexpr int kGroup = 4;   // tokens whose loads are under way together
 
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, uint4& r) { r = *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, uint32_t& r) { r = *reinterpret_cast<const uint32_t*>(p); }
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, uint16_t& r) { r = *reinterpret_cast<const uint16_t*>(p); }
-
-// kVec consecutive BF16 values as loaded: 8, or 2 or 1 where rows start at any element.
+// kVec consecutive BF16 values as loaded, and as pairs of FP32 values (of one: with
+// a zero): 4, or 2 or 1 where rows start at any element.
 template <int kVec>
 struct Raw;
 template <>
-struct Raw<8> {
-    using type = uint4;
-    __device__ static void unpack(const uint4& r, float (&x)[8]) { unpack8(r, x); }
-    __device__ static uint4 zero() { return make_uint4(0, 0, 0, 0); }
+struct Raw<4> {
+    using type = uint2;
+    __device__ __forceinline__ static void unpack(uint2 r, uint64_t (&x)[2]) {
+        x[0] = pair(bf16_lo(r.x), bf16_hi(r.x));
+        x[1] = pair(bf16_lo(r.y), bf16_hi(r.y));
+    }
+    __device__ __forceinline__ static uint2 pack(const uint64_t (&x)[2]) {
+        const float2 a = halves(x[0]), b = halves(x[1]);
+        return make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+    }
+    __device__ __forceinline__ static uint2 zero() { return make_uint2(0, 0); }
 };
 template <>
 struct Raw<2> {
     using type = uint32_t;
-    __device__ static void unpack(uint32_t r, float (&x)[2]) {
-        x[0] = bf16_lo(r);
-        x[1] = bf16_hi(r);
+    __device__ __forceinline__ static void unpack(uint32_t r, uint64_t (&x)[1]) { x[0] = pair(bf16_lo(r), bf16_hi(r)); }
+    __device__ __forceinline__ static uint32_t pack(const uint64_t (&x)[1]) {
+        const float2 a = halves(x[0]);
+        return pack_bf16(a.x, a.y);
     }
-    __device__ static uint32_t zero() { return 0; }
+    __device__ __forceinline__ static uint32_t zero() { return 0; }
 };
 template <>
 struct Raw<1> {
     using type = uint16_t;
-    __device__ static void unpack(uint16_t r, float (&x)[1]) { x[0] = bf16_lo(r); }
-    __device__ static uint16_t zero() { return 0; }
+    __device__ __forceinline__ static void unpack(uint16_t r, uint64_t (&x)[1]) { x[0] = pair(bf16_lo(r), 0.f); }
+    __device__ __forceinline__ static uint16_t pack(const uint64_t (&x)[1]) {
+        return static_cast<uint16_t>(pack_bf16(halves(x[0]).x, 0.f));
+    }
+    __device__ __forceinline__ static uint16_t zero() { return 0; }
 };
+template <int kVec>
+using RawT = typename Raw<kVec>::type;
+template <int kVec>
+__device__ __forceinline__ RawT<kVec> load_raw(const __nv_bfloat16* p) {
+    return *reinterpret_cast<const RawT<kVec>*>(p);
+}
+template <int kVec>
+__device__ __forceinline__ void store_raw(__nv_bfloat16* p, RawT<kVec> r) {
+    *reinterpret_cast<RawT<kVec>*>(p) = r;
+}
 
 // A thread's filter: kVec channels with kW taps each, and their bias.
 template <int kW, int kVec>
 struct Filter {
-    float w[kW][kVec], b[kVec];
+    static constexpr int kPairs = (kVec + 1) / 2;
+    uint64_t w[kW][kPairs], b[kPairs];
 
     template <typename T>
-    __device__ __forceinline__ void load_as(const void* weight, const void* bias, int64_t ch) {
-        float flat[kW * kVec];
+    __device__ __forceinline__ void load_as(const T* weight, const T* bias, int64_t ch) {
+        float f[2 * kPairs * kW] = {}, c[2 * kPairs] = {};
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            float part[kVec];
-            load_vec<kVec>(static_cast<const T*>(weight) + ch * kW + i * kVec, part);
+        for (int i = 0; i < kW; ++i) load_vec<kVec>(weight + ch * kW + i * kVec, *reinterpret_cast<float(*)[kVec]>(f + i * kVec));
+        if (bias) load_vec<kVec>(bias + ch, *reinterpret_cast<float(*)[kVec]>(c));
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) flat[i * kVec + j] = part[j];
+        for (int j = 0; j < kPairs; ++j) {
+            b[j] = pair(c[2 * j], c[2 * j + 1]);
+#pragma unroll
+            for (int i = 0; i < kW; ++i) w[i][j] = pair(f[2 * j * kW + i], f[(2 * j + 1) * kW + i]);
         }
-#pragma unroll
-        for (int i = 0; i < kW; ++i)
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) w[i][j] = flat[j * kW + i];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) b[j] = 0.f;
-        if (bias) load_vec<kVec>(static_cast<const T*>(bias) + ch, b);
     }
     __device__ __forceinline__ void load(const ConvArgs& a, int64_t ch) {
         if (a.weight_f32)
-            load_as<float>(a.weight, a.bias, ch);
+            load_as(static_cast<const float*>(a.weight), static_cast<const float*>(a.bias), ch);
         else
-            load_as<__nv_bfloat16>(a.weight, a.bias, ch);
+            load_as(static_cast<const __nv_bfloat16*>(a.weight), static_cast<const __nv_bfloat16*>(a.bias), ch);
     }
     // Row kW - 1 of x is the token's own.
-    __device__ __forceinline__ void apply(const float (*x)[kVec], bool silu, __nv_bfloat16* out) const {
-        float y[kVec];
+    __device__ __forceinline__ RawT<kVec> apply(const uint64_t (*x)[kPairs], bool silu) const {
+        uint64_t y[kPairs];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
             y[j] = b[j];
 #pragma unroll
-            for (int i = 0; i < kW; ++i) y[j] = fmaf(w[i][j], x[i][j], y[j]);
-            if (silu) y[j] *= sigmoid(y[j]);
+            for (int i = 0; i < kW; ++i) y[j] = fma_pair(w[i][j], x[i][j], y[j]);
+            if (silu) y[j] = silu_pair(y[j]);
         }
-        store_vec<kVec>(out, y);
+        return Raw<kVec>::pack(y);
     }
 };
 
@@ -101,7 +115,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
     const int64_t run = at / vecs, ch = (at - run * vecs) * kVec;
     if (run >= a.runs) return;
     using R = Raw<kVec>;
-    constexpr int kKeep = kW - 1;
+    constexpr int kKeep = kW - 1, kPairs = Filter<kW, kVec>::kPairs;
     const auto x = static_cast<const __nv_bfloat16*>(a.x) + ch;
     const auto init = static_cast<const __nv_bfloat16*>(a.init_state) + ch;
     const auto out = static_cast<__nv_bfloat16*>(a.out) + ch;
@@ -126,59 +140,72 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
     Filter<kW, kVec> filter;
     filter.load(a, ch);
 
-    float win[kKeep + kGroup][kVec];   // the kKeep rows before token t, oldest first, and a group's own
-    // Row `back` rows before token t of the sequence.
-    auto before = [&](int back, float (&row)[kVec]) {
-        typename R::type r = R::zero();
-        if (t - back >= begin)
-            load_bf16(x + (t - back) * a.ldx, r);
-        else if (a.init_state)
-            load_bf16(init + (seq * kKeep + kKeep + (t - back - begin)) * a.D, r);
-        R::unpack(r, row);
-    };
+    uint64_t win[kKeep + kGroup][kPairs];   // the kKeep rows before token t, oldest first, and a group's own
     auto window = [&]() {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) before(kKeep - i, win[i]);
+        for (int i = 0; i < kKeep; ++i) {
+            RawT<kVec> r = R::zero();
+            const int64_t at = t - kKeep + i;   // below the sequence's first token: the initial state
+            if (at >= begin)
+                r = load_raw<kVec>(x + at * a.ldx);
+            else if (a.init_state)
+                r = load_raw<kVec>(init + (seq * kKeep + kKeep + (at - begin)) * a.D);
+            R::unpack(r, win[i]);
+        }
     };
     // The states of the sequences that end at token t; the next one's window.
     auto close = [&]() {
         while (t == seq_end) {
             if (a.final_state)
 #pragma unroll
-                for (int i = 0; i < kKeep; ++i) store_vec<kVec>(final_state + (seq * kKeep + i) * a.D, win[i]);
+                for (int i = 0; i < kKeep; ++i) store_raw<kVec>(final_state + (seq * kKeep + i) * a.D, R::pack(win[i]));
             if (!kPacked || ++seq >= a.N) break;
             begin = seq_end;
             seq_end = a.cu_seqlens[seq + 1];
             window();
         }
     };
+    auto shift = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) win[i][j] = win[n + i][j];
+    };
+    // The group after the one at hand is on its way while that is worked on.
+    RawT<kVec> ahead[kGroup];
+    const __nv_bfloat16* next = x + t * a.ldx;
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) ahead[i] = load_raw<kVec>(next + i * a.ldx);
+    };
+    bool fetched = t + kGroup <= end;
+    if (fetched) fetch();
     window();
     close();
     while (t < end) {
         // A whole group within the sequence, or a token at a time.
-        if (t + kGroup <= end && t + kGroup <= seq_end) {
-            typename R::type raw[kGroup];
+        if (fetched && t + kGroup <= seq_end) {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) load_bf16(x + (t + i) * a.ldx, raw[i]);
+            for (int i = 0; i < kGroup; ++i) R::unpack(ahead[i], win[kKeep + i]);
+            next += kGroup * a.ldx;
+            fetched = t + 2 * kGroup <= end;
+            if (fetched) fetch();
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) R::unpack(raw[i], win[kKeep + i]);
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) filter.apply(win + i, a.silu, out + (t + i) * a.D);
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) win[i][j] = win[kGroup + i][j];
+            for (int i = 0; i < kGroup; ++i) store_raw<kVec>(out + (t + i) * a.D, filter.apply(win + i, a.silu));
+            shift(kGroup);
             t += kGroup;
         } else {
-            typename R::type raw;
-            load_bf16(x + t * a.ldx, raw);
-            R::unpack(raw, win[kKeep]);
-            filter.apply(win, a.silu, out + t * a.D);
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) win[i][j] = win[i + 1][j];
-            ++t;
+            for (int i = 0; i < kGroup && t < end; ++i) {
+                R::unpack(load_raw<kVec>(next), win[kKeep]);
+                next += a.ldx;
+                store_raw<kVec>(out + t * a.D, filter.apply(win, a.silu));
+                shift(1);
+                ++t;
+                close();
+            }
+            fetched = t + kGroup <= end;
+            if (fetched) fetch();
+            continue;
         }
         close();
     }
@@ -206,13 +233,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_decode_kernel(ConvArgs a) {
             slot[i] = -1;
         }
     }
-    typename R::type raw[kSeqs][kW];
+    RawT<kVec> raw[kSeqs][kW];
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i)
         if (slot[i] >= 0) {
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) load_bf16(state + (slot[i] * kKeep + j) * a.D, raw[i][j]);
-            load_bf16(x + (part * kSeqs + i) * a.ldx, raw[i][kKeep]);
+            for (int j = 0; j < kKeep; ++j) raw[i][j] = load_raw<kVec>(state + (slot[i] * kKeep + j) * a.D);
+            raw[i][kKeep] = load_raw<kVec>(x + (part * kSeqs + i) * a.ldx);
         }
     Filter<kW, kVec> filter;
     filter.load(a, ch);
@@ -220,27 +247,25 @@ __global__ void __launch_bounds__(kConvThreads) conv_decode_kernel(ConvArgs a) {
     for (int i = 0; i < kSeqs; ++i) {
         const int64_t n = part * kSeqs + i;
         if (slot[i] >= 0) {
-            float win[kW][kVec];
+            uint64_t win[kW][Filter<kW, kVec>::kPairs];
 #pragma unroll
             for (int j = 0; j < kW; ++j) {
                 R::unpack(raw[i][j], win[j]);
-                if (j > 0) *reinterpret_cast<typename R::type*>(state + (slot[i] * kKeep + j - 1) * a.D) = raw[i][j];
+                if (j > 0) store_raw<kVec>(state + (slot[i] * kKeep + j - 1) * a.D, raw[i][j]);
             }
-            filter.apply(win, a.silu, out + n * a.D);
+            store_raw<kVec>(out + n * a.D, filter.apply(win, a.silu));
         } else if (n < a.N) {
-            *reinterpret_cast<typename R::type*>(out + n * a.D) = R::zero();
+            store_raw<kVec>(out + n * a.D, R::zero());
         }
     }
 }
 
-bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-bool on4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
-
-// The widest vector that every row starts on: 8 channels need rows and filters
-// on 16 bytes, 2 on 4 (filters are 16-byte aligned tensors).
+// The widest vector that every row of x starts on (the other tensors start on 16 bytes).
 int conv_vec(const ConvArgs& a) {
-    if (a.D % 8 == 0 && (a.rows < 2 || a.ldx % 8 == 0) && on16(a.x)) return 8;
-    return a.D % 2 == 0 && (a.rows < 2 || a.ldx % 2 == 0) && on4(a.x) ? 2 : 1;
+    auto fits = [&](int n) {
+        return a.D % n == 0 && (a.rows < 2 || a.ldx % n == 0) && reinterpret_cast<uintptr_t>(a.x) % (2 * n) == 0;
+    };
+    return fits(4) ? 4 : fits(2) ? 2 : 1;
 }
 
 template <int kW, int kVec>
@@ -284,7 +309,7 @@ cudaError_t pick(const ConvArgs& a, bool decode, int sms, cudaStream_t stream) {
 template <int kW>
 cudaError_t pick(const ConvArgs& a, bool decode, int sms, cudaStream_t stream) {
     const int vec = conv_vec(a);
-    if (vec == 8) return pick<kW, 8>(a, decode, sms, stream);
+    if (vec == 4) return pick<kW, 4>(a, decode, sms, stream);
     return vec == 2 ? pick<kW, 2>(a, decode, sms, stream) : pick<kW, 1>(a, decode, sms, stream);
 }
 cudaError_t pick(const ConvArgs& a, bool decode, int sms, cudaStream_t stream) {

@@ -328,7 +328,7 @@ constexpr int kSsmChannels = 32;
 constexpr int64_t kSsmMaxState = 64;
 // Adds the kernels it launches to *launches.
 cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches);
-cudaError_t launch_ssm_decode(const SsmArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_ssm_decode(SsmArgs a, cudaStream_t stream);
 // Up to this many offsets every CTA checks them itself.
 constexpr int64_t kMaxSelfChecked = 1024;
 

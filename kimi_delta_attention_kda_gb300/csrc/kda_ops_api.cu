@@ -735,7 +735,7 @@ extern "C" int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_
     rc = device_view(&d);
     if (rc != KDA_OK || N == 0) return rc;
     a.status = d.status;
-    if (launch_ssm_decode(a, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    if (launch_ssm_decode(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return KDA_ERR_CUDA;
     }

@@ -22,6 +22,8 @@
 // forms the state each span ends with (and the sum of its dt: the decay over a
 // span is exp(A sum dt)), a second one each span's incoming state from those
 // before it, and its outputs.
+#include <type_traits>
+
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
@@ -31,44 +33,52 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kRole = 128;               // threads that walk, and threads that stage and finish
+constexpr int kThreads = 2 * kRole;
 constexpr int kTile = kSsmTile;          // tokens at a time
 constexpr int kChannels = kSsmChannels;  // channels of a CTA, 8 a warp
-static_assert(kThreads == 4 * kTile && kChannels == 32, "a thread stages 8 channels of one token");
+static_assert(kRole == 4 * kTile && kChannels == 32, "a thread stages 8 channels of one token");
 constexpr float kLog2e = 1.4426950408889634f;
 
-// log(1 + t) / t on [0, 1]: a polynomial of degree 8 fitted to the least relative
-// error (3e-8; 1.8e-7 as evaluated in FP32).
-__device__ __forceinline__ uint64_t log1p_over(uint64_t t) {
+// softplus(u) = max(u, 0) + log(1 + exp(-|u|)) of n pairs.  log(1 + t) / t on [0, 1]
+// is a polynomial of degree 8 fitted to the least relative error (3e-8; 1.8e-7 as
+// evaluated in FP32), all pairs a coefficient at a time.  NaN stays (through exp).
+template <int n>
+__device__ __forceinline__ void softplus(float2 (&u)[n]) {
     constexpr float c[] = {0.99999994f,   -0.499994934f, 0.333190978f,  -0.24842982f, 0.191060051f,
                            -0.136632428f, 0.0782259107f, -0.0295052137f, 0.00523268804f};
-    uint64_t p = pair(c[8], c[8]);
+    uint64_t t[n], p[n];
 #pragma unroll
-    for (int i = 7; i >= 0; --i) p = fma_pair(p, t, pair(c[i], c[i]));
-    return p;
-}
-// softplus(u) = max(u, 0) + log(1 + exp(-|u|)) of two values.  NaN stays.
-__device__ __forceinline__ float2 softplus(float2 u) {
-    const float2 m = make_float2(-fabsf(u.x) * kLog2e, -fabsf(u.y) * kLog2e);
-    const uint64_t t = pair(exp2_fast(m.x), exp2_fast(m.y));
-    const uint64_t top = pair(u.x < 0.f ? 0.f : u.x, u.y < 0.f ? 0.f : u.y);
-    return halves(fma_pair(t, log1p_over(t), top));
+    for (int i = 0; i < n; ++i) {
+        t[i] = pair(exp2_fast(fabsf(u[i].x) * -kLog2e), exp2_fast(fabsf(u[i].y) * -kLog2e));
+        p[i] = pair(c[8], c[8]);
+    }
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+        const uint64_t ck = pair(c[k], c[k]);
+#pragma unroll
+        for (int i = 0; i < n; ++i) p[i] = fma_pair(p[i], t[i], ck);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) u[i] = halves(fma_pair(t[i], p[i], pair(fmaxf(u[i].x, 0.f), fmaxf(u[i].y, 0.f))));
 }
 
-// Shared memory of one of two buffers: (dt, dt x) as [channel][token] pairs, the
-// rows of B and C, and y.  Strides that keep the lanes' accesses on different banks:
-// a warp reads two tokens of 8 channels (16 bytes, 68 words apart), a thread
-// writes one token of 8 channels (8 words more for each 8 channels).
-constexpr int kStepStride = 2 * (kTile + 2);
+// Shared memory of one of two buffers: (dt, dt, dt x, dt x) for each channel and
+// token, as the packed instructions take them (made from one value each, the pairs
+// cost two more instructions a token), the rows of B and C, and y.  Strides that keep the lanes'
+// accesses on different banks: a warp reads one token of 8 channels (16 bytes each),
+// a thread writes 8 channels of one token (8 words more for each 8 channels).
+constexpr int kStepStride = 4 * (kTile + 1);
 constexpr int kStepWords = kChannels * kStepStride + 8 * (kChannels / 8);
 constexpr int kYStride = kChannels + 4;
 template <int kBlocks, bool kStates>
 struct Buffer {
     static constexpr int kRow = 16 * kBlocks;
     static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRow);
-    static constexpr int kWords = kY + (kStates ? 0 : kTile * kYStride);
+    static constexpr int kXZ = kY + (kStates ? 0 : kTile * kYStride);   // x and z of each staging thread, for its outputs
+    static constexpr int kWords = kXZ + (kStates ? 0 : 8 * kRole);
 };
-__device__ __forceinline__ int step_at(int ch, int token) { return ch * kStepStride + 8 * (ch >> 3) + 2 * token; }
+__device__ __forceinline__ int step_at(int ch, int token) { return ch * kStepStride + 8 * (ch >> 3) + 4 * token; }
 
 // What a thread stages of a tile, as loaded: 8 channels of one token, and for
 // each block of 16 states 4 values of B and of C.
@@ -157,6 +167,28 @@ __device__ __forceinline__ void store_row(void* p, bool f32, int64_t row, int c,
             store_states(static_cast<__nv_bfloat16*>(p) + row * S, 16 * k + 4 * c, S, v);
     }
 }
+// A lane's values of a row of B or C, `at` elements behind p.
+template <int kBlocks>
+__device__ __forceinline__ void load_keys(const void* p, bool f32, bool wide, int64_t at, int c, int S, uint64_t (&v)[kBlocks][2]) {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const int n0 = 16 * k + 4 * c;
+        float x[4] = {};
+        if (f32 && wide) {
+            if (n0 < S) load_vec<4>(static_cast<const float*>(p) + at + n0, x);
+        } else if (wide) {
+            if (n0 < S) load_vec<4>(static_cast<const __nv_bfloat16*>(p) + at + n0, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n0 + i < S)
+                    x[i] = f32 ? static_cast<const float*>(p)[at + n0 + i]
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + n0 + i]);
+        }
+        v[k][0] = pair(x[0], x[1]);
+        v[k][1] = pair(x[2], x[3]);
+    }
+}
 // h <- exp2(A s) h + b for a lane's states (A in units of log 2).
 template <int kBlocks>
 __device__ __forceinline__ void decay(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt, const uint64_t (&b)[kBlocks][2]) {
@@ -169,7 +201,13 @@ __device__ __forceinline__ void decay(State<kBlocks>& s, const State<kBlocks>& r
         }
 }
 
-// D = A B for one m16n8k8 tile of TF32 operands, the sum in FP32.
+// D = A B, or A B + D, for one m16n8k8 tile of TF32 operands, the sum in FP32.
+__device__ __forceinline__ void mma_tf32_first(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(0.f));
+}
 __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -227,160 +265,204 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
     return w;
 }
 
+// Half of the warps walk; the other half stage the tile ahead and finish the one
+// behind, so that there are warps enough to hide each other's latencies.
 template <int kBlocks, bool kStates, bool kPacked>
-__global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
     using Buf = Buffer<kBlocks, kStates>;
     extern __shared__ __align__(16) float smem[];
     wait_for_kernel_before();
     if (kStates) let_next_kernel_come();
     if (kPacked && !offsets_hold(a.cu_seqlens, a.N, a.tokens, a.valid, a.status)) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
     const int64_t span = blockIdx.x / a.tiles, tile = blockIdx.x - span * a.tiles;
-    Part w = part_of<kStates, kPacked>(a, span);
+    const Part w = part_of<kStates, kPacked>(a, span);
     if (!w.run) return;
     const int64_t group = tile / a.tiles_per_group, per = a.dim / a.groups;
     const int64_t ch0 = group * per + (tile - group * a.tiles_per_group) * kChannels;
     const int channels = static_cast<int>((group + 1) * per - ch0 < kChannels ? (group + 1) * per - ch0 : kChannels);
     const int S = static_cast<int>(a.nstate);
+    const int tid = threadIdx.x & (kRole - 1);
+    const int64_t total = w.end - w.begin;   // tokens; tiles i = 0 .. tiles - 1 of them
+    const int tiles = static_cast<int>((total + kTile - 1) / kTile);
 
-    // ---- staging: 8 channels of a token, a quarter of its rows of B and C
-    const int mine = 8 * (tid & 3), tok = tid >> 2;   // first channel within the CTA, token within the tile
-    const int count = channels - mine < 8 ? (channels - mine > 0 ? channels - mine : 0) : 8;
-    const bool wide = a.vec && count == 8;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = a.dt_bias && i < count ? a.dt_bias[ch0 + mine + i] : 0.f;
-        skip[i] = !kStates && a.D && i < count ? a.D[ch0 + mine + i] : 0.f;
-    }
-    auto fetch = [&](int64_t base, Fetched<kBlocks>& f) {
-        const int64_t t = base + tok;
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        f.x = f.z = f.dt[0] = f.dt[1] = none;
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) f.b[k] = f.c[k] = none;
-        if (t >= w.end) return;
-        const auto x = static_cast<const __nv_bfloat16*>(a.x) + t * a.ldx + ch0 + mine;
-        const auto z = static_cast<const __nv_bfloat16*>(a.z) + t * a.ldz + ch0 + mine;
-        const int64_t dt_at = t * a.lddt + ch0 + mine;
-        if (wide) {
-            f.x = *reinterpret_cast<const uint4*>(x);
-            if (!kStates && a.z) f.z = *reinterpret_cast<const uint4*>(z);
-            if (a.dt_f32) {
-                const auto p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.dt) + dt_at);
-                f.dt[0] = p[0];
-                f.dt[1] = p[1];
-            } else {
-                f.dt[0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dt) + dt_at);
-            }
-        } else {
-            f.x = gather8(x, count);
-            if (!kStates && a.z) f.z = gather8(z, count);
-            if (a.dt_f32) {
-                f.dt[0] = gather4(static_cast<const float*>(a.dt) + dt_at, count);
-                f.dt[1] = gather4(static_cast<const float*>(a.dt) + dt_at + 4, count - 4);
-            } else {
-                f.dt[0] = gather8(static_cast<const __nv_bfloat16*>(a.dt) + dt_at, count);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-            const int n0 = 16 * k + 4 * (tid & 3);
-            const int64_t b_at = t * a.ldb + group * S + n0, c_at = t * a.ldc + group * S + n0;
-            const int have = S - n0;
-            if (have <= 0) continue;
-            if (a.bc_f32) {
-                const float *b = static_cast<const float*>(a.B) + b_at, *cc = static_cast<const float*>(a.C) + c_at;
-                if (a.vec_bc) {
-                    f.b[k] = *reinterpret_cast<const uint4*>(b);
-                    if (!kStates) f.c[k] = *reinterpret_cast<const uint4*>(cc);
-                } else {
-                    f.b[k] = gather4(b, have);
-                    if (!kStates) f.c[k] = gather4(cc, have);
-                }
-            } else {
-                const auto b = static_cast<const __nv_bfloat16*>(a.B) + b_at, cc = static_cast<const __nv_bfloat16*>(a.C) + c_at;
-                if (a.vec_bc) {
-                    const uint2 rb = *reinterpret_cast<const uint2*>(b);
-                    f.b[k] = make_uint4(rb.x, rb.y, 0, 0);
-                    if (!kStates) {
-                        const uint2 rc = *reinterpret_cast<const uint2*>(cc);
-                        f.c[k] = make_uint4(rc.x, rc.y, 0, 0);
-                    }
-                } else {
-                    f.b[k] = gather8(b, have < 4 ? have : 4);
-                    if (!kStates) f.c[k] = gather8(cc, have < 4 ? have : 4);
-                }
-            }
-        }
-    };
-    // To the nearest TF32 value, which a BF16 one is.
-    auto tf32 = [](float v) {
-        uint32_t r;
-        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-        return __uint_as_float(r);
-    };
-    auto four = [&](const uint4& r) {
-        return a.bc_f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
-                        : make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
-    };
-    auto stage = [&](int64_t base, const Fetched<kBlocks>& f, float* buf) {
-        float u[8], x[8];
-        unpack8(f.x, x);
-        if (a.dt_f32) {
-            u[0] = __uint_as_float(f.dt[0].x); u[1] = __uint_as_float(f.dt[0].y);
-            u[2] = __uint_as_float(f.dt[0].z); u[3] = __uint_as_float(f.dt[0].w);
-            u[4] = __uint_as_float(f.dt[1].x); u[5] = __uint_as_float(f.dt[1].y);
-            u[6] = __uint_as_float(f.dt[1].z); u[7] = __uint_as_float(f.dt[1].w);
-        } else {
-            unpack8(f.dt[0], u);
-        }
-        const bool here = base + tok < w.end;   // behind the end nothing decays and nothing is added
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float2 dt = make_float2(u[i] + bias[i], u[i + 1] + bias[i + 1]);
-            if (a.softplus) dt = softplus(dt);
-            if (!here) dt = make_float2(0.f, 0.f);
-            *reinterpret_cast<float2*>(buf + step_at(mine + i, tok)) = make_float2(dt.x, dt.x * x[i]);
-            *reinterpret_cast<float2*>(buf + step_at(mine + i + 1, tok)) = make_float2(dt.y, dt.y * x[i + 1]);
-        }
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-            const int at = tok * Buf::kRow + 16 * k + 4 * (tid & 3);
-            *reinterpret_cast<float4*>(buf + Buf::kB + at) = four(f.b[k]);
-            if (!kStates) {
-                float4 keys = four(f.c[k]);
-                if (a.bc_f32) keys = make_float4(tf32(keys.x), tf32(keys.y), tf32(keys.z), tf32(keys.w));
-                *reinterpret_cast<float4*>(buf + Buf::kC + at) = keys;
-            }
-        }
-    };
-    // A token's outputs from its y: the skip, the gate and one rounding.
-    auto finish = [&](int64_t base, const uint4& xr, const uint4& zr, const float* buf) {
-        const int64_t t = base + tok;
-        if (t >= w.end) return;
-        float y[8], x[8], z[8];
-        const float4* p = reinterpret_cast<const float4*>(buf + Buf::kY + tok * kYStride + mine);
-        const float4 lo = p[0], hi = p[1];
-        y[0] = lo.x; y[1] = lo.y; y[2] = lo.z; y[3] = lo.w; y[4] = hi.x; y[5] = hi.y; y[6] = hi.z; y[7] = hi.w;
-        unpack8(xr, x);
-        unpack8(zr, z);
+    if (threadIdx.x >= kRole) {
+        // ---- staging: 8 channels of a token, a quarter of its rows of B and C
+        const int mine = 8 * (tid & 3), tok = tid >> 2;   // first channel within the CTA, token within the tile
+        const int count = channels - mine < 8 ? (channels - mine > 0 ? channels - mine : 0) : 8;
+        const bool wide = a.vec && count == 8, gated = !kStates && a.z;
+        float bias[8], skip[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (a.D) y[i] = fmaf(skip[i], x[i], y[i]);
-            if (a.z) y[i] *= z[i] * sigmoid(z[i]);
+            bias[i] = a.dt_bias && i < count ? a.dt_bias[ch0 + mine + i] : 0.f;
+            skip[i] = !kStates && a.D && i < count ? a.D[ch0 + mine + i] : 0.f;
         }
-        const auto out = static_cast<__nv_bfloat16*>(a.out) + t * a.dim + ch0 + mine;
-        if (a.vec && count == 8) {
-            store8(out, y);
-        } else {
+        // This thread's rows of the tile to fetch next, and to finish.
+        const int es = a.bc_f32 ? 4 : 2, dts = a.dt_f32 ? 4 : 2;
+        const int64_t t0 = w.begin + tok;
+        auto xp = static_cast<const __nv_bfloat16*>(a.x) + t0 * a.ldx + ch0 + mine;
+        auto zp = static_cast<const __nv_bfloat16*>(a.z) + t0 * a.ldz + ch0 + mine;
+        auto dp = static_cast<const uint8_t*>(a.dt) + (t0 * a.lddt + ch0 + mine) * dts;
+        auto bp = static_cast<const uint8_t*>(a.B) + (t0 * a.ldb + group * S + 4 * (tid & 3)) * es;
+        auto cp = static_cast<const uint8_t*>(a.C) + (t0 * a.ldc + group * S + 4 * (tid & 3)) * es;
+        auto op = static_cast<__nv_bfloat16*>(a.out) + t0 * a.dim + ch0 + mine;
+        const int64_t xs = kTile * a.ldx, zs = kTile * a.ldz, ds = kTile * a.lddt * dts, bs = kTile * a.ldb * es,
+                      cs = kTile * a.ldc * es, os = kTile * a.dim;
+        auto fetch = [&](int i, Fetched<kBlocks>& f) {
+            if (i * kTile + tok < total) {
+                if (wide) {
+                    f.x = *reinterpret_cast<const uint4*>(xp);
+                    if (gated) f.z = *reinterpret_cast<const uint4*>(zp);
+                    f.dt[0] = *reinterpret_cast<const uint4*>(dp);
+                    if (a.dt_f32) f.dt[1] = *reinterpret_cast<const uint4*>(dp + 16);
+                } else {
+                    f.x = gather8(xp, count);
+                    if (gated) f.z = gather8(zp, count);
+                    if (a.dt_f32) {
+                        f.dt[0] = gather4(reinterpret_cast<const float*>(dp), count);
+                        f.dt[1] = gather4(reinterpret_cast<const float*>(dp) + 4, count - 4);
+                    } else {
+                        f.dt[0] = gather8(reinterpret_cast<const __nv_bfloat16*>(dp), count);
+                    }
+                }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < count) out[i] = __float2bfloat16_rn(y[i]);
+                for (int k = 0; k < kBlocks; ++k) {
+                    const int have = S - 16 * k - 4 * (tid & 3);
+                    const uint8_t *b = bp + 16 * k * es, *cc = cp + 16 * k * es;
+                    if (have <= 0) {
+                        f.b[k] = f.c[k] = make_uint4(0, 0, 0, 0);
+                    } else if (a.vec_bc && a.bc_f32) {
+                        f.b[k] = *reinterpret_cast<const uint4*>(b);
+                        if (!kStates) f.c[k] = *reinterpret_cast<const uint4*>(cc);
+                    } else if (a.vec_bc) {
+                        const uint2 rb = *reinterpret_cast<const uint2*>(b);
+                        f.b[k].x = rb.x;
+                        f.b[k].y = rb.y;
+                        if (!kStates) {
+                            const uint2 rc = *reinterpret_cast<const uint2*>(cc);
+                            f.c[k].x = rc.x;
+                            f.c[k].y = rc.y;
+                        }
+                    } else if (a.bc_f32) {
+                        f.b[k] = gather4(reinterpret_cast<const float*>(b), have);
+                        if (!kStates) f.c[k] = gather4(reinterpret_cast<const float*>(cc), have);
+                    } else {
+                        f.b[k] = gather8(reinterpret_cast<const __nv_bfloat16*>(b), have < 4 ? have : 4);
+                        if (!kStates) f.c[k] = gather8(reinterpret_cast<const __nv_bfloat16*>(cc), have < 4 ? have : 4);
+                    }
+                }
+            } else {
+                f.x = f.z = f.dt[0] = f.dt[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) f.b[k] = f.c[k] = make_uint4(0, 0, 0, 0);
+            }
+            xp += xs;
+            if (gated) zp += zs;
+            dp += ds;
+            bp += bs;
+            if (!kStates) cp += cs;
+        };
+        // To the nearest TF32 value, which a BF16 one is.
+        auto tf32 = [](float v) {
+            uint32_t r;
+            asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+            return __uint_as_float(r);
+        };
+        auto four = [&](const uint4& r) {
+            return a.bc_f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
+                            : make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+        };
+        auto stage = [&](int i, const Fetched<kBlocks>& f) {
+            float* buf = smem + (i & 1) * Buf::kWords;
+            float u[8], x[8];
+            unpack8(f.x, x);
+            if (a.dt_f32) {
+                u[0] = __uint_as_float(f.dt[0].x); u[1] = __uint_as_float(f.dt[0].y);
+                u[2] = __uint_as_float(f.dt[0].z); u[3] = __uint_as_float(f.dt[0].w);
+                u[4] = __uint_as_float(f.dt[1].x); u[5] = __uint_as_float(f.dt[1].y);
+                u[6] = __uint_as_float(f.dt[1].z); u[7] = __uint_as_float(f.dt[1].w);
+            } else {
+                unpack8(f.dt[0], u);
+            }
+            float2 dt[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dt[j] = make_float2(u[2 * j] + bias[2 * j], u[2 * j + 1] + bias[2 * j + 1]);
+            if (a.softplus) softplus(dt);
+            if (i * kTile + tok >= total)   // behind the end nothing decays and nothing is added
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dt[j] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float v = dt[j].x * x[2 * j], v1 = dt[j].y * x[2 * j + 1];
+                *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j, tok)) = make_float4(dt[j].x, dt[j].x, v, v);
+                *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j + 1, tok)) = make_float4(dt[j].y, dt[j].y, v1, v1);
+            }
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                const int at = tok * Buf::kRow + 16 * k + 4 * (tid & 3);
+                *reinterpret_cast<float4*>(buf + Buf::kB + at) = four(f.b[k]);
+                if (!kStates) {
+                    // (In the order in which the product's B operand takes them.)
+                    const float4 v = four(f.c[k]);
+                    *reinterpret_cast<float4*>(buf + Buf::kC + at) =
+                        a.bc_f32 ? make_float4(tf32(v.x), tf32(v.z), tf32(v.y), tf32(v.w)) : make_float4(v.x, v.z, v.y, v.w);
+                }
+            }
+            if (!kStates) {
+                uint4* xz = reinterpret_cast<uint4*>(buf + Buf::kXZ) + tid;
+                xz[0] = f.x;
+                if (gated) xz[kRole] = f.z;
+            }
+        };
+        // A token's outputs from its y: the skip, the gate and one rounding.
+        auto finish = [&](int i) {
+            const float* buf = smem + (i & 1) * Buf::kWords;
+            if (i * kTile + tok < total) {
+                float y[8], x[8], z[8];
+                const float4* p = reinterpret_cast<const float4*>(buf + Buf::kY + tok * kYStride + mine);
+                const float4 lo = p[0], hi = p[1];
+                y[0] = lo.x; y[1] = lo.y; y[2] = lo.z; y[3] = lo.w; y[4] = hi.x; y[5] = hi.y; y[6] = hi.z; y[7] = hi.w;
+                const uint4* xz = reinterpret_cast<const uint4*>(buf + Buf::kXZ) + tid;
+                if (a.D) {
+                    unpack8(xz[0], x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = fmaf(skip[j], x[j], y[j]);
+                }
+                if (gated) {
+                    unpack8(xz[kRole], z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] *= z[j] * sigmoid(z[j]);
+                }
+                if (wide) {
+                    store8(op, y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < count) op[j] = __float2bfloat16_rn(y[j]);
+                }
+            }
+            op += os;
+        };
+        Fetched<kBlocks> f;
+        if (tiles > 0) {
+            fetch(0, f);
+            stage(0, f);
+            fetch(1, f);
         }
-    };
+        __syncthreads();
+        for (int i = 0; i < tiles; ++i) {
+            if (!kStates && i > 0) finish(i - 1);
+            if (i + 1 < tiles) {
+                stage(i + 1, f);
+                fetch(i + 2, f);
+            }
+            __syncthreads();
+        }
+        if (!kStates && tiles > 0) finish(tiles - 1);
+        return;
+    }
 
     // ---- the walk: a warp's 8 channels, four lanes each
+    const int warp = tid >> 5, lane = tid & 31, c = lane & 3;
     const int local = 8 * warp + (lane >> 2);
     const bool live = local < channels;
     const int64_t ch = ch0 + (live ? local : 0);
@@ -398,8 +480,6 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs a) {
     auto ending = [&](int64_t seq) {
         if (a.final_state && live) store_row<kBlocks>(a.final_state, a.state_f32, seq * a.dim + ch, c, S, s);
     };
-    Fetched<kBlocks> f;
-    if (w.begin < w.end) fetch(w.begin, f);
     if (w.fresh) {
         initial(w.seq);
     } else {
@@ -417,101 +497,107 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs a) {
             }
         }
     }
-    // The states of the sequences that end at token t, and the next one's.
-    int64_t seq = w.seq, seq_end = w.seq_end;
+    // The states of the sequences that end at token t of the span, and the next one's.
+    int64_t seq = w.seq, seq_end = w.seq_end - w.begin;
     auto close = [&](int64_t t) {
         while (t == seq_end) {
             ending(seq);
             if (!kPacked || ++seq >= a.N) break;
-            seq_end = a.cu_seqlens[seq + 1];
+            seq_end = a.cu_seqlens[seq + 1] - w.begin;
             initial(seq);
         }
     };
-    if (!kStates) close(w.begin);
-
+    if (!kStates) close(0);
     float steps = 0.f;   // the sum of dt
-    if (w.begin < w.end) {
-        stage(w.begin, f, smem);
-        __syncthreads();
-    }
-    int which = 0;
-    for (int64_t base = w.begin; base < w.end; base += kTile) {
-        float* buf = smem + which * Buf::kWords;
-        const uint4 xr = f.x, zr = f.z;
-        const bool more = base + kTile < w.end;
-        if (more) fetch(base + kTile, f);
-        const float* step = buf + step_at(local, 0);
-        const float* rows = buf + Buf::kB + 4 * c;
-        const float* keys = buf + Buf::kC + ((lane >> 3) * Buf::kRow) + 4 * c + 2 * ((lane >> 2) & 1);
-        const int n = static_cast<int>(w.end - base < kTile ? w.end - base : kTile);
-        // Where the sequence ends within the tile (packed).
-        int left = kPacked && !kStates && seq_end - base <= kTile ? static_cast<int>(seq_end - base) : kTile + 4;
-#pragma unroll 1
-        for (int t = 0; t < n; t += 4) {
-            float dts[4], dus[4], ck[kBlocks][2], y = 0.f;
-            {
-                const float4 p = *reinterpret_cast<const float4*>(step + 2 * t), q = *reinterpret_cast<const float4*>(step + 2 * t + 4);
-                dts[0] = p.x; dus[0] = p.y; dts[1] = p.z; dus[1] = p.w;
-                dts[2] = q.x; dus[2] = q.y; dts[3] = q.z; dus[3] = q.w;
+    const int step0 = step_at(local, 0), rows0 = Buf::kB + 4 * c, y0 = Buf::kY + c * kYStride + local;
+    const int keys0 = Buf::kC + (lane >> 3) * Buf::kRow + 4 * c + 2 * ((lane >> 2) & 1);
+    // Four tokens from t on of the tile at `base`; with `ends`, sequences may end
+    // among them.  (Tokens behind the span's end change nothing: only the last span
+    // has them, and no sequence behind it.)
+    auto walk = [&](auto ends, const float* buf, int64_t base, int t) {
+        float ck[kBlocks][2], y = 0.f;
+        if (!kStates)
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRow + 16 * k);
+                ck[k][0] = v.x;
+                ck[k][1] = v.y;
             }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint64_t b[kBlocks][2];
+            const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(buf + step0 + 4 * (t + j));   // dt twice, dt x twice
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(buf + rows0 + (t + j) * Buf::kRow + 16 * k);
+                b[k][0] = mul_pair(dd.y, v.x);
+                b[k][1] = mul_pair(dd.y, v.y);
+            }
+            decay<kBlocks>(s, rate, dd.x, b);
+            if (kStates) {
+                steps += halves(dd.x).x;
+            } else {
+                float acc[4];
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) {
+                    const float2 lo = halves(s.h[k][0]), hi = halves(s.h[k][1]);
+                    if (k == 0)
+                        mma_tf32_first(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
+                    else
+                        mma_tf32(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
+                }
+                // (The columns of the group's other tokens hold nothing of use.)
+                if (c == j) y = acc[0] + acc[3];
+                if (decltype(ends)::value) close(base + t + j + 1);
+            }
+        }
+        return y;   // of token t + c
+    };
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        float* buf = smem + (i & 1) * Buf::kWords;
+        const int64_t base = static_cast<int64_t>(i) * kTile;
+        if (base + kTile <= total && (!kPacked || kStates || seq_end >= base + kTile)) {
+            // (y is stored behind all loads: the compiler keeps their order.)
+            float y[kTile / 4];
+#pragma unroll
+            for (int t = 0; t < kTile; t += 4) y[t / 4] = walk(std::false_type{}, buf, base, t);
             if (!kStates)
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
-                    const float2 v = *reinterpret_cast<const float2*>(keys + t * Buf::kRow + 16 * k);
-                    ck[k][0] = v.x;
-                    ck[k][1] = v.y;
-                }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint64_t b[kBlocks][2];
-                const uint64_t du = pair(dus[j], dus[j]);
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(rows + (t + j) * Buf::kRow + 16 * k);
-                    b[k][0] = mul_pair(du, pair(v.x, v.y));
-                    b[k][1] = mul_pair(du, pair(v.z, v.w));
-                }
-                decay<kBlocks>(s, rate, pair(dts[j], dts[j]), b);
-                if (kStates) {
-                    steps += dts[j];
-                } else {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) {
-                        const float2 lo = halves(s.h[k][0]), hi = halves(s.h[k][1]);
-                        mma_tf32(acc, lo.x, hi.x, lo.y, hi.y, ck[k][0], ck[k][1]);
-                    }
-                    // (The columns of the group's other tokens hold nothing of use.)
-                    if (c == j) y = acc[0] + acc[3];
-                    if (kPacked && t + j + 1 == left) {
-                        close(base + left);
-                        left = seq_end - base <= kTile ? static_cast<int>(seq_end - base) : kTile + 4;
-                    }
-                }
+                for (int t = 0; t < kTile; t += 4) buf[y0 + t * kYStride] = y[t / 4];
+            if (kPacked && !kStates) close(base + kTile);
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < kTile && base + t < total; t += 4) {
+                const float y = walk(std::integral_constant<bool, kPacked && !kStates>{}, buf, base, t);
+                if (!kStates) buf[y0 + t * kYStride] = y;
             }
-            if (!kStates) buf[Buf::kY + (t + c) * kYStride + local] = y;
         }
-        if (!kPacked && !kStates && base + n == seq_end) close(seq_end);
-        if (more) stage(base + kTile, f, smem + (which ^ 1) * Buf::kWords);
         __syncthreads();
-        if (!kStates) finish(base, xr, zr, buf);
-        which ^= 1;
     }
+    if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
     if (kStates && live) {
         store_row<kBlocks>(a.span_states, true, span * a.dim + ch, c, 16 * kBlocks, s);
         if (c == 0) a.span_steps[span * a.dim + ch] = steps;
     }
 }
 
-// ---- single tokens: four lanes a channel, kSeqs sequences a thread
-template <int kBlocks, int kSeqs>
+// ---- single tokens: four lanes a channel, and four sequences
+// Bound by HBM: each state is read and written once, 2 x 4 S bytes (FP32) a
+// channel.  Lane i of a channel's four loads x, dt and z of sequence i, forms its
+// step and its gate and hands the step to the other three; the sums over the
+// states come back to it, so that nothing is computed four times, and the
+// rates are read once for four sequences.
+template <int kBlocks>
 __global__ void __launch_bounds__(256) ssm_decode_kernel(SsmArgs a) {
+    constexpr int kSeqs = 4;
     wait_for_kernel_before();
     const int c = threadIdx.x & 3, S = static_cast<int>(a.nstate);
     const int64_t blocks = (a.dim + 63) / 64, part = blockIdx.x / blocks;
     const int64_t ch_raw = (blockIdx.x - part * blocks) * 64 + (threadIdx.x >> 2);
     const bool live = ch_raw < a.dim;
     const int64_t ch = live ? ch_raw : a.dim - 1, group = ch / (a.dim / a.groups);
+    // (The sequences and their slots are the same for the whole CTA.)
     int64_t slot[kSeqs];
     State<kBlocks> s[kSeqs];
 #pragma unroll
@@ -522,70 +608,63 @@ __global__ void __launch_bounds__(256) ssm_decode_kernel(SsmArgs a) {
             if (ch_raw == 0 && c == 0) atomicOr(a.status, kDevBadSlots);
             slot[i] = -1;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i)
         if (slot[i] >= 0) load_row<kBlocks>(a.state, a.state_f32, slot[i] * a.dim + ch, c, S, s[i]);
+    const int64_t own = part * kSeqs + c;
+    const int64_t own_slot = c == 0 ? slot[0] : c == 1 ? slot[1] : c == 2 ? slot[2] : slot[3];
+    float x = 0.f, z = 0.f;
+    float2 dt[1] = {};
+    if (own_slot >= 0) {
+        auto bf16_at = [](const void* p, int64_t at) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]); };
+        x = bf16_at(a.x, own * a.ldx + ch);
+        dt[0].x = a.dt_f32 ? static_cast<const float*>(a.dt)[own * a.lddt + ch] : bf16_at(a.dt, own * a.lddt + ch);
+        if (a.z) z = bf16_at(a.z, own * a.ldz + ch);
     }
     State<kBlocks> rate;
     load_row<kBlocks>(a.A, true, ch, c, S, rate);
+    if (a.dt_bias) dt[0].x += a.dt_bias[ch];
+    const float skip = a.D ? a.D[ch] : 0.f;
+    if (a.softplus) softplus(dt);
+    const float du = dt[0].x * x;
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) rate.h[k][i] = mul_pair(rate.h[k][i], pair(kLog2e, kLog2e));
-    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
-    auto bf16_at = [](const void* p, int64_t at) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]); };
+    float y[kSeqs];
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
+        const float step = __shfl_sync(0xffffffffu, dt[0].x, i, 4), add = __shfl_sync(0xffffffffu, du, i, 4);
+        y[i] = 0.f;
+        if (slot[i] < 0) continue;
         const int64_t n = part * kSeqs + i;
-        if (n >= a.N) break;
-        float y = 0.f;
-        if (slot[i] >= 0) {   // (the same for the whole CTA)
-            const float x = bf16_at(a.x, n * a.ldx + ch);
-            float dt = (a.dt_f32 ? static_cast<const float*>(a.dt)[n * a.lddt + ch] : bf16_at(a.dt, n * a.lddt + ch)) + bias;
-            if (a.softplus) dt = softplus(make_float2(dt, dt)).x;
-            uint64_t b[kBlocks][2];
-            const uint64_t du = pair(dt * x, dt * x);
-            const int es = a.bc_f32 ? 4 : 2;
-            State<kBlocks> bs, cs;
+        uint64_t b[kBlocks][2], sum = 0ull;
+        State<kBlocks> keys;
+        load_keys<kBlocks>(a.B, a.bc_f32, a.vec_bc, n * a.ldb + group * S, c, S, b);
+        load_keys<kBlocks>(a.C, a.bc_f32, a.vec_bc, n * a.ldc + group * S, c, S, keys.h);
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                const int n0 = 16 * k + 4 * c;
-                const auto bp = static_cast<const uint8_t*>(a.B) + (n * a.ldb + group * S) * es,
-                           cp = static_cast<const uint8_t*>(a.C) + (n * a.ldc + group * S) * es;
-                float v[4], u[4];
+        for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] = u[j] = 0.f;
-                    if (n0 + j < S) {
-                        v[j] = a.bc_f32 ? reinterpret_cast<const float*>(bp)[n0 + j] : bf16_at(bp, n0 + j);
-                        u[j] = a.bc_f32 ? reinterpret_cast<const float*>(cp)[n0 + j] : bf16_at(cp, n0 + j);
-                    }
-                }
-                bs.h[k][0] = pair(v[0], v[1]);
-                bs.h[k][1] = pair(v[2], v[3]);
-                cs.h[k][0] = pair(u[0], u[1]);
-                cs.h[k][1] = pair(u[2], u[3]);
-                b[k][0] = mul_pair(du, bs.h[k][0]);
-                b[k][1] = mul_pair(du, bs.h[k][1]);
-            }
-            decay<kBlocks>(s[i], rate, pair(dt, dt), b);
-            uint64_t sum = 0ull;
+            for (int j = 0; j < 2; ++j) b[k][j] = mul_pair(b[k][j], pair(add, add));
+        decay<kBlocks>(s[i], rate, pair(step, step), b);
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                sum = fma_pair(cs.h[k][0], s[i].h[k][0], sum);
-                sum = fma_pair(cs.h[k][1], s[i].h[k][1], sum);
-            }
-            const float2 both = halves(sum);
-            y = both.x + both.y;
-            y += __shfl_xor_sync(0xffffffffu, y, 1);
-            y += __shfl_xor_sync(0xffffffffu, y, 2);
-            if (a.D) y = fmaf(skip, x, y);
-            if (a.z) {
-                const float z = bf16_at(a.z, n * a.ldz + ch);
-                y *= z * sigmoid(z);
-            }
-            if (live) store_row<kBlocks>(a.state, a.state_f32, slot[i] * a.dim + ch, c, S, s[i]);
-        }
-        if (live && c == 0) static_cast<__nv_bfloat16*>(a.out)[n * a.dim + ch] = __float2bfloat16_rn(y);
+        for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sum = fma_pair(keys.h[k][j], s[i].h[k][j], sum);
+        y[i] = halves(sum).x + halves(sum).y;
+        if (live) store_row<kBlocks>(a.state, a.state_f32, slot[i] * a.dim + ch, c, S, s[i]);
     }
+    // Lane i gets the sum of sequence i over the four lanes.
+    const bool up = c & 2, odd = c & 1;
+    float keep0 = up ? y[2] : y[0], keep1 = up ? y[3] : y[1];
+    keep0 += __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 2);
+    keep1 += __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 2);
+    float sum = odd ? keep1 : keep0;
+    sum += __shfl_xor_sync(0xffffffffu, odd ? keep0 : keep1, 1);
+    if (a.D) sum = fmaf(skip, x, sum);
+    if (a.z) sum *= z * sigmoid(z);
+    if (live && own < a.N) static_cast<__nv_bfloat16*>(a.out)[own * a.dim + ch] = __float2bfloat16_rn(own_slot >= 0 ? sum : 0.f);
 }
 
 template <int kBlocks, bool kStates, bool kPacked>
@@ -618,45 +697,40 @@ cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
     return e;
 }
 
-template <int kBlocks, int kSeqs>
-cudaError_t decode(const SsmArgs& a, cudaStream_t stream) {
-    const int64_t blocks = (a.dim + 63) / 64, parts = (a.N + kSeqs - 1) / kSeqs;
-    if (parts > 0x7fffffffLL / blocks) return cudaErrorInvalidValue;
-    return launch_after(ssm_decode_kernel<kBlocks, kSeqs>, dim3(static_cast<unsigned>(parts * blocks)), dim3(256), 0, stream, a);
-}
 template <int kBlocks>
-cudaError_t pick_decode(const SsmArgs& a, int sms, cudaStream_t stream) {
-    // Four sequences a thread share its rates where that still fills the SMs.
-    constexpr int kMany = kBlocks == 1 ? 4 : 2;
-    if (a.N / kMany * ((a.dim + 63) / 64) >= 4 * static_cast<int64_t>(sms)) return decode<kBlocks, kMany>(a, stream);
-    return decode<kBlocks, 1>(a, stream);
+cudaError_t decode(const SsmArgs& a, cudaStream_t stream) {
+    const int64_t blocks = (a.dim + 63) / 64, parts = (a.N + 3) / 4;
+    if (parts > 0x7fffffffLL / blocks) return cudaErrorInvalidValue;
+    return launch_after(ssm_decode_kernel<kBlocks>, dim3(static_cast<unsigned>(parts * blocks)), dim3(256), 0, stream, a);
 }
 
 bool multiple(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// Rows of a tensor that can be read n elements of `size` bytes at a time.
+bool rows_of(const void* p, int64_t ld, int64_t tokens, int size, int n) {
+    return !p || (multiple(p, static_cast<uintptr_t>(size * n)) && (tokens < 2 || ld % n == 0));
+}
+void set_vectors(SsmArgs* a) {
+    a->vec = a->dim / a->groups % 8 == 0 && rows_of(a->x, a->ldx, a->tokens, 2, 8) && rows_of(a->z, a->ldz, a->tokens, 2, 8) &&
+             (a->dt_f32 ? rows_of(a->dt, a->lddt, a->tokens, 4, 4) : rows_of(a->dt, a->lddt, a->tokens, 2, 8));
+    const int size = a->bc_f32 ? 4 : 2;
+    a->vec_bc = a->nstate % 4 == 0 && rows_of(a->B, a->ldb, a->tokens, size, 4) && rows_of(a->C, a->ldc, a->tokens, size, 4);
+}
 
 }  // namespace
 
 cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches) {
     if (a.N <= 0 || a.dim <= 0) return cudaSuccess;
-    const int64_t per = a.dim / a.groups;
-    // Rows that can be read 8 channels (4 states) at a time.
-    auto rows = [&](const void* p, int64_t ld, int size, int n) {
-        return !p || (multiple(p, static_cast<uintptr_t>(size * n)) && (a.tokens < 2 || ld % n == 0));
-    };
-    a.vec = per % 8 == 0 && rows(a.x, a.ldx, 2, 8) && rows(a.z, a.ldz, 2, 8) &&
-            (a.dt_f32 ? rows(a.dt, a.lddt, 4, 4) : rows(a.dt, a.lddt, 2, 8));
-    const int size = a.bc_f32 ? 4 : 2;
-    a.vec_bc = a.nstate % 4 == 0 && rows(a.B, a.ldb, size, 4) && rows(a.C, a.ldc, size, 4);
+    set_vectors(&a);
     if (a.nstate <= 16) return prefill<1>(a, stream, launches);
     if (a.nstate <= 32) return prefill<2>(a, stream, launches);
     return prefill<4>(a, stream, launches);
 }
 
-cudaError_t launch_ssm_decode(const SsmArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_ssm_decode(SsmArgs a, cudaStream_t stream) {
     if (a.N <= 0 || a.dim <= 0) return cudaSuccess;
-    if (a.nstate <= 16) return pick_decode<1>(a, sms, stream);
-    if (a.nstate <= 32) return pick_decode<2>(a, sms, stream);
-    return pick_decode<4>(a, sms, stream);
+    set_vectors(&a);
+    if (a.nstate <= 16) return decode<1>(a, stream);
+    return a.nstate <= 32 ? decode<2>(a, stream) : decode<4>(a, stream);
 }
 
 }  // namespace kda

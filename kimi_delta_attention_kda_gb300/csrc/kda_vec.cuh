@@ -47,11 +47,17 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
-// kVec consecutive elements: 8, or 2 or 1 where rows start at any element.
+// kVec consecutive elements: 8 or 4, or 2 or 1 where rows start at any element.
 template <int kVec, typename T>
 __device__ __forceinline__ void load_vec(const T* p, float (&x)[kVec]) {
     if constexpr (kVec == 8) {
         load8(p, x);
+    } else if constexpr (kVec == 4 && sizeof(T) == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else if constexpr (kVec == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
     } else if constexpr (kVec == 1) {
         x[0] = static_cast<float>(*p);
     } else if constexpr (sizeof(T) == 4) {
@@ -102,6 +108,18 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// x sigmoid(x) of two values, as sigmoid() has it.
+__device__ __forceinline__ uint64_t silu_pair(uint64_t x) {
+    const float2 v = halves(x);
+    float h0, h1, r0, r1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h0) : "f"(fabsf(v.x) * -0.72134752044448170f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h1) : "f"(fabsf(v.y) * -0.72134752044448170f));
+    const uint64_t h = pair(h0, h1), t = mul_pair(h, h);
+    const float2 e = halves(t), d = halves(add_pair(t, pair(1.f, 1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
+    return mul_pair(mul_pair(x, pair(v.x < 0.f ? e.x : 1.f, v.y < 0.f ? e.y : 1.f)), pair(r0, r1));
 }
 // 2^x, off by 1.4e-7 of its value at most (2e-8 on average; 8e-8 and 6e-9 on
 // [-0.001, 0]): measured on GB300.
