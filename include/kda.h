@@ -577,7 +577,7 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  *   out         : BF16 [tokens, dim], contiguous
  *   init_state  : [N, dim, nstate] or NULL for zeros; BF16, or FP32 with KDA_FLAG_STATE_F32
  *   final_state : the same type, or NULL (not written); may be init_state
- *   nstate      : 1 .. 64 (multiples of 16 waste nothing); groups divides dim
+ *   nstate      : 1 .. 64 (16, 32 and 64 waste nothing); dim below 2^24; groups divides dim
  * Fixed and packed layouts, cu_seqlens, empty sequences, the T = 0 rule (A is
  * still needed) and the limit on tokens are those of kda_prefill.  Alignment: A, out
  * and the states 16 bytes, cu_seqlens 8, the rest an element's size (rows on 16

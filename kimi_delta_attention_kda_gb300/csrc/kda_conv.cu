@@ -18,8 +18,12 @@
 namespace kda {
 namespace {
 
-constexpr int kConvThreads = 256;
-constexpr int kGroup = 4;   // tokens whose loads are under way together
+// Eight rows are under way while eight are worked on, in five CTAs of 128 threads (95
+// registers).  8192 x 12288: 72 us; groups of four in three to four CTAs of 256
+// threads 77 to 80, pairs of channels a thread 76 to 91, six CTAs (spilled) 93.
+constexpr int kConvThreads = 128;
+constexpr int kConvCtas = 5;   // an SM
+constexpr int kGroup = 8;
 
 // kVec consecutive BF16 values as loaded, and as pairs of FP32 values (of one: with
 // a zero): 4, or 2 or 1 where rows start at any element.
@@ -107,45 +111,48 @@ struct Filter {
     }
 };
 
+// (Tokens are counted in 32 bits: there are fewer than 2^31.)
 template <int kW, int kVec, bool kPacked>
-__global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(ConvArgs a) {
     wait_for_kernel_before();
     if (kPacked && !offsets_hold(a.cu_seqlens, a.N, a.tokens, a.valid, a.status)) return;
     const int64_t vecs = a.D / kVec, at = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
-    const int64_t run = at / vecs, ch = (at - run * vecs) * kVec;
+    const int64_t run = quotient(at, vecs), ch = (at - run * vecs) * kVec;
     if (run >= a.runs) return;
     using R = Raw<kVec>;
     constexpr int kKeep = kW - 1, kPairs = Filter<kW, kVec>::kPairs;
     const auto x = static_cast<const __nv_bfloat16*>(a.x) + ch;
     const auto init = static_cast<const __nv_bfloat16*>(a.init_state) + ch;
-    const auto out = static_cast<__nv_bfloat16*>(a.out) + ch;
     const auto final_state = static_cast<__nv_bfloat16*>(a.final_state) + ch;
 
-    int64_t seq, begin, t, end;   // the sequence, its first token, this run's tokens
-    int64_t seq_end;
-    if (kPacked) {
-        t = run * a.run_tokens;
-        end = t + a.run_tokens < a.tokens ? t + a.run_tokens : a.tokens;
-        // The first run also has the empty sequences before the first token.
-        seq = run == 0 ? 0 : ended_by(a.cu_seqlens, a.N, t);
-        begin = a.cu_seqlens[seq];
-        seq_end = a.cu_seqlens[seq + 1];
-    } else {
-        seq = run / a.runs_per_seq;
-        begin = seq * a.tokens_per_seq;
-        t = begin + (run - seq * a.runs_per_seq) * a.run_tokens;
-        seq_end = begin + a.tokens_per_seq;
-        end = t + a.run_tokens < seq_end ? t + a.run_tokens : seq_end;
-    }
+    // The run's tokens [t, end).
+    int64_t seq = kPacked ? 0 : quotient(run, a.runs_per_seq);
+    int begin = kPacked ? 0 : static_cast<int>(seq * a.tokens_per_seq);
+    int t = kPacked ? static_cast<int>(run * a.run_tokens) : begin + static_cast<int>((run - seq * a.runs_per_seq) * a.run_tokens);
+    int seq_end = static_cast<int>(kPacked ? a.tokens : begin + a.tokens_per_seq);
+    const int end = t + a.run_tokens < seq_end ? static_cast<int>(t + a.run_tokens) : seq_end;
+    // The group after the one at hand is on its way while that is worked on.
+    RawT<kVec> ahead[kGroup];
+    const __nv_bfloat16* next = x + t * a.ldx;
+    auto out = static_cast<__nv_bfloat16*>(a.out) + ch + t * a.D;
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) ahead[i] = load_raw<kVec>(next + i * a.ldx);
+    };
+    if (t + kGroup <= end) fetch();
     Filter<kW, kVec> filter;
     filter.load(a, ch);
-
+    if (kPacked) {   // the sequence and its first token; the first run also has the empty ones before that
+        seq = run == 0 ? 0 : ended_by(a.cu_seqlens, a.N, t);
+        begin = static_cast<int>(a.cu_seqlens[seq]);
+        seq_end = static_cast<int>(a.cu_seqlens[seq + 1]);
+    }
     uint64_t win[kKeep + kGroup][kPairs];   // the kKeep rows before token t, oldest first, and a group's own
     auto window = [&]() {
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             RawT<kVec> r = R::zero();
-            const int64_t at = t - kKeep + i;   // below the sequence's first token: the initial state
+            const int at = t - kKeep + i;   // below the sequence's first token: the initial state
             if (at >= begin)
                 r = load_raw<kVec>(x + at * a.ldx);
             else if (a.init_state)
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
                 for (int i = 0; i < kKeep; ++i) store_raw<kVec>(final_state + (seq * kKeep + i) * a.D, R::pack(win[i]));
             if (!kPacked || ++seq >= a.N) break;
             begin = seq_end;
-            seq_end = a.cu_seqlens[seq + 1];
+            seq_end = static_cast<int>(a.cu_seqlens[seq + 1]);
             window();
         }
     };
@@ -171,43 +178,35 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) win[i][j] = win[n + i][j];
     };
-    // The group after the one at hand is on its way while that is worked on.
-    RawT<kVec> ahead[kGroup];
-    const __nv_bfloat16* next = x + t * a.ldx;
-    auto fetch = [&]() {
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) ahead[i] = load_raw<kVec>(next + i * a.ldx);
-    };
-    bool fetched = t + kGroup <= end;
-    if (fetched) fetch();
     window();
-    close();
-    while (t < end) {
-        // A whole group within the sequence, or a token at a time.
-        if (fetched && t + kGroup <= seq_end) {
+    for (;;) {
+        close();
+        if (t >= end) return;
+        // Whole groups within the sequence, then a token at a time.
+        const int last = end < seq_end ? end : seq_end;
+        while (t + kGroup <= last) {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) R::unpack(ahead[i], win[kKeep + i]);
-            next += kGroup * a.ldx;
-            fetched = t + 2 * kGroup <= end;
-            if (fetched) fetch();
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) store_raw<kVec>(out + (t + i) * a.D, filter.apply(win + i, a.silu));
-            shift(kGroup);
             t += kGroup;
-        } else {
-            for (int i = 0; i < kGroup && t < end; ++i) {
-                R::unpack(load_raw<kVec>(next), win[kKeep]);
-                next += a.ldx;
-                store_raw<kVec>(out + t * a.D, filter.apply(win, a.silu));
-                shift(1);
-                ++t;
-                close();
+            next += kGroup * a.ldx;
+            if (t + kGroup <= end) fetch();
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                store_raw<kVec>(out, filter.apply(win + i, a.silu));
+                out += a.D;
             }
-            fetched = t + kGroup <= end;
-            if (fetched) fetch();
-            continue;
+            shift(kGroup);
         }
-        close();
+        if (t == last) continue;
+#pragma unroll 1
+        for (; t < last; ++t) {
+            R::unpack(load_raw<kVec>(next), win[kKeep]);
+            next += a.ldx;
+            store_raw<kVec>(out, filter.apply(win, a.silu));
+            out += a.D;
+            shift(1);
+        }
+        if (t + kGroup <= end) fetch();
     }
 }
 
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_decode_kernel(ConvArgs a) {
     using R = Raw<kVec>;
     constexpr int kKeep = kW - 1;
     const int64_t vecs = a.D / kVec, at = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
-    const int64_t part = at / vecs, ch = (at - part * vecs) * kVec;
+    const int64_t part = quotient(at, vecs), ch = (at - part * vecs) * kVec;
     if (part * kSeqs >= a.N) return;
     const auto x = static_cast<const __nv_bfloat16*>(a.x) + ch;
     const auto state = static_cast<__nv_bfloat16*>(a.state) + ch;
@@ -270,10 +269,10 @@ int conv_vec(const ConvArgs& a) {
 
 template <int kW, int kVec>
 cudaError_t run_prefill(ConvArgs a, int sms, cudaStream_t stream) {
-    // Runs of 32 tokens, and shorter ones where there are too few threads: the
-    // rows before a run are read twice, W - 1 for each.
-    a.run_tokens = 32;
-    while (a.run_tokens > 4 && a.rows / a.run_tokens * (a.D / kVec) < static_cast<int64_t>(sms) * 1024) a.run_tokens /= 2;
+    // Runs of 64 tokens, and shorter ones, of a group at least, for two waves of threads:
+    // a run begins with its filter and the W - 1 rows before it.
+    a.run_tokens = 64;
+    while (a.run_tokens > kGroup && a.rows / a.run_tokens * (a.D / kVec) < 2 * kConvCtas * kConvThreads * static_cast<int64_t>(sms)) a.run_tokens /= 2;
     if (a.cu_seqlens) {
         a.runs = (a.rows + a.run_tokens - 1) / a.run_tokens;
         if (a.runs == 0) a.runs = 1;   // no tokens: the states alone

@@ -325,7 +325,7 @@ struct SsmArgs {
 };
 constexpr int kSsmTile = 32;
 constexpr int kSsmChannels = 32;
-constexpr int64_t kSsmMaxState = 64;
+constexpr int64_t kSsmMaxState = 64, kSsmMaxDim = (int64_t(1) << 24) - 1;
 // Adds the kernels it launches to *launches.
 cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches);
 cudaError_t launch_ssm_decode(SsmArgs a, cudaStream_t stream);

@@ -215,7 +215,7 @@ int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, 
     if (rc != KDA_OK) return rc;
     if (dim < 1 || groups < 1 || dim % groups || nstate < 1 || nstate > kSsmMaxState) return KDA_ERR_SHAPE;
     const int64_t wide = nstate <= 16 ? 16 : nstate <= 32 ? 32 : 64;
-    if (dim > 0x7fffffffLL || N > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
+    if (dim > kSsmMaxDim || N > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
     c->tiles_per_group = (dim / groups + kSsmChannels - 1) / kSsmChannels;
     c->tiles = c->tiles_per_group * groups;
     const int64_t chains = packed ? 1 : N;        // that go on for `length` tokens
@@ -700,7 +700,7 @@ extern "C" int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_
                               int64_t groups, int64_t nstate, int64_t pool, uint32_t flags, void* stream) {
     reset_launches();
     if (flags & ~kSsmFlags) return KDA_ERR_ARG;
-    if (N < 0 || N > 0x7fffffffLL || pool < 0 || dim < 1 || dim > 0x7fffffffLL || groups < 1 || dim % groups || nstate < 1 ||
+    if (N < 0 || N > 0x7fffffffLL / 4 || pool < 0 || dim < 1 || dim > kSsmMaxDim || groups < 1 || dim % groups || nstate < 1 ||
         nstate > kSsmMaxState || pool > kMaxElems / (dim * nstate * 4) || (!slots && N > pool))
         return KDA_ERR_SHAPE;
     SsmArgs a = {};

@@ -13,6 +13,11 @@ __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddep
 // The next kernel may be placed where this one leaves room.
 __device__ __forceinline__ void let_next_kernel_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// a / b for a >= 0 and b > 0: 64-bit division costs a hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // The number of sequences that end at or before token `key`, for non-decreasing offsets.
 __device__ __forceinline__ int64_t ended_by(const int64_t* cu, int64_t n_seqs, int64_t key) {
     int64_t lo = 0, hi = n_seqs;

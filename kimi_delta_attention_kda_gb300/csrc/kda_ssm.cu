@@ -167,28 +167,57 @@ __device__ __forceinline__ void store_row(void* p, bool f32, int64_t row, int c,
             store_states(static_cast<__nv_bfloat16*>(p) + row * S, 16 * k + 4 * c, S, v);
     }
 }
-// A lane's values of a row of B or C, `at` elements behind p.
-template <int kBlocks>
-__device__ __forceinline__ void load_keys(const void* p, bool f32, bool wide, int64_t at, int c, int S, uint64_t (&v)[kBlocks][2]) {
+// A lane's values of a row of S as loaded, four at a time.  With kFull S is 16
+// kBlocks and they can be read so.
+template <int kBlocks, typename T>
+struct Row {
+    using Four = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+    Four r[kBlocks];
+
+    template <bool kFull>
+    __device__ __forceinline__ void load(const T* row, int c, int S) {
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-        const int n0 = 16 * k + 4 * c;
-        float x[4] = {};
-        if (f32 && wide) {
-            if (n0 < S) load_vec<4>(static_cast<const float*>(p) + at + n0, x);
-        } else if (wide) {
-            if (n0 < S) load_vec<4>(static_cast<const __nv_bfloat16*>(p) + at + n0, x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < S)
-                    x[i] = f32 ? static_cast<const float*>(p)[at + n0 + i]
-                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + n0 + i]);
+        for (int k = 0; k < kBlocks; ++k) {
+            const int n0 = 16 * k + 4 * c;
+            if constexpr (kFull) {
+                r[k] = *reinterpret_cast<const Four*>(row + n0);
+            } else if constexpr (sizeof(T) == 4) {
+                r[k] = gather4(row + n0, S - n0);
+            } else {
+                const uint4 v = gather8(row + n0, S - n0 < 4 ? S - n0 : 4);
+                r[k] = make_uint2(v.x, v.y);
+            }
         }
-        v[k][0] = pair(x[0], x[1]);
-        v[k][1] = pair(x[2], x[3]);
     }
-}
+    __device__ __forceinline__ void unpack(State<kBlocks>& s) const {
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                s.h[k][0] = pair(__uint_as_float(r[k].x), __uint_as_float(r[k].y));
+                s.h[k][1] = pair(__uint_as_float(r[k].z), __uint_as_float(r[k].w));
+            } else {
+                s.h[k][0] = pair(bf16_lo(r[k].x), bf16_hi(r[k].x));
+                s.h[k][1] = pair(bf16_lo(r[k].y), bf16_hi(r[k].y));
+            }
+        }
+    }
+    template <bool kFull>
+    __device__ static __forceinline__ void store(T* row, int c, int S, const State<kBlocks>& s) {
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            const int n0 = 16 * k + 4 * c;
+            const float2 a = halves(s.h[k][0]), b = halves(s.h[k][1]);
+            const float v[4] = {a.x, a.y, b.x, b.y};
+            if constexpr (kFull) {
+                store_states(row, n0, 16 * kBlocks, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n0 + i < S) from_f32(row + n0 + i, v[i]);
+            }
+        }
+    }
+};
 // h <- exp2(A s) h + b for a lane's states (A in units of log 2).
 template <int kBlocks>
 __device__ __forceinline__ void decay(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt, const uint64_t (&b)[kBlocks][2]) {
@@ -249,11 +278,11 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
             w.seq = span == 0 ? 0 : ended_by(a.cu_seqlens, a.N, w.begin);
             const int64_t first = a.cu_seqlens[w.seq];
             w.fresh = first >= w.begin;
-            w.first_span = w.fresh ? span : first / a.span_tokens;
+            w.first_span = w.fresh ? span : quotient(first, a.span_tokens);
             w.seq_end = a.cu_seqlens[w.seq + 1];
         }
     } else {
-        w.seq = span / a.spans_per_seq;
+        w.seq = quotient(span, a.spans_per_seq);
         const int64_t s = span - w.seq * a.spans_per_seq, first = w.seq * a.tokens_per_seq;
         w.begin = first + s * a.span_tokens;
         w.seq_end = first + a.tokens_per_seq;
@@ -274,10 +303,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     wait_for_kernel_before();
     if (kStates) let_next_kernel_come();
     if (kPacked && !offsets_hold(a.cu_seqlens, a.N, a.tokens, a.valid, a.status)) return;
-    const int64_t span = blockIdx.x / a.tiles, tile = blockIdx.x - span * a.tiles;
+    const int64_t span = quotient(blockIdx.x, a.tiles), tile = blockIdx.x - span * a.tiles;
     const Part w = part_of<kStates, kPacked>(a, span);
     if (!w.run) return;
-    const int64_t group = tile / a.tiles_per_group, per = a.dim / a.groups;
+    const int64_t group = quotient(tile, a.tiles_per_group), per = quotient(a.dim, a.groups);
     const int64_t ch0 = group * per + (tile - group * a.tiles_per_group) * kChannels;
     const int channels = static_cast<int>((group + 1) * per - ch0 < kChannels ? (group + 1) * per - ch0 : kChannels);
     const int S = static_cast<int>(a.nstate);
@@ -582,89 +611,116 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     }
 }
 
-// ---- single tokens: four lanes a channel, and four sequences
+// ---- single tokens: four lanes a channel, four sequences a thread
 // Bound by HBM: each state is read and written once, 2 x 4 S bytes (FP32) a
 // channel.  Lane i of a channel's four loads x, dt and z of sequence i, forms its
 // step and its gate and hands the step to the other three; the sums over the
-// states come back to it, so that nothing is computed four times, and the
-// rates are read once for four sequences.
-template <int kBlocks>
-__global__ void __launch_bounds__(256) ssm_decode_kernel(SsmArgs a) {
-    constexpr int kSeqs = 4;
+// states come back to it, so that nothing is computed four times, and the rates are
+// read once for four sequences.  All loads are issued before the first value is
+// used.  kFull: 16 kBlocks states, and rows of B and C that can be read four
+// values at a time.
+constexpr int kStepThreads = 4 * kChannels;
+template <int kBlocks, bool kFull, bool kStateF32, bool kKeysF32>
+__global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 ? 4 : 3) ssm_decode_kernel(SsmArgs a, int blocks) {
     wait_for_kernel_before();
-    const int c = threadIdx.x & 3, S = static_cast<int>(a.nstate);
-    const int64_t blocks = (a.dim + 63) / 64, part = blockIdx.x / blocks;
-    const int64_t ch_raw = (blockIdx.x - part * blocks) * 64 + (threadIdx.x >> 2);
-    const bool live = ch_raw < a.dim;
-    const int64_t ch = live ? ch_raw : a.dim - 1, group = ch / (a.dim / a.groups);
-    // (The sequences and their slots are the same for the whole CTA.)
-    int64_t slot[kSeqs];
-    State<kBlocks> s[kSeqs];
+    constexpr int kTogether = kBlocks == 1 ? 4 : 1;   // sequences whose states and rows are under way together
+    using StateT = std::conditional_t<kStateF32, float, __nv_bfloat16>;
+    using KeyT = std::conditional_t<kKeysF32, float, __nv_bfloat16>;
+    const int c = threadIdx.x & 3, S = kFull ? 16 * kBlocks : static_cast<int>(a.nstate);
+    const int part = static_cast<int>(blockIdx.x / static_cast<uint32_t>(blocks)), n0 = 4 * part;
+    const int ch_raw = (static_cast<int>(blockIdx.x) - part * blocks) * kChannels + static_cast<int>(threadIdx.x >> 2);
+    const int dim = static_cast<int>(a.dim), N = static_cast<int>(a.N);
+    const bool live = ch_raw < dim;
+    const int ch = live ? ch_raw : dim - 1;
+    const int group = a.groups > 1 ? static_cast<uint32_t>(ch) / static_cast<uint32_t>(dim / static_cast<int>(a.groups)) : 0;
+
+    // The sequences' slots (-1: none) are the same for the whole CTA.
+    int slot[4];
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i) {
-        const int64_t n = part * kSeqs + i;
-        slot[i] = n < a.N ? (a.slots ? a.slots[n] : n) : -1;
+    for (int i = 0; i < 4; ++i) slot[i] = n0 + i < N ? (a.slots ? a.slots[n0 + i] : n0 + i) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
         if (slot[i] >= a.pool) {
             if (ch_raw == 0 && c == 0) atomicOr(a.status, kDevBadSlots);
             slot[i] = -1;
         }
-    }
+    // (A state's row is below 2^32 bytes, see kSsmMaxDim.)
+    const uint32_t state_bytes = static_cast<uint32_t>(dim) * S * sizeof(StateT);
+    uint8_t* base = static_cast<uint8_t*>(a.state) + static_cast<uint64_t>(static_cast<uint32_t>(ch)) * (S * sizeof(StateT));
+    auto row_at = [&](int i) { return reinterpret_cast<StateT*>(base + static_cast<uint64_t>(static_cast<uint32_t>(slot[i])) * state_bytes); };
+    Row<kBlocks, StateT> states[kTogether];
+    Row<kBlocks, KeyT> bs[kTogether], cs[kTogether];
+    const KeyT *b_row = static_cast<const KeyT*>(a.B) + n0 * a.ldb + group * S, *c_row = static_cast<const KeyT*>(a.C) + n0 * a.ldc + group * S;
+    auto load = [&](int i, int to) {
+        if (slot[i] >= 0) {
+            states[to].template load<kFull>(row_at(i), c, S);
+            bs[to].template load<kFull>(b_row, c, S);
+            cs[to].template load<kFull>(c_row, c, S);
+        }
+        b_row += a.ldb;
+        c_row += a.ldc;
+    };
+    if (kTogether == 4)
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i)
-        if (slot[i] >= 0) load_row<kBlocks>(a.state, a.state_f32, slot[i] * a.dim + ch, c, S, s[i]);
-    const int64_t own = part * kSeqs + c;
-    const int64_t own_slot = c == 0 ? slot[0] : c == 1 ? slot[1] : c == 2 ? slot[2] : slot[3];
-    float x = 0.f, z = 0.f;
-    float2 dt[1] = {};
-    if (own_slot >= 0) {
-        auto bf16_at = [](const void* p, int64_t at) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]); };
-        x = bf16_at(a.x, own * a.ldx + ch);
-        dt[0].x = a.dt_f32 ? static_cast<const float*>(a.dt)[own * a.lddt + ch] : bf16_at(a.dt, own * a.lddt + ch);
-        if (a.z) z = bf16_at(a.z, own * a.ldz + ch);
+        for (int i = 0; i < kTogether; ++i) load(i, i);
+    const int own = n0 + c;
+    __nv_bfloat16 x_raw = __float2bfloat16_rn(0.f), z_raw = x_raw;
+    uint32_t dt_raw = 0;
+    if (own < N) {   // (read for a padding row too, and not used)
+        x_raw = static_cast<const __nv_bfloat16*>(a.x)[own * a.ldx + ch];
+        if (a.z) z_raw = static_cast<const __nv_bfloat16*>(a.z)[own * a.ldz + ch];
+        dt_raw = a.dt_f32 ? static_cast<const uint32_t*>(a.dt)[own * a.lddt + ch] : static_cast<const uint16_t*>(a.dt)[own * a.lddt + ch];
     }
-    State<kBlocks> rate;
-    load_row<kBlocks>(a.A, true, ch, c, S, rate);
-    if (a.dt_bias) dt[0].x += a.dt_bias[ch];
-    const float skip = a.D ? a.D[ch] : 0.f;
+    Row<kBlocks, float> rates;
+    rates.template load<kFull>(a.A + static_cast<uint64_t>(static_cast<uint32_t>(ch)) * S, c, S);
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
+
+    float2 dt[1] = {make_float2(__uint_as_float(a.dt_f32 ? dt_raw : dt_raw << 16) + bias, 0.f)};
     if (a.softplus) softplus(dt);
-    const float du = dt[0].x * x;
+    const float x = __bfloat162float(x_raw), z = __bfloat162float(z_raw), du = dt[0].x * x;
+    State<kBlocks> rate;
+    rates.unpack(rate);
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) rate.h[k][i] = mul_pair(rate.h[k][i], pair(kLog2e, kLog2e));
-    float y[kSeqs];
+    float y[4];
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        const int at = kTogether == 4 ? i : 0;
+        if (kTogether == 1) load(i, 0);
         const float step = __shfl_sync(0xffffffffu, dt[0].x, i, 4), add = __shfl_sync(0xffffffffu, du, i, 4);
         y[i] = 0.f;
-        if (slot[i] < 0) continue;
-        const int64_t n = part * kSeqs + i;
-        uint64_t b[kBlocks][2], sum = 0ull;
-        State<kBlocks> keys;
-        load_keys<kBlocks>(a.B, a.bc_f32, a.vec_bc, n * a.ldb + group * S, c, S, b);
-        load_keys<kBlocks>(a.C, a.bc_f32, a.vec_bc, n * a.ldc + group * S, c, S, keys.h);
+        if (slot[i] >= 0) {
+            State<kBlocks> s, b, key;
+            states[at].unpack(s);
+            bs[at].unpack(b);
+            cs[at].unpack(key);
+            uint64_t sum = 0ull;
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k)
+            for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) b[k][j] = mul_pair(b[k][j], pair(add, add));
-        decay<kBlocks>(s[i], rate, pair(step, step), b);
+                for (int j = 0; j < 2; ++j) b.h[k][j] = mul_pair(b.h[k][j], pair(add, add));
+            decay<kBlocks>(s, rate, pair(step, step), b.h);
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k)
+            for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) sum = fma_pair(keys.h[k][j], s[i].h[k][j], sum);
-        y[i] = halves(sum).x + halves(sum).y;
-        if (live) store_row<kBlocks>(a.state, a.state_f32, slot[i] * a.dim + ch, c, S, s[i]);
+                for (int j = 0; j < 2; ++j) sum = fma_pair(key.h[k][j], s.h[k][j], sum);
+            y[i] = halves(sum).x + halves(sum).y;
+            if (live) Row<kBlocks, StateT>::template store<kFull>(row_at(i), c, S, s);
+        }
     }
     // Lane i gets the sum of sequence i over the four lanes.
-    const bool up = c & 2, odd = c & 1;
+    const bool up = c & 2, right = c & 1;
     float keep0 = up ? y[2] : y[0], keep1 = up ? y[3] : y[1];
     keep0 += __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 2);
     keep1 += __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 2);
-    float sum = odd ? keep1 : keep0;
-    sum += __shfl_xor_sync(0xffffffffu, odd ? keep0 : keep1, 1);
+    float sum = right ? keep1 : keep0;
+    sum += __shfl_xor_sync(0xffffffffu, right ? keep0 : keep1, 1);
     if (a.D) sum = fmaf(skip, x, sum);
     if (a.z) sum *= z * sigmoid(z);
-    if (live && own < a.N) static_cast<__nv_bfloat16*>(a.out)[own * a.dim + ch] = __float2bfloat16_rn(own_slot >= 0 ? sum : 0.f);
+    const int mine = right ? (up ? slot[3] : slot[1]) : up ? slot[2] : slot[0];
+    if (live && own < N) static_cast<__nv_bfloat16*>(a.out)[own * a.dim + ch] = __float2bfloat16_rn(mine >= 0 ? sum : 0.f);
 }
 
 template <int kBlocks, bool kStates, bool kPacked>
@@ -697,11 +753,23 @@ cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
     return e;
 }
 
-template <int kBlocks>
+template <int kBlocks, bool kFull, bool kStateF32, bool kKeysF32>
 cudaError_t decode(const SsmArgs& a, cudaStream_t stream) {
-    const int64_t blocks = (a.dim + 63) / 64, parts = (a.N + 3) / 4;
+    const int64_t blocks = (a.dim + kChannels - 1) / kChannels, parts = (a.N + 3) / 4;
     if (parts > 0x7fffffffLL / blocks) return cudaErrorInvalidValue;
-    return launch_after(ssm_decode_kernel<kBlocks>, dim3(static_cast<unsigned>(parts * blocks)), dim3(256), 0, stream, a);
+    return launch_after(ssm_decode_kernel<kBlocks, kFull, kStateF32, kKeysF32>, dim3(static_cast<unsigned>(blocks * parts)),
+                        dim3(kStepThreads), 0, stream, a, static_cast<int>(blocks));
+}
+template <int kBlocks, bool kFull>
+cudaError_t pick_decode(const SsmArgs& a, cudaStream_t stream) {
+    if (a.state_f32)
+        return a.bc_f32 ? decode<kBlocks, kFull, true, true>(a, stream) : decode<kBlocks, kFull, true, false>(a, stream);
+    return a.bc_f32 ? decode<kBlocks, kFull, false, true>(a, stream) : decode<kBlocks, kFull, false, false>(a, stream);
+}
+template <int kBlocks>
+cudaError_t pick_decode(const SsmArgs& a, cudaStream_t stream) {
+    return a.nstate == 16 * kBlocks && a.vec_bc ? pick_decode<kBlocks, true>(a, stream)
+                                                : pick_decode<kBlocks, false>(a, stream);
 }
 
 bool multiple(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -729,8 +797,8 @@ cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches) {
 cudaError_t launch_ssm_decode(SsmArgs a, cudaStream_t stream) {
     if (a.N <= 0 || a.dim <= 0) return cudaSuccess;
     set_vectors(&a);
-    if (a.nstate <= 16) return decode<1>(a, stream);
-    return a.nstate <= 32 ? decode<2>(a, stream) : decode<4>(a, stream);
+    if (a.nstate <= 16) return pick_decode<1>(a, stream);
+    return a.nstate <= 32 ? pick_decode<2>(a, stream) : pick_decode<4>(a, stream);
 }
 
 }  // namespace kda
