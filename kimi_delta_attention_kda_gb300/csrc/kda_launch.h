@@ -320,7 +320,10 @@ struct SsmArgs {
     float *span_states, *span_steps;
     int64_t tiles, tiles_per_group;      // of kSsmChannels channels
     bool dt_f32, bc_f32, state_f32, softplus;
-    bool vec, vec_bc;                    // (set by the launch)
+    // Set by the launch: rows that can be read four values at a time; bytes (out:
+    // elements) from a row to that 32 tokens on.
+    bool vec, vec_bc;
+    int64_t tile_x, tile_z, tile_dt, tile_b, tile_c, tile_out;
     int* status;
 };
 constexpr int kSsmTile = 32;

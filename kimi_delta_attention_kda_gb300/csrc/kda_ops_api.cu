@@ -206,8 +206,16 @@ struct SsmCut {
     int64_t bytes() const { return align256(state_bytes) + align256(step_bytes); }
 };
 
-// A span for every quarter of an SM, of at least kSsmMinSpan tokens.
-constexpr int64_t kSsmMinSpan = 4 * kSsmTile;
+// Costs of the scan on GB300, in microseconds for 32 tokens (rows: up to 16, 32 and 64
+// states): uncut, of a CTA with one, two and three of them on its SM, of which
+// the fullest SM decides; cut, for each CTA's part on every SM, states and outputs.
+// T = 8192, uncut and cut: 5,120 channels 494 and 366 us, 8,192 492 and 573, 9,728
+// 489 and 634.
+constexpr double kSsmTileUs[3][3] = {{1.46, 1.92, 2.59}, {2.5, 3.6, 0}, {4.5, 6.6, 0}};
+constexpr double kSsmCutTileUs[3] = {1.36, 2.6, 5.0}, kSsmCutUs = 10;
+// A span is this long at least: where that leaves more than one wave of CTAs, whole
+// waves of them (a last one that is not full costs as much), the more the better balanced.
+constexpr int64_t kSsmMinSpan = 2 * kSsmTile, kSsmGoodSpan = 14 * kSsmTile;
 
 int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, bool packed, bool state_f32, int sms,
              int allowed, int64_t forced, int64_t* tokens, SsmCut* c) {
@@ -224,10 +232,19 @@ int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, 
     if (allowed && length > 0) {
         if (forced > 0) {
             c->span_tokens = forced > length / 16 ? length : (16 * forced + kSsmTile - 1) / kSsmTile * kSsmTile;
-        } else if (4 * c->tiles * chains < 5 * sms && length >= 2 * kSsmMinSpan) {
-            const int64_t want = 4 * static_cast<int64_t>(sms) / (c->tiles * chains);
-            c->span_tokens = ((length + want - 1) / want + kSsmTile - 1) / kSsmTile * kSsmTile;
-            if (c->span_tokens < kSsmMinSpan) c->span_tokens = kSsmMinSpan;
+        } else {
+            const int row = nstate <= 16 ? 0 : nstate <= 32 ? 1 : 2;
+            const int64_t units = c->tiles * chains, resident = row == 0 ? 3 : 2, room = resident * sms;
+            const int64_t full = units / room, rest = (units - full * room + sms - 1) / sms;
+            const double tiles_each = static_cast<double>(length) / kSsmTile;
+            const double uncut = tiles_each * (full * kSsmTileUs[row][resident - 1] + (rest ? kSsmTileUs[row][rest - 1] : 0));
+            const double cut = kSsmCutUs + tiles_each * units / sms * kSsmCutTileUs[row];
+            const int64_t most = length / kSsmGoodSpan * units / room;   // waves that spans of that length fill
+            const int64_t want = (most < 1 ? 1 : most < 8 ? most : 8) * room / units;   // spans of each chain
+            if (want > 1 && length >= 2 * kSsmMinSpan && cut < uncut) {
+                c->span_tokens = ((length + want - 1) / want + kSsmTile - 1) / kSsmTile * kSsmTile;
+                if (c->span_tokens < kSsmMinSpan) c->span_tokens = kSsmMinSpan;
+            }
         }
     }
     c->spans_per_seq = length > 0 ? (length + c->span_tokens - 1) / c->span_tokens : 1;

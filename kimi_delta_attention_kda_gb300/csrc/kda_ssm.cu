@@ -7,16 +7,16 @@
 //
 // Prompts (ssm_kernel).  The decays differ in every channel and state, so there is
 // no product of matrices in it: 8 S + 20 operations for 8 bytes, of which S
-// exponentials, bound by the SMs' arithmetic.  A CTA has 32 channels and a span of
-// tokens, 32 at a time: its threads form dt, dt x and the rows of B and C as FP32
-// in shared memory, then a warp walks 8 channels through the tokens with the
-// states in registers, four lanes a channel and S / 4 states a lane.  The states
-// lie as the A operand of an m16n8k8 product (TF32): for one token, its rows are
-// the 8 channels' states twice over, half of the 16 states in each, and
-// column 2 t + i of the B operand has half i of token t's C, so that one
-// instruction gives sum_n C[n] h[n] of 8 channels, without shuffles.  That takes
-// h to TF32 on its way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own
-// rounding to BF16 is 2^-9 of out); the states themselves stay FP32.
+// exponentials, bound by the SMs.  A CTA has 32 channels and a span of tokens, 32 at
+// a time: half of its threads form dt, dt x and the rows of B and C as FP32 in
+// shared memory; the warps of the other half walk 16 channels and half of the states
+// through the tokens, two channels and two states (of every 16) in a lane's
+// registers, so that what a lane reads serves four.  The states lie as the A operand of an
+// m16n8k8 product (TF32), four registers that it takes as they are: rows are
+// channels, and column j of the B operand is token j's C, so that one instruction
+// gives sum_n C[n] h[n] of 16 channels, without shuffles.  That takes h to TF32 on its
+// way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own rounding to
+// BF16 is 2^-9 of out); the states themselves stay FP32.
 //
 // Few (sequence, channel) chains are cut into spans of tokens: a first launch
 // forms the state each span ends with (and the sum of its dt: the decay over a
@@ -40,52 +40,73 @@ constexpr int kChannels = kSsmChannels;  // channels of a CTA, 8 a warp
 static_assert(kRole == 4 * kTile && kChannels == 32, "a thread stages 8 channels of one token");
 constexpr float kLog2e = 1.4426950408889634f;
 
-// softplus(u) = max(u, 0) + log(1 + exp(-|u|)) of n pairs.  log(1 + t) / t on [0, 1]
-// is a polynomial of degree 8 fitted to the least relative error (3e-8; 1.8e-7 as
-// evaluated in FP32), all pairs a coefficient at a time.  NaN stays (through exp).
-template <int n>
-__device__ __forceinline__ void softplus(float2 (&u)[n]) {
-    constexpr float c[] = {0.99999994f,   -0.499994934f, 0.333190978f,  -0.24842982f, 0.191060051f,
-                           -0.136632428f, 0.0782259107f, -0.0295052137f, 0.00523268804f};
-    uint64_t t[n], p[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-        t[i] = pair(exp2_fast(fabsf(u[i].x) * -kLog2e), exp2_fast(fabsf(u[i].y) * -kLog2e));
-        p[i] = pair(c[8], c[8]);
-    }
-#pragma unroll
-    for (int k = 7; k >= 0; --k) {
-        const uint64_t ck = pair(c[k], c[k]);
-#pragma unroll
-        for (int i = 0; i < n; ++i) p[i] = fma_pair(p[i], t[i], ck);
-    }
-#pragma unroll
-    for (int i = 0; i < n; ++i) u[i] = halves(fma_pair(t[i], p[i], pair(fmaxf(u[i].x, 0.f), fmaxf(u[i].y, 0.f))));
+// softplus(u) = max(u, 0) + log(1 + exp(-|u|)).  log(1 + t) / t on [0, 1] is a
+// polynomial of degree 8 fitted to the least relative error (3e-8; 1.8e-7 as evaluated
+// in FP32).  (Packed pairs would cost more: their operands take three registers'
+// reads each, where a constant is part of the scalar instruction.)  NaN stays,
+// through the exponential.
+__device__ __forceinline__ float softplus(float u) {
+    const float t = exp2_fast(fabsf(u) * -kLog2e);
+    float p = 0.00523268804f;
+    p = fmaf(p, t, -0.0295052137f);
+    p = fmaf(p, t, 0.0782259107f);
+    p = fmaf(p, t, -0.136632428f);
+    p = fmaf(p, t, 0.191060051f);
+    p = fmaf(p, t, -0.24842982f);
+    p = fmaf(p, t, 0.333190978f);
+    p = fmaf(p, t, -0.499994934f);
+    p = fmaf(p, t, 0.99999994f);
+    return fmaf(t, p, fmaxf(u, 0.f));
 }
 
-// Shared memory of one of two buffers: (dt, dt, dt x, dt x) for each channel and
-// token, as the packed instructions take them (made from one value each, the pairs
-// cost two more instructions a token), the rows of B and C, and y.  Strides that keep the lanes'
-// accesses on different banks: a warp reads one token of 8 channels (16 bytes each),
-// a thread writes 8 channels of one token (8 words more for each 8 channels).
-constexpr int kStepStride = 4 * (kTile + 1);
-constexpr int kStepWords = kChannels * kStepStride + 8 * (kChannels / 8);
+// y <- y silu(z), eight times.  Above -80, z / (1 + exp(-z)) as it stands, six
+// instructions where sigmoid(), whose small values keep their bits, takes ten.
+__device__ __forceinline__ void gate8(const float (&z)[8], float (&y)[8]) {
+    float least = z[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) least = fminf(least, z[j]);
+    if (least > -80.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(z[j] * -kLog2e)));
+            y[j] *= z[j] * r;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= z[j] * sigmoid(z[j]);
+    }
+}
+
+// Shared memory of one of two buffers, which the walk is bound by (256 bytes a cycle
+// where neighbouring lanes read the same 16 bytes, 128 else): for each token and two
+// channels 8 apart (dt, dt, dt x, dt x), the rows of B and of C, and y, a sum over each
+// half of the states.  Strides that keep the lanes' accesses on different banks.
+constexpr int kStepStride = 4 * (kTile + 1), kStepHalf = 8 * kStepStride + 8;
+constexpr int kStepWords = 2 * kStepHalf;
 constexpr int kYStride = kChannels + 4;
 template <int kBlocks, bool kStates>
 struct Buffer {
-    static constexpr int kRow = 16 * kBlocks;
-    static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRow);
-    static constexpr int kXZ = kY + (kStates ? 0 : kTile * kYStride);   // x and z of each staging thread, for its outputs
+    static constexpr int kRow = 16 * kBlocks, kRowC = kRow + 8;
+    static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRowC);
+    static constexpr int kHalf = kTile * kYStride;   // of y
+    static constexpr int kXZ = kY + (kStates ? 0 : 2 * kHalf);   // x and z of each staging thread, for its outputs
     static constexpr int kWords = kXZ + (kStates ? 0 : 8 * kRole);
 };
-__device__ __forceinline__ int step_at(int ch, int token) { return ch * kStepStride + 8 * (ch >> 3) + 4 * token; }
+// The pair of channels that channel ch is of, at a token: (dt, dt, dt x, dt x).
+__device__ __forceinline__ int step_at(int ch, int token) { return (ch >> 4) * kStepHalf + (ch & 7) * kStepStride + 4 * token; }
 
-// What a thread stages of a tile, as loaded: 8 channels of one token, and for
-// each block of 16 states 4 values of B and of C.
+// What a staging thread fetches of a tile: of one token eight channels' x, z and dt, and
+// four values of every 16 of B and C.
 template <int kBlocks>
 struct Fetched {
     uint4 x, z, dt[2], b[kBlocks], c[kBlocks];
 };
+__device__ __forceinline__ uint4 two_pieces(const uint8_t* p) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 16);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Up to 8 (4) values as loaded where they cannot be read as a vector.
 __device__ __forceinline__ uint4 gather8(const __nv_bfloat16* p, int n) {
@@ -101,71 +122,74 @@ __device__ __forceinline__ uint4 gather4(const float* p, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A lane's states.  Prompts: pairs of two channels, 16 k + 8 half + 2 c + i of
+// channels g and g + 8 of the warp's 16 (g the lane's place among eight, c among
+// four).  Single tokens: states 16 k + 4 c + 2 i and the next of one channel.
 template <int kBlocks>
-struct State {   // a lane's 4 kBlocks states of its channel: 16 k + 4 c + {0 .. 3}, c the lane's place among four
+struct State {
     uint64_t h[kBlocks][2];
 };
 
-// Four values from state n0 on of a row of S.
+// Two values from state n0 on of a row of S.
 template <typename T>
-__device__ __forceinline__ void load_states(const T* row, int n0, int S, float (&v)[4]) {
-    if (S % 4 == 0) {
-        if (n0 < S) {
-            if constexpr (sizeof(T) == 4) {
-                const float4 r = *reinterpret_cast<const float4*>(row + n0);
-                v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
-            } else {
-                const uint2 r = *reinterpret_cast<const uint2*>(row + n0);
-                v[0] = bf16_lo(r.x); v[1] = bf16_hi(r.x); v[2] = bf16_lo(r.y); v[3] = bf16_hi(r.y);
-            }
+__device__ __forceinline__ float2 load_two(const T* row, int n0, int S) {
+    if (S % 2 == 0) {
+        float v[2] = {0.f, 0.f};
+        if (n0 < S) load_vec<2>(row + n0, v);
+        return make_float2(v[0], v[1]);
+    }
+    return make_float2(n0 < S ? static_cast<float>(row[n0]) : 0.f, n0 + 1 < S ? static_cast<float>(row[n0 + 1]) : 0.f);
+}
+template <typename T>
+__device__ __forceinline__ void store_two(T* row, int n0, int S, float2 v) {
+    if (S % 2 == 0) {
+        const float w[2] = {v.x, v.y};
+        if (n0 < S) store_vec<2>(row + n0, w);
+    } else {
+        if (n0 < S) from_f32(row + n0, v.x);
+        if (n0 + 1 < S) from_f32(row + n0 + 1, v.y);
+    }
+}
+// The lane's states of two rows of S (of channels 8 apart).
+template <int kBlocks>
+__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row8, int n0, int S, State<kBlocks>& s) {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        float2 a, b;
+        if (f32) {
+            a = load_two(static_cast<const float*>(p) + row * S, 16 * k + n0, S);
+            b = load_two(static_cast<const float*>(p) + row8 * S, 16 * k + n0, S);
         } else {
-            v[0] = v[1] = v[2] = v[3] = 0.f;
+            a = load_two(static_cast<const __nv_bfloat16*>(p) + row * S, 16 * k + n0, S);
+            b = load_two(static_cast<const __nv_bfloat16*>(p) + row8 * S, 16 * k + n0, S);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = n0 + i < S ? static_cast<float>(row[n0 + i]) : 0.f;
+        s.h[k][0] = pair(a.x, b.x);
+        s.h[k][1] = pair(a.y, b.y);
     }
 }
+template <int kBlocks>
+__device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool live, int64_t row8, bool live8, int n0, int S,
+                                           const State<kBlocks>& s) {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const float2 x = halves(s.h[k][0]), y = halves(s.h[k][1]);
+        const float2 a = make_float2(x.x, y.x), b = make_float2(x.y, y.y);
+        if (f32) {
+            if (live) store_two(static_cast<float*>(p) + row * S, 16 * k + n0, S, a);
+            if (live8) store_two(static_cast<float*>(p) + row8 * S, 16 * k + n0, S, b);
+        } else {
+            if (live) store_two(static_cast<__nv_bfloat16*>(p) + row * S, 16 * k + n0, S, a);
+            if (live8) store_two(static_cast<__nv_bfloat16*>(p) + row8 * S, 16 * k + n0, S, b);
+        }
+    }
+}
+// Four values, for single tokens.
 template <typename T>
-__device__ __forceinline__ void store_states(T* row, int n0, int S, const float (&v)[4]) {
-    if (S % 4 == 0) {
-        if (n0 < S) {
-            if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<float4*>(row + n0) = make_float4(v[0], v[1], v[2], v[3]);
-            else
-                *reinterpret_cast<uint2*>(row + n0) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n0 + i < S) from_f32(row + n0 + i, v[i]);
-    }
-}
-
-template <int kBlocks>
-__device__ __forceinline__ void load_row(const void* p, bool f32, int64_t row, int c, int S, State<kBlocks>& s) {
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-        float v[4];
-        if (f32)
-            load_states(static_cast<const float*>(p) + row * S, 16 * k + 4 * c, S, v);
-        else
-            load_states(static_cast<const __nv_bfloat16*>(p) + row * S, 16 * k + 4 * c, S, v);
-        s.h[k][0] = pair(v[0], v[1]);
-        s.h[k][1] = pair(v[2], v[3]);
-    }
-}
-template <int kBlocks>
-__device__ __forceinline__ void store_row(void* p, bool f32, int64_t row, int c, int S, const State<kBlocks>& s) {
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-        const float2 a = halves(s.h[k][0]), b = halves(s.h[k][1]);
-        const float v[4] = {a.x, a.y, b.x, b.y};
-        if (f32)
-            store_states(static_cast<float*>(p) + row * S, 16 * k + 4 * c, S, v);
-        else
-            store_states(static_cast<__nv_bfloat16*>(p) + row * S, 16 * k + 4 * c, S, v);
-    }
+__device__ __forceinline__ void store_four(T* row, const float (&v)[4]) {
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(row) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2*>(row) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 // A lane's values of a row of S as loaded, four at a time.  With kFull S is 16
 // kBlocks and they can be read so.
@@ -209,7 +233,7 @@ struct Row {
             const float2 a = halves(s.h[k][0]), b = halves(s.h[k][1]);
             const float v[4] = {a.x, a.y, b.x, b.y};
             if constexpr (kFull) {
-                store_states(row, n0, 16 * kBlocks, v);
+                store_four(row + n0, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -296,7 +320,10 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
 
 // Half of the warps walk; the other half stage the tile ahead and finish the one
 // behind, so that there are warps enough to hide each other's latencies.
-template <int kBlocks, bool kStates, bool kPacked>
+// kFast: BF16 dt, B and C, 16 kBlocks states, groups of whole 32 channels, a
+// softplus, and rows that can be read four values at a time, which leaves out two
+// fifths of the staging's instructions.
+template <int kBlocks, bool kStates, bool kPacked, bool kFast>
 __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
     using Buf = Buffer<kBlocks, kStates>;
     extern __shared__ __align__(16) float smem[];
@@ -308,61 +335,75 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     if (!w.run) return;
     const int64_t group = quotient(tile, a.tiles_per_group), per = quotient(a.dim, a.groups);
     const int64_t ch0 = group * per + (tile - group * a.tiles_per_group) * kChannels;
-    const int channels = static_cast<int>((group + 1) * per - ch0 < kChannels ? (group + 1) * per - ch0 : kChannels);
-    const int S = static_cast<int>(a.nstate);
+    const int channels = kFast || (group + 1) * per - ch0 > kChannels ? kChannels : static_cast<int>((group + 1) * per - ch0);
+    const int S = kFast ? 16 * kBlocks : static_cast<int>(a.nstate);
     const int tid = threadIdx.x & (kRole - 1);
-    const int64_t total = w.end - w.begin;   // tokens; tiles i = 0 .. tiles - 1 of them
-    const int tiles = static_cast<int>((total + kTile - 1) / kTile);
+    const int total = static_cast<int>(w.end - w.begin);   // tokens; tiles i = 0 .. tiles - 1 of them
+    const int tiles = (total + kTile - 1) / kTile;
 
     if (threadIdx.x >= kRole) {
-        // ---- staging: 8 channels of a token, a quarter of its rows of B and C
-        const int mine = 8 * (tid & 3), tok = tid >> 2;   // first channel within the CTA, token within the tile
-        const int count = channels - mine < 8 ? (channels - mine > 0 ? channels - mine : 0) : 8;
-        const bool wide = a.vec && count == 8, gated = !kStates && a.z;
+        // ---- staging: of one token four channels and the four 8 further on, and a
+        // quarter of its rows of B and C
+        const int tok = tid >> 2, mine = 16 * (tid >> 1 & 1) + 4 * (tid & 1);
+        auto clip = [](int n) { return n < 0 ? 0 : n < 4 ? n : 4; };
+        const int count = clip(channels - mine), count8 = clip(channels - mine - 8);
+        const bool wide = kFast || (a.vec && count8 == 4), wide_keys = kFast || a.vec_bc, gated = !kStates && a.z;
+        const bool dt_f32 = !kFast && a.dt_f32, bc_f32 = !kFast && a.bc_f32;
         float bias[8], skip[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            bias[i] = a.dt_bias && i < count ? a.dt_bias[ch0 + mine + i] : 0.f;
-            skip[i] = !kStates && a.D && i < count ? a.D[ch0 + mine + i] : 0.f;
+            const int at = mine + (i & 3) + 2 * (i & 4);
+            bias[i] = a.dt_bias && at < channels ? a.dt_bias[ch0 + at] : 0.f;
+            skip[i] = !kStates && a.D && at < channels ? a.D[ch0 + at] : 0.f;
         }
         // This thread's rows of the tile to fetch next, and to finish.
-        const int es = a.bc_f32 ? 4 : 2, dts = a.dt_f32 ? 4 : 2;
+        const int es = bc_f32 ? 4 : 2, dts = dt_f32 ? 4 : 2;
         const int64_t t0 = w.begin + tok;
-        auto xp = static_cast<const __nv_bfloat16*>(a.x) + t0 * a.ldx + ch0 + mine;
-        auto zp = static_cast<const __nv_bfloat16*>(a.z) + t0 * a.ldz + ch0 + mine;
+        auto xp = static_cast<const uint8_t*>(a.x) + (t0 * a.ldx + ch0 + mine) * 2;
+        auto zp = static_cast<const uint8_t*>(a.z) + (t0 * a.ldz + ch0 + mine) * 2;
         auto dp = static_cast<const uint8_t*>(a.dt) + (t0 * a.lddt + ch0 + mine) * dts;
         auto bp = static_cast<const uint8_t*>(a.B) + (t0 * a.ldb + group * S + 4 * (tid & 3)) * es;
         auto cp = static_cast<const uint8_t*>(a.C) + (t0 * a.ldc + group * S + 4 * (tid & 3)) * es;
         auto op = static_cast<__nv_bfloat16*>(a.out) + t0 * a.dim + ch0 + mine;
-        const int64_t xs = kTile * a.ldx, zs = kTile * a.ldz, ds = kTile * a.lddt * dts, bs = kTile * a.ldb * es,
-                      cs = kTile * a.ldc * es, os = kTile * a.dim;
-        auto fetch = [&](int i, Fetched<kBlocks>& f) {
-            if (i * kTile + tok < total) {
+        int ahead = total - tok;   // tokens from this thread's next one to fetch to the end
+        Fetched<kBlocks> f;
+        auto fetch = [&]() {
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            if (ahead > 0) {
                 if (wide) {
-                    f.x = *reinterpret_cast<const uint4*>(xp);
-                    if (gated) f.z = *reinterpret_cast<const uint4*>(zp);
-                    f.dt[0] = *reinterpret_cast<const uint4*>(dp);
-                    if (a.dt_f32) f.dt[1] = *reinterpret_cast<const uint4*>(dp + 16);
-                } else {
-                    f.x = gather8(xp, count);
-                    if (gated) f.z = gather8(zp, count);
-                    if (a.dt_f32) {
-                        f.dt[0] = gather4(reinterpret_cast<const float*>(dp), count);
-                        f.dt[1] = gather4(reinterpret_cast<const float*>(dp) + 4, count - 4);
+                    f.x = two_pieces(xp);
+                    if (gated) f.z = two_pieces(zp);
+                    if (dt_f32) {
+                        f.dt[0] = *reinterpret_cast<const uint4*>(dp);
+                        f.dt[1] = *reinterpret_cast<const uint4*>(dp + 32);
                     } else {
-                        f.dt[0] = gather8(reinterpret_cast<const __nv_bfloat16*>(dp), count);
+                        f.dt[0] = two_pieces(dp);
+                    }
+                } else {
+                    auto eight = [&](const uint8_t* p) {
+                        const uint4 lo = gather8(reinterpret_cast<const __nv_bfloat16*>(p), count),
+                                    hi = gather8(reinterpret_cast<const __nv_bfloat16*>(p + 16), count8);
+                        return make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    };
+                    f.x = eight(xp);
+                    if (gated) f.z = eight(zp);
+                    if (dt_f32) {
+                        f.dt[0] = gather4(reinterpret_cast<const float*>(dp), count);
+                        f.dt[1] = gather4(reinterpret_cast<const float*>(dp + 32), count8);
+                    } else {
+                        f.dt[0] = eight(dp);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k) {
                     const int have = S - 16 * k - 4 * (tid & 3);
                     const uint8_t *b = bp + 16 * k * es, *cc = cp + 16 * k * es;
-                    if (have <= 0) {
-                        f.b[k] = f.c[k] = make_uint4(0, 0, 0, 0);
-                    } else if (a.vec_bc && a.bc_f32) {
+                    if (!kFast && have <= 0) {
+                        f.b[k] = f.c[k] = none;
+                    } else if (wide_keys && bc_f32) {
                         f.b[k] = *reinterpret_cast<const uint4*>(b);
                         if (!kStates) f.c[k] = *reinterpret_cast<const uint4*>(cc);
-                    } else if (a.vec_bc) {
+                    } else if (wide_keys) {
                         const uint2 rb = *reinterpret_cast<const uint2*>(b);
                         f.b[k].x = rb.x;
                         f.b[k].y = rb.y;
@@ -371,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
                             f.c[k].x = rc.x;
                             f.c[k].y = rc.y;
                         }
-                    } else if (a.bc_f32) {
+                    } else if (bc_f32) {
                         f.b[k] = gather4(reinterpret_cast<const float*>(b), have);
                         if (!kStates) f.c[k] = gather4(reinterpret_cast<const float*>(cc), have);
                     } else {
@@ -379,16 +420,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
                         if (!kStates) f.c[k] = gather8(reinterpret_cast<const __nv_bfloat16*>(cc), have < 4 ? have : 4);
                     }
                 }
-            } else {
-                f.x = f.z = f.dt[0] = f.dt[1] = make_uint4(0, 0, 0, 0);
+            } else {   // behind the end nothing is added
+                f.x = f.z = f.dt[0] = f.dt[1] = none;
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k) f.b[k] = f.c[k] = make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < kBlocks; ++k) f.b[k] = f.c[k] = none;
             }
-            xp += xs;
-            if (gated) zp += zs;
-            dp += ds;
-            bp += bs;
-            if (!kStates) cp += cs;
+            xp += a.tile_x;
+            if (gated) zp += a.tile_z;
+            dp += a.tile_dt;
+            bp += a.tile_b;
+            if (!kStates) cp += a.tile_c;
+            ahead -= kTile;
         };
         // To the nearest TF32 value, which a BF16 one is.
         auto tf32 = [](float v) {
@@ -397,43 +439,40 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
             return __uint_as_float(r);
         };
         auto four = [&](const uint4& r) {
-            return a.bc_f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
-                            : make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+            return bc_f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
+                          : make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
         };
-        auto stage = [&](int i, const Fetched<kBlocks>& f) {
-            float* buf = smem + (i & 1) * Buf::kWords;
-            float u[8], x[8];
+        // (dt and what it stands for are of the tile before the next to fetch.)
+        auto stage = [&](float* buf) {
+            float dt[8], x[8];
             unpack8(f.x, x);
-            if (a.dt_f32) {
-                u[0] = __uint_as_float(f.dt[0].x); u[1] = __uint_as_float(f.dt[0].y);
-                u[2] = __uint_as_float(f.dt[0].z); u[3] = __uint_as_float(f.dt[0].w);
-                u[4] = __uint_as_float(f.dt[1].x); u[5] = __uint_as_float(f.dt[1].y);
-                u[6] = __uint_as_float(f.dt[1].z); u[7] = __uint_as_float(f.dt[1].w);
+            if (dt_f32) {
+                dt[0] = __uint_as_float(f.dt[0].x); dt[1] = __uint_as_float(f.dt[0].y);
+                dt[2] = __uint_as_float(f.dt[0].z); dt[3] = __uint_as_float(f.dt[0].w);
+                dt[4] = __uint_as_float(f.dt[1].x); dt[5] = __uint_as_float(f.dt[1].y);
+                dt[6] = __uint_as_float(f.dt[1].z); dt[7] = __uint_as_float(f.dt[1].w);
             } else {
-                unpack8(f.dt[0], u);
+                unpack8(f.dt[0], dt);
             }
-            float2 dt[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dt[j] = make_float2(u[2 * j] + bias[2 * j], u[2 * j + 1] + bias[2 * j + 1]);
-            if (a.softplus) softplus(dt);
-            if (i * kTile + tok >= total)   // behind the end nothing decays and nothing is added
-#pragma unroll
-                for (int j = 0; j < 4; ++j) dt[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = dt[j].x * x[2 * j], v1 = dt[j].y * x[2 * j + 1];
-                *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j, tok)) = make_float4(dt[j].x, dt[j].x, v, v);
-                *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j + 1, tok)) = make_float4(dt[j].y, dt[j].y, v1, v1);
+            for (int j = 0; j < 8; ++j) {
+                dt[j] += bias[j];
+                if (kFast || a.softplus) dt[j] = softplus(dt[j]);
             }
+            if (ahead <= -kTile)   // behind the end nothing decays either
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dt[j] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(buf + step_at(mine + j, tok)) = make_float4(dt[j], dt[j + 4], dt[j] * x[j], dt[j + 4] * x[j + 4]);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
-                const int at = tok * Buf::kRow + 16 * k + 4 * (tid & 3);
-                *reinterpret_cast<float4*>(buf + Buf::kB + at) = four(f.b[k]);
+                const int n0 = 16 * k + 4 * (tid & 3);
+                *reinterpret_cast<float4*>(buf + Buf::kB + tok * Buf::kRow + n0) = four(f.b[k]);
                 if (!kStates) {
-                    // (In the order in which the product's B operand takes them.)
                     const float4 v = four(f.c[k]);
-                    *reinterpret_cast<float4*>(buf + Buf::kC + at) =
-                        a.bc_f32 ? make_float4(tf32(v.x), tf32(v.z), tf32(v.y), tf32(v.w)) : make_float4(v.x, v.z, v.y, v.w);
+                    *reinterpret_cast<float4*>(buf + Buf::kC + tok * Buf::kRowC + n0) =
+                        bc_f32 ? make_float4(tf32(v.x), tf32(v.y), tf32(v.z), tf32(v.w)) : v;
                 }
             }
             if (!kStates) {
@@ -443,14 +482,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
             }
         };
         // A token's outputs from its y: the skip, the gate and one rounding.
-        auto finish = [&](int i) {
-            const float* buf = smem + (i & 1) * Buf::kWords;
-            if (i * kTile + tok < total) {
-                float y[8], x[8], z[8];
-                const float4* p = reinterpret_cast<const float4*>(buf + Buf::kY + tok * kYStride + mine);
-                const float4 lo = p[0], hi = p[1];
-                y[0] = lo.x; y[1] = lo.y; y[2] = lo.z; y[3] = lo.w; y[4] = hi.x; y[5] = hi.y; y[6] = hi.z; y[7] = hi.w;
+        int left = total - tok;   // tokens from this thread's next one to finish to the end
+        auto finish = [&](const float* buf) {
+            if (left > 0) {
+                const float* p = buf + Buf::kY + tok * kYStride + mine;
                 const uint4* xz = reinterpret_cast<const uint4*>(buf + Buf::kXZ) + tid;
+                float y[8], x[8], z[8];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + 8 * j), u = *reinterpret_cast<const float4*>(p + Buf::kHalf + 8 * j);
+                    y[4 * j] = v.x + u.x; y[4 * j + 1] = v.y + u.y; y[4 * j + 2] = v.z + u.z; y[4 * j + 3] = v.w + u.w;
+                }
                 if (a.D) {
                     unpack8(xz[0], x);
 #pragma unroll
@@ -458,45 +500,52 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
                 }
                 if (gated) {
                     unpack8(xz[kRole], z);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] *= z[j] * sigmoid(z[j]);
+                    gate8(z, y);
                 }
                 if (wide) {
-                    store8(op, y);
+                    *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                    *reinterpret_cast<uint2*>(op + 8) = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 4; ++j) {
                         if (j < count) op[j] = __float2bfloat16_rn(y[j]);
+                        if (j < count8) op[j + 8] = __float2bfloat16_rn(y[j + 4]);
+                    }
                 }
             }
-            op += os;
+            op += a.tile_out;
+            left -= kTile;
         };
-        Fetched<kBlocks> f;
+        // While tile i is walked, i - 1 is finished, i + 1 staged and i + 2 fetched.
+        float *buf = smem, *other = smem + Buf::kWords;
         if (tiles > 0) {
-            fetch(0, f);
-            stage(0, f);
-            fetch(1, f);
+            fetch();
+            stage(buf);
+            if (tiles > 1) fetch();
         }
         __syncthreads();
         for (int i = 0; i < tiles; ++i) {
-            if (!kStates && i > 0) finish(i - 1);
+            if (!kStates && i > 0) finish(other);
             if (i + 1 < tiles) {
-                stage(i + 1, f);
-                fetch(i + 2, f);
+                stage(other);
+                if (i + 2 < tiles) fetch();
             }
             __syncthreads();
+            float* const was = buf;
+            buf = other;
+            other = was;
         }
-        if (!kStates && tiles > 0) finish(tiles - 1);
+        if (!kStates && tiles > 0) finish(other);
         return;
     }
 
-    // ---- the walk: a warp's 8 channels, four lanes each
-    const int warp = tid >> 5, lane = tid & 31, c = lane & 3;
-    const int local = 8 * warp + (lane >> 2);
-    const bool live = local < channels;
-    const int64_t ch = ch0 + (live ? local : 0);
+    // ---- the walk: 16 channels and a half of every 16 states for each warp
+    const int warp = tid >> 5, lane = tid & 31, c = lane & 3, half = warp & 1;
+    const int local = 16 * (warp >> 1) + (lane >> 2), n0 = 8 * half + 2 * c;
+    const bool live = local < channels, live8 = local + 8 < channels;
+    const int64_t ch = ch0 + (live ? local : 0), ch8 = ch0 + (live8 ? local + 8 : 0);
     State<kBlocks> rate, s;
-    load_row<kBlocks>(a.A, true, ch, c, S, rate);
+    load_rows<kBlocks>(a.A, true, ch, ch8, n0, S, rate);
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
@@ -504,10 +553,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     auto initial = [&](int64_t seq) {
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) s.h[k][0] = s.h[k][1] = 0ull;
-        if (a.init_state) load_row<kBlocks>(a.init_state, a.state_f32, seq * a.dim + ch, c, S, s);
+        if (a.init_state) load_rows<kBlocks>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch8, n0, S, s);
     };
     auto ending = [&](int64_t seq) {
-        if (a.final_state && live) store_row<kBlocks>(a.final_state, a.state_f32, seq * a.dim + ch, c, S, s);
+        if (a.final_state)
+            store_rows<kBlocks>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch8, live8, n0, S, s);
     };
     if (w.fresh) {
         initial(w.seq);
@@ -520,9 +570,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
 #pragma unroll 4
             for (int64_t i = w.first_span; i < span; ++i) {
                 State<kBlocks> add;
-                load_row<kBlocks>(a.span_states, true, i * a.dim + ch, c, 16 * kBlocks, add);
-                const float dt = a.span_steps[i * a.dim + ch];
-                decay<kBlocks>(s, rate, pair(dt, dt), add.h);
+                load_rows<kBlocks>(a.span_states, true, i * a.dim + ch, i * a.dim + ch8, n0, 16 * kBlocks, add);
+                decay<kBlocks>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch8]), add.h);
             }
         }
     }
@@ -537,34 +586,36 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
         }
     };
     if (!kStates) close(0);
-    float steps = 0.f;   // the sum of dt
-    const int step0 = step_at(local, 0), rows0 = Buf::kB + 4 * c, y0 = Buf::kY + c * kYStride + local;
-    const int keys0 = Buf::kC + (lane >> 3) * Buf::kRow + 4 * c + 2 * ((lane >> 2) & 1);
-    // Four tokens from t on of the tile at `base`; with `ends`, sequences may end
+    uint64_t steps = 0ull;   // the sums of dt
+    const int step0 = step_at(local, 0), rows0 = Buf::kB + n0;
+    const int keys0 = Buf::kC + (lane >> 2) * Buf::kRowC + n0, y0 = Buf::kY + half * Buf::kHalf + 2 * c * kYStride + local;
+    // Eight tokens from t on of the tile at `base`; with `ends`, sequences may end
     // among them.  (Tokens behind the span's end change nothing: only the last span
-    // has them, and no sequence behind it.)
-    auto walk = [&](auto ends, const float* buf, int64_t base, int t) {
-        float ck[kBlocks][2], y = 0.f;
+    // has them, and no sequence behind it.)  y: of tokens 2 c and 2 c + 1, and of
+    // the second channel, as the product's accumulators have them.
+    auto walk = [&](auto ends, const float* buf, int64_t base, int t, float (&y)[4]) {
+        float ck[kBlocks][2];
         if (!kStates)
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRow + 16 * k);
+                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRowC + 16 * k);
                 ck[k][0] = v.x;
                 ck[k][1] = v.y;
             }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             uint64_t b[kBlocks][2];
-            const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(buf + step0 + 4 * (t + j));   // dt twice, dt x twice
+            const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(buf + step0 + 4 * (t + j));   // both dt, both dt x
+            const float2 du = halves(dd.y);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(buf + rows0 + (t + j) * Buf::kRow + 16 * k);
-                b[k][0] = mul_pair(dd.y, v.x);
-                b[k][1] = mul_pair(dd.y, v.y);
+                const float2 v = *reinterpret_cast<const float2*>(buf + rows0 + (t + j) * Buf::kRow + 16 * k);
+                b[k][0] = pair(du.x * v.x, du.y * v.x);
+                b[k][1] = pair(du.x * v.y, du.y * v.y);
             }
             decay<kBlocks>(s, rate, dd.x, b);
             if (kStates) {
-                steps += halves(dd.x).x;
+                steps = add_pair(steps, dd.x);
             } else {
                 float acc[4];
 #pragma unroll
@@ -575,12 +626,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
                     else
                         mma_tf32(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
                 }
-                // (The columns of the group's other tokens hold nothing of use.)
-                if (c == j) y = acc[0] + acc[3];
+                // (The columns of the other tokens hold nothing of use.)
+                if (c == j >> 1) {
+                    y[j & 1] = acc[j & 1];
+                    y[2 + (j & 1)] = acc[2 + (j & 1)];
+                }
                 if (decltype(ends)::value) close(base + t + j + 1);
             }
         }
-        return y;   // of token t + c
+    };
+    auto store_y = [&](float* buf, int t, const float (&y)[4]) {
+        float* at = buf + y0 + t * kYStride;
+        at[0] = y[0];
+        at[kYStride] = y[1];
+        at[8] = y[2];
+        at[kYStride + 8] = y[3];
     };
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
@@ -588,26 +648,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
         const int64_t base = static_cast<int64_t>(i) * kTile;
         if (base + kTile <= total && (!kPacked || kStates || seq_end >= base + kTile)) {
             // (y is stored behind all loads: the compiler keeps their order.)
-            float y[kTile / 4];
+            float y[kTile / 8][4];
 #pragma unroll
-            for (int t = 0; t < kTile; t += 4) y[t / 4] = walk(std::false_type{}, buf, base, t);
+            for (int t = 0; t < kTile; t += 8) walk(std::false_type{}, buf, base, t, y[t / 8]);
             if (!kStates)
 #pragma unroll
-                for (int t = 0; t < kTile; t += 4) buf[y0 + t * kYStride] = y[t / 4];
+                for (int t = 0; t < kTile; t += 8) store_y(buf, t, y[t / 8]);
             if (kPacked && !kStates) close(base + kTile);
         } else {
 #pragma unroll 1
-            for (int t = 0; t < kTile && base + t < total; t += 4) {
-                const float y = walk(std::integral_constant<bool, kPacked && !kStates>{}, buf, base, t);
-                if (!kStates) buf[y0 + t * kYStride] = y;
+            for (int t = 0; t < kTile && base + t < total; t += 8) {
+                float y[4];
+                walk(std::integral_constant<bool, kPacked && !kStates>{}, buf, base, t, y);
+                if (!kStates) store_y(buf, t, y);
             }
         }
         __syncthreads();
     }
     if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
-    if (kStates && live) {
-        store_row<kBlocks>(a.span_states, true, span * a.dim + ch, c, 16 * kBlocks, s);
-        if (c == 0) a.span_steps[span * a.dim + ch] = steps;
+    if (kStates) {
+        store_rows<kBlocks>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch8, live8, n0, 16 * kBlocks, s);
+        if (c == 0 && half == 0) {
+            if (live) a.span_steps[span * a.dim + ch] = halves(steps).x;
+            if (live8) a.span_steps[span * a.dim + ch8] = halves(steps).y;
+        }
     }
 }
 
@@ -675,9 +739,9 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
     rates.template load<kFull>(a.A + static_cast<uint64_t>(static_cast<uint32_t>(ch)) * S, c, S);
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
 
-    float2 dt[1] = {make_float2(__uint_as_float(a.dt_f32 ? dt_raw : dt_raw << 16) + bias, 0.f)};
-    if (a.softplus) softplus(dt);
-    const float x = __bfloat162float(x_raw), z = __bfloat162float(z_raw), du = dt[0].x * x;
+    float dt = __uint_as_float(a.dt_f32 ? dt_raw : dt_raw << 16) + bias;
+    if (a.softplus) dt = softplus(dt);
+    const float x = __bfloat162float(x_raw), z = __bfloat162float(z_raw), du = dt * x;
     State<kBlocks> rate;
     rates.unpack(rate);
 #pragma unroll
@@ -689,7 +753,7 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
     for (int i = 0; i < 4; ++i) {
         const int at = kTogether == 4 ? i : 0;
         if (kTogether == 1) load(i, 0);
-        const float step = __shfl_sync(0xffffffffu, dt[0].x, i, 4), add = __shfl_sync(0xffffffffu, du, i, 4);
+        const float step = __shfl_sync(0xffffffffu, dt, i, 4), add = __shfl_sync(0xffffffffu, du, i, 4);
         y[i] = 0.f;
         if (slot[i] >= 0) {
             State<kBlocks> s, b, key;
@@ -723,34 +787,40 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
     if (live && own < N) static_cast<__nv_bfloat16*>(a.out)[own * a.dim + ch] = __float2bfloat16_rn(mine >= 0 ? sum : 0.f);
 }
 
-template <int kBlocks, bool kStates, bool kPacked>
-cudaError_t run(const SsmArgs& a, int64_t spans, cudaStream_t stream) {
-    constexpr int bytes = 2 * Buffer<kBlocks, kStates>::kWords * 4;
+template <int kBlocks, bool kStates, bool kPacked, bool kFast>
+cudaError_t run(const SsmArgs& a, cudaStream_t stream) {
+    constexpr int bytes = 8 * Buffer<kBlocks, kStates>::kWords;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(ssm_kernel<kBlocks, kStates, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(ssm_kernel<kBlocks, kStates, kPacked, kFast>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    if (spans > 0x7fffffffLL / a.tiles) return cudaErrorInvalidValue;
-    return launch_after(ssm_kernel<kBlocks, kStates, kPacked>, dim3(static_cast<unsigned>(spans * a.tiles)), dim3(kThreads),
+    if (a.spans > 0x7fffffffLL / a.tiles) return cudaErrorInvalidValue;
+    return launch_after(ssm_kernel<kBlocks, kStates, kPacked, kFast>, dim3(static_cast<unsigned>(a.spans * a.tiles)), dim3(kThreads),
                         bytes, stream, a);
 }
 
-template <int kBlocks>
+template <int kBlocks, bool kFast>
 cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
     cudaError_t e;
     if (a.span_states) {
-        e = a.cu_seqlens ? run<kBlocks, true, true>(a, a.spans, stream) : run<kBlocks, true, false>(a, a.spans, stream);
+        e = a.cu_seqlens ? run<kBlocks, true, true, kFast>(a, stream) : run<kBlocks, true, false, kFast>(a, stream);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
-    e = a.cu_seqlens ? run<kBlocks, false, true>(a, a.spans, stream) : run<kBlocks, false, false>(a, a.spans, stream);
+    e = a.cu_seqlens ? run<kBlocks, false, true, kFast>(a, stream) : run<kBlocks, false, false, kFast>(a, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
+}
+template <int kBlocks>
+cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
+    const bool fast = a.vec && a.vec_bc && !a.dt_f32 && !a.bc_f32 && a.softplus && a.nstate == 16 * kBlocks &&
+                      a.dim / a.groups % kChannels == 0;
+    return fast ? prefill<kBlocks, true>(a, stream, launches) : prefill<kBlocks, false>(a, stream, launches);
 }
 
 template <int kBlocks, bool kFull, bool kStateF32, bool kKeysF32>
@@ -778,8 +848,8 @@ bool rows_of(const void* p, int64_t ld, int64_t tokens, int size, int n) {
     return !p || (multiple(p, static_cast<uintptr_t>(size * n)) && (tokens < 2 || ld % n == 0));
 }
 void set_vectors(SsmArgs* a) {
-    a->vec = a->dim / a->groups % 8 == 0 && rows_of(a->x, a->ldx, a->tokens, 2, 8) && rows_of(a->z, a->ldz, a->tokens, 2, 8) &&
-             (a->dt_f32 ? rows_of(a->dt, a->lddt, a->tokens, 4, 4) : rows_of(a->dt, a->lddt, a->tokens, 2, 8));
+    a->vec = a->dim / a->groups % 4 == 0 && rows_of(a->x, a->ldx, a->tokens, 2, 4) && rows_of(a->z, a->ldz, a->tokens, 2, 4) &&
+             rows_of(a->dt, a->lddt, a->tokens, a->dt_f32 ? 4 : 2, 4);
     const int size = a->bc_f32 ? 4 : 2;
     a->vec_bc = a->nstate % 4 == 0 && rows_of(a->B, a->ldb, a->tokens, size, 4) && rows_of(a->C, a->ldc, a->tokens, size, 4);
 }
@@ -789,6 +859,13 @@ void set_vectors(SsmArgs* a) {
 cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches) {
     if (a.N <= 0 || a.dim <= 0) return cudaSuccess;
     set_vectors(&a);
+    const int64_t bc = a.bc_f32 ? 4 : 2;
+    a.tile_x = kTile * a.ldx * 2;
+    a.tile_z = kTile * a.ldz * 2;
+    a.tile_dt = kTile * a.lddt * (a.dt_f32 ? 4 : 2);
+    a.tile_b = kTile * a.ldb * bc;
+    a.tile_c = kTile * a.ldc * bc;
+    a.tile_out = kTile * a.dim;
     if (a.nstate <= 16) return prefill<1>(a, stream, launches);
     if (a.nstate <= 32) return prefill<2>(a, stream, launches);
     return prefill<4>(a, stream, launches);
