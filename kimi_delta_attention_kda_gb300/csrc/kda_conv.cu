@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(C
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) ahead[i] = load_raw<kVec>(next + i * a.ldx);
     };
-    if (t + kGroup <= end) fetch();
+    if (end - t >= kGroup) fetch();
     Filter<kW, kVec> filter;
     filter.load(a, ch);
     if (kPacked) {   // the sequence and its first token; the first run also has the empty ones before that
@@ -184,12 +184,12 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(C
         if (t >= end) return;
         // Whole groups within the sequence, then a token at a time.
         const int last = end < seq_end ? end : seq_end;
-        while (t + kGroup <= last) {
+        while (last - t >= kGroup) {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) R::unpack(ahead[i], win[kKeep + i]);
             t += kGroup;
             next += kGroup * a.ldx;
-            if (t + kGroup <= end) fetch();
+            if (end - t >= kGroup) fetch();
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 store_raw<kVec>(out, filter.apply(win + i, a.silu));
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(C
             out += a.D;
             shift(1);
         }
-        if (t + kGroup <= end) fetch();
+        if (end - t >= kGroup) fetch();
     }
 }
 

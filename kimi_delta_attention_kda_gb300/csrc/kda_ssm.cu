@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     const int S = kFast ? 16 * kBlocks : static_cast<int>(a.nstate);
     const int tid = threadIdx.x & (kRole - 1);
     const int total = static_cast<int>(w.end - w.begin);   // tokens; tiles i = 0 .. tiles - 1 of them
-    const int tiles = (total + kTile - 1) / kTile;
+    const int tiles = total / kTile + (total % kTile > 0);
 
     if (threadIdx.x >= kRole) {
         // ---- staging: of one token four channels and the four 8 further on, and a
