@@ -3,17 +3,22 @@ KDA and blocks with per-head-decay linear attention in turn, prompts as one
 packed batch, then single tokens on a pool of states.
 
     python -m kimi_delta_attention_kda_gb300.example_block
+    python -m kimi_delta_attention_kda_gb300.example_block --kinds kda+conv ssm la+conv ssm
 
 runs every sequence twice: whole, and as a prompt whose last tokens come one by
 one; and prints how far the two are apart.  The weights are random.  The
 projections are torch matrix products; everything between them is this
 library: ``kda_prefill`` or ``la_prefill`` (``kda_decode`` or ``la_decode``)
-for the mixer, ``gated_norm`` after it, ``residual_norm`` between blocks.
+for the mixer, ``gated_norm`` after it, ``residual_norm`` between blocks; with
+``+conv`` a short convolution (``conv_prefill``, ``conv_decode``) of q, k and v in
+front of the mixer; and in blocks of the kind ``ssm`` the convolution and the
+selective scan (``ssm_prefill``, ``ssm_decode``) for the mixer.
 """
 
 from __future__ import annotations
 
 import argparse
+import math
 
 import torch
 import torch.nn.functional as F
@@ -21,15 +26,18 @@ import torch.nn.functional as F
 import kimi_delta_attention_kda_gb300 as kda
 
 D = kda.HEAD_DIM
+KINDS = ("kda", "la", "kda", "la")
 
 
 class Block:
     """One mixer with its projections: "kda" (a decay for each key channel, the
-    delta rule) or "la" (a decay for each head, key heads shared by two)."""
+    delta rule) or "la" (a decay for each head, key heads shared by two), either with
+    "+conv".  Its states, and their pools, are lists."""
 
     def __init__(self, kind, heads, gen):
         width = heads * D
-        self.kind, self.heads = kind, heads
+        self.kind, _, conv = kind.partition("+")
+        self.heads, self.conv, kind = heads, bool(conv), self.kind
         self.key_heads = heads // 2 if kind == "la" and heads % 2 == 0 else heads
         decays = heads if kind == "la" else width
         self.sizes = [self.key_heads * D, self.key_heads * D, width, width, decays] + ([heads] if kind == "kda" else [])
@@ -40,10 +48,16 @@ class Block:
         self.w_in, self.w_out = weight(sum(self.sizes), width), weight(width, width)
         self.norm, self.mix_norm, self.post_norm = (
             (1 + 0.1 * torch.randn(n, generator=gen)).bfloat16().cuda() for n in (width, D, width))
+        if self.conv:
+            self.filter = weight(sum(self.sizes[:3]), 4)
 
-    def project(self, y):
+    def project(self, y, convolve):
         """q, k, v and the output gate as heads, the log-decays, and beta's logits."""
-        p = [x.contiguous() for x in (y @ self.w_in.t()).split(self.sizes, dim=-1)]
+        p = y @ self.w_in.t()
+        if self.conv:   # of q, k and v together, where they lie in the projection
+            n = sum(self.sizes[:3])
+            p = torch.cat([convolve(p[:, :n]), p[:, n:]], dim=-1)
+        p = [x.contiguous() for x in p.split(self.sizes, dim=-1)]
         q, k = (x.view(-1, self.key_heads, D) for x in p[:2])
         v, z = (x.view(-1, self.heads, D) for x in p[2:4])
         if self.kind == "la":
@@ -55,30 +69,79 @@ class Block:
         return o.view(o.shape[0], -1) @ self.w_out.t()
 
     def prompt(self, y, cu):
-        """Packed tokens [T, width]; (what the block adds, the final states in FP32)."""
-        q, k, v, z, g, beta = self.project(y)
+        """Packed tokens [T, width]; (what the block adds, the final states, the mixer's in FP32)."""
+        states = []
+
+        def convolve(x):
+            x, state = kda.conv_prefill(x[None], self.filter, cu_seqlens=cu)
+            states.append(state)
+            return x[0]
+        q, k, v, z, g, beta = self.project(y, convolve)
         one = [x[None] for x in (q, k, v, g)]
         if self.kind == "la":
             o, state = kda.la_prefill(*one, cu_seqlens=cu)
         else:
             o, state = kda.kda_prefill(*one, beta[None], cu_seqlens=cu, beta_is_logit=True)
-        return self.finish(o[0], z), state.float()
+        return self.finish(o[0], z), states + [state.float()]
 
-    def token(self, y, pool, slots):
-        """One token of each sequence [N, width], its state in its row of the pool."""
-        q, k, v, z, g, beta = self.project(y)
+    def token(self, y, pools, slots):
+        """One token of each sequence [N, width], its states in its row of the pools."""
+        q, k, v, z, g, beta = self.project(y, lambda x: kda.conv_decode(x, self.filter, pools[0], slots=slots))
         if self.kind == "la":
-            o = kda.la_decode(q, k, v, g, pool, slots)
+            o = kda.la_decode(q, k, v, g, pools[-1], slots)
         else:
-            o = kda.kda_decode(q, k, v, g, beta, pool, slots, beta_is_logit=True)
+            o = kda.kda_decode(q, k, v, g, beta, pools[-1], slots, beta_is_logit=True)
         return self.finish(o, z)
 
 
+class ScanBlock:
+    """The selective scan behind its convolution: a decay for each channel and
+    state, step sizes, B and C from the convolved channels."""
+
+    STATES = 16
+
+    def __init__(self, heads, gen):
+        width, S = heads * D, self.STATES
+        self.width, self.rank = width, width // 16
+
+        def weight(*shape):
+            return (torch.randn(shape, generator=gen) * shape[-1] ** -0.5).bfloat16().cuda()
+
+        self.w_in, self.w_out = weight(2 * width, width), weight(width, width)
+        self.w_keys, self.w_dt, self.filter = weight(self.rank + 2 * S, width), weight(width, self.rank), weight(width, 4)
+        self.norm, self.post_norm = ((1 + 0.1 * torch.randn(width, generator=gen)).bfloat16().cuda() for _ in range(2))
+        self.A = -torch.arange(1, S + 1).float().repeat(width, 1).cuda()
+        self.skip = torch.ones(width).cuda()
+        step = torch.exp(math.log(1e-3) + math.log(100) * torch.rand(width, generator=gen))
+        self.dt_bias = torch.log(torch.expm1(step)).cuda()
+
+    def keys(self, x):
+        """dt, B and C of convolved channels [rows, width]."""
+        p = x @ self.w_keys.t()
+        B, C = (y.unflatten(-1, (1, self.STATES)) for y in p[:, self.rank:].split(self.STATES, dim=-1))
+        return p[:, :self.rank] @ self.w_dt.t(), B, C
+
+    def prompt(self, y, cu):
+        p = y @ self.w_in.t()
+        x, conv_state = kda.conv_prefill(p[None, :, :self.width], self.filter, cu_seqlens=cu)
+        dt, B, C = self.keys(x[0])
+        o, state = kda.ssm_prefill(x, dt[None], self.A, B[None], C[None], self.skip, p[None, :, self.width:], self.dt_bias,
+                                   cu_seqlens=cu)
+        return o[0] @ self.w_out.t(), [conv_state, state]
+
+    def token(self, y, pools, slots):
+        p = y @ self.w_in.t()
+        x = kda.conv_decode(p[:, :self.width], self.filter, pools[0], slots=slots)
+        dt, B, C = self.keys(x)
+        o = kda.ssm_decode(x, dt, self.A, B, C, pools[1], self.skip, p[:, self.width:], self.dt_bias, slots=slots)
+        return o @ self.w_out.t()
+
+
 class Stack:
-    def __init__(self, kinds=("kda", "la", "kda", "la"), heads=4, seed=0):
+    def __init__(self, kinds=KINDS, heads=4, seed=0):
         gen = torch.Generator().manual_seed(seed)
         self.width = heads * D
-        self.blocks = [Block(kind, heads, gen) for kind in kinds]
+        self.blocks = [ScanBlock(heads, gen) if kind == "ssm" else Block(kind, heads, gen) for kind in kinds]
         self.last = torch.ones(self.width, dtype=torch.bfloat16, device="cuda")
 
     def run(self, x, mix):
@@ -90,7 +153,7 @@ class Stack:
         return y
 
     def prompt(self, x, cu):
-        """(outputs [T, width], each block's states [N, heads, 128, 128])."""
+        """(outputs [T, width], each block's states)."""
         states = []
 
         def mix(i, y):
@@ -103,10 +166,10 @@ class Stack:
         return self.run(x, lambda i, y: self.blocks[i].token(y, pools[i], slots))
 
 
-def compare(lengths=(300, 17, 1200, 64), tokens=16, heads=4, seed=0):
+def compare(lengths=(300, 17, 1200, 64), tokens=16, heads=4, seed=0, kinds=KINDS):
     """The relative distance (Frobenius norm) between each sequence's last
     ``tokens`` outputs computed whole and token by token."""
-    stack = Stack(heads=heads, seed=seed)
+    stack = Stack(kinds, heads, seed)
     gen = torch.Generator().manual_seed(seed + 1)
     seqs = [torch.randn(n + tokens, stack.width, generator=gen).bfloat16().cuda() for n in lengths]
 
@@ -124,10 +187,12 @@ def compare(lengths=(300, 17, 1200, 64), tokens=16, heads=4, seed=0):
     n = len(lengths)
     slots = torch.tensor(list(range(n, 0, -1)) + [-1], dtype=torch.int32, device="cuda")
     pools = []
-    for s in states:
-        pool = torch.zeros((n + 2,) + s.shape[1:], device="cuda")
-        pool[slots[:n].long()] = s
-        pools.append(pool)
+    for block in states:
+        pools.append([])
+        for s in block:
+            pool = torch.zeros((n + 2,) + s.shape[1:], dtype=s.dtype, device="cuda")
+            pool[slots[:n].long()] = s
+            pools[-1].append(pool)
     got = []
     for t in range(tokens):
         now = torch.stack([s[s.shape[0] - tokens + t] for s in seqs] + [seqs[0][0]])
@@ -143,9 +208,10 @@ def main():
     ap.add_argument("--lengths", type=int, nargs="+", default=[300, 17, 1200, 64])
     ap.add_argument("--tokens", type=int, default=16)
     ap.add_argument("--heads", type=int, default=4)
+    ap.add_argument("--kinds", nargs="+", default=list(KINDS), choices=["kda", "la", "kda+conv", "la+conv", "ssm"])
     a = ap.parse_args()
     print("%d sequences, the last %d tokens one by one: relative distance %.2e from the whole prompts"
-          % (len(a.lengths), a.tokens, compare(a.lengths, a.tokens, a.heads)))
+          % (len(a.lengths), a.tokens, compare(a.lengths, a.tokens, a.heads, kinds=a.kinds)))
 
 
 if __name__ == "__main__":
