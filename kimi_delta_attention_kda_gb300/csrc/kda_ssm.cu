@@ -183,13 +183,14 @@ __device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool 
         }
     }
 }
-// Four values, for single tokens.
+// Four values of a single token's state, which nobody reads before the next token:
+// a streaming store (128 sequences of 12,288 channels 35 us, with a plain one 40).
 template <typename T>
 __device__ __forceinline__ void store_four(T* row, const float (&v)[4]) {
     if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4*>(row) = make_float4(v[0], v[1], v[2], v[3]);
+        __stcs(reinterpret_cast<float4*>(row), make_float4(v[0], v[1], v[2], v[3]));
     else
-        *reinterpret_cast<uint2*>(row) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        __stcs(reinterpret_cast<uint2*>(row), make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
 }
 // A lane's values of a row of S as loaded, four at a time.  With kFull S is 16
 // kBlocks and they can be read so.
