@@ -332,6 +332,11 @@ constexpr int64_t kSsmMaxState = 64, kSsmMaxDim = (int64_t(1) << 24) - 1;
 // Adds the kernels it launches to *launches.
 cudaError_t launch_ssm_prefill(SsmArgs a, cudaStream_t stream, int* launches);
 cudaError_t launch_ssm_decode(SsmArgs a, cudaStream_t stream);
+// launch_ssm_prefill's kernels for rows of up to 16, 32 and 64 states.
+cudaError_t ssm_prefill_16(const SsmArgs& a, cudaStream_t stream, int* launches);
+cudaError_t ssm_prefill_32(const SsmArgs& a, cudaStream_t stream, int* launches);
+cudaError_t ssm_prefill_64(const SsmArgs& a, cudaStream_t stream, int* launches);
+void set_ssm_vectors(SsmArgs* a);   // sets a->vec and a->vec_bc
 // Up to this many offsets every CTA checks them itself.
 constexpr int64_t kMaxSelfChecked = 1024;
 

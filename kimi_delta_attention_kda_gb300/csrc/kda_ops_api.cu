@@ -254,8 +254,9 @@ int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, 
         if (c->spans > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
         c->state_bytes = c->spans * dim * wide * 4;
         c->step_bytes = c->spans * dim * 4;
-        c->init_bytes = N * dim * nstate * (state_f32 ? 4 : 2);
     }
+    // (Where a group is no whole 32 channels two CTAs have some of them.)
+    if (c->spans_per_seq > 1 || dim / groups % kSsmChannels) c->init_bytes = N * dim * nstate * (state_f32 ? 4 : 2);
     return KDA_OK;
 }
 
@@ -681,7 +682,7 @@ extern "C" int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64
     a.tiles = cut.tiles;
     a.tiles_per_group = cut.tiles_per_group;
     const auto stream = static_cast<cudaStream_t>(stream_ptr);
-    const bool many = cu_seqlens && B > kMaxSelfChecked, copied = cut.cut() && init_state && init_state == final_state;
+    const bool many = cu_seqlens && B > kMaxSelfChecked, copied = cut.init_bytes > 0 && init_state && init_state == final_state;
     Scratch ws;
     if (!ws.take((many ? 256 : 0) + cut.bytes() + (copied ? align256(state) : 0), d.pool, stream)) return KDA_ERR_CUDA;
     if (many) {
@@ -693,7 +694,7 @@ extern "C" int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64
         a.span_states = reinterpret_cast<float*>(ws.part(cut.state_bytes));
         a.span_steps = reinterpret_cast<float*>(ws.part(cut.step_bytes));
     }
-    if (copied) {   // one CTA ends a sequence while another begins it
+    if (copied) {   // one CTA ends a sequence that another has yet to begin
         void* copy = ws.part(state);
         if (cudaMemcpyAsync(copy, init_state, static_cast<size_t>(state), cudaMemcpyDeviceToDevice, stream) != cudaSuccess) {
             cudaGetLastError();

@@ -297,6 +297,37 @@ def test_large_and_small_steps(kda):
     assert torch.allclose(f[0, 5:7].cpu().double(), want[1][0, 5:7], rtol=1e-5, atol=0)
 
 
+@pytest.mark.parametrize("dim,G", [(36, 1), (44, 1), (72, 2), (132, 3)])
+@pytest.mark.parametrize("S", [4, 12, 16, 20, 48])
+@pytest.mark.parametrize("dt,bc", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+def test_last_channels(kda, dim, G, S, dt, bc):
+    """Groups that are no whole 32 channels: whole, in spans, packed, and in place."""
+    d = draw((1, 140), dim, S, dim + S, G=G, dt=dt, bc=bc, init=1)
+    want = want_of(d)
+    for on, chunks in ((False, 0), (True, 4)):
+        kda.set_segments(on, chunks)
+        out, fin = check(kda, d, want=want)
+        dev = on_gpu(d)
+        got = kda.ssm_prefill(**dev, final_state=dev["init_state"])
+        assert torch.equal(got[0], out) and torch.equal(dev["init_state"], fin)
+    cu = [0, 3, 64, 64, 140]
+    check(kda, draw((1, 140), dim, S, dim + S, G=G, dt=dt, bc=bc, z=False, init=4, state=BF16), cu)
+
+
+@pytest.mark.parametrize("rate", [float("-inf"), torch.finfo(F32).min])
+@pytest.mark.parametrize("S", [16, 5, 32])
+def test_rates_without_bound(kda, rate, S):
+    """States that no step keeps, as with a rate of -1e30, also behind the last token."""
+    for chunks, cu in ((0, None), (1, None), (0, [0, 37, 37, 45, 77]), (1, [0, 37, 37, 45, 77])):
+        kda.set_segments(True, chunks)
+        d = on_gpu(draw((1, 77), 40, S, S, init=4 if cu else 1))
+        cu = None if cu is None else torch.tensor(cu, device="cuda")
+        d["A"][3] = d["A"][17, 1] = -1e30
+        want = kda.ssm_prefill(**d, cu_seqlens=cu)
+        d["A"][3] = d["A"][17, 1] = rate
+        assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(kda.ssm_prefill(**d, cu_seqlens=cu), want))
+
+
 # ------------------------------------------------------------- single tokens
 
 def check_step(kda, d, slots, status=0, softplus=True):
@@ -338,6 +369,13 @@ def test_step(kda, N, dim, S, state):
 @pytest.mark.parametrize("dim,G", [(64, 2), (72, 2), (30, 5)])
 def test_step_groups(kda, dim, G):
     check_step(kda, draw((9,), dim, 16, dim, G=G, init=9), None)
+
+
+@pytest.mark.parametrize("S", [4, 8, 12, 16, 20, 48])
+@pytest.mark.parametrize("dt,bc", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+def test_step_types(kda, S, dt, bc):
+    for state in (F32, BF16):
+        check_step(kda, draw((6,), 36, S, S, G=2, dt=dt, bc=bc, init=8, state=state), [7, -1, 0, 3, 1, 5])
 
 
 @pytest.mark.parametrize("N", [4, 2500])
