@@ -573,15 +573,16 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  *   dt          : BF16 or FP32 (KDA_FLAG_DT_F32), a row of dim for each token
  *   Bm, Cm      : BF16 or FP32 (KDA_FLAG_BC_F32), a row of [groups, nstate] for each token
  *   ldx, lddt, ldb, ldc, ldz : elements between rows, at least a row's width
- *   A           : FP32 [dim, nstate], contiguous, finite; D, dt_bias: FP32 [dim] or NULL
+ *   A           : FP32 [dim, nstate], contiguous, below infinity; D, dt_bias: FP32 [dim] or NULL
  *   out         : BF16 [tokens, dim], contiguous
  *   init_state  : [N, dim, nstate] or NULL for zeros; BF16, or FP32 with KDA_FLAG_STATE_F32
  *   final_state : the same type, or NULL (not written); may be init_state
  *   nstate      : 1 .. 64 (16, 32 and 64 waste nothing); dim below 2^24; groups divides dim
  * Fixed and packed layouts, cu_seqlens, empty sequences, the T = 0 rule (A is
  * still needed) and the limit on tokens are those of kda_prefill.  Alignment: A, out
- * and the states 16 bytes, cu_seqlens 8, the rest an element's size (rows on 16
- * bytes and channels of a group in multiples of 8 are read fastest).
+ * and the states 16 bytes, cu_seqlens 8, the rest an element's size (rows on 8
+ * bytes, dt, B and C in FP32 on 16, 32 channels or more to a group in multiples of 4, and
+ * nstate a multiple of 4 run fastest).
  * out and final_state may overlap no input and not each other.
  * The states and all sums are FP32; on the way to out each state is cut to TF32
  * (2^-10 of a product at most) before its product with C, and out is rounded
@@ -590,10 +591,11 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  * When there are too few channels to fill the GPU the tokens are cut into
  * spans: one launch forms the state each span ends with, one the outputs from
  * what the spans before leave.  kda_set_segments governs this (off: no cut; a
- * forced length is rounded up to whole 32 tokens).  Equal calls give equal
- * bits.  Scratch comes from the library's stream-ordered pool: with a cut an
- * FP32 state for each span and channel, and a copy of the initial states where
- * final_state is init_state.
+ * forced length is rounded up to whole 32 tokens).  Where there are more than fill
+ * it evenly, spans may run one after the other, which changes no bit and is governed by
+ * nothing.  Equal calls give equal bits.  Scratch comes from the library's
+ * stream-ordered pool: with spans of either kind an FP32 state for each span and
+ * channel, and a copy of the initial states where final_state is init_state.
  */
 int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A,
                     const void* Bm, int64_t ldb, const void* Cm, int64_t ldc, const float* D,
@@ -615,7 +617,7 @@ int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_t lddt, con
 
 /*
  * Spans kda_ssm_prefill cuts each sequence of a call of this shape into
- * (packed: the whole batch; 0: no cut), and the bytes of scratch it takes at
+ * (packed: the whole batch; 0: no cut, or spans one after the other), and the bytes of scratch it takes at
  * most (HOST out).  As kda_plan_segments and kda_workspace_bytes.
  */
 int kda_ssm_plan_segments(int64_t B, int64_t T, int64_t dim, int64_t groups, int64_t nstate,

@@ -318,6 +318,10 @@ struct SsmArgs {
     // ([spans][dim][16, 32 or 64]) and its sum of dt ([spans][dim]).
     int64_t spans, spans_per_seq, span_tokens;
     float *span_states, *span_steps;
+    // Not null: spans of a sequence one after the other (see kda_ssm_scan.cuh), a
+    // count of the CTAs that began, then a flag for each span and tile: its state is
+    // there.  All 0 before the launch.
+    int32_t* relay;
     int64_t tiles, tiles_per_group;      // of kSsmChannels channels
     bool dt_f32, bc_f32, state_f32, softplus;
     // Set by the launch: rows that can be read four values at a time; bytes (out:

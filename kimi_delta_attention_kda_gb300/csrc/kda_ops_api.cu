@@ -198,27 +198,35 @@ int check_conv(const ConvArgs& a, int activation) {
 
 // The cut of a call of the scan (see kda_ssm_prefill).
 struct SsmCut {
-    int64_t tiles_per_group, tiles;
+    int64_t tiles_per_group = 0, tiles = 0;
     int64_t spans = 0, spans_per_seq = 1, span_tokens = 0;
     int64_t state_bytes = 0, step_bytes = 0;   // of the spans' states, with more than one
+    int64_t relay_bytes = 0;                   // of the flags of spans that run one after the other
     int64_t init_bytes = 0;                    // a copy of initial states that final ones overwrite
     bool cut() const { return state_bytes > 0; }
-    int64_t bytes() const { return align256(state_bytes) + align256(step_bytes); }
+    int64_t bytes() const { return align256(state_bytes) + align256(step_bytes) + align256(relay_bytes); }
 };
 
 // Costs of the scan on GB300, in microseconds for 32 tokens (rows: up to 16, 32 and 64
 // states): uncut, of a CTA with one, two and three of them on its SM, of which
 // the fullest SM decides; cut, for each CTA's part on every SM, states and outputs.
-// T = 8192, uncut and cut: 5,120 channels 494 and 366 us, 8,192 492 and 573, 9,728
-// 489 and 634.
-constexpr double kSsmTileUs[3][3] = {{1.46, 1.92, 2.59}, {2.5, 3.6, 0}, {4.5, 6.6, 0}};
-constexpr double kSsmCutTileUs[3] = {1.36, 2.6, 5.0}, kSsmCutUs = 10;
+// T = 8192, uncut and cut: 5,120 channels 494 and 361 us, 6,144 495 and 438, 8,192
+// 480 and 573.
+constexpr double kSsmTileUs[3][3] = {{1.49, 1.87, 2.54}, {2.03, 2.93, 0}, {4.33, 5.54, 0}};
+constexpr double kSsmCutTileUs[3] = {1.36, 2.4, 4.4}, kSsmCutUs = 10;
+// Spans one after the other (more chains than SMs), a sixteenth of the tokens each, 512
+// at least: for the flags' clearing, and for each span that takes up a state.  Uncut and so:
+// 8192 tokens of 12,288 channels 651 and 610 us, of 10,240 648 and 590, two prompts of
+// 4096 tokens 643 and 573, 4096 tokens with 64 states 1,233 and 974.
+constexpr double kSsmRelayUs = 10, kSsmRelaySpanUs = 2.2;
+constexpr int64_t kSsmRelaySpans = 16, kSsmRelayMin = 16 * kSsmTile;
 // A span is this long at least: where that leaves more than one wave of CTAs, whole
 // waves of them (a last one that is not full costs as much), the more the better balanced.
 constexpr int64_t kSsmMinSpan = 2 * kSsmTile, kSsmGoodSpan = 14 * kSsmTile;
 
 int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, bool packed, bool state_f32, int sms,
              int allowed, int64_t forced, int64_t* tokens, SsmCut* c) {
+    *c = SsmCut{};
     int rc = count_tokens(N, T, packed, tokens);
     if (rc != KDA_OK) return rc;
     if (dim < 1 || groups < 1 || dim % groups || nstate < 1 || nstate > kSsmMaxState) return KDA_ERR_SHAPE;
@@ -229,21 +237,41 @@ int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, 
     const int64_t chains = packed ? 1 : N;        // that go on for `length` tokens
     const int64_t length = packed ? *tokens : T;
     c->span_tokens = length > 0 ? length : 1;
-    if (allowed && length > 0) {
-        if (forced > 0) {
-            c->span_tokens = forced > length / 16 ? length : (16 * forced + kSsmTile - 1) / kSsmTile * kSsmTile;
-        } else {
-            const int row = nstate <= 16 ? 0 : nstate <= 32 ? 1 : 2;
-            const int64_t units = c->tiles * chains, resident = row == 0 ? 3 : 2, room = resident * sms;
-            const int64_t full = units / room, rest = (units - full * room + sms - 1) / sms;
-            const double tiles_each = static_cast<double>(length) / kSsmTile;
-            const double uncut = tiles_each * (full * kSsmTileUs[row][resident - 1] + (rest ? kSsmTileUs[row][rest - 1] : 0));
-            const double cut = kSsmCutUs + tiles_each * units / sms * kSsmCutTileUs[row];
-            const int64_t most = length / kSsmGoodSpan * units / room;   // waves that spans of that length fill
-            const int64_t want = (most < 1 ? 1 : most < 8 ? most : 8) * room / units;   // spans of each chain
-            if (want > 1 && length >= 2 * kSsmMinSpan && cut < uncut) {
-                c->span_tokens = ((length + want - 1) / want + kSsmTile - 1) / kSsmTile * kSsmTile;
-                if (c->span_tokens < kSsmMinSpan) c->span_tokens = kSsmMinSpan;
+    bool relay = false;
+    if (allowed && forced > 0 && length > 0) {
+        c->span_tokens = forced > length / 16 ? length : (16 * forced + kSsmTile - 1) / kSsmTile * kSsmTile;
+    } else if (length > 0) {
+        const int row = nstate <= 16 ? 0 : nstate <= 32 ? 1 : 2;
+        const int64_t units = c->tiles * chains, resident = row == 0 ? 3 : 2, room = resident * sms;
+        const int64_t full = units / room, rest = (units - full * room + sms - 1) / sms;
+        const double tiles_each = static_cast<double>(length) / kSsmTile;
+        const double uncut = tiles_each * (full * kSsmTileUs[row][resident - 1] + (rest ? kSsmTileUs[row][rest - 1] : 0));
+        const double cut = kSsmCutUs + tiles_each * units / sms * kSsmCutTileUs[row];
+        const int64_t most = length / kSsmGoodSpan * units / room;   // waves that spans of that length fill
+        const int64_t want = (most < 1 ? 1 : most < 8 ? most : 8) * room / units;   // spans of each chain
+        double best = uncut;
+        if (allowed && want > 1 && length >= 2 * kSsmMinSpan && cut < best) {
+            best = cut;
+            c->span_tokens = ((length + want - 1) / want + kSsmTile - 1) / kSsmTile * kSsmTile;
+            if (c->span_tokens < kSsmMinSpan) c->span_tokens = kSsmMinSpan;
+        }
+        if (units > sms && length >= 2 * kSsmRelayMin) {
+            // Each of an SM's places has a chain that runs with the same probability.
+            const double p = units < room ? static_cast<double>(units) / room : 1;
+            double rate = 0, ways = 1, with = 1;   // of one SM; places out of those resident; p^n
+            for (int64_t n = 1; n <= resident; ++n) {
+                ways = ways * (resident - n + 1) / n;
+                with *= p;
+                double without = 1;
+                for (int64_t k = n; k < resident; ++k) without *= 1 - p;
+                rate += ways * with * without * n / kSsmTileUs[row][n - 1];
+            }
+            const int64_t each = length / kSsmRelaySpans / kSsmTile * kSsmTile;
+            const int64_t span = each > kSsmRelayMin ? each : kSsmRelayMin;
+            const double relays = static_cast<double>(length) / span * (units > room ? static_cast<double>(units) / room : 1);
+            if (tiles_each * units / sms / rate + kSsmRelayUs + kSsmRelaySpanUs * relays < 0.97 * best) {
+                relay = true;
+                c->span_tokens = span;
             }
         }
     }
@@ -253,7 +281,10 @@ int plan_ssm(int64_t N, int64_t T, int64_t dim, int64_t groups, int64_t nstate, 
     if (c->spans_per_seq > 1) {
         if (c->spans > kMaxElems / (dim * wide * 4)) return KDA_ERR_SHAPE;
         c->state_bytes = c->spans * dim * wide * 4;
-        c->step_bytes = c->spans * dim * 4;
+        if (relay)
+            c->relay_bytes = (1 + c->spans * c->tiles) * 4;
+        else
+            c->step_bytes = c->spans * dim * 4;
     }
     // (Where a group is no whole 32 channels two CTAs have some of them.)
     if (c->spans_per_seq > 1 || dim / groups % kSsmChannels) c->init_bytes = N * dim * nstate * (state_f32 ? 4 : 2);
@@ -694,6 +725,13 @@ extern "C" int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64
         a.span_states = reinterpret_cast<float*>(ws.part(cut.state_bytes));
         a.span_steps = reinterpret_cast<float*>(ws.part(cut.step_bytes));
     }
+    if (cut.relay_bytes) {
+        a.relay = reinterpret_cast<int32_t*>(ws.part(cut.relay_bytes));
+        if (cudaMemsetAsync(a.relay, 0, static_cast<size_t>(cut.relay_bytes), stream) != cudaSuccess) {
+            cudaGetLastError();
+            return KDA_ERR_CUDA;
+        }
+    }
     if (copied) {   // one CTA ends a sequence that another has yet to begin
         void* copy = ws.part(state);
         if (cudaMemcpyAsync(copy, init_state, static_cast<size_t>(state), cudaMemcpyDeviceToDevice, stream) != cudaSuccess) {
@@ -771,7 +809,7 @@ extern "C" int kda_ssm_plan_segments(int64_t B, int64_t T, int64_t dim, int64_t 
     DeviceView d;
     if ((rc = device_view(&d)) != KDA_OK) return rc;
     rc = plan_ssm(B, T, dim, groups, nstate, packed != 0, true, d.sms, d.segments, d.seg_chunks, &tokens, &cut);
-    if (rc == KDA_OK) *segs = cut.cut() ? cut.spans_per_seq : 0;
+    if (rc == KDA_OK) *segs = cut.cut() && !cut.relay_bytes ? cut.spans_per_seq : 0;
     return rc;
 }
 

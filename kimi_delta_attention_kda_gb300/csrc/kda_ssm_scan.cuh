@@ -17,7 +17,7 @@
 // way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own rounding to
 // BF16 is 2^-9 of out); the states themselves stay FP32.
 //
-// 8192 tokens of 12,288 channels and 16 states: 664 us, where the bytes take 119 and
+// 8192 tokens of 12,288 channels and 16 states: 610 us, where the bytes take 119 and
 // the exponentials alone 172.  What bounds it is the schedulers' issue: a walking
 // warp takes 29 cycles of it a token (of 4 x 32 elements: two packed and four scalar
 // products for dt A and dt x B, 4 exponentials of 4 cycles' worth of a unit, two packed
@@ -28,6 +28,13 @@
 // forms the state each span ends with (and the sum of its dt: the decay over a
 // span is exp(A sum dt)), a second one each span's incoming state from those
 // before it, and its outputs.  8192 tokens of 768 channels take 65 us so, 351 uncut.
+//
+// Many chains that do not fill the SMs evenly are cut too, and their spans run one
+// after the other (SsmArgs::relay): a CTA takes up the state that the span before
+// it left.  Nothing is computed twice and no bit changes; but a chain's spans run
+// on whichever SM has room, where whole chains would stay on an SM that is
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 610 us
+// so, 651 uncut.
 #pragma once
 
 #include <cfloat>
@@ -157,6 +164,24 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, floa
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
+// The walking warps' barrier.
+__device__ __forceinline__ void walkers_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kRole) : "memory"); }
+// A span's state is there: waits for `flag` with one thread, for kWaitBoundCycles at most.
+__device__ __forceinline__ void wait_for_state(const int32_t* flag, int* status) {
+    const long long start = clock64();
+    int32_t there;
+    for (;;) {
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(flag) : "memory");
+        if (there) return;
+        if (clock64() - start > kWaitBoundCycles) break;
+        __nanosleep(100);
+    }
+    atomicOr(status, kDevPipeTimeout);
+}
+__device__ __forceinline__ void state_is_there(int32_t* flag) {
+    asm volatile("fence.acq_rel.gpu;\n st.release.gpu.global.s32 [%0], 1;" ::"l"(flag) : "memory");
+}
+
 // A CTA's part of the work: a group's channels from ch0 on, and tokens [begin, end).
 struct Part {
     int64_t begin, end;
@@ -213,7 +238,7 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
 // rows that can be read four values at a time, and groups of 32 channels or more (of
 // which the last CTA then also has some of the one before it, and writes the same
 // values).  That leaves out two fifths of the staging's instructions: 8192 x 12288,
-// 16 states 664 us, as kAny 780.
+// 16 states, uncut 651 us, as kAny 780.
 constexpr int kAny = 0, kPlain = 1, kDtF32 = 1, kKeysF32 = 2;   // kPlain plus the types that are FP32
 template <int kBlocks, bool kStates, bool kPacked, int kMode>
 __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
@@ -223,7 +248,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     wait_for_kernel_before();
     if (kStates) let_next_kernel_come();
     if (kPacked && !offsets_hold(a.cu_seqlens, a.N, a.tokens, a.valid, a.status)) return;
-    const int64_t span = quotient(blockIdx.x, a.tiles), tile = blockIdx.x - span * a.tiles;
+    int64_t span, tile;
+    if (!kStates && a.relay) {
+        // In the order in which CTAs begin: the span before is under way or done.
+        __shared__ int32_t ticket;
+        if (threadIdx.x == 0) ticket = atomicAdd(a.relay, 1);
+        __syncthreads();
+        const int64_t chains = kPacked ? 1 : a.N, each = quotient(ticket, a.tiles * chains), rest = ticket - each * a.tiles * chains;
+        const int64_t chain = quotient(rest, a.tiles);
+        span = chain * a.spans_per_seq + each;
+        tile = rest - chain * a.tiles;
+    } else {
+        span = quotient(blockIdx.x, a.tiles);
+        tile = blockIdx.x - span * a.tiles;
+    }
     const Part w = part_of<kStates, kPacked>(a, span);
     if (!w.run) return;
     const int64_t group = quotient(tile, a.tiles_per_group), per = quotient(a.dim, a.groups);
@@ -462,7 +500,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     } else {
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) s.h[k][0] = s.h[k][1] = 0ull;
-        if (!kStates) {
+        if (!kStates && a.relay) {
+            if (tid == 0) wait_for_state(a.relay + 1 + (span - 1) * a.tiles + tile, a.status);
+            walkers_meet();
+            load_rows<kBlocks>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch8, n0, 16 * kBlocks, s);
+        } else if (!kStates) {
             // The states of the sequence's spans before this one, each decayed over
             // those behind it; the first one's has the initial state in it.
 #pragma unroll 4
@@ -564,8 +606,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
         __syncthreads();
     }
     if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
-    if (kStates) {
+    if (kStates || a.relay)
         store_rows<kBlocks>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch8, live8, n0, 16 * kBlocks, s);
+    if (!kStates && a.relay) {
+        walkers_meet();
+        if (tid == 0) state_is_there(a.relay + 1 + span * a.tiles + tile);
+    }
+    if (kStates) {
         if (c == 0 && half == 0) {
             if (live) a.span_steps[span * a.dim + ch] = halves(steps).x;
             if (live8) a.span_steps[span * a.dim + ch8] = halves(steps).y;
@@ -593,7 +640,7 @@ cudaError_t run(const SsmArgs& a, cudaStream_t stream) {
 template <int kBlocks, int kMode>
 cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
     cudaError_t e;
-    if (a.span_states) {
+    if (a.span_states && !a.relay) {
         e = a.cu_seqlens ? run<kBlocks, true, true, kMode>(a, stream) : run<kBlocks, true, false, kMode>(a, stream);
         if (e != cudaSuccess) return e;
         ++*launches;

@@ -314,6 +314,66 @@ def test_last_channels(kda, dim, G, S, dt, bc):
     check(kda, draw((1, 140), dim, S, dim + S, G=G, dt=dt, bc=bc, z=False, init=4, state=BF16), cu)
 
 
+@pytest.mark.parametrize("dim,S,B,T,cu", [
+    (5000, 16, 1, 2100, None), (2500, 16, 3, 700, None), (10300, 64, 1, 530, None), (6000, 5, 1, 1111, None),
+    (9000, 32, 1, 1300, [0, 128, 128, 400, 401, 1290, 1300, 1300]), (12200, 16, 1, 3333, [0, 1, 3000, 3333])])
+@pytest.mark.parametrize("state", [F32, BF16])
+def test_wide(kda, dim, S, B, T, cu, state):
+    """More chains than SMs: the bits of the same channels a few at a time, and in
+    place, captured and replayed likewise."""
+    kda.set_segments(False, 0)
+    n = B if cu is None else len(cu) - 1
+    d = on_gpu(draw((B, T), dim, S, dim, init=n, state=state))
+    if cu is not None:
+        d["cu_seqlens"] = torch.tensor(cu, device="cuda")
+    out, fin = kda.ssm_prefill(**d)
+    for lo in range(0, dim, 1000):
+        hi = min(dim, lo + 1000)
+        part = {key: t if key in ("B", "C", "cu_seqlens") else t[lo:hi] if key in ("A", "D", "dt_bias") else
+                t[:, lo:hi].contiguous() if key == "init_state" else t[..., lo:hi] for key, t in d.items()}
+        got = kda.ssm_prefill(**part)
+        assert torch.equal(got[0], out[..., lo:hi]) and torch.equal(got[1], fin[:, lo:hi])
+    kda.set_segments(True, 0)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        kept = d["init_state"].clone()
+        graph = torch.cuda.CUDAGraph()
+        d["out"] = torch.empty_like(out)
+        with torch.cuda.graph(graph, stream=stream):
+            kda.ssm_prefill(**d, final_state=d["init_state"])
+        want = kda.ssm_prefill(**{**d, "out": None})
+        for _ in range(3):
+            d["init_state"].copy_(kept)
+            d["out"].zero_()
+            graph.replay()
+            stream.synchronize()
+            assert torch.equal(d["out"], want[0]) and torch.equal(d["init_state"], want[1])
+    assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("T,dim", [(4000, 128), (1645, 128), (600, 768), (1100, 5000), (2100, 10300)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_scratch_as_it_was_left(kda, T, dim, packed):
+    """What calls before left in the scratch is not read: their numbers are 1e30."""
+    d = on_gpu(draw((1, T), dim, 16, T))
+    if packed:
+        d["cu_seqlens"] = torch.tensor([0, T], device="cuda")
+    kda.set_segments(False, 0)
+    want = kda.ssm_prefill(**d)
+    kda.set_segments(True, 0)
+    for before in (512, 12200):
+        big = on_gpu(draw((1, 4096), 512, 16, 1))
+        big["x"] *= 1e30
+        if before > 512:
+            big = {k: t.repeat(24, 1) if k == "A" else t.repeat(24) if k in ("D", "dt_bias") else
+                   t.repeat(1, 1, 24) if k in ("x", "dt", "z") else t for k, t in big.items()}
+        kda.ssm_prefill(**big)
+        out, fin = kda.ssm_prefill(**d)
+        # A span's state comes by fewer and other products than the walk's; both are off by 2^-18 or so.
+        assert torch.allclose(fin, want[1], rtol=1e-4, atol=1e-5)
+        assert torch.allclose(out.float(), want[0].float(), rtol=2 ** -6, atol=2e-3)
+
+
 @pytest.mark.parametrize("rate", [float("-inf"), torch.finfo(F32).min])
 @pytest.mark.parametrize("S", [16, 5, 32])
 def test_rates_without_bound(kda, rate, S):

@@ -139,8 +139,10 @@ def test_scan_queries(lib):
     def need(N, T, dim, S, packed):
         assert lib.kda_ssm_workspace_bytes(N, T, dim, 1, S, packed, ctypes.byref(n)) == 0
         return n.value
-    assert need(1, 16, 64, 16, 0) == 0 and need(1, 8192, 12288, 16, 0) == 0
+    assert need(1, 16, 64, 16, 0) == 0 and need(1, 400, 12288, 16, 0) == 0
     assert need(2000, 16, 64, 16, 1) == 256            # many offsets: a verdict
+    # Spans one after the other: a state each, sixteen at most for each sequence, and flags.
+    assert need(1, 8192, 12288, 16, 0) <= 16 * 12288 * 16 * 4 + 16 * 384 * 4 + 12288 * 16 * 4 + 512
     # A cut never takes more than eight waves of CTAs, each with 32 channels' states.
     for dim, S in ((64, 16), (768, 16), (5120, 16), (768, 64)):
         states = 8 * 3 * 152 * 32 * (64 if S == 64 else 16) * 4
