@@ -212,12 +212,12 @@ struct SsmCut {
 // the fullest SM decides; cut, for each CTA's part on every SM, states and outputs.
 // T = 8192, uncut and cut: 5,120 channels 494 and 361 us, 6,144 495 and 438, 8,192
 // 480 and 573.
-constexpr double kSsmTileUs[3][3] = {{1.49, 1.87, 2.54}, {2.03, 2.93, 0}, {4.33, 5.54, 0}};
-constexpr double kSsmCutTileUs[3] = {1.36, 2.4, 4.4}, kSsmCutUs = 10;
+constexpr double kSsmTileUs[3][3] = {{1.49, 1.87, 2.54}, {2.03, 2.93, 0}, {2.97, 4.75, 0}};
+constexpr double kSsmCutTileUs[3] = {1.36, 2.4, 3.9}, kSsmCutUs = 10;
 // Spans one after the other (more chains than SMs), a sixteenth of the tokens each, 512
 // at least: for the flags' clearing, and for each span that takes up a state.  Uncut and so:
-// 8192 tokens of 12,288 channels 651 and 610 us, of 10,240 648 and 590, two prompts of
-// 4096 tokens 643 and 573, 4096 tokens with 64 states 1,233 and 974.
+// 8192 tokens of 12,288 channels 660 and 617 us, of 10,240 658 and 600, two prompts of
+// 4096 tokens 653 and 584, 4096 tokens of 12,288 with 64 states 963 and 827.
 constexpr double kSsmRelayUs = 10, kSsmRelaySpanUs = 2.2;
 constexpr int64_t kSsmRelaySpans = 16, kSsmRelayMin = 16 * kSsmTile;
 // A span is this long at least: where that leaves more than one wave of CTAs, whole

@@ -7,17 +7,17 @@
 //
 // The decays differ in every channel and state, so there is no product of matrices
 // in it: 8 S + 20 operations for 8 bytes, of which S exponentials.  A CTA has 32
-// channels and a span of tokens, 32 at a time: half of its threads form dt, dt x and the rows of B and C as FP32 in
-// shared memory; the warps of the other half walk 16 channels and half of the states
-// through the tokens, two channels and two states (of every 16) in a lane's
-// registers, so that what a lane reads serves four.  The states lie as the A operand of an
+// channels and a span of tokens, 32 at a time: some of its threads form dt, dt x and the rows of B and C as FP32 in
+// shared memory; the warps of the others walk 16 channels and a half (of 64 states
+// a quarter) of the states through the tokens, two channels and two states of every eight
+// in a lane's registers, so that what a lane reads serves four.  The states lie as the A operand of an
 // m16n8k8 product (TF32), four registers that it takes as they are: rows are
 // channels, and column j of the B operand is token j's C, so that one instruction
 // gives sum_n C[n] h[n] of 16 channels, without shuffles.  That takes h to TF32 on its
 // way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own rounding to
 // BF16 is 2^-9 of out); the states themselves stay FP32.
 //
-// 8192 tokens of 12,288 channels and 16 states: 610 us, where the bytes take 119 and
+// 8192 tokens of 12,288 channels and 16 states: 618 us, where the bytes take 119 and
 // the exponentials alone 172.  What bounds it is the schedulers' issue: a walking
 // warp takes 29 cycles of it a token (of 4 x 32 elements: two packed and four scalar
 // products for dt A and dt x B, 4 exponentials of 4 cycles' worth of a unit, two packed
@@ -33,8 +33,8 @@
 // after the other (SsmArgs::relay): a CTA takes up the state that the span before
 // it left.  Nothing is computed twice and no bit changes; but a chain's spans run
 // on whichever SM has room, where whole chains would stay on an SM that is
-// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 610 us
-// so, 651 uncut.
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 618 us
+// so, 660 uncut.
 #pragma once
 
 #include <cfloat>
@@ -45,8 +45,14 @@
 namespace kda {
 namespace {
 
-constexpr int kRole = 128;               // threads that walk, and threads that stage and finish
-constexpr int kThreads = 2 * kRole;
+constexpr int kRole = 128;               // threads that stage and finish
+// Warps that share the states of 16 channels, and threads that walk.  Four for 64 states:
+// 4096 tokens of 12,288 channels 827 us, with two 969; for 32 two and four are within
+// 3 %, two faster where the SMs are full.
+template <int kBlocks>
+constexpr int kSplit = kBlocks == 4 ? 4 : 2;
+template <int kBlocks>
+constexpr int kWalkers = 64 * kSplit<kBlocks>;
 constexpr int kTile = kSsmTile;          // tokens at a time
 static_assert(kRole == 4 * kTile && kChannels == 32, "a thread stages 8 channels of one token");
 
@@ -70,8 +76,9 @@ __device__ __forceinline__ void gate8(const float (&z)[8], float (&y)[8]) {
 }
 
 // Shared memory of one of two buffers (read at 256 bytes a cycle where neighbouring
-// lanes read the same 16 bytes, at 128 else): for each token and two channels 8 apart (dt, dt, dt x, dt x), the rows of B and of C, and y, a sum over each
-// half of the states.  Strides that keep the lanes' accesses on different banks.
+// lanes read the same 16 bytes, at 128 else): for each token and two channels 8 apart
+// (dt, dt, dt x, dt x), the rows of B and of C, and y, a sum over each warp's part of
+// the states.  Strides that keep the lanes' accesses on different banks.
 constexpr int kStepStride = 4 * (kTile + 1), kStepHalf = 8 * kStepStride + 8;
 constexpr int kStepWords = 2 * kStepHalf;
 constexpr int kYStride = kChannels + 4;
@@ -80,7 +87,7 @@ struct Buffer {
     static constexpr int kRow = 16 * kBlocks, kRowC = kRow + 8;
     static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRowC);
     static constexpr int kHalf = kTile * kYStride;   // of y
-    static constexpr int kXZ = kY + (kStates ? 0 : 2 * kHalf);   // x and z of each staging thread, for its outputs
+    static constexpr int kXZ = kY + (kStates ? 0 : kSplit<kBlocks> * kHalf);   // x and z of each staging thread, for its outputs
     static constexpr int kWords = kXZ + (kStates ? 0 : 8 * kRole);
 };
 // The pair of channels that channel ch is of, at a token: (dt, dt, dt x, dt x).
@@ -117,39 +124,59 @@ __device__ __forceinline__ void store_two(T* row, int n0, int S, float2 v) {
         if (n0 + 1 < S) from_f32(row + n0 + 1, v.y);
     }
 }
-// The lane's states of two rows of S (of channels 8 apart).
-template <int kBlocks>
-__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row8, int n0, int S, State<kBlocks>& s) {
+// The lane's states of two rows of S (of channels 8 apart), from n0 on in steps of kStep.
+template <int kStep, int kHold>
+__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row8, int n0, int S, State<kHold>& s) {
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
+    for (int k = 0; k < kHold; ++k) {
         float2 a, b;
         if (f32) {
-            a = load_two(static_cast<const float*>(p) + row * S, 16 * k + n0, S);
-            b = load_two(static_cast<const float*>(p) + row8 * S, 16 * k + n0, S);
+            a = load_two(static_cast<const float*>(p) + row * S, kStep * k + n0, S);
+            b = load_two(static_cast<const float*>(p) + row8 * S, kStep * k + n0, S);
         } else {
-            a = load_two(static_cast<const __nv_bfloat16*>(p) + row * S, 16 * k + n0, S);
-            b = load_two(static_cast<const __nv_bfloat16*>(p) + row8 * S, 16 * k + n0, S);
+            a = load_two(static_cast<const __nv_bfloat16*>(p) + row * S, kStep * k + n0, S);
+            b = load_two(static_cast<const __nv_bfloat16*>(p) + row8 * S, kStep * k + n0, S);
         }
         s.h[k][0] = pair(a.x, b.x);
         s.h[k][1] = pair(a.y, b.y);
     }
 }
-template <int kBlocks>
+template <int kStep, int kHold>
 __device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool live, int64_t row8, bool live8, int n0, int S,
-                                           const State<kBlocks>& s) {
+                                           const State<kHold>& s) {
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
+    for (int k = 0; k < kHold; ++k) {
         const float2 x = halves(s.h[k][0]), y = halves(s.h[k][1]);
         const float2 a = make_float2(x.x, y.x), b = make_float2(x.y, y.y);
         if (f32) {
-            if (live) store_two(static_cast<float*>(p) + row * S, 16 * k + n0, S, a);
-            if (live8) store_two(static_cast<float*>(p) + row8 * S, 16 * k + n0, S, b);
+            if (live) store_two(static_cast<float*>(p) + row * S, kStep * k + n0, S, a);
+            if (live8) store_two(static_cast<float*>(p) + row8 * S, kStep * k + n0, S, b);
         } else {
-            if (live) store_two(static_cast<__nv_bfloat16*>(p) + row * S, 16 * k + n0, S, a);
-            if (live8) store_two(static_cast<__nv_bfloat16*>(p) + row8 * S, 16 * k + n0, S, b);
+            if (live) store_two(static_cast<__nv_bfloat16*>(p) + row * S, kStep * k + n0, S, a);
+            if (live8) store_two(static_cast<__nv_bfloat16*>(p) + row8 * S, kStep * k + n0, S, b);
         }
     }
 }
+// A tile's decays are off on average: the exponential comes out 6e-9 too small for
+// arguments above -2^-8, and 2.2e-8 below (measured on GB300 in steps of a half octave:
+// 5e-9 .. 1e-8 and 1.4e-8 .. 3e-8), which adds up in states that last for hundreds of
+// tokens, where roundings cancel.  Once a tile, in its middle, the states get it back,
+// by the argument that one token's step gives.  1024 tokens with arguments around -0.0014: off
+// by 1.5e-6 (as exact exponentials in FP32: 1e-6), without this by 5.6e-6; around -0.014 by
+// 3.2e-6 and 2.5e-5.  (Where the state is gone by the tile's end it does not matter.)  2 %
+// of the time.
+template <int kBlocks>
+__device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt) {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 x = halves(mul_pair(rate.h[k][i], dt));
+            const uint64_t part = pair(x.x > -0x1p-8f ? kTile * 6e-9f : kTile * 2.2e-8f, x.y > -0x1p-8f ? kTile * 6e-9f : kTile * 2.2e-8f);
+            s.h[k][i] = fma_pair(s.h[k][i], part, s.h[k][i]);
+        }
+}
+
 // D = A B, or A B + D, for one m16n8k8 tile of TF32 operands, the sum in FP32.
 __device__ __forceinline__ void mma_tf32_first(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -165,7 +192,10 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, floa
 }
 
 // The walking warps' barrier.
-__device__ __forceinline__ void walkers_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kRole) : "memory"); }
+template <int kBlocks>
+__device__ __forceinline__ void walkers_meet() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kWalkers<kBlocks>) : "memory");
+}
 // A span's state is there: waits for `flag` with one thread, for kWaitBoundCycles at most.
 __device__ __forceinline__ void wait_for_state(const int32_t* flag, int* status) {
     const long long start = clock64();
@@ -232,16 +262,15 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
     return w;
 }
 
-// Half of the warps walk; the other half stage the tile ahead and finish the one
-// behind, so that there are warps enough to hide each other's latencies.
+// Some warps walk; four others stage the tile ahead and finish the one behind, so that there are warps enough to hide each other's latencies.
 // kMode: any inputs (kAny), or, with the types of dt and of B and C known, a softplus,
 // rows that can be read four values at a time, and groups of 32 channels or more (of
 // which the last CTA then also has some of the one before it, and writes the same
 // values).  That leaves out two fifths of the staging's instructions: 8192 x 12288,
-// 16 states, uncut 651 us, as kAny 780.
+// 16 states, uncut 660 us, as kAny 780.
 constexpr int kAny = 0, kPlain = 1, kDtF32 = 1, kKeysF32 = 2;   // kPlain plus the types that are FP32
 template <int kBlocks, bool kStates, bool kPacked, int kMode>
-__global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
     using Buf = Buffer<kBlocks, kStates>;
     constexpr bool kFast = kMode != kAny;
     extern __shared__ __align__(16) float smem[];
@@ -273,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     const int total = static_cast<int>(w.end - w.begin);   // tokens; tiles i = 0 .. tiles - 1 of them
     const int tiles = total / kTile + (total % kTile > 0);
 
-    if (threadIdx.x >= kRole) {
+    if (threadIdx.x >= kWalkers<kBlocks>) {
         // ---- staging: of one token four channels and the four 8 further on, and a
         // quarter of its rows of B and C
         const int tok = tid >> 2, mine = 16 * (tid >> 1 & 1) + 4 * (tid & 1);
@@ -424,6 +453,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
                 for (int j = 0; j < 2; ++j) {
                     const float4 v = *reinterpret_cast<const float4*>(p + 8 * j), u = *reinterpret_cast<const float4*>(p + Buf::kHalf + 8 * j);
                     y[4 * j] = v.x + u.x; y[4 * j + 1] = v.y + u.y; y[4 * j + 2] = v.z + u.z; y[4 * j + 3] = v.w + u.w;
+#pragma unroll
+                    for (int i = 2; i < kSplit<kBlocks>; ++i) {
+                        const float4 w = *reinterpret_cast<const float4*>(p + i * Buf::kHalf + 8 * j);
+                        y[4 * j] += w.x; y[4 * j + 1] += w.y; y[4 * j + 2] += w.z; y[4 * j + 3] += w.w;
+                    }
                 }
                 if (a.D) {
                     unpack8(xz[0], x);
@@ -471,15 +505,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
         return;
     }
 
-    // ---- the walk: 16 channels and a half of every 16 states for each warp
-    const int warp = tid >> 5, lane = tid & 31, c = lane & 3, half = warp & 1;
-    const int local = 16 * (warp >> 1) + (lane >> 2), n0 = 8 * half + 2 * c;
+    // ---- the walk: 16 channels and eight of every kStep states for each warp
+    constexpr int kStep = 8 * kSplit<kBlocks>, kHold = 2 * kBlocks / kSplit<kBlocks>;
+    const int walker = kWalkers<kBlocks> == kRole ? tid : threadIdx.x;
+    const int warp = walker >> 5, lane = walker & 31, c = lane & 3, part = warp % kSplit<kBlocks>;
+    const int local = 16 * (warp / kSplit<kBlocks>) + (lane >> 2), n0 = 8 * part + 2 * c;
     const bool live = local < channels, live8 = local + 8 < channels;
     const int64_t ch = ch0 + (live ? local : 0), ch8 = ch0 + (live8 ? local + 8 : 0);
-    State<kBlocks> rate, s;
-    load_rows<kBlocks>(a.A, true, ch, ch8, n0, S, rate);
+    State<kHold> rate, s;
+    load_rows<kStep>(a.A, true, ch, ch8, n0, S, rate);
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k)
+    for (int k = 0; k < kHold; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             // (Finite, for the zero steps behind the end; 2^-FLT_MAX is 0 for any other step.)
@@ -488,30 +524,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
         }
     auto initial = [&](int64_t seq) {
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k) s.h[k][0] = s.h[k][1] = 0ull;
-        if (a.init_state) load_rows<kBlocks>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch8, n0, S, s);
+        for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
+        if (a.init_state) load_rows<kStep>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch8, n0, S, s);
     };
     auto ending = [&](int64_t seq) {
         if (a.final_state)
-            store_rows<kBlocks>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch8, live8, n0, S, s);
+            store_rows<kStep>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch8, live8, n0, S, s);
     };
     if (w.fresh) {
         initial(w.seq);
     } else {
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k) s.h[k][0] = s.h[k][1] = 0ull;
+        for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
         if (!kStates && a.relay) {
-            if (tid == 0) wait_for_state(a.relay + 1 + (span - 1) * a.tiles + tile, a.status);
-            walkers_meet();
-            load_rows<kBlocks>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch8, n0, 16 * kBlocks, s);
+            if (walker == 0) wait_for_state(a.relay + 1 + (span - 1) * a.tiles + tile, a.status);
+            walkers_meet<kBlocks>();
+            load_rows<kStep>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch8, n0, 16 * kBlocks, s);
         } else if (!kStates) {
             // The states of the sequence's spans before this one, each decayed over
             // those behind it; the first one's has the initial state in it.
 #pragma unroll 4
             for (int64_t i = w.first_span; i < span; ++i) {
-                State<kBlocks> add;
-                load_rows<kBlocks>(a.span_states, true, i * a.dim + ch, i * a.dim + ch8, n0, 16 * kBlocks, add);
-                decay<kBlocks>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch8]), add.h);
+                State<kHold> add;
+                load_rows<kStep>(a.span_states, true, i * a.dim + ch, i * a.dim + ch8, n0, 16 * kBlocks, add);
+                decay<kHold>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch8]), add.h);
             }
         }
     }
@@ -528,38 +564,38 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     if (!kStates) close(0);
     uint64_t steps = 0ull;   // the sums of dt
     const int step0 = step_at(local, 0), rows0 = Buf::kB + n0;
-    const int keys0 = Buf::kC + (lane >> 2) * Buf::kRowC + n0, y0 = Buf::kY + half * Buf::kHalf + 2 * c * kYStride + local;
+    const int keys0 = Buf::kC + (lane >> 2) * Buf::kRowC + n0, y0 = Buf::kY + part * Buf::kHalf + 2 * c * kYStride + local;
     // Eight tokens from t on of the tile at `base`; with `ends`, sequences may end
     // among them.  (Tokens behind the span's end change nothing: only the last span
     // has them, and no sequence behind it.)  y: of tokens 2 c and 2 c + 1, and of
     // the second channel, as the product's accumulators have them.
     auto walk = [&](auto ends, const float* buf, int64_t base, int t, float (&y)[4]) {
-        float ck[kBlocks][2];
+        float ck[kHold][2];
         if (!kStates)
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRowC + 16 * k);
+            for (int k = 0; k < kHold; ++k) {
+                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRowC + kStep * k);
                 ck[k][0] = v.x;
                 ck[k][1] = v.y;
             }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            uint64_t b[kBlocks][2];
+            uint64_t b[kHold][2];
             const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(buf + step0 + 4 * (t + j));   // both dt, both dt x
             const float2 du = halves(dd.y);
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(buf + rows0 + (t + j) * Buf::kRow + 16 * k);
+            for (int k = 0; k < kHold; ++k) {
+                const float2 v = *reinterpret_cast<const float2*>(buf + rows0 + (t + j) * Buf::kRow + kStep * k);
                 b[k][0] = pair(du.x * v.x, du.y * v.x);
                 b[k][1] = pair(du.x * v.y, du.y * v.y);
             }
-            decay<kBlocks>(s, rate, dd.x, b);
+            decay<kHold>(s, rate, dd.x, b);
             if (kStates) {
                 steps = add_pair(steps, dd.x);
             } else {
                 float acc[4];
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
+                for (int k = 0; k < kHold; ++k) {
                     const float2 lo = halves(s.h[k][0]), hi = halves(s.h[k][1]);
                     if (k == 0)
                         mma_tf32_first(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
@@ -590,7 +626,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
             // (y is stored behind all loads: the compiler keeps their order.)
             float y[kTile / 8][4];
 #pragma unroll
-            for (int t = 0; t < kTile; t += 8) walk(std::false_type{}, buf, base, t, y[t / 8]);
+            for (int t = 0; t < kTile; t += 8) {
+                if (t == kTile / 2) settle<kHold>(s, rate, *reinterpret_cast<const uint64_t*>(buf + step0 + 4 * t));
+                walk(std::false_type{}, buf, base, t, y[t / 8]);
+            }
             if (!kStates)
 #pragma unroll
                 for (int t = 0; t < kTile; t += 8) store_y(buf, t, y[t / 8]);
@@ -607,13 +646,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmA
     }
     if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
     if (kStates || a.relay)
-        store_rows<kBlocks>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch8, live8, n0, 16 * kBlocks, s);
+        store_rows<kStep>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch8, live8, n0, 16 * kBlocks, s);
     if (!kStates && a.relay) {
-        walkers_meet();
-        if (tid == 0) state_is_there(a.relay + 1 + span * a.tiles + tile);
+        walkers_meet<kBlocks>();
+        if (walker == 0) state_is_there(a.relay + 1 + span * a.tiles + tile);
     }
     if (kStates) {
-        if (c == 0 && half == 0) {
+        if (c == 0 && part == 0) {
             if (live) a.span_steps[span * a.dim + ch] = halves(steps).x;
             if (live8) a.span_steps[span * a.dim + ch8] = halves(steps).y;
         }
@@ -633,7 +672,8 @@ cudaError_t run(const SsmArgs& a, cudaStream_t stream) {
         configured[dev] = true;
     }
     if (a.spans > 0x7fffffffLL / a.tiles) return cudaErrorInvalidValue;
-    return launch_after(ssm_kernel<kBlocks, kStates, kPacked, kMode>, dim3(static_cast<unsigned>(a.spans * a.tiles)), dim3(kThreads),
+    return launch_after(ssm_kernel<kBlocks, kStates, kPacked, kMode>, dim3(static_cast<unsigned>(a.spans * a.tiles)),
+                        dim3(kWalkers<kBlocks> + kRole),
                         bytes, stream, a);
 }
 
