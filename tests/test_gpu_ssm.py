@@ -410,6 +410,25 @@ def test_slow_states(kda, mean, packed):
         assert off.pow(2).mean().sqrt() < 1.6e-6 + 1e-8 * T
 
 
+@pytest.mark.parametrize("S", [16, 32, 64, 5])
+@pytest.mark.parametrize("T,dim", [(1000, 40), (1000, 6000)])
+def test_steps_of_zero(kda, T, dim, S):
+    """Tokens without a step leave the states as they are, bit for bit, and so do rates of
+    zero those that get nothing added."""
+    d = draw((1, T), dim, S, 3, bias=False, init=1)
+    d["dt"].zero_()
+    for on, chunks in ((False, 0), (True, 0), (True, 4)):
+        kda.set_segments(on, chunks)
+        out, fin = kda.ssm_prefill(**on_gpu(d), dt_softplus=False)
+        assert torch.equal(fin.cpu(), d["init_state"])
+    d["dt_bias"] = torch.full((dim,), -200.0)
+    assert torch.equal(kda.ssm_prefill(**on_gpu(d))[1].cpu(), d["init_state"])
+    d["dt_bias"] = torch.full((dim,), 1.0)
+    d["A"].zero_()
+    d["x"].zero_()
+    assert torch.equal(kda.ssm_prefill(**on_gpu(d))[1].cpu(), d["init_state"])
+
+
 # ------------------------------------------------------------- single tokens
 
 def check_step(kda, d, slots, status=0, softplus=True):
