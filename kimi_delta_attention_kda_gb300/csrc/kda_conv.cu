@@ -18,9 +18,10 @@
 namespace kda {
 namespace {
 
-// Eight rows are under way while eight are worked on, in five CTAs of 128 threads (95
-// registers).  8192 x 12288: 72 us; groups of four in three to four CTAs of 256
-// threads 77 to 80, pairs of channels a thread 76 to 91, six CTAs (spilled) 93.
+// Two groups of eight rows are under way while one is worked on, in five CTAs of 128
+// threads (96 registers).  8192 x 12288: 68 us (a copy of as many bytes 62, without the SiLU
+// 64); one group ahead 71, in registers instead of shared memory 72, three 70, four 73;
+// groups of four and six rows 70 to 76, four CTAs 73, six (spilled) 90.
 constexpr int kConvThreads = 128;
 constexpr int kConvCtas = 5;   // an SM
 constexpr int kGroup = 8;
@@ -111,9 +112,56 @@ struct Filter {
     }
 };
 
+// A thread's rows on their way, kGroups groups of them in shared memory, which it alone
+// copies and reads (asynchronous copies are of four bytes at least: single elements wait
+// in registers, one group of them).
+template <int kVec>
+struct Ring {
+    static constexpr int kGroups = kVec > 1 ? 2 : 1;
+    RawT<kVec>* mine;   // [kGroups * kGroup][kConvThreads]
+    RawT<kVec> held[kVec > 1 ? 1 : kGroup];
+
+    // The rows from p on, the first n of a group, to its place.
+    __device__ __forceinline__ void fetch(int group, const __nv_bfloat16* p, int64_t ld, int n) {
+        if constexpr (kVec > 1) {
+            const uint32_t to = smem_u32(mine + (group % kGroups) * kGroup * kConvThreads);
+            if (n >= kGroup) {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + i * kConvThreads * 2 * kVec), "l"(p + i * ld), "n"(2 * kVec) : "memory");
+            } else {
+                for (int i = 0; i < n; ++i)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + i * kConvThreads * 2 * kVec), "l"(p + i * ld), "n"(2 * kVec) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else if (n >= kGroup) {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) held[i] = load_raw<kVec>(p + i * ld);
+        }
+    }
+    // The oldest group is there.
+    __device__ __forceinline__ void wait() {
+        if constexpr (kVec > 1) asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
+    }
+    // Row i of a group, of a whole one; or of any, from p where it is not held.
+    __device__ __forceinline__ RawT<kVec> row(int group, int i) const {
+        if constexpr (kVec > 1)
+            return mine[((group % kGroups) * kGroup + i) * kConvThreads];
+        else
+            return held[i];
+    }
+    __device__ __forceinline__ RawT<kVec> any_row(int group, int i, const __nv_bfloat16* p) const {
+        if constexpr (kVec > 1)
+            return row(group, i);
+        else
+            return load_raw<kVec>(p);
+    }
+};
+
 // (Tokens are counted in 32 bits: there are fewer than 2^31.)
 template <int kW, int kVec, bool kPacked>
 __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(ConvArgs a) {
+    __shared__ RawT<kVec> places[Ring<kVec>::kGroups * kGroup * kConvThreads];
     wait_for_kernel_before();
     if (kPacked && !offsets_hold(a.cu_seqlens, a.N, a.tokens, a.valid, a.status)) return;
     const int64_t vecs = a.D / kVec, at = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
@@ -131,15 +179,18 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(C
     int t = kPacked ? static_cast<int>(run * a.run_tokens) : begin + static_cast<int>((run - seq * a.runs_per_seq) * a.run_tokens);
     int seq_end = static_cast<int>(kPacked ? a.tokens : begin + a.tokens_per_seq);
     const int end = t + a.run_tokens < seq_end ? static_cast<int>(t + a.run_tokens) : seq_end;
-    // The group after the one at hand is on its way while that is worked on.
-    RawT<kVec> ahead[kGroup];
-    const __nv_bfloat16* next = x + t * a.ldx;
+    const __nv_bfloat16* next = x + t * a.ldx;   // of the group to fetch next
     auto out = static_cast<__nv_bfloat16*>(a.out) + ch + t * a.D;
-    auto fetch = [&]() {
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) ahead[i] = load_raw<kVec>(next + i * a.ldx);
+    Ring<kVec> ring;
+    ring.mine = places + threadIdx.x;
+    int left = end - t;   // tokens from there on
+    auto fetch = [&](int group) {
+        ring.fetch(group, next, a.ldx, left);
+        next += kGroup * a.ldx;
+        left -= kGroup;
     };
-    if (end - t >= kGroup) fetch();
+#pragma unroll
+    for (int i = 0; i < Ring<kVec>::kGroups; ++i) fetch(i);
     Filter<kW, kVec> filter;
     filter.load(a, ch);
     if (kPacked) {   // the sequence and its first token; the first run also has the empty ones before that
@@ -179,34 +230,35 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) conv_prefill_kernel(C
             for (int j = 0; j < kPairs; ++j) win[i][j] = win[n + i][j];
     };
     window();
-    for (;;) {
+    for (int group = 0;; ++group) {
         close();
         if (t >= end) return;
-        // Whole groups within the sequence, then a token at a time.
+        ring.wait();
         const int last = end < seq_end ? end : seq_end;
-        while (last - t >= kGroup) {
+        if (last - t >= kGroup) {   // a whole group within the sequence
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) R::unpack(ahead[i], win[kKeep + i]);
+            for (int i = 0; i < kGroup; ++i) R::unpack(ring.row(group, i), win[kKeep + i]);
+            fetch(group + Ring<kVec>::kGroups);
             t += kGroup;
-            next += kGroup * a.ldx;
-            if (end - t >= kGroup) fetch();
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 store_raw<kVec>(out, filter.apply(win + i, a.silu));
                 out += a.D;
             }
             shift(kGroup);
-        }
-        if (t == last) continue;
+        } else {   // a token at a time
+            const int n = end - t < kGroup ? end - t : kGroup;
 #pragma unroll 1
-        for (; t < last; ++t) {
-            R::unpack(load_raw<kVec>(next), win[kKeep]);
-            next += a.ldx;
-            store_raw<kVec>(out, filter.apply(win, a.silu));
-            out += a.D;
-            shift(1);
+            for (int i = 0; i < n; ++i) {
+                close();
+                R::unpack(ring.any_row(group, i, x + t * a.ldx), win[kKeep]);
+                ++t;
+                store_raw<kVec>(out, filter.apply(win, a.silu));
+                out += a.D;
+                shift(1);
+            }
+            fetch(group + Ring<kVec>::kGroups);
         }
-        if (end - t >= kGroup) fetch();
     }
 }
 
