@@ -324,9 +324,9 @@ struct SsmArgs {
     int32_t* relay;
     int64_t tiles, tiles_per_group;      // of kSsmChannels channels
     bool dt_f32, bc_f32, state_f32, softplus;
-    // Set by the launch: rows that can be read four values at a time; bytes (out:
-    // elements) from a row to that 32 tokens on.
-    bool vec, vec_bc;
+    // Set by the launch: rows that can be read four values at a time, eight for BF16 ones
+    // (vec8); bytes (out: elements) from a row to that 32 tokens on.
+    bool vec, vec8, vec_bc;
     int64_t tile_x, tile_z, tile_dt, tile_b, tile_c, tile_out;
     int* status;
 };

@@ -15,6 +15,8 @@ bool rows_of(const void* p, int64_t ld, int64_t tokens, int size, int n) {
 void set_ssm_vectors(SsmArgs* a) {
     a->vec = a->dim / a->groups % 4 == 0 && rows_of(a->x, a->ldx, a->tokens, 2, 4) && rows_of(a->z, a->ldz, a->tokens, 2, 4) &&
              rows_of(a->dt, a->lddt, a->tokens, a->dt_f32 ? 4 : 2, 4);
+    a->vec8 = a->vec && a->dim / a->groups % 8 == 0 && rows_of(a->x, a->ldx, a->tokens, 2, 8) && rows_of(a->z, a->ldz, a->tokens, 2, 8) &&
+              (a->dt_f32 || rows_of(a->dt, a->lddt, a->tokens, 2, 8));
     const int size = a->bc_f32 ? 4 : 2;
     a->vec_bc = a->nstate % 4 == 0 && rows_of(a->B, a->ldb, a->tokens, size, 4) && rows_of(a->C, a->ldc, a->tokens, size, 4);
 }

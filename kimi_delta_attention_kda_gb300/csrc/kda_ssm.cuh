@@ -46,7 +46,7 @@ __device__ __forceinline__ uint4 gather4(const float* p, int n) {
 }
 
 // A lane's states.  Prompts: pairs of two channels, 8 (w k + part) + 2 c + i of
-// channels g and g + 8 of the warp's 16 (part the warp's place among the w that share
+// channels 2 g and 2 g + 1 of the warp's 16 (part the warp's place among the w that share
 // them, g the lane's among eight, c among four).  Single tokens: states 16 k + 4 c + 2 i and the next of one channel.
 template <int kBlocks>
 struct State {

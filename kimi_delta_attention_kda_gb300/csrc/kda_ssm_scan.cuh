@@ -76,7 +76,7 @@ __device__ __forceinline__ void gate8(const float (&z)[8], float (&y)[8]) {
 }
 
 // Shared memory of one of two buffers (read at 256 bytes a cycle where neighbouring
-// lanes read the same 16 bytes, at 128 else): for each token and two channels 8 apart
+// lanes read the same 16 bytes, at 128 else): for each token and two channels
 // (dt, dt, dt x, dt x), the rows of B and of C, and y, a sum over each warp's part of
 // the states.  Strides that keep the lanes' accesses on different banks.
 constexpr int kStepStride = 4 * (kTile + 1), kStepHalf = 8 * kStepStride + 8;
@@ -90,8 +90,8 @@ struct Buffer {
     static constexpr int kXZ = kY + (kStates ? 0 : kSplit<kBlocks> * kHalf);   // x and z of each staging thread, for its outputs
     static constexpr int kWords = kXZ + (kStates ? 0 : 8 * kRole);
 };
-// The pair of channels that channel ch is of, at a token: (dt, dt, dt x, dt x).
-__device__ __forceinline__ int step_at(int ch, int token) { return (ch >> 4) * kStepHalf + (ch & 7) * kStepStride + 4 * token; }
+// Channels ch (even) and ch + 1 at a token: (dt, dt, dt x, dt x).
+__device__ __forceinline__ int step_at(int ch, int token) { return (ch >> 4) * kStepHalf + (ch >> 1 & 7) * kStepStride + 4 * token; }
 
 // What a staging thread fetches of a tile: of one token eight channels' x, z and dt, and
 // four values of every 16 of B and C.
@@ -99,8 +99,10 @@ template <int kBlocks>
 struct Fetched {
     uint4 x, z, dt[2], b[kBlocks], c[kBlocks];
 };
-__device__ __forceinline__ uint4 two_pieces(const uint8_t* p) {
-    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 16);
+// 16 bytes at once, or 8 and 8.
+__device__ __forceinline__ uint4 load16(const uint8_t* p, bool whole) {
+    if (whole) return *reinterpret_cast<const uint4*>(p);
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 8);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
@@ -124,25 +126,25 @@ __device__ __forceinline__ void store_two(T* row, int n0, int S, float2 v) {
         if (n0 + 1 < S) from_f32(row + n0 + 1, v.y);
     }
 }
-// The lane's states of two rows of S (of channels 8 apart), from n0 on in steps of kStep.
+// The lane's states of two rows of S (of two channels), from n0 on in steps of kStep.
 template <int kStep, int kHold>
-__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row8, int n0, int S, State<kHold>& s) {
+__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row1, int n0, int S, State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
         float2 a, b;
         if (f32) {
             a = load_two(static_cast<const float*>(p) + row * S, kStep * k + n0, S);
-            b = load_two(static_cast<const float*>(p) + row8 * S, kStep * k + n0, S);
+            b = load_two(static_cast<const float*>(p) + row1 * S, kStep * k + n0, S);
         } else {
             a = load_two(static_cast<const __nv_bfloat16*>(p) + row * S, kStep * k + n0, S);
-            b = load_two(static_cast<const __nv_bfloat16*>(p) + row8 * S, kStep * k + n0, S);
+            b = load_two(static_cast<const __nv_bfloat16*>(p) + row1 * S, kStep * k + n0, S);
         }
         s.h[k][0] = pair(a.x, b.x);
         s.h[k][1] = pair(a.y, b.y);
     }
 }
 template <int kStep, int kHold>
-__device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool live, int64_t row8, bool live8, int n0, int S,
+__device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool live, int64_t row1, bool live1, int n0, int S,
                                            const State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
@@ -150,10 +152,10 @@ __device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool 
         const float2 a = make_float2(x.x, y.x), b = make_float2(x.y, y.y);
         if (f32) {
             if (live) store_two(static_cast<float*>(p) + row * S, kStep * k + n0, S, a);
-            if (live8) store_two(static_cast<float*>(p) + row8 * S, kStep * k + n0, S, b);
+            if (live1) store_two(static_cast<float*>(p) + row1 * S, kStep * k + n0, S, b);
         } else {
             if (live) store_two(static_cast<__nv_bfloat16*>(p) + row * S, kStep * k + n0, S, a);
-            if (live8) store_two(static_cast<__nv_bfloat16*>(p) + row8 * S, kStep * k + n0, S, b);
+            if (live1) store_two(static_cast<__nv_bfloat16*>(p) + row1 * S, kStep * k + n0, S, b);
         }
     }
 }
@@ -307,17 +309,16 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     const int tiles = total / kTile + (total % kTile > 0);
 
     if (threadIdx.x >= kWalkers<kBlocks>) {
-        // ---- staging: of one token four channels and the four 8 further on, and a
-        // quarter of its rows of B and C
-        const int tok = tid >> 2, mine = 16 * (tid >> 1 & 1) + 4 * (tid & 1);
+        // ---- staging: of one token eight channels, and a quarter of its rows of B and C
+        const int tok = tid >> 2, mine = 8 * (tid & 3);
         auto clip = [](int n) { return n < 0 ? 0 : n < 4 ? n : 4; };
-        const int count = clip(channels - mine), count8 = clip(channels - mine - 8);
-        const bool wide = kFast || (a.vec && count8 == 4), wide_keys = kFast || a.vec_bc, gated = !kStates && a.z;
+        const int count = clip(channels - mine), count4 = clip(channels - mine - 4);
+        const bool wide = kFast || (a.vec && count4 == 4), whole = a.vec8, wide_keys = kFast || a.vec_bc, gated = !kStates && a.z;
         const bool dt_f32 = kFast ? ((kMode - kPlain) & kDtF32) != 0 : a.dt_f32, bc_f32 = kFast ? ((kMode - kPlain) & kKeysF32) != 0 : a.bc_f32;
         float bias[8], skip[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int at = mine + (i & 3) + 2 * (i & 4);
+            const int at = mine + i;
             bias[i] = a.dt_bias && at < channels ? a.dt_bias[ch0 + at] : 0.f;
             skip[i] = !kStates && a.D && at < channels ? a.D[ch0 + at] : 0.f;
         }
@@ -336,25 +337,25 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             const uint4 none = make_uint4(0, 0, 0, 0);
             if (ahead > 0) {
                 if (wide) {
-                    f.x = two_pieces(xp);
-                    if (gated) f.z = two_pieces(zp);
+                    f.x = load16(xp, whole);
+                    if (gated) f.z = load16(zp, whole);
                     if (dt_f32) {
                         f.dt[0] = *reinterpret_cast<const uint4*>(dp);
-                        f.dt[1] = *reinterpret_cast<const uint4*>(dp + 32);
+                        f.dt[1] = *reinterpret_cast<const uint4*>(dp + 16);
                     } else {
-                        f.dt[0] = two_pieces(dp);
+                        f.dt[0] = load16(dp, whole);
                     }
                 } else {
                     auto eight = [&](const uint8_t* p) {
                         const uint4 lo = gather8(reinterpret_cast<const __nv_bfloat16*>(p), count),
-                                    hi = gather8(reinterpret_cast<const __nv_bfloat16*>(p + 16), count8);
+                                    hi = gather8(reinterpret_cast<const __nv_bfloat16*>(p + 8), count4);
                         return make_uint4(lo.x, lo.y, hi.x, hi.y);
                     };
                     f.x = eight(xp);
                     if (gated) f.z = eight(zp);
                     if (dt_f32) {
                         f.dt[0] = gather4(reinterpret_cast<const float*>(dp), count);
-                        f.dt[1] = gather4(reinterpret_cast<const float*>(dp + 32), count8);
+                        f.dt[1] = gather4(reinterpret_cast<const float*>(dp + 16), count4);
                     } else {
                         f.dt[0] = eight(dp);
                     }
@@ -429,7 +430,8 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
                 for (int j = 0; j < 8; ++j) dt[j] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4*>(buf + step_at(mine + j, tok)) = make_float4(dt[j], dt[j + 4], dt[j] * x[j], dt[j + 4] * x[j + 4]);
+                *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j, tok)) =
+                    make_float4(dt[2 * j], dt[2 * j + 1], dt[2 * j] * x[2 * j], dt[2 * j + 1] * x[2 * j + 1]);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
                 const int n0 = 16 * k + 4 * (tid & 3);
@@ -455,11 +457,11 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
                 float y[8], x[8], z[8];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(p + 8 * j), u = *reinterpret_cast<const float4*>(p + Buf::kHalf + 8 * j);
+                    const float4 v = *reinterpret_cast<const float4*>(p + 4 * j), u = *reinterpret_cast<const float4*>(p + Buf::kHalf + 4 * j);
                     y[4 * j] = v.x + u.x; y[4 * j + 1] = v.y + u.y; y[4 * j + 2] = v.z + u.z; y[4 * j + 3] = v.w + u.w;
 #pragma unroll
                     for (int i = 2; i < kSplit<kBlocks>; ++i) {
-                        const float4 w = *reinterpret_cast<const float4*>(p + i * Buf::kHalf + 8 * j);
+                        const float4 w = *reinterpret_cast<const float4*>(p + i * Buf::kHalf + 4 * j);
                         y[4 * j] += w.x; y[4 * j + 1] += w.y; y[4 * j + 2] += w.z; y[4 * j + 3] += w.w;
                     }
                 }
@@ -472,15 +474,15 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
                     unpack8(xz[kRole], z);
                     gate8(z, y);
                 }
-                if (wide) {
+                if (wide && whole) {
+                    store8(op, y);
+                } else if (wide) {
                     *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-                    *reinterpret_cast<uint2*>(op + 8) = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                    *reinterpret_cast<uint2*>(op + 4) = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j < count) op[j] = __float2bfloat16_rn(y[j]);
-                        if (j < count8) op[j + 8] = __float2bfloat16_rn(y[j + 4]);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        if (mine + j < channels) op[j] = __float2bfloat16_rn(y[j]);
                 }
             }
             op += a.tile_out;
@@ -513,11 +515,11 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     constexpr int kStep = 8 * kSplit<kBlocks>, kHold = 2 * kBlocks / kSplit<kBlocks>;
     const int walker = kWalkers<kBlocks> == kRole ? tid : threadIdx.x;
     const int warp = walker >> 5, lane = walker & 31, c = lane & 3, part = warp % kSplit<kBlocks>;
-    const int local = 16 * (warp / kSplit<kBlocks>) + (lane >> 2), n0 = 8 * part + 2 * c;
-    const bool live = local < channels, live8 = local + 8 < channels;
-    const int64_t ch = ch0 + (live ? local : 0), ch8 = ch0 + (live8 ? local + 8 : 0);
+    const int local = 16 * (warp / kSplit<kBlocks>) + 2 * (lane >> 2), n0 = 8 * part + 2 * c;
+    const bool live = local < channels, live1 = local + 1 < channels;
+    const int64_t ch = ch0 + (live ? local : 0), ch1 = ch0 + (live1 ? local + 1 : 0);
     State<kHold> rate, s;
-    load_rows<kStep>(a.A, true, ch, ch8, n0, S, rate);
+    load_rows<kStep>(a.A, true, ch, ch1, n0, S, rate);
 #pragma unroll
     for (int k = 0; k < kHold; ++k)
 #pragma unroll
@@ -529,11 +531,11 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     auto initial = [&](int64_t seq) {
 #pragma unroll
         for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
-        if (a.init_state) load_rows<kStep>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch8, n0, S, s);
+        if (a.init_state) load_rows<kStep>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch1, n0, S, s);
     };
     auto ending = [&](int64_t seq) {
         if (a.final_state)
-            store_rows<kStep>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch8, live8, n0, S, s);
+            store_rows<kStep>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch1, live1, n0, S, s);
     };
     if (w.fresh) {
         initial(w.seq);
@@ -543,15 +545,15 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         if (!kStates && a.relay) {
             if (walker == 0) wait_for_state(a.relay + 1 + (span - 1) * a.tiles + tile, a.status);
             walkers_meet<kBlocks>();
-            load_rows<kStep>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch8, n0, 16 * kBlocks, s);
+            load_rows<kStep>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch1, n0, 16 * kBlocks, s);
         } else if (!kStates) {
             // The states of the sequence's spans before this one, each decayed over
             // those behind it; the first one's has the initial state in it.
 #pragma unroll 4
             for (int64_t i = w.first_span; i < span; ++i) {
                 State<kHold> add;
-                load_rows<kStep>(a.span_states, true, i * a.dim + ch, i * a.dim + ch8, n0, 16 * kBlocks, add);
-                decay<kHold>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch8]), add.h);
+                load_rows<kStep>(a.span_states, true, i * a.dim + ch, i * a.dim + ch1, n0, 16 * kBlocks, add);
+                decay<kHold>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch1]), add.h);
             }
         }
     }
@@ -617,10 +619,8 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     };
     auto store_y = [&](float* buf, int t, const float (&y)[4]) {
         float* at = buf + y0 + t * kYStride;
-        at[0] = y[0];
-        at[kYStride] = y[1];
-        at[8] = y[2];
-        at[kYStride + 8] = y[3];
+        *reinterpret_cast<float2*>(at) = make_float2(y[0], y[2]);
+        *reinterpret_cast<float2*>(at + kYStride) = make_float2(y[1], y[3]);
     };
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     }
     if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
     if (kStates || a.relay)
-        store_rows<kStep>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch8, live8, n0, 16 * kBlocks, s);
+        store_rows<kStep>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch1, live1, n0, 16 * kBlocks, s);
     if (!kStates && a.relay) {
         walkers_meet<kBlocks>();
         if (walker == 0) state_is_there(a.relay + 1 + span * a.tiles + tile);
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     if (kStates) {
         if (c == 0 && part == 0) {
             if (live) a.span_steps[span * a.dim + ch] = halves(steps).x;
-            if (live8) a.span_steps[span * a.dim + ch8] = halves(steps).y;
+            if (live1) a.span_steps[span * a.dim + ch1] = halves(steps).y;
         }
     }
 }
