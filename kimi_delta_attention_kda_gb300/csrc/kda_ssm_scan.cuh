@@ -627,16 +627,13 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         float* buf = smem + (i & 1) * Buf::kWords;
         const int64_t base = static_cast<int64_t>(i) * kTile;
         if (base + kTile <= total && (!kPacked || kStates || seq_end >= base + kTile)) {
-            // (y is stored behind all loads: the compiler keeps their order.)
-            float y[kTile / 8][4];
 #pragma unroll
             for (int t = 0; t < kTile; t += 8) {
                 if (t == kTile / 2) settle<kHold>(s, rate, *reinterpret_cast<const uint64_t*>(buf + step0 + 4 * t));
-                walk(std::false_type{}, buf, base, t, y[t / 8]);
+                float y[4];
+                walk(std::false_type{}, buf, base, t, y);
+                if (!kStates) store_y(buf, t, y);
             }
-            if (!kStates)
-#pragma unroll
-                for (int t = 0; t < kTile; t += 8) store_y(buf, t, y[t / 8]);
             if (kPacked && !kStates) close(base + kTile);
         } else {
 #pragma unroll 1
