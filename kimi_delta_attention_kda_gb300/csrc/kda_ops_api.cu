@@ -210,14 +210,14 @@ struct SsmCut {
 // Costs of the scan on GB300, in microseconds for 32 tokens (rows: up to 16, 32 and 64
 // states): uncut, of a CTA with one, two and three of them on its SM, of which
 // the fullest SM decides; cut, for each CTA's part on every SM, states and outputs.
-// T = 8192, uncut and cut: 5,120 channels 494 and 361 us, 6,144 495 and 438, 8,192
-// 480 and 573.
-constexpr double kSsmTileUs[3][3] = {{1.49, 1.87, 2.54}, {2.03, 2.93, 0}, {2.97, 4.75, 0}};
-constexpr double kSsmCutTileUs[3] = {1.36, 2.4, 3.9}, kSsmCutUs = 10;
+// T = 8192, uncut and cut: 5,120 channels 429 and 343 us, 6,144 429 and 415, 8,192
+// 428 and 556.
+constexpr double kSsmTileUs[3][3] = {{1.43, 1.68, 2.35}, {1.68, 2.49, 0}, {2.66, 4.51, 0}};
+constexpr double kSsmCutTileUs[3] = {1.27, 2.05, 3.65}, kSsmCutUs = 10;
 // Spans one after the other (more chains than SMs), a sixteenth of the tokens each, 512
 // at least: for the flags' clearing, and for each span that takes up a state.  Uncut and so:
-// 8192 tokens of 12,288 channels 660 and 617 us, of 10,240 658 and 600, two prompts of
-// 4096 tokens 653 and 584, 4096 tokens of 12,288 with 64 states 963 and 827.
+// 8192 tokens of 12,288 channels 602 and 547 us, of 10,240 600 and 523, two prompts of
+// 4096 tokens 591 and 523, 4096 tokens of 12,288 with 64 states 882 and 771.
 constexpr double kSsmRelayUs = 10, kSsmRelaySpanUs = 2.2;
 constexpr int64_t kSsmRelaySpans = 16, kSsmRelayMin = 16 * kSsmTile;
 // A span is this long at least: where that leaves more than one wave of CTAs, whole

@@ -17,7 +17,7 @@
 // way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own rounding to
 // BF16 is 2^-9 of out); the states themselves stay FP32.
 //
-// 8192 tokens of 12,288 channels and 16 states: 618 us, where the bytes take 119 and
+// 8192 tokens of 12,288 channels and 16 states: 547 us, where the bytes take 119 and
 // the exponentials alone 172.  What bounds it is the schedulers' issue: a walking
 // warp takes 29 cycles of it a token (of 4 x 32 elements: two packed and four scalar
 // products for dt A and dt x B, 4 exponentials of 4 cycles' worth of a unit, two packed
@@ -27,14 +27,14 @@
 // Few (sequence, channel) chains are cut into spans of tokens: a first launch
 // forms the state each span ends with (and the sum of its dt: the decay over a
 // span is exp(A sum dt)), a second one each span's incoming state from those
-// before it, and its outputs.  8192 tokens of 768 channels take 65 us so, 351 uncut.
+// before it, and its outputs.  8192 tokens of 768 channels take 62 us so, 338 uncut.
 //
 // Many chains that do not fill the SMs evenly are cut too, and their spans run one
 // after the other (SsmArgs::relay): a CTA takes up the state that the span before
 // it left.  Nothing is computed twice and no bit changes; but a chain's spans run
 // on whichever SM has room, where whole chains would stay on an SM that is
-// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 618 us
-// so, 660 uncut.
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 547 us
+// so, 602 uncut.
 #pragma once
 
 #include <cfloat>
@@ -47,8 +47,8 @@ namespace {
 
 constexpr int kRole = 128;               // threads that stage and finish
 // Warps that share the states of 16 channels, and threads that walk.  Four for 64 states:
-// 4096 tokens of 12,288 channels 827 us, with two 969; for 32 two and four are within
-// 3 %, two faster where the SMs are full.
+// 2 x 2000 tokens of 1536 channels 162 us, with two 167 (128 registers); for 32
+// (4096 x 12,288) two 436 and four 475.
 template <int kBlocks>
 constexpr int kSplit = kBlocks == 4 ? 4 : 2;
 template <int kBlocks>
@@ -273,7 +273,10 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
 // rows that can be read four values at a time, and groups of 32 channels or more (of
 // which the last CTA then also has some of the one before it, and writes the same
 // values).  That leaves out two fifths of the staging's instructions: 8192 x 12288,
-// 16 states, uncut 660 us, as kAny 780.
+// 16 states, uncut 602 us, as kAny 690.
+// Registers are short: with three CTAs an SM (80 registers) values that wait in them spill,
+// and each spill costs more than it seems (16 of y held for the tile's end: 612 us for 549).
+// Two CTAs (128 registers) 615 us, four 686.
 constexpr int kAny = 0, kPlain = 1, kDtF32 = 1, kKeysF32 = 2;   // kPlain plus the types that are FP32
 template <int kBlocks, bool kStates, bool kPacked, int kMode>
 __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {
@@ -315,13 +318,17 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         const int count = clip(channels - mine), count4 = clip(channels - mine - 4);
         const bool wide = kFast || (a.vec && count4 == 4), whole = a.vec8, wide_keys = kFast || a.vec_bc, gated = !kStates && a.z;
         const bool dt_f32 = kFast ? ((kMode - kPlain) & kDtF32) != 0 : a.dt_f32, bc_f32 = kFast ? ((kMode - kPlain) & kKeysF32) != 0 : a.bc_f32;
-        float bias[8], skip[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = mine + i;
-            bias[i] = a.dt_bias && at < channels ? a.dt_bias[ch0 + at] : 0.f;
-            skip[i] = !kStates && a.D && at < channels ? a.D[ch0 + at] : 0.f;
+        // The channels' biases and skips, which would take 16 registers.
+        float* const of_channel = smem + 2 * Buf::kWords;
+        if (tid < kChannels) {
+            of_channel[tid] = a.dt_bias && tid < channels ? a.dt_bias[ch0 + tid] : 0.f;
+            if (!kStates) of_channel[kChannels + tid] = a.D && tid < channels ? a.D[ch0 + tid] : 0.f;
         }
+        asm volatile("bar.sync 2, %0;" ::"n"(kRole) : "memory");
+        auto eight_of = [&](const float* p, float (&v)[8]) {
+            const float4 lo = *reinterpret_cast<const float4*>(p + mine), hi = *reinterpret_cast<const float4*>(p + mine + 4);
+            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        };
         // This thread's rows of the tile to fetch next, and to finish.
         const int es = bc_f32 ? 4 : 2, dts = dt_f32 ? 4 : 2;
         const int64_t t0 = w.begin + tok;
@@ -410,7 +417,8 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         };
         // (dt and what it stands for are of the tile before the next to fetch.)
         auto stage = [&](float* buf) {
-            float dt[8], x[8];
+            float dt[8], x[8], bias[8];
+            eight_of(of_channel, bias);
             unpack8(f.x, x);
             if (dt_f32) {
                 dt[0] = __uint_as_float(f.dt[0].x); dt[1] = __uint_as_float(f.dt[0].y);
@@ -466,6 +474,8 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
                     }
                 }
                 if (a.D) {
+                    float skip[8];
+                    eight_of(of_channel + kChannels, skip);
                     unpack8(xz[0], x);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = fmaf(skip[j], x[j], y[j]);
@@ -662,7 +672,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
 
 template <int kBlocks, bool kStates, bool kPacked, int kMode>
 cudaError_t run(const SsmArgs& a, cudaStream_t stream) {
-    constexpr int bytes = 8 * Buffer<kBlocks, kStates>::kWords;
+    constexpr int bytes = 8 * Buffer<kBlocks, kStates>::kWords + 4 * 2 * kChannels;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
