@@ -342,7 +342,8 @@ def la_workspace_bytes(B: int, T: int, H: int, packed: bool) -> int:
 
 def ssm_plan_segments(B: int, T: int, dim: int, groups: int, nstate: int, packed: bool) -> int:
     """Spans ssm_prefill cuts each sequence of this shape into (packed: the
-    whole batch); 0: no cut."""
+    whole batch); 0: no cut, or spans one after
+    the other."""
     out = ctypes.c_int64(0)
     _check(load().kda_ssm_plan_segments(int(B), int(T), int(dim), int(groups), int(nstate),
                                         1 if packed else 0, ctypes.byref(out)),

@@ -374,6 +374,34 @@ def test_scratch_as_it_was_left(kda, T, dim, packed):
         assert torch.allclose(out.float(), want[0].float(), rtol=2 ** -6, atol=2e-3)
 
 
+def test_wide_ones_at_once(kda):
+    """Calls whose spans wait for one another, on three streams at the same time: two
+    of them as captured graphs, and a call cut into spans beside them."""
+    calls = [on_gpu(draw((1, 1500), dim, 16, dim, init=1)) for dim in (5000, 10300, 600)]
+    want = [kda.ssm_prefill(**d) for d in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [(torch.empty_like(o), torch.empty_like(f)) for o, f in want]
+    graphs = []
+    for i in (0, 1):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            kda.ssm_prefill(**calls[i], out=outs[i][0], final_state=outs[i][1])
+    for _ in range(5):
+        for o, f in outs:
+            o.zero_(), f.zero_()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            kda.ssm_prefill(**calls[2], out=outs[2][0], final_state=outs[2][1])
+        torch.cuda.synchronize()
+        assert kda.device_status() == 0
+        for got, right in zip(outs, want):
+            assert all(torch.equal(x, y) for x, y in zip(got, right))
+
+
 @pytest.mark.parametrize("rate", [float("-inf"), torch.finfo(F32).min])
 @pytest.mark.parametrize("S", [16, 5, 32])
 def test_rates_without_bound(kda, rate, S):
