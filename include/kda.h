@@ -584,9 +584,7 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  * bytes, dt, B and C in FP32 on 16, 32 channels or more to a group in multiples of 4, and
  * nstate a multiple of 4 run fastest).
  * out and final_state may overlap no input and not each other.
- * The states and all sums are FP32; on the way to out each state is cut to TF32
- * (2^-10 of a product at most) before its product with C, and out is rounded
- * once.  A NaN or an infinity in a token reaches no earlier token, no other
+ * The states and all sums are FP32, and out is rounded once.  A NaN or an infinity in a token reaches no earlier token, no other
  * channel (but through B and C, its group's) and no other sequence.
  * When there are too few channels to fill the GPU the tokens are cut into
  * spans: one launch forms the state each span ends with, one the outputs from

@@ -45,9 +45,8 @@ __device__ __forceinline__ uint4 gather4(const float* p, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane's states.  Prompts: pairs of two channels, 8 (w k + part) + 2 c + i of
-// channels 2 g and 2 g + 1 of the warp's 16 (part the warp's place among the w that share
-// them, g the lane's among eight, c among four).  Single tokens: states 16 k + 4 c + 2 i and the next of one channel.
+// A lane's states, of one channel: 16 k + 4 c + 2 i and the next (c the lane's place among
+// the four that share the channel).
 template <int kBlocks>
 struct State {
     uint64_t h[kBlocks][2];

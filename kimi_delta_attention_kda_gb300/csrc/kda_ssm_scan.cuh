@@ -8,22 +8,16 @@
 // The decays differ in every channel and state, so there is no product of matrices
 // in it: 8 S + 20 operations for 8 bytes, of which S exponentials.  A CTA has 32
 // channels and a span of tokens, 32 at a time: some of its threads form dt, dt x and the rows of B and C as FP32 in
-// shared memory; the warps of the others walk 16 channels and a half (of 64 states
-// a quarter) of the states through the tokens, two channels and two states of every eight
-// in a lane's registers, so that what a lane reads serves four.  The states lie as the A operand of an
-// m16n8k8 product (TF32), four registers that it takes as they are: rows are
-// channels, and column j of the B operand is token j's C, so that one instruction
-// gives sum_n C[n] h[n] of 16 channels, without shuffles.  That takes h to TF32 on its
-// way to out (cut to 10 bits: at most 2^-10 of |C[n] h[n]|, where out's own rounding to
-// BF16 is 2^-9 of out); the states themselves stay FP32.
+// shared memory; the warps of the others walk 8 channels each through the tokens, four lanes a
+// channel with four of every 16 states in their registers (64 states: two warps).  A lane sums
+// its products with C, and every four tokens the four lanes of a channel hand each
+// other their sums, so that each ends with one token's.  All of it is FP32.  (Summed on the
+// tensor cores, TF32, the call below took 546 us, but cut the states to 10 bits on the
+// way to out: outputs too small by 3.5e-4 on average.)
 //
-// 8192 tokens of 12,288 channels and 16 states: 547 us, where the bytes take 119 and
-// the exponentials alone 172.  What bounds it is the schedulers' issue: a walking
-// warp takes 29 cycles of it a token (of 4 x 32 elements: two packed and four scalar
-// products for dt A and dt x B, 4 exponentials of 4 cycles' worth of a unit, two packed
-// multiply-adds, the step's, B's and C's loads, the product), a staging warp 17, the
-// exponentials' unit is busy for a third of the time and shared memory for half.
-//
+// 8192 tokens of 12,288 channels and 16 states: 571 us, where the bytes take 119 and
+// the exponentials alone 172.
+
 // Few (sequence, channel) chains are cut into spans of tokens: a first launch
 // forms the state each span ends with (and the sum of its dt: the decay over a
 // span is exp(A sum dt)), a second one each span's incoming state from those
@@ -33,8 +27,8 @@
 // after the other (SsmArgs::relay): a CTA takes up the state that the span before
 // it left.  Nothing is computed twice and no bit changes; but a chain's spans run
 // on whichever SM has room, where whole chains would stay on an SM that is
-// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 547 us
-// so, 602 uncut.
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 571 us
+// so.
 #pragma once
 
 #include <cfloat>
@@ -46,13 +40,11 @@ namespace kda {
 namespace {
 
 constexpr int kRole = 128;               // threads that stage and finish
-// Warps that share the states of 16 channels, and threads that walk.  Four for 64 states:
-// 2 x 2000 tokens of 1536 channels 162 us, with two 167 (128 registers); for 32
-// (4096 x 12,288) two 436 and four 475.
+// Warps that share the states of 8 channels, and threads that walk.
 template <int kBlocks>
-constexpr int kSplit = kBlocks == 4 ? 4 : 2;
+constexpr int kSplit = kBlocks == 4 ? 2 : 1;
 template <int kBlocks>
-constexpr int kWalkers = 64 * kSplit<kBlocks>;
+constexpr int kWalkers = 128 * kSplit<kBlocks>;
 constexpr int kTile = kSsmTile;          // tokens at a time
 static_assert(kRole == 4 * kTile && kChannels == 32, "a thread stages 8 channels of one token");
 
@@ -75,23 +67,23 @@ __device__ __forceinline__ void gate8(const float (&z)[8], float (&y)[8]) {
     }
 }
 
-// Shared memory of one of two buffers (read at 256 bytes a cycle where neighbouring
-// lanes read the same 16 bytes, at 128 else): for each token and two channels
-// (dt, dt, dt x, dt x), the rows of B and of C, and y, a sum over each warp's part of
-// the states.  Strides that keep the lanes' accesses on different banks.
-constexpr int kStepStride = 4 * (kTile + 1), kStepHalf = 8 * kStepStride + 8;
-constexpr int kStepWords = 2 * kStepHalf;
+// Shared memory of one of two buffers: for each token (dt, dt x) of every channel, the
+// rows of B and of C, and y, a sum over each warp's part of the states.  Strides and
+// places that keep the lanes' accesses on different banks.
+constexpr int kStepStride = 2 * kChannels + 8, kStepWords = kTile * kStepStride;
 constexpr int kYStride = kChannels + 4;
 template <int kBlocks, bool kStates>
 struct Buffer {
-    static constexpr int kRow = 16 * kBlocks, kRowC = kRow + 8;
-    static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRowC);
+    static constexpr int kRow = 16 * kBlocks;
+    static constexpr int kB = kStepWords, kC = kB + kTile * kRow, kY = kC + (kStates ? 0 : kTile * kRow);
     static constexpr int kHalf = kTile * kYStride;   // of y
     static constexpr int kXZ = kY + (kStates ? 0 : kSplit<kBlocks> * kHalf);   // x and z of each staging thread, for its outputs
     static constexpr int kWords = kXZ + (kStates ? 0 : 8 * kRole);
 };
-// Channels ch (even) and ch + 1 at a token: (dt, dt, dt x, dt x).
-__device__ __forceinline__ int step_at(int ch, int token) { return (ch >> 4) * kStepHalf + (ch >> 1 & 7) * kStepStride + 4 * token; }
+// Channels ch (even) and ch + 1 at a token: (dt, dt x, dt, dt x).
+__device__ __forceinline__ int step_at(int ch, int token) {
+    return token * kStepStride + (ch >> 3) * 16 + 4 * ((ch >> 1 & 3) ^ (ch >> 4));
+}
 
 // What a staging thread fetches of a tile: of one token eight channels' x, z and dt, and
 // four values of every 16 of B and C.
@@ -106,58 +98,54 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p, bool whole) {
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// Two values from state n0 on of a row of S.
-template <typename T>
-__device__ __forceinline__ float2 load_two(const T* row, int n0, int S) {
-    if (S % 2 == 0) {
-        float v[2] = {0.f, 0.f};
-        if (n0 < S) load_vec<2>(row + n0, v);
-        return make_float2(v[0], v[1]);
-    }
-    return make_float2(n0 < S ? static_cast<float>(row[n0]) : 0.f, n0 + 1 < S ? static_cast<float>(row[n0 + 1]) : 0.f);
-}
-template <typename T>
-__device__ __forceinline__ void store_two(T* row, int n0, int S, float2 v) {
-    if (S % 2 == 0) {
-        const float w[2] = {v.x, v.y};
-        if (n0 < S) store_vec<2>(row + n0, w);
-    } else {
-        if (n0 < S) from_f32(row + n0, v.x);
-        if (n0 + 1 < S) from_f32(row + n0 + 1, v.y);
-    }
-}
-// The lane's states of two rows of S (of two channels), from n0 on in steps of kStep.
-template <int kStep, int kHold>
-__device__ __forceinline__ void load_rows(const void* p, bool f32, int64_t row, int64_t row1, int n0, int S, State<kHold>& s) {
+// A lane's states of a row of S: four from n0 on, and from every 16 behind.
+template <int kHold, typename T>
+__device__ __forceinline__ void load_row(const T* row, int n0, int S, State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        float2 a, b;
-        if (f32) {
-            a = load_two(static_cast<const float*>(p) + row * S, kStep * k + n0, S);
-            b = load_two(static_cast<const float*>(p) + row1 * S, kStep * k + n0, S);
+        const int n = n0 + 16 * k;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (S % 4 == 0) {
+            if (n < S) load_vec<4>(row + n, v);
         } else {
-            a = load_two(static_cast<const __nv_bfloat16*>(p) + row * S, kStep * k + n0, S);
-            b = load_two(static_cast<const __nv_bfloat16*>(p) + row1 * S, kStep * k + n0, S);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < S) v[i] = static_cast<float>(row[n + i]);
         }
-        s.h[k][0] = pair(a.x, b.x);
-        s.h[k][1] = pair(a.y, b.y);
+        s.h[k][0] = pair(v[0], v[1]);
+        s.h[k][1] = pair(v[2], v[3]);
     }
 }
-template <int kStep, int kHold>
-__device__ __forceinline__ void store_rows(void* p, bool f32, int64_t row, bool live, int64_t row1, bool live1, int n0, int S,
-                                           const State<kHold>& s) {
+template <int kHold, typename T>
+__device__ __forceinline__ void store_row(T* row, int n0, int S, const State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        const float2 x = halves(s.h[k][0]), y = halves(s.h[k][1]);
-        const float2 a = make_float2(x.x, y.x), b = make_float2(x.y, y.y);
-        if (f32) {
-            if (live) store_two(static_cast<float*>(p) + row * S, kStep * k + n0, S, a);
-            if (live1) store_two(static_cast<float*>(p) + row1 * S, kStep * k + n0, S, b);
+        const int n = n0 + 16 * k;
+        const float2 a = halves(s.h[k][0]), b = halves(s.h[k][1]);
+        const float v[4] = {a.x, a.y, b.x, b.y};
+        if (S % 4 == 0) {
+            if (n < S) store_vec<4>(row + n, v);
         } else {
-            if (live) store_two(static_cast<__nv_bfloat16*>(p) + row * S, kStep * k + n0, S, a);
-            if (live1) store_two(static_cast<__nv_bfloat16*>(p) + row1 * S, kStep * k + n0, S, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < S) from_f32(row + n + i, v[i]);
         }
     }
+}
+// Row `row` of states of either type.
+template <int kHold>
+__device__ __forceinline__ void load_states(const void* p, bool f32, int64_t row, int n0, int S, State<kHold>& s) {
+    if (f32)
+        load_row(static_cast<const float*>(p) + row * S, n0, S, s);
+    else
+        load_row(static_cast<const __nv_bfloat16*>(p) + row * S, n0, S, s);
+}
+template <int kHold>
+__device__ __forceinline__ void store_states(void* p, bool f32, int64_t row, int n0, int S, const State<kHold>& s) {
+    if (f32)
+        store_row(static_cast<float*>(p) + row * S, n0, S, s);
+    else
+        store_row(static_cast<__nv_bfloat16*>(p) + row * S, n0, S, s);
 }
 // A tile's decays are off on average: the exponential comes out 6e-9 too small for
 // arguments above -2^-8, and 2.2e-8 below (measured on GB300 in steps of a half octave:
@@ -181,20 +169,6 @@ __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& 
             const float2 x = halves(mul_pair(rate.h[k][i], dt));
             s.h[k][i] = fma_pair(s.h[k][i], pair(lost(x.x), lost(x.y)), s.h[k][i]);
         }
-}
-
-// D = A B, or A B + D, for one m16n8k8 tile of TF32 operands, the sum in FP32.
-__device__ __forceinline__ void mma_tf32_first(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
-          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(0.f));
-}
-__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
-          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
 // The walking warps' barrier.
@@ -405,12 +379,6 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             if (!kStates) cp += a.tile_c;
             ahead -= kTile;
         };
-        // To the nearest TF32 value, which a BF16 one is.
-        auto tf32 = [](float v) {
-            uint32_t r;
-            asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-            return __uint_as_float(r);
-        };
         auto four = [&](const uint4& r) {
             return bc_f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
                           : make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
@@ -439,16 +407,12 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<float4*>(buf + step_at(mine + 2 * j, tok)) =
-                    make_float4(dt[2 * j], dt[2 * j + 1], dt[2 * j] * x[2 * j], dt[2 * j + 1] * x[2 * j + 1]);
+                    make_float4(dt[2 * j], dt[2 * j] * x[2 * j], dt[2 * j + 1], dt[2 * j + 1] * x[2 * j + 1]);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k) {
                 const int n0 = 16 * k + 4 * (tid & 3);
                 *reinterpret_cast<float4*>(buf + Buf::kB + tok * Buf::kRow + n0) = four(f.b[k]);
-                if (!kStates) {
-                    const float4 v = four(f.c[k]);
-                    *reinterpret_cast<float4*>(buf + Buf::kC + tok * Buf::kRowC + n0) =
-                        bc_f32 ? make_float4(tf32(v.x), tf32(v.y), tf32(v.z), tf32(v.w)) : v;
-                }
+                if (!kStates) *reinterpret_cast<float4*>(buf + Buf::kC + tok * Buf::kRow + n0) = four(f.c[k]);
             }
             if (!kStates) {
                 uint4* xz = reinterpret_cast<uint4*>(buf + Buf::kXZ) + tid;
@@ -465,10 +429,10 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
                 float y[8], x[8], z[8];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(p + 4 * j), u = *reinterpret_cast<const float4*>(p + Buf::kHalf + 4 * j);
-                    y[4 * j] = v.x + u.x; y[4 * j + 1] = v.y + u.y; y[4 * j + 2] = v.z + u.z; y[4 * j + 3] = v.w + u.w;
+                    const float4 v = *reinterpret_cast<const float4*>(p + 4 * j);
+                    y[4 * j] = v.x; y[4 * j + 1] = v.y; y[4 * j + 2] = v.z; y[4 * j + 3] = v.w;
 #pragma unroll
-                    for (int i = 2; i < kSplit<kBlocks>; ++i) {
+                    for (int i = 1; i < kSplit<kBlocks>; ++i) {
                         const float4 w = *reinterpret_cast<const float4*>(p + i * Buf::kHalf + 4 * j);
                         y[4 * j] += w.x; y[4 * j + 1] += w.y; y[4 * j + 2] += w.z; y[4 * j + 3] += w.w;
                     }
@@ -521,15 +485,15 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         return;
     }
 
-    // ---- the walk: 16 channels and eight of every kStep states for each warp
-    constexpr int kStep = 8 * kSplit<kBlocks>, kHold = 2 * kBlocks / kSplit<kBlocks>;
+    // ---- the walk: 8 channels a warp, four lanes each, with four of every 16 states
+    constexpr int kHold = kBlocks / kSplit<kBlocks>;
     const int walker = kWalkers<kBlocks> == kRole ? tid : threadIdx.x;
-    const int warp = walker >> 5, lane = walker & 31, c = lane & 3, part = warp % kSplit<kBlocks>;
-    const int local = 16 * (warp / kSplit<kBlocks>) + 2 * (lane >> 2), n0 = 8 * part + 2 * c;
-    const bool live = local < channels, live1 = local + 1 < channels;
-    const int64_t ch = ch0 + (live ? local : 0), ch1 = ch0 + (live1 ? local + 1 : 0);
+    const int warp = walker >> 5, lane = walker & 31, c = lane >> 3, part = warp >> 2;
+    const int local = 8 * (warp & 3) + (lane & 7), n0 = 16 * kHold * part + 4 * c;
+    const bool live = local < channels;
+    const int64_t ch = ch0 + (live ? local : 0);
     State<kHold> rate, s;
-    load_rows<kStep>(a.A, true, ch, ch1, n0, S, rate);
+    load_states(a.A, true, ch, n0, S, rate);
 #pragma unroll
     for (int k = 0; k < kHold; ++k)
 #pragma unroll
@@ -538,32 +502,34 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             const float2 v = halves(mul_pair(rate.h[k][i], pair(kLog2e, kLog2e)));
             rate.h[k][i] = pair(v.x < -FLT_MAX ? -FLT_MAX : v.x, v.y < -FLT_MAX ? -FLT_MAX : v.y);
         }
-    auto initial = [&](int64_t seq) {
+    auto none = [&]() {
 #pragma unroll
         for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
-        if (a.init_state) load_rows<kStep>(a.init_state, a.state_f32, seq * a.dim + ch, seq * a.dim + ch1, n0, S, s);
+    };
+    auto initial = [&](int64_t seq) {
+        none();
+        if (a.init_state) load_states(a.init_state, a.state_f32, seq * a.dim + ch, n0, S, s);
     };
     auto ending = [&](int64_t seq) {
-        if (a.final_state)
-            store_rows<kStep>(a.final_state, a.state_f32, seq * a.dim + ch, live, seq * a.dim + ch1, live1, n0, S, s);
+        if (a.final_state && live) store_states(a.final_state, a.state_f32, seq * a.dim + ch, n0, S, s);
     };
     if (w.fresh) {
         initial(w.seq);
     } else {
-#pragma unroll
-        for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
+        none();
         if (!kStates && a.relay) {
             if (walker == 0) wait_for_state(a.relay + 1 + (span - 1) * a.tiles + tile, a.status);
             walkers_meet<kBlocks>();
-            load_rows<kStep>(a.span_states, true, (span - 1) * a.dim + ch, (span - 1) * a.dim + ch1, n0, 16 * kBlocks, s);
+            load_states(a.span_states, true, (span - 1) * a.dim + ch, n0, 16 * kBlocks, s);
         } else if (!kStates) {
             // The states of the sequence's spans before this one, each decayed over
             // those behind it; the first one's has the initial state in it.
 #pragma unroll 4
             for (int64_t i = w.first_span; i < span; ++i) {
                 State<kHold> add;
-                load_rows<kStep>(a.span_states, true, i * a.dim + ch, i * a.dim + ch1, n0, 16 * kBlocks, add);
-                decay<kHold>(s, rate, pair(a.span_steps[i * a.dim + ch], a.span_steps[i * a.dim + ch1]), add.h);
+                load_states(a.span_states, true, i * a.dim + ch, n0, 16 * kBlocks, add);
+                const float step = a.span_steps[i * a.dim + ch];
+                decay<kHold>(s, rate, pair(step, step), add.h);
             }
         }
     }
@@ -578,59 +544,55 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         }
     };
     if (!kStates) close(0);
-    uint64_t steps = 0ull;   // the sums of dt
-    const int step0 = step_at(local, 0), rows0 = Buf::kB + n0;
-    const int keys0 = Buf::kC + (lane >> 2) * Buf::kRowC + n0, y0 = Buf::kY + part * Buf::kHalf + 2 * c * kYStride + local;
-    // Eight tokens from t on of the tile at `base`; with `ends`, sequences may end
-    // among them.  (Tokens behind the span's end change nothing: only the last span
-    // has them, and no sequence behind it.)  y: of tokens 2 c and 2 c + 1, and of
-    // the second channel, as the product's accumulators have them.
-    auto walk = [&](auto ends, const float* buf, int64_t base, int t, float (&y)[4]) {
-        float ck[kHold][2];
-        if (!kStates)
+    float steps = 0.f;   // the sum of dt
+    const int step0 = step_at(local, 0) + 2 * (local & 1), rows0 = Buf::kB + n0;
+    const int keys0 = Buf::kC + n0, y0 = Buf::kY + part * Buf::kHalf + c * kYStride + local;
+    auto four_of = [&](const float* p, uint64_t (&v)[2]) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(p);
+        v[0] = r.x;
+        v[1] = r.y;
+    };
+    // Four tokens from t on of the tile at `base`, and their y; with `ends`, sequences
+    // may end among them.  (Tokens behind the span's end change nothing: only the last
+    // span has them, and no sequence behind it.)
+    auto walk = [&](auto ends, float* buf, int64_t base, int t) {
+        float y[4];
 #pragma unroll
-            for (int k = 0; k < kHold; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(buf + keys0 + t * Buf::kRowC + kStep * k);
-                ck[k][0] = v.x;
-                ck[k][1] = v.y;
-            }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             uint64_t b[kHold][2];
-            const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(buf + step0 + 4 * (t + j));   // both dt, both dt x
-            const float2 du = halves(dd.y);
+            const float2 dd = *reinterpret_cast<const float2*>(buf + step0 + (t + j) * kStepStride);   // dt, dt x
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(buf + rows0 + (t + j) * Buf::kRow + kStep * k);
-                b[k][0] = pair(du.x * v.x, du.y * v.x);
-                b[k][1] = pair(du.x * v.y, du.y * v.y);
+                four_of(buf + rows0 + (t + j) * Buf::kRow + 16 * k, b[k]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) b[k][i] = mul_pair(b[k][i], pair(dd.y, dd.y));
             }
-            decay<kHold>(s, rate, dd.x, b);
+            decay<kHold>(s, rate, pair(dd.x, dd.x), b);
             if (kStates) {
-                steps = add_pair(steps, dd.x);
+                steps += dd.x;
             } else {
-                float acc[4];
+                uint64_t sum = 0ull;
 #pragma unroll
                 for (int k = 0; k < kHold; ++k) {
-                    const float2 lo = halves(s.h[k][0]), hi = halves(s.h[k][1]);
-                    if (k == 0)
-                        mma_tf32_first(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
-                    else
-                        mma_tf32(acc, lo.x, lo.y, hi.x, hi.y, ck[k][0], ck[k][1]);
+                    uint64_t key[2];
+                    four_of(buf + keys0 + (t + j) * Buf::kRow + 16 * k, key);
+                    sum = k == 0 ? mul_pair(key[0], s.h[k][0]) : fma_pair(key[0], s.h[k][0], sum);
+                    sum = fma_pair(key[1], s.h[k][1], sum);
                 }
-                // (The columns of the other tokens hold nothing of use.)
-                if (c == j >> 1) {
-                    y[j & 1] = acc[j & 1];
-                    y[2 + (j & 1)] = acc[2 + (j & 1)];
-                }
+                const float2 v = halves(sum);
+                y[j] = v.x + v.y;
                 if (decltype(ends)::value) close(base + t + j + 1);
             }
         }
-    };
-    auto store_y = [&](float* buf, int t, const float (&y)[4]) {
-        float* at = buf + y0 + t * kYStride;
-        *reinterpret_cast<float2*>(at) = make_float2(y[0], y[2]);
-        *reinterpret_cast<float2*>(at + kYStride) = make_float2(y[1], y[3]);
+        if (!kStates) {
+            // Lane c of a channel's four gets the sum of token t + c over them.
+            const bool up = c & 2, right = c & 1;
+            float keep0 = up ? y[2] : y[0], keep1 = up ? y[3] : y[1];
+            keep0 += __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 16);
+            keep1 += __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 16);
+            const float keep = right ? keep1 : keep0;
+            buf[y0 + t * kYStride] = keep + __shfl_xor_sync(0xffffffffu, right ? keep0 : keep1, 8);
+        }
     };
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
@@ -638,36 +600,28 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         const int64_t base = static_cast<int64_t>(i) * kTile;
         if (base + kTile <= total && (!kPacked || kStates || seq_end >= base + kTile)) {
 #pragma unroll
-            for (int t = 0; t < kTile; t += 8) {
-                if (t == kTile / 2) settle<kHold>(s, rate, *reinterpret_cast<const uint64_t*>(buf + step0 + 4 * t));
-                float y[4];
-                walk(std::false_type{}, buf, base, t, y);
-                if (!kStates) store_y(buf, t, y);
+            for (int t = 0; t < kTile; t += 4) {
+                if (t == kTile / 2) {
+                    const float step = buf[step0 + t * kStepStride];
+                    settle<kHold>(s, rate, pair(step, step));
+                }
+                walk(std::false_type{}, buf, base, t);
             }
             if (kPacked && !kStates) close(base + kTile);
         } else {
 #pragma unroll 1
-            for (int t = 0; t < kTile && base + t < total; t += 8) {
-                float y[4];
-                walk(std::integral_constant<bool, kPacked && !kStates>{}, buf, base, t, y);
-                if (!kStates) store_y(buf, t, y);
-            }
+            for (int t = 0; t < kTile && base + t < total; t += 4)
+                walk(std::integral_constant<bool, kPacked && !kStates>{}, buf, base, t);
         }
         __syncthreads();
     }
     if (!kPacked && !kStates && total == seq_end && total > 0) close(total);
-    if (kStates || a.relay)
-        store_rows<kStep>(a.span_states, true, span * a.dim + ch, live, span * a.dim + ch1, live1, n0, 16 * kBlocks, s);
+    if ((kStates || a.relay) && live) store_states(a.span_states, true, span * a.dim + ch, n0, 16 * kBlocks, s);
     if (!kStates && a.relay) {
         walkers_meet<kBlocks>();
         if (walker == 0) state_is_there(a.relay + 1 + span * a.tiles + tile);
     }
-    if (kStates) {
-        if (c == 0 && part == 0) {
-            if (live) a.span_steps[span * a.dim + ch] = halves(steps).x;
-            if (live1) a.span_steps[span * a.dim + ch1] = halves(steps).y;
-        }
-    }
+    if (kStates && live && c == 0 && part == 0) a.span_steps[span * a.dim + ch] = steps;
 }
 
 template <int kBlocks, bool kStates, bool kPacked, int kMode>

@@ -76,6 +76,10 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[kVec]) {
         store8(p, x);
     else if constexpr (kVec == 1)
         from_f32(p, x[0]);
+    else if constexpr (kVec == 4 && sizeof(T) == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else if constexpr (kVec == 4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     else if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
     else

@@ -457,7 +457,7 @@ def ssm_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, 
     ``B == 1``).  x, dt, B, C and z may be parts of wider rows.  ``final_state`` may
     be ``init_state``; a new one takes its type, or ``state_dtype`` without one.
 
-    States and sums are FP32; on the way to ``out`` the states are cut to TF32.
+    States and sums are FP32.
     """
     if stream is not None:
         _check_ssm(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens, out, final_state, state_dtype)
