@@ -15,7 +15,7 @@
 // tensor cores, TF32, the call below took 546 us, but cut the states to 10 bits on the
 // way to out: outputs too small by 3.5e-4 on average.)
 //
-// 8192 tokens of 12,288 channels and 16 states: 571 us, where the bytes take 119 and
+// 8192 tokens of 12,288 channels and 16 states: 584 us, where the bytes take 119 and
 // the exponentials alone 172.
 
 // Few (sequence, channel) chains are cut into spans of tokens: a first launch
@@ -27,7 +27,7 @@
 // after the other (SsmArgs::relay): a CTA takes up the state that the span before
 // it left.  Nothing is computed twice and no bit changes; but a chain's spans run
 // on whichever SM has room, where whole chains would stay on an SM that is
-// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 571 us
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 584 us
 // so.
 #pragma once
 
@@ -150,15 +150,17 @@ __device__ __forceinline__ void store_states(void* p, bool f32, int64_t row, int
 // A tile's decays are off on average: the exponential comes out 6e-9 too small for
 // arguments above -2^-8, and 2.2e-8 below (measured on GB300 in steps of a half octave:
 // 5e-9 .. 1e-8 and 1.4e-8 .. 3e-8), which adds up in states that last for hundreds of
-// tokens, where roundings cancel.  Once a tile, in its middle, the states get it back,
-// by the argument that one token's step gives (none if that is 0: what stands still
-// keeps its bits).  1024 tokens with arguments around -0.0014: off
+// tokens, where roundings cancel.  Once a tile, in its middle, the states get it back, by the
+// argument that the least step of the tile's first half gives, below which no token of
+// that half is: none if that is 0 (what stands still keeps its bits), and where the second
+// half stands still at most twice what was lost, so that it never adds more error than it
+// takes away.  1024 tokens with arguments around -0.0014: off
 // by 1.5e-6 (as exact exponentials in FP32: 1e-6), without this by 5.6e-6; around -0.014 by
-// 3.2e-6 and 2.5e-5.  (Where the state is gone by the tile's end it does not matter.)  2 %
-// of the time.
+// 3.2e-6 and 2.5e-5.  (Where the state is gone by the tile's end it does not matter.)  3 %
+// of the time, most of it for the least step.
 __device__ __forceinline__ float lost(float x) {
     const float part = x > -0x1p-8f ? kTile * 6e-9f : kTile * 2.2e-8f;
-    return x > -0x1p-23f ? 0.f : part;   // (the exponential is 1 there)
+    return x > -0x1p-23f ? 1e-30f : part;   // (the exponential is 1 there; not 0, for states that are infinite)
 }
 template <int kBlocks>
 __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt) {
@@ -594,17 +596,25 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             buf[y0 + t * kYStride] = keep + __shfl_xor_sync(0xffffffffu, right ? keep0 : keep1, 8);
         }
     };
+    // The least step of a tile's first half, 0 where there are negative ones: each of a
+    // channel's lanes looks at every fourth.
+    auto least_step = [&](const float* buf) {
+        float least = buf[step0 + c * kStepStride];
+#pragma unroll
+        for (int t = 4; t < kTile / 2; t += 4) least = fminf(least, buf[step0 + (t + c) * kStepStride]);
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 8));
+        return fmaxf(fminf(least, __shfl_xor_sync(0xffffffffu, least, 16)), 0.f);
+    };
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
         float* buf = smem + (i & 1) * Buf::kWords;
         const int64_t base = static_cast<int64_t>(i) * kTile;
+        float least = 0.f;
         if (base + kTile <= total && (!kPacked || kStates || seq_end >= base + kTile)) {
 #pragma unroll
             for (int t = 0; t < kTile; t += 4) {
-                if (t == kTile / 2) {
-                    const float step = buf[step0 + t * kStepStride];
-                    settle<kHold>(s, rate, pair(step, step));
-                }
+                if (t == kTile / 2 - 4) least = least_step(buf);
+                if (t == kTile / 2) settle<kHold>(s, rate, pair(least, least));
                 walk(std::false_type{}, buf, base, t);
             }
             if (kPacked && !kStates) close(base + kTile);

@@ -1,0 +1,66 @@
+"""The decays of kda_ssm_prefill and kda_ssm_decode at their edges: steps that differ from token
+to token, rates without bound, growing states, and states that last for thousands of tokens."""
+
+import pytest
+import torch
+
+import ops_reference as ref
+import scan_reference as scan
+from test_gpu_ssm import BF16, F32, check, cuts, draw, kda, on_gpu, want_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def decayed(kda, dt, A, init):  # noqa: F811
+    """What is left of the initial states [1, dim, S] behind steps dt [1, T, dim] alone."""
+    zero = torch.zeros(dt.shape, dtype=BF16, device="cuda")
+    keys = torch.zeros(1, dt.shape[1], 1, A.shape[1], dtype=BF16, device="cuda")
+    return kda.ssm_prefill(zero, dt.cuda(), A.cuda(), keys, keys, init_state=init.cuda(), dt_softplus=False)[1]
+
+
+def left(dt, A, init):
+    return init.double() * torch.exp(dt.double().sum(1)[..., None] * A.double())
+
+
+@pytest.mark.parametrize("phase", [0, 5, 15, 16, 31])
+@pytest.mark.parametrize("T,step,other", [(8192, 2.5e-3, 0.0), (8192, 2.6e-3, 1e-9), (16384, 1e-4, 0.0)])
+def test_one_step_in_32(kda, T, step, other, phase):  # noqa: F811
+    """Steps that count at one token of every 32 (the others' decays are 1 in FP32).  Each rounds its decay
+    and its product by at most 2^-24, uncorrelated, and the exponential is off by at
+    most 3e-8 on average: nothing that is made up for may add more than that."""
+    gen = torch.Generator().manual_seed(phase)
+    dim, S = 96, 16
+    dt = torch.full((1, T, dim), other)
+    dt[:, phase::32] = step * (0.9 + 0.2 * torch.rand(1, T // 32, dim, generator=gen))
+    A, init = -(0.9 + 0.2 * torch.rand(dim, S, generator=gen)), 1 + torch.rand(1, dim, S, generator=gen)
+    n = T // 32
+    for on in (False, True):
+        kda.set_segments(on, 0)
+        off = decayed(kda, dt, A, init).cpu().double() / left(dt, A, init) - 1
+        assert off.pow(2).mean().sqrt() < 2.0 ** -24 * (n * 2 / 3) ** 0.5 + 3e-8 * n
+
+
+def test_small_arguments(kda):  # noqa: F811
+    """The mean over many states: their roundings (1.6e-6 each, as test_slow_states has them) cancel to
+    5 x 1.6e-6 / sqrt(96 x 16) < 2.1e-7, and the exponential's mean error, 5e-9 to 1e-8 here, is
+    made up for to 4e-9."""
+    gen = torch.Generator().manual_seed(2)
+    T, dim, S = 1024, 96, 16
+    dt = 1e-3 * (0.5 + torch.rand(1, T, dim, generator=gen))
+    A, init = -(0.7 + 0.6 * torch.rand(dim, S, generator=gen)), 1 + torch.rand(1, dim, S, generator=gen)
+    for on in (False, True):
+        kda.set_segments(on, 0)
+        off = decayed(kda, dt, A, init).cpu().double() / left(dt, A, init) - 1
+        assert off.mean().abs() < 2.1e-7 + 4e-9 * T
+
+
+@pytest.mark.parametrize("S", [16, 32, 64])
+def test_infinite_states_stay(kda, S):  # noqa: F811
+    """Where no step is taken an infinite state stays one, and with a step that decays it too."""
+    for T, step in ((200, 0.0), (200, 1e-3)):
+        init = torch.ones(1, 40, S)
+        init[0, 3, 1], init[0, 7, 0] = float("inf"), float("-inf")
+        for on, chunks in ((False, 0), (True, 4)):
+            kda.set_segments(on, chunks)
+            fin = decayed(kda, torch.full((1, T, 40), step), -torch.ones(40, S), init).cpu()
+            assert torch.equal(torch.isinf(fin), torch.isinf(init)) and torch.equal(fin.sign(), init.sign())
