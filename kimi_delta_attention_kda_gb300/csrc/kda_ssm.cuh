@@ -2,6 +2,8 @@
 // have in common: the step, a lane's states and their decay (sm_103a).
 #pragma once
 
+#include <cfloat>
+
 #include "kda_common.cuh"
 #include "kda_launch.h"
 #include "kda_seq.cuh"
@@ -51,6 +53,19 @@ template <int kBlocks>
 struct State {
     uint64_t h[kBlocks][2];
 };
+
+// Rates in units of log 2, finite: 2^-FLT_MAX is 0 for every step but 0, and 1 for that,
+// where minus infinity would give NaN.  (NaN stays.)
+template <int kBlocks>
+__device__ __forceinline__ void to_log2(State<kBlocks>& rate) {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 v = halves(mul_pair(rate.h[k][i], pair(kLog2e, kLog2e)));
+            rate.h[k][i] = pair(v.x < -FLT_MAX ? -FLT_MAX : v.x, v.y < -FLT_MAX ? -FLT_MAX : v.y);
+        }
+}
 
 // h <- exp2(A s) h + b for a lane's states (A in units of log 2).
 template <int kBlocks>

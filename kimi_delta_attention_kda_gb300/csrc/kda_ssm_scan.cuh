@@ -31,7 +31,6 @@
 // so.
 #pragma once
 
-#include <cfloat>
 #include <type_traits>
 
 #include "kda_ssm.cuh"
@@ -496,14 +495,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     const int64_t ch = ch0 + (live ? local : 0);
     State<kHold> rate, s;
     load_states(a.A, true, ch, n0, S, rate);
-#pragma unroll
-    for (int k = 0; k < kHold; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            // (Finite, for the zero steps behind the end; 2^-FLT_MAX is 0 for any other step.)
-            const float2 v = halves(mul_pair(rate.h[k][i], pair(kLog2e, kLog2e)));
-            rate.h[k][i] = pair(v.x < -FLT_MAX ? -FLT_MAX : v.x, v.y < -FLT_MAX ? -FLT_MAX : v.y);
-        }
+    to_log2(rate);
     auto none = [&]() {
 #pragma unroll
         for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;

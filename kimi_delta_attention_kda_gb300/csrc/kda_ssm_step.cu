@@ -146,10 +146,7 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
     const float x = __bfloat162float(x_raw), z = __bfloat162float(z_raw), du = dt * x;
     State<kBlocks> rate;
     rates.unpack(rate);
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) rate.h[k][i] = mul_pair(rate.h[k][i], pair(kLog2e, kLog2e));
+    to_log2(rate);
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

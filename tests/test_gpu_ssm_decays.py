@@ -64,3 +64,27 @@ def test_infinite_states_stay(kda, S):  # noqa: F811
             kda.set_segments(on, chunks)
             fin = decayed(kda, torch.full((1, T, 40), step), -torch.ones(40, S), init).cpu()
             assert torch.equal(torch.isinf(fin), torch.isinf(init)) and torch.equal(fin.sign(), init.sign())
+
+
+@pytest.mark.parametrize("rate", [float("-inf"), torch.finfo(F32).min])
+@pytest.mark.parametrize("S", [16, 5, 8, 32, 64])
+@pytest.mark.parametrize("state", [F32, BF16])
+@pytest.mark.parametrize("softplus", [False, True])
+def test_single_tokens_without_a_step(kda, rate, S, state, softplus):  # noqa: F811
+    """A step of zero leaves the states as they are, whatever the rates; any other step leaves
+    nothing of states whose rate has no bound."""
+    N, dim = 6, 40
+    d = on_gpu(draw((N,), dim, S, S, dt=F32, init=N, state=state, bias=False))
+    pool = d.pop("init_state")
+    d["A"][3] = d["A"][17, 0] = rate
+    d["dt"][:] = -200.0 if softplus else 0.0   # softplus(-200) is 0 in FP32
+    before = pool.clone()
+    out = kda.ssm_decode(**d, state=pool, dt_softplus=softplus)
+    assert torch.equal(pool, before) and torch.isfinite(out).all()
+    d["dt"].fill_(0.5)
+    d["A"][3] = d["A"][17, 0] = -1e30
+    want_pool = pool.clone()
+    want = kda.ssm_decode(**d, state=want_pool, dt_softplus=softplus)
+    d["A"][3] = d["A"][17, 0] = rate
+    got = kda.ssm_decode(**d, state=pool, dt_softplus=softplus)
+    assert torch.equal(got, want) and torch.equal(pool, want_pool) and torch.isfinite(pool).all()
