@@ -172,6 +172,22 @@ __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& 
         }
 }
 
+// h <- exp2(A s) h + b over a whole span, s the sum of its steps.  In two factors, each
+// finite: a state of zero stays zero whatever it would grow by, and one that grows beyond 2^128
+// from far below 1, or comes back from far above it, keeps its value as in the walk.
+// (A growth of more than 2^254, cut to that, leaves no normal number finite.)
+template <int kHold>
+__device__ __forceinline__ void decay_span(State<kHold>& s, const State<kHold>& rate, float step, const State<kHold>& add) {
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 x = halves(mul_pair(rate.h[k][i], pair(0.5f * step, 0.5f * step)));
+            const uint64_t e = pair(exp2_fast(fminf(x.x, 127.f)), exp2_fast(fminf(x.y, 127.f)));
+            s.h[k][i] = fma_pair(e, mul_pair(e, s.h[k][i]), add.h[k][i]);
+        }
+}
+
 // The walking warps' barrier.
 template <int kBlocks>
 __device__ __forceinline__ void walkers_meet() {
@@ -522,8 +538,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             for (int64_t i = w.first_span; i < span; ++i) {
                 State<kHold> add;
                 load_states(a.span_states, true, i * a.dim + ch, n0, 16 * kBlocks, add);
-                const float step = a.span_steps[i * a.dim + ch];
-                decay<kHold>(s, rate, pair(step, step), add.h);
+                decay_span(s, rate, a.span_steps[i * a.dim + ch], add);
             }
         }
     }

@@ -88,3 +88,33 @@ def test_single_tokens_without_a_step(kda, rate, S, state, softplus):  # noqa: F
     d["A"][3] = d["A"][17, 0] = rate
     got = kda.ssm_decode(**d, state=pool, dt_softplus=softplus)
     assert torch.equal(got, want) and torch.equal(pool, want_pool) and torch.isfinite(pool).all()
+
+
+@pytest.mark.parametrize("S", [16, 5, 64])
+def test_growing_states(kda, S):  # noqa: F811
+    """Rates above zero, and steps below it, over spans in which an exponential of the whole
+    growth would not be finite: states of zero stay zero, and what has grown is a number
+    where the tokens one by one give one."""
+    T, dim = 2048, 40
+    d = draw((1, T), dim, S, 5, dt=F32, init=1, bias=False, z=False)
+    gen = torch.Generator().manual_seed(3)
+    d["dt"] = 0.2 * (0.9 + 0.2 * torch.rand(1, T, dim, generator=gen))
+    # Even channels: a rate above 0, nothing but zeros up to the last 100 tokens.
+    d["A"][0::2] = 1.0
+    d["x"][:, :-100, 0::2] = 0
+    d["init_state"][:, 0::2] = 0
+    # Odd ones: 512 tokens grow from 1e-30 by about exp(102), as many take it back, and so on;
+    # of four channels by exp(-102) first.
+    d["A"][1::2] = -1.0
+    sign = torch.ones(T)
+    sign[:512] = sign[1024:1536] = -1
+    d["dt"][:, :, 1::2] *= sign[:, None]
+    d["x"][:, :, 1::2] = 0
+    d["dt"][:, :, 1:9:2] *= -1
+    d["init_state"][:, 1:9:2] *= 1e30
+    d["init_state"][:, 9::2] *= 1e-30
+    want = want_of(d, softplus=False)
+    assert torch.isfinite(want[1]).all()
+    for on, chunks in ((False, 0), (True, 32), (True, 0)):
+        kda.set_segments(on, chunks)
+        check(kda, d, softplus=False, want=want)
