@@ -67,6 +67,14 @@ __device__ __forceinline__ void to_log2(State<kBlocks>& rate) {
         }
 }
 
+// What the exponential of x takes from a state, on average: it comes out 6e-9 too small for
+// arguments above -2^-8, and 2.2e-8 below (measured on GB300 in steps of a half octave:
+// 5e-9 .. 1e-8 and 1.4e-8 .. 3e-8), and is 1 above -2^-23.
+__device__ __forceinline__ float lost(float x) {
+    const float part = x > -0x1p-8f ? 6e-9f : 2.2e-8f;
+    return x > -0x1p-23f ? 1e-30f : part;   // (not 0, for states that are infinite)
+}
+
 // h <- exp2(A s) h + b for a lane's states (A in units of log 2).
 template <int kBlocks>
 __device__ __forceinline__ void decay(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt, const uint64_t (&b)[kBlocks][2]) {

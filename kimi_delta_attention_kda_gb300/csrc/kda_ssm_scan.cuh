@@ -146,9 +146,7 @@ __device__ __forceinline__ void store_states(void* p, bool f32, int64_t row, int
     else
         store_row(static_cast<__nv_bfloat16*>(p) + row * S, n0, S, s);
 }
-// A tile's decays are off on average: the exponential comes out 6e-9 too small for
-// arguments above -2^-8, and 2.2e-8 below (measured on GB300 in steps of a half octave:
-// 5e-9 .. 1e-8 and 1.4e-8 .. 3e-8), which adds up in states that last for hundreds of
+// A tile's decays are off on average, see lost(), which adds up in states that last for hundreds of
 // tokens, where roundings cancel.  Once a tile, in its middle, the states get it back, by the
 // argument that the least step of the tile's first half gives, below which no token of
 // that half is: none if that is 0 (what stands still keeps its bits), and where the second
@@ -157,10 +155,6 @@ __device__ __forceinline__ void store_states(void* p, bool f32, int64_t row, int
 // by 1.5e-6 (as exact exponentials in FP32: 1e-6), without this by 5.6e-6; around -0.014 by
 // 3.2e-6 and 2.5e-5.  (Where the state is gone by the tile's end it does not matter.)  3 %
 // of the time, most of it for the least step.
-__device__ __forceinline__ float lost(float x) {
-    const float part = x > -0x1p-8f ? kTile * 6e-9f : kTile * 2.2e-8f;
-    return x > -0x1p-23f ? 1e-30f : part;   // (the exponential is 1 there; not 0, for states that are infinite)
-}
 template <int kBlocks>
 __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& rate, uint64_t dt) {
 #pragma unroll
@@ -168,7 +162,7 @@ __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float2 x = halves(mul_pair(rate.h[k][i], dt));
-            s.h[k][i] = fma_pair(s.h[k][i], pair(lost(x.x), lost(x.y)), s.h[k][i]);
+            s.h[k][i] = fma_pair(s.h[k][i], pair(kTile * lost(x.x), kTile * lost(x.y)), s.h[k][i]);
         }
 }
 

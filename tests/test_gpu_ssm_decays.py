@@ -118,3 +118,34 @@ def test_growing_states(kda, S):  # noqa: F811
     for on, chunks in ((False, 0), (True, 32), (True, 0)):
         kda.set_segments(on, chunks)
         check(kda, d, softplus=False, want=want)
+
+
+def test_long_conversations(kda):  # noqa: F811
+    """2000 single tokens on FP32 states that only decay: bounds as in test_small_arguments and
+    test_slow_states."""
+    gen = torch.Generator().manual_seed(4)
+    T, N, dim, S = 2000, 2, 64, 16
+    for mean in (1e-3, 1e-2):
+        dt = mean * (0.5 + torch.rand(T, N, dim, generator=gen))
+        A, init = -(0.7 + 0.6 * torch.rand(dim, S, generator=gen)), 1 + torch.rand(N, dim, S, generator=gen)
+        pool, dev, A_dev = init.cuda(), dt.cuda(), A.cuda()
+        zero, keys = torch.zeros(N, dim, dtype=BF16, device="cuda"), torch.zeros(N, 1, S, dtype=BF16, device="cuda")
+        for t in range(T):
+            kda.ssm_decode(zero, dev[t], A_dev, keys, keys, pool, dt_softplus=False)
+        want = init.double() * torch.exp(dt.double().sum(0)[..., None] * A.double())
+        off = pool.cpu().double() / want - 1
+        rms = 2.0 ** -24 * (T * 2 / 3) ** 0.5
+        assert off.mean().abs() < 5 * rms / (N * dim * S) ** 0.5 + (4e-9 if mean < 2e-3 else 1e-8) * T
+        assert off.pow(2).mean().sqrt() < rms + 1e-8 * T
+
+
+def test_infinite_states_stay_in_pools(kda):  # noqa: F811
+    """As test_infinite_states_stay, for single tokens."""
+    for step in (0.0, 1e-3):
+        pool = torch.ones(3, 40, 16, device="cuda")
+        pool[0, 3, 1], pool[2, 7, 0] = float("inf"), float("-inf")
+        before = pool.clone()
+        zero, keys = torch.zeros(3, 40, dtype=BF16, device="cuda"), torch.zeros(3, 1, 16, dtype=BF16, device="cuda")
+        for _ in range(3):
+            kda.ssm_decode(zero, zero.float() + step, -torch.ones(40, 16, device="cuda"), keys, keys, pool, dt_softplus=False)
+        assert torch.equal(torch.isinf(pool), torch.isinf(before)) and torch.equal(pool.sign(), before.sign())
