@@ -47,8 +47,7 @@ __device__ __forceinline__ uint4 gather4(const float* p, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane's states, of one channel: 16 k + 4 c + 2 i and the next (c the lane's place among
-// the four that share the channel).
+// A lane's states, of one channel, kBlocks times four of them in pairs.
 template <int kBlocks>
 struct State {
     uint64_t h[kBlocks][2];
@@ -65,6 +64,13 @@ __device__ __forceinline__ void to_log2(State<kBlocks>& rate) {
             const float2 v = halves(mul_pair(rate.h[k][i], pair(kLog2e, kLog2e)));
             rate.h[k][i] = pair(v.x < -FLT_MAX ? -FLT_MAX : v.x, v.y < -FLT_MAX ? -FLT_MAX : v.y);
         }
+}
+
+// The rates of states behind S, which the lanes of a short row have: any below 0, as an infinite step
+// times 0 would make NaN of them, and so of y.  Two from state n on.
+__device__ __forceinline__ void no_rates(uint64_t& rate, int n, int S) {
+    const float2 v = halves(rate);
+    rate = pair(n < S ? v.x : -1.f, n + 1 < S ? v.y : -1.f);
 }
 
 // What the exponential of x takes from a state, on average: it comes out 6e-9 too small for

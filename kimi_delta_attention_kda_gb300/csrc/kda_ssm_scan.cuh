@@ -9,7 +9,7 @@
 // in it: 8 S + 20 operations for 8 bytes, of which S exponentials.  A CTA has 32
 // channels and a span of tokens, 32 at a time: some of its threads form dt, dt x and the rows of B and C as FP32 in
 // shared memory; the warps of the others walk 8 channels each through the tokens, four lanes a
-// channel with four of every 16 states in their registers (64 states: two warps).  A lane sums
+// channel with a quarter of the states in their registers (64 states: two warps, an eighth).  A lane sums
 // its products with C, and every four tokens the four lanes of a channel hand each
 // other their sums, so that each ends with one token's.  All of it is FP32.  (Summed on the
 // tensor cores, TF32, the call below took 546 us, but cut the states to 10 bits on the
@@ -70,6 +70,7 @@ __device__ __forceinline__ void gate8(const float (&z)[8], float (&y)[8]) {
 // rows of B and of C, and y, a sum over each warp's part of the states.  Strides and
 // places that keep the lanes' accesses on different banks.
 constexpr int kStepStride = 2 * kChannels + 8, kStepWords = kTile * kStepStride;
+constexpr int kNoStep = 2 * kChannels;   // two words of 0 behind every token's
 constexpr int kYStride = kChannels + 4;
 template <int kBlocks, bool kStates>
 struct Buffer {
@@ -97,12 +98,12 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p, bool whole) {
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// A lane's states of a row of S: four from n0 on, and from every 16 behind.
+// A lane's states of a row of S: 4 kHold from n0 on.
 template <int kHold, typename T>
 __device__ __forceinline__ void load_row(const T* row, int n0, int S, State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        const int n = n0 + 16 * k;
+        const int n = n0 + 4 * k;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (S % 4 == 0) {
             if (n < S) load_vec<4>(row + n, v);
@@ -119,7 +120,7 @@ template <int kHold, typename T>
 __device__ __forceinline__ void store_row(T* row, int n0, int S, const State<kHold>& s) {
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        const int n = n0 + 16 * k;
+        const int n = n0 + 4 * k;
         const float2 a = halves(s.h[k][0]), b = halves(s.h[k][1]);
         const float v[4] = {a.x, a.y, b.x, b.y};
         if (S % 4 == 0) {
@@ -169,7 +170,8 @@ __device__ __forceinline__ void settle(State<kBlocks>& s, const State<kBlocks>& 
 // h <- exp2(A s) h + b over a whole span, s the sum of its steps.  In two factors, each
 // finite: a state of zero stays zero whatever it would grow by, and one that grows beyond 2^128
 // from far below 1, or comes back from far above it, keeps its value as in the walk.
-// (A growth of more than 2^254, cut to that, leaves no normal number finite.)
+// (A growth of more than 2^254, cut to that, leaves no normal number finite, and a decay to
+// 2^-252 nothing of one; an infinite state stays one.)
 template <int kHold>
 __device__ __forceinline__ void decay_span(State<kHold>& s, const State<kHold>& rate, float step, const State<kHold>& add) {
 #pragma unroll
@@ -177,7 +179,7 @@ __device__ __forceinline__ void decay_span(State<kHold>& s, const State<kHold>& 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float2 x = halves(mul_pair(rate.h[k][i], pair(0.5f * step, 0.5f * step)));
-            const uint64_t e = pair(exp2_fast(fminf(x.x, 127.f)), exp2_fast(fminf(x.y, 127.f)));
+            const uint64_t e = pair(exp2_fast(fminf(fmaxf(x.x, -126.f), 127.f)), exp2_fast(fminf(fmaxf(x.y, -126.f), 127.f)));
             s.h[k][i] = fma_pair(e, mul_pair(e, s.h[k][i]), add.h[k][i]);
         }
 }
@@ -309,6 +311,8 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             of_channel[tid] = a.dt_bias && tid < channels ? a.dt_bias[ch0 + tid] : 0.f;
             if (!kStates) of_channel[kChannels + tid] = a.D && tid < channels ? a.D[ch0 + tid] : 0.f;
         }
+        if (tid < 2 * kTile)
+            *reinterpret_cast<float2*>(smem + (tid / kTile) * Buf::kWords + tid % kTile * kStepStride + kNoStep) = make_float2(0.f, 0.f);
         asm volatile("bar.sync 2, %0;" ::"n"(kRole) : "memory");
         auto eight_of = [&](const float* p, float (&v)[8]) {
             const float4 lo = *reinterpret_cast<const float4*>(p + mine), hi = *reinterpret_cast<const float4*>(p + mine + 4);
@@ -496,16 +500,21 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
         return;
     }
 
-    // ---- the walk: 8 channels a warp, four lanes each, with four of every 16 states
+    // ---- the walk: 8 channels a warp, four lanes each, with 4 kHold states
     constexpr int kHold = kBlocks / kSplit<kBlocks>;
     const int walker = kWalkers<kBlocks> == kRole ? tid : threadIdx.x;
     const int warp = walker >> 5, lane = walker & 31, c = lane >> 3, part = warp >> 2;
-    const int local = 8 * (warp & 3) + (lane & 7), n0 = 16 * kHold * part + 4 * c;
+    const int local = 8 * (warp & 3) + (lane & 7), n0 = 4 * kHold * (4 * part + c);
     const bool live = local < channels;
     const int64_t ch = ch0 + (live ? local : 0);
     State<kHold> rate, s;
     load_states(a.A, true, ch, n0, S, rate);
     to_log2(rate);
+    if (!kFast)
+#pragma unroll
+        for (int k = 0; k < kHold; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) no_rates(rate.h[k][i], n0 + 4 * k + 2 * i, S);
     auto none = [&]() {
 #pragma unroll
         for (int k = 0; k < kHold; ++k) s.h[k][0] = s.h[k][1] = 0ull;
@@ -548,7 +557,9 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     };
     if (!kStates) close(0);
     float steps = 0.f;   // the sum of dt
-    const int step0 = step_at(local, 0) + 2 * (local & 1), rows0 = Buf::kB + n0;
+    // States behind S, which the lanes of a short row have, stay 0: an infinite dt x would
+    // make NaN of them, and so of y.  Whole lanes of them read steps of 0 (kNoStep).
+    const int own0 = step_at(local, 0) + 2 * (local & 1), step0 = n0 < S ? own0 : kNoStep, rows0 = Buf::kB + n0;
     const int keys0 = Buf::kC + n0, y0 = Buf::kY + part * Buf::kHalf + c * kYStride + local;
     auto four_of = [&](const float* p, uint64_t (&v)[2]) {
         const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(p);
@@ -566,9 +577,12 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
             const float2 dd = *reinterpret_cast<const float2*>(buf + step0 + (t + j) * kStepStride);   // dt, dt x
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
-                four_of(buf + rows0 + (t + j) * Buf::kRow + 16 * k, b[k]);
+                four_of(buf + rows0 + (t + j) * Buf::kRow + 4 * k, b[k]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) b[k][i] = mul_pair(b[k][i], pair(dd.y, dd.y));
+                for (int i = 0; i < 2; ++i) {
+                    const int n = n0 + 4 * k + 2 * i;
+                    b[k][i] = mul_pair(b[k][i], pair(kFast || n < S ? dd.y : 0.f, kFast || n + 1 < S ? dd.y : 0.f));
+                }
             }
             decay<kHold>(s, rate, pair(dd.x, dd.x), b);
             if (kStates) {
@@ -578,7 +592,7 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
 #pragma unroll
                 for (int k = 0; k < kHold; ++k) {
                     uint64_t key[2];
-                    four_of(buf + keys0 + (t + j) * Buf::kRow + 16 * k, key);
+                    four_of(buf + keys0 + (t + j) * Buf::kRow + 4 * k, key);
                     sum = k == 0 ? mul_pair(key[0], s.h[k][0]) : fma_pair(key[0], s.h[k][0], sum);
                     sum = fma_pair(key[1], s.h[k][1], sum);
                 }
@@ -600,9 +614,9 @@ __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3
     // The least step of a tile's first half, 0 where there are negative ones: each of a
     // channel's lanes looks at every fourth.
     auto least_step = [&](const float* buf) {
-        float least = buf[step0 + c * kStepStride];
+        float least = buf[own0 + c * kStepStride];
 #pragma unroll
-        for (int t = 4; t < kTile / 2; t += 4) least = fminf(least, buf[step0 + (t + c) * kStepStride]);
+        for (int t = 4; t < kTile / 2; t += 4) least = fminf(least, buf[own0 + (t + c) * kStepStride]);
         least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 8));
         return fmaxf(fminf(least, __shfl_xor_sync(0xffffffffu, least, 16)), 0.f);
     };
@@ -667,7 +681,9 @@ cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
 }
 template <int kBlocks>
 cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
-    if (!a.vec || !a.vec_bc || !a.softplus || a.dim / a.groups < kChannels) return prefill<kBlocks, kAny>(a, stream, launches);
+    // (Lanes with states in the row and behind it are kAny's.)
+    const bool mixed = a.nstate % (4 * kBlocks / kSplit<kBlocks>) != 0;
+    if (!a.vec || !a.vec_bc || !a.softplus || mixed || a.dim / a.groups < kChannels) return prefill<kBlocks, kAny>(a, stream, launches);
     if (a.bc_f32)
         return a.dt_f32 ? prefill<kBlocks, kPlain + kDtF32 + kKeysF32>(a, stream, launches)
                         : prefill<kBlocks, kPlain + kKeysF32>(a, stream, launches);

@@ -163,6 +163,11 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
     State<kBlocks> rate;
     rates.unpack(rate);
     to_log2(rate);
+    if (kRows != kWhole)
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) no_rates(rate.h[k][j], 16 * k + 4 * c + 2 * j, S);
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -180,7 +185,13 @@ __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) b.h[k][j] = mul_pair(b.h[k][j], pair(add, add));
+                for (int j = 0; j < 2; ++j) {
+                    // States behind S, which the lanes of a short row have, stay 0: an infinite
+                    // dt x would make NaN of them, and so of y.
+                    const int n = 16 * k + 4 * c + (kRows == kOnes ? 2 * j : 0);
+                    const float lo = kRows == kWhole || n < S ? add : 0.f, hi = kRows != kOnes ? lo : n + 1 < S ? add : 0.f;
+                    b.h[k][j] = mul_pair(b.h[k][j], pair(lo, hi));
+                }
             advance<kBlocks, kStateF32>(s, rate, step, b.h);
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
@@ -218,8 +229,9 @@ cudaError_t pick_decode(const SsmArgs& a, cudaStream_t stream) {
 }
 template <int kBlocks>
 cudaError_t pick_decode(const SsmArgs& a, cudaStream_t stream) {
-    // (16 states, 128 x 12288: 35 us as kWhole, 38 as kFours; 32 and 64 as fast as kFours.)
-    if (kBlocks == 1 && a.vec_bc && a.nstate == 16) return pick_decode<kBlocks, kBlocks == 1 ? kWhole : kFours>(a, stream);
+    // (16 states, 128 x 12288: 35 us as kWhole, 38 as kFours; 64 states, 32 x 12288, 35 and 40; but 32 states,
+    // 64 x 12288, 40 and 38.7.)
+    if (kBlocks != 2 && a.vec_bc && a.nstate == 16 * kBlocks) return pick_decode<kBlocks, kBlocks != 2 ? kWhole : kFours>(a, stream);
     return a.vec_bc ? pick_decode<kBlocks, kFours>(a, stream) : pick_decode<kBlocks, kOnes>(a, stream);
 }
 

@@ -149,3 +149,33 @@ def test_infinite_states_stay_in_pools(kda):  # noqa: F811
         for _ in range(3):
             kda.ssm_decode(zero, zero.float() + step, -torch.ones(40, 16, device="cuda"), keys, keys, pool, dt_softplus=False)
         assert torch.equal(torch.isinf(pool), torch.isinf(before)) and torch.equal(pool.sign(), before.sign())
+
+
+@pytest.mark.parametrize("S", [1, 3, 5, 8, 16, 20, 24, 48, 64])
+@pytest.mark.parametrize("bc", [BF16, F32])
+def test_infinite_inputs(kda, S, bc):  # noqa: F811
+    """An infinite x or step gives infinite states and outputs where the definition does, not NaN,
+    whatever the length of a row of states."""
+    T, dim = 150, 40
+    d = draw((1, T), dim, S, S, dt=F32, bc=bc, init=1, z=False, D=False)
+    d["B"], d["C"] = d["B"].abs() + 1, d["C"].abs() + 1
+    d["A"] = -torch.arange(1, S + 1).expand(dim, S).contiguous() / 64.0
+    d["x"][0, 10, 3], d["x"][0, 60, 5] = float("inf"), float("-inf")
+    d["dt"][0, 12, 7], d["x"][0, 12, 7] = float("inf"), 1.0
+
+    def same(got, want, what):
+        for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(kind(got).cpu(), kind(want)), what
+    o, f, _, _ = want_of(d)
+    assert torch.isposinf(o[0, 12:, [3, 7]]).all() and torch.isneginf(o[0, 60:, 5]).all()
+    for on, chunks in ((False, 0), (True, 4)):
+        kda.set_segments(on, chunks)
+        out, fin = kda.ssm_prefill(**on_gpu(d))
+        same(out, o, "out")
+        same(fin, f, "final")
+    for state in (F32, BF16):
+        dev = on_gpu(d)
+        pool = dev.pop("init_state").to(state)
+        for t in range(70):
+            one = {key: v[:, t] if key in ("x", "dt", "B", "C") and v is not None else v for key, v in dev.items()}
+            same(kda.ssm_decode(**one, state=pool), o[:, t], "token %d" % t)
