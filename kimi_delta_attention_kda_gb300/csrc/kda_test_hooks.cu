@@ -4,13 +4,14 @@
 // Compiled only into the test library libkda_testhooks.so, with
 // KDA_TEST_HOOKS defined and KDA_WAIT_BOUND_CYCLES = 10^5 (about 50 us), never
 // into libkda.so.  Each hook launches one CTA that uses the waits of the real
-// kernels (kda_common.cuh, kda_wait.cuh) on a ring or a barrier nobody completes
-// or a ready flag nobody sets.  A wait that runs out sets kDevPipeTimeout and returns; the kernel
+// kernels (kda_common.cuh, kda_wait.cuh, kda_ssm_scan.cuh) on a ring or a barrier nobody
+// completes or a ready flag nobody sets.  A wait that runs out sets kDevPipeTimeout and returns; the kernel
 // then leaves with nothing in flight, and the context stays usable.  Nothing
 // here faults or hangs: every wait is bounded, every copy stays inside the
 // caller's buffer and the CTA's shared memory.
 #ifdef KDA_TEST_HOOKS
 #include "kda_common.cuh"
+#include "kda_ssm_scan.cuh"
 #include "kda_wait.cuh"
 
 namespace kda {
@@ -149,6 +150,36 @@ extern "C" int kda_test_left_ring(const void* src, int filled, int left, int* st
 extern "C" int kda_test_wait_phase(int* status, int* out, void* stream_ptr) {
     stalled_phase_kernel<<<1, 96, 0, static_cast<cudaStream_t>(stream_ptr)>>>(status, out);
     return static_cast<int>(cudaGetLastError());
+}
+
+// The scan's second of two spans that run in turn, alone, on `stream`: 64 tokens of 32 channels
+// with 16 states (BF16 x, dt and out [64, 32], B and C [64, 16]; FP32 A [32, 16]), whose first
+// span's state is in states ([2, 32, 16] FP32; the second's is written).  relay: three ints,
+// (1, whether the first span's state is there, 0).  Without that flag the wait runs out.
+extern "C" int kda_test_span_wait(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm, void* out,
+                                  float* states, int* relay, int* status, void* stream_ptr) {
+    SsmArgs a = {};
+    a.x = x;
+    a.dt = dt;
+    a.A = A;
+    a.B = Bm;
+    a.C = Cm;
+    a.out = out;
+    a.span_states = states;
+    a.relay = relay;
+    a.status = status;
+    a.ldx = a.lddt = a.dim = 32;
+    a.ldb = a.ldc = a.nstate = 16;
+    a.N = a.groups = a.tiles = a.tiles_per_group = 1;
+    a.tokens = a.tokens_per_seq = 64;
+    a.spans_per_seq = 2;
+    a.span_tokens = 32;
+    a.spans = 1;   // of the launch
+    a.softplus = a.vec = a.vec8 = a.vec_bc = true;
+    a.tile_x = a.tile_dt = kSsmTile * 32 * 2;
+    a.tile_b = a.tile_c = kSsmTile * 16 * 2;
+    a.tile_out = kSsmTile * 32;
+    return static_cast<int>(run<1, false, false, kPlain>(a, static_cast<cudaStream_t>(stream_ptr)));
 }
 
 // The wait bound this library was compiled with, in clock cycles.
