@@ -210,14 +210,14 @@ struct SsmCut {
 // Costs of the scan on GB300, in microseconds for 32 tokens (rows: up to 16, 32 and 64
 // states): uncut, of a CTA with one, two and three of them on its SM, of which
 // the fullest SM decides; cut, for each CTA's part on every SM, states and outputs.
-// T = 8192, uncut and cut: 5,120 channels 429 and 343 us, 6,144 429 and 415, 8,192
-// 428 and 556.
-constexpr double kSsmTileUs[3][3] = {{1.43, 1.68, 2.35}, {1.68, 2.49, 0}, {2.66, 4.51, 0}};
-constexpr double kSsmCutTileUs[3] = {1.27, 2.05, 3.65}, kSsmCutUs = 10;
+// T = 8192, uncut and cut: 5,120 channels 458 and 354 us, 6,144 459 and 429, 8,192
+// 459 and 559.
+constexpr double kSsmTileUs[3][3] = {{1.42, 1.81, 2.47}, {1.69, 2.65, 0}, {2.63, 4.52, 0}};
+constexpr double kSsmCutTileUs[3] = {1.27, 2.1, 3.7}, kSsmCutUs = 10;
 // Spans one after the other (more chains than SMs), a sixteenth of the tokens each, 512
 // at least: for the flags' clearing, and for each span that takes up a state.  Uncut and so:
-// 8192 tokens of 12,288 channels 602 and 547 us, of 10,240 600 and 523, two prompts of
-// 4096 tokens 591 and 523, 4096 tokens of 12,288 with 64 states 882 and 771.
+// 8192 tokens of 12,288 channels 633 and 586 us, of 10,240 632 and 566, two prompts of
+// 4096 tokens 627 and 555, 4096 tokens of 12,288 with 64 states 895 and 784.
 constexpr double kSsmRelayUs = 10, kSsmRelaySpanUs = 2.2;
 constexpr int64_t kSsmRelaySpans = 16, kSsmRelayMin = 16 * kSsmTile;
 // A span is this long at least: where that leaves more than one wave of CTAs, whole
