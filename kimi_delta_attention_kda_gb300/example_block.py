@@ -49,15 +49,14 @@ class Block:
         self.norm, self.mix_norm, self.post_norm = (
             (1 + 0.1 * torch.randn(n, generator=gen)).bfloat16().cuda() for n in (width, D, width))
         if self.conv:
-            self.filter = weight(sum(self.sizes[:3]), 4)
+            self.filters = weight(sum(self.sizes[:3]), 4).split(self.sizes[:3])
 
     def project(self, y, convolve):
         """q, k, v and the output gate as heads, the log-decays, and beta's logits."""
-        p = y @ self.w_in.t()
-        if self.conv:   # of q, k and v together, where they lie in the projection
-            n = sum(self.sizes[:3])
-            p = torch.cat([convolve(p[:, :n]), p[:, n:]], dim=-1)
-        p = [x.contiguous() for x in p.split(self.sizes, dim=-1)]
+        p = (y @ self.w_in.t()).split(self.sizes, dim=-1)
+        # (q, k and v are read where they lie in the projection, and written as the mixer takes them.)
+        done = [convolve(i, x) for i, x in enumerate(p[:3])] if self.conv else []
+        p = done + [x.contiguous() for x in p[len(done):]]
         q, k = (x.view(-1, self.key_heads, D) for x in p[:2])
         v, z = (x.view(-1, self.heads, D) for x in p[2:4])
         if self.kind == "la":
@@ -72,8 +71,8 @@ class Block:
         """Packed tokens [T, width]; (what the block adds, the final states, the mixer's in FP32)."""
         states = []
 
-        def convolve(x):
-            x, state = kda.conv_prefill(x[None], self.filter, cu_seqlens=cu)
+        def convolve(i, x):
+            x, state = kda.conv_prefill(x[None], self.filters[i], cu_seqlens=cu)
             states.append(state)
             return x[0]
         q, k, v, z, g, beta = self.project(y, convolve)
@@ -86,7 +85,7 @@ class Block:
 
     def token(self, y, pools, slots):
         """One token of each sequence [N, width], its states in its row of the pools."""
-        q, k, v, z, g, beta = self.project(y, lambda x: kda.conv_decode(x, self.filter, pools[0], slots=slots))
+        q, k, v, z, g, beta = self.project(y, lambda i, x: kda.conv_decode(x, self.filters[i], pools[i], slots=slots))
         if self.kind == "la":
             o = kda.la_decode(q, k, v, g, pools[-1], slots)
         else:
