@@ -545,7 +545,7 @@ int kda_la_workspace_bytes(int64_t B, int64_t T, int64_t H, int packed, int64_t*
  * needed) and the limit on tokens are those of kda_prefill.  Alignment: 16 bytes
  * but for x and cu_seqlens (8).  out may overlap no input; it and final_state no
  * input and not each other.  FP32 inside, one rounding of out.  Rows and
- * channels in multiples of 8 (ldx, D, and x on 16 bytes) are read fastest.
+ * channels in multiples of 4 (ldx, D, and x on 8 bytes) are read fastest.
  */
 int kda_conv_prefill(const void* x, int64_t ldx, const void* weight, const void* bias,
                      const void* init_state, void* out, void* final_state, int64_t B, int64_t T,
@@ -573,7 +573,8 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  *   dt          : BF16 or FP32 (KDA_FLAG_DT_F32), a row of dim for each token
  *   Bm, Cm      : BF16 or FP32 (KDA_FLAG_BC_F32), a row of [groups, nstate] for each token
  *   ldx, lddt, ldb, ldc, ldz : elements between rows, at least a row's width
- *   A           : FP32 [dim, nstate], contiguous, below infinity; D, dt_bias: FP32 [dim] or NULL
+ *   A           : FP32 [dim, nstate], contiguous, below infinity (minus infinity: a state
+ *                 that any step above 1e-36 clears); D, dt_bias: FP32 [dim] or NULL
  *   out         : BF16 [tokens, dim], contiguous
  *   init_state  : [N, dim, nstate] or NULL for zeros; BF16, or FP32 with KDA_FLAG_STATE_F32
  *   final_state : the same type, or NULL (not written); may be init_state
@@ -584,14 +585,15 @@ int kda_conv_decode(const void* x, int64_t ldx, const void* weight, const void* 
  * bytes, dt, B and C in FP32 on 16, 32 channels or more to a group in multiples of 4, and
  * nstate a multiple of 4 run fastest).
  * out and final_state may overlap no input and not each other.
- * The states and all sums are FP32, and out is rounded once.  A NaN or an infinity in a token reaches no earlier token, no other
+ * The states and all sums are FP32, and out is rounded once.  The exponential's mean error
+ * (6e-9 to 2.2e-8 of a state a token) is made up for by the 32 tokens.  A NaN or an infinity in a token reaches no earlier token, no other
  * channel (but through B and C, its group's) and no other sequence.
  * When there are too few channels to fill the GPU the tokens are cut into
  * spans: one launch forms the state each span ends with, one the outputs from
  * what the spans before leave.  kda_set_segments governs this (off: no cut; a
  * forced length is rounded up to whole 32 tokens).  Where there are more than fill
- * it evenly, spans may run one after the other, which changes no bit and is governed by
- * nothing.  Equal calls give equal bits.  Scratch comes from the library's
+ * it evenly, spans may run one after the other, which changes no bit, whether cuts are on or
+ * off; a forced length takes their place.  Equal calls give equal bits.  Scratch comes from the library's
  * stream-ordered pool: with spans of either kind an FP32 state for each span and
  * channel, and a copy of the initial states where final_state is init_state.
  */
@@ -605,7 +607,8 @@ int kda_ssm_prefill(const void* x, int64_t ldx, const void* dt, int64_t lddt, co
 /*
  * One token per sequence of the same operation, on a pool of states: rows are
  * the sequences' tokens, state [pool, dim, nstate] (BF16 or FP32 as above) is updated in
- * place, slots as kda_la_decode.
+ * place, slots as kda_la_decode.  FP32 states: the exponential's mean error is made up for
+ * at every token.
  */
 int kda_ssm_decode(const void* x, int64_t ldx, const void* dt, int64_t lddt, const float* A,
                    const void* Bm, int64_t ldb, const void* Cm, int64_t ldc, const float* D,

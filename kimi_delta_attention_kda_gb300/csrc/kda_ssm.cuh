@@ -53,8 +53,8 @@ struct State {
     uint64_t h[kBlocks][2];
 };
 
-// Rates in units of log 2, finite: 2^-FLT_MAX is 0 for every step but 0, and 1 for that,
-// where minus infinity would give NaN.  (NaN stays.)
+// Rates in units of log 2, finite: 2^(-FLT_MAX s) is 0 for every step s above 1e-36, and 1 for
+// a step of 0, where minus infinity would give NaN.  (NaN stays.)
 template <int kBlocks>
 __device__ __forceinline__ void to_log2(State<kBlocks>& rate) {
 #pragma unroll

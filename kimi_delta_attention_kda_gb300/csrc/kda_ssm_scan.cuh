@@ -15,20 +15,22 @@
 // tensor cores, TF32, the call below took 546 us, but cut the states to 10 bits on the
 // way to out: outputs too small by 3.5e-4 on average.)
 //
-// 8192 tokens of 12,288 channels and 16 states: 584 us, where the bytes take 119 and
-// the exponentials alone 172.
+// 8192 tokens of 12,288 channels and 16 states: 586 us, where the bytes take 119 and
+// the exponentials alone 172.  Of the time shared memory's pipe is busy 80 % (a walking lane reads
+// 40 bytes a token), the exponentials' unit 35 %, and 61 % of the issue slots are used; warps
+// wait most at the barrier between staging and walking, then for shared memory.
 
 // Few (sequence, channel) chains are cut into spans of tokens: a first launch
 // forms the state each span ends with (and the sum of its dt: the decay over a
 // span is exp(A sum dt)), a second one each span's incoming state from those
-// before it, and its outputs.  8192 tokens of 768 channels take 62 us so, 338 uncut.
+// before it, and its outputs.  8192 tokens of 768 channels take 62 us so, 332 uncut.
 //
 // Many chains that do not fill the SMs evenly are cut too, and their spans run one
 // after the other (SsmArgs::relay): a CTA takes up the state that the span before
 // it left.  Nothing is computed twice and no bit changes; but a chain's spans run
 // on whichever SM has room, where whole chains would stay on an SM that is
-// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 584 us
-// so.
+// fuller than others: 8192 tokens of 12,288 channels (384 chains on 152 SMs) take 586 us
+// so, 633 uncut.
 #pragma once
 
 #include <type_traits>
@@ -260,10 +262,8 @@ __device__ __forceinline__ Part part_of(const SsmArgs& a, int64_t span) {
 // rows that can be read four values at a time, and groups of 32 channels or more (of
 // which the last CTA then also has some of the one before it, and writes the same
 // values).  That leaves out two fifths of the staging's instructions: 8192 x 12288,
-// 16 states, uncut 602 us, as kAny 690.
-// Registers are short: with three CTAs an SM (80 registers) values that wait in them spill,
-// and each spill costs more than it seems (16 of y held for the tile's end: 612 us for 549).
-// Two CTAs (128 registers) 615 us, four 686.
+// 16 states, uncut 634 us, as kAny 705.
+// Three CTAs an SM (80 registers): 587 us; two (128) 645, four (64) 656.
 constexpr int kAny = 0, kPlain = 1, kDtF32 = 1, kKeysF32 = 2;   // kPlain plus the types that are FP32
 template <int kBlocks, bool kStates, bool kPacked, int kMode>
 __global__ void __launch_bounds__(kWalkers<kBlocks> + kRole, kBlocks > 1 ? 2 : 3) ssm_kernel(SsmArgs a) {

@@ -92,8 +92,8 @@ __device__ __forceinline__ void advance(State<kBlocks>& s, const State<kBlocks>&
 // all loads are issued before the first value is used.
 // Bound by HBM: each state is read and written once, 2 x 4 S bytes (FP32) a channel.
 // 128 sequences of 12,288 channels and 16 states take 35 us, of which the bytes 31 at
-// the rate of a copy; with BF16 states 26 and 17, where the issue binds (440
-// instructions a warp, 72 % of the slots).
+// the rate of a copy; with BF16 states 26 and 17, where the issue binds (441
+// instructions a warp, 73 % of the slots; with FP32 states 505 and 65 %).
 constexpr int kStepThreads = 4 * kChannels;
 template <int kBlocks, Rows kRows, bool kStateF32, bool kKeysF32>
 __global__ void __launch_bounds__(kStepThreads, kBlocks == 1 ? 8 : kBlocks == 2 ? 4 : 3) ssm_decode_kernel(SsmArgs a, int blocks) {

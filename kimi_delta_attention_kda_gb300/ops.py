@@ -457,7 +457,8 @@ def ssm_prefill(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, 
     ``B == 1``).  x, dt, B, C and z may be parts of wider rows.  ``final_state`` may
     be ``init_state``; a new one takes its type, or ``state_dtype`` without one.
 
-    States and sums are FP32.
+    States and sums are FP32.  A rate of minus infinity clears its state at every
+    step above 1e-36; a step of 0 leaves all states as they are.
     """
     if stream is not None:
         _check_ssm(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens, out, final_state, state_dtype)
