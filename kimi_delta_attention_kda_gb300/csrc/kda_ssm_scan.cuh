@@ -681,7 +681,8 @@ cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
 }
 template <int kBlocks>
 cudaError_t prefill(const SsmArgs& a, cudaStream_t stream, int* launches) {
-    // (Lanes with states in the row and behind it are kAny's.)
+    // (Lanes with states in the row and behind it are kAny's, which keeps those behind at 0: 4096 tokens
+    // of 12,288 channels with 20 states 531 us, as the others 467.)
     const bool mixed = a.nstate % (4 * kBlocks / kSplit<kBlocks>) != 0;
     if (!a.vec || !a.vec_bc || !a.softplus || mixed || a.dim / a.groups < kChannels) return prefill<kBlocks, kAny>(a, stream, launches);
     if (a.bc_f32)
